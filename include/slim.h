@@ -19,6 +19,10 @@
  *   slim_lwc_calibrate  learnable weight clipping in place of SQC (SliM-LLM+)  (FAQ: GPTQ / AWQ / OmniQuant)
  *   slim_pack           group-structured bit-planes, no bitmap                (FAQ: storage)
  *   slim_qlinear        Y = X W_hat^T read from the planes (decode batches)    (FAQ: deployment)
+ *   slim_pack4          codes of up to 4 bits with their scales and zeros in one buffer  (FAQ: deployment)
+ *   slim_q4_linear      Y = X W_hat^T read from that buffer                    (FAQ: deployment)
+ *   slim_q4_experts     the same grouped by expert over sorted rows            (evaluation: Mixtral)
+ *   slim_token_logprobs log probabilities, entropy and best entries of logits  (evaluation: perplexity)
  *
  * Conventions shared by every call:
  *  - Pointers are DEVICE pointers unless the parameter says "host".  Arrays
@@ -394,6 +398,102 @@ size_t slim_qlinear_noalloc_scratch_bytes(void);
 int slim_qlinear_noalloc(const void *X, int xdt, int64_t t, int64_t m, const uint32_t *packed, const int8_t *bits,
                          int avg_bits, const float *scale, const float *zero, int64_t n, int group, float *Y,
                          void *stream);
+
+/* ------------------------------------------------------------------------
+ * Packing for the 4-bit products (rkmt.cn digest, FAQ on deployment; scime.ai
+ * summary, "Limitations": the cost of dequantization at inference).
+ *
+ * Every allocation whose widths are at most 4 (averages of 2 and 3 bits, or
+ * uniform widths up to 4) fits four bits a code; this layout spends them all
+ * so that a code is expanded in under one instruction, where the planes of
+ * slim_pack store exactly the average width.
+ *
+ * codes: uint8 [e, n, m] (e matrices; 1 for a single layer), scale and zero:
+ * float32 [e, n, k].  packed: uint32 [slim_pack4_words(e, n, m, g)], 16-byte
+ * aligned.  A record of 256 + 32 (128 / g) words holds rows 16 rb .. +15 and
+ * columns 128 ch .. +127 of a matrix; record (x, rb, ch) is number
+ * (x ceil(n/16) + rb) ceil(m/128) + ch.  Word 4 (16 lg + r) + i (lg, i < 4)
+ * has the codes of row 16 rb + r, columns c0 = 128 ch + 32 i + 8 lg .. +7:
+ * byte b is the code of column c0 + b plus 16 times that of c0 + 4 + b.  From
+ * word 256 on, words 2 (16 q + r) and + 1 are the float32 scale and zero of
+ * row 16 rb + r and group 128 ch / g + q.  What lies past n or m is zero.
+ * Bits of a code above the low four are ignored, and *info (device int32, may
+ * be NULL) is set to 1 if there are any (it is not written otherwise).
+ * e = 0 or n = 0 is a no-op.
+ * ---------------------------------------------------------------------- */
+#define SLIM_Q4_MAX_N (1 << 20)
+#define SLIM_Q4_MAX_EXPERTS 1024
+int64_t slim_pack4_words(int64_t e, int64_t n, int64_t m, int group);
+int slim_pack4(const uint8_t *codes, const float *scale, const float *zero, int64_t e, int64_t n, int64_t m,
+               int group, uint32_t *packed, int32_t *info, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Linear layer on the 4-bit layout.
+ *
+ *   Y[a, i] = sum_c X[a, c] * (q[i, c] - zero[i, c/g]) * scale[i, c/g]
+ *
+ * X: [t, m] in dtype xdt, Y: [t, n] in dtype ydt, packed: one matrix of
+ * slim_pack4.  0 <= t <= SLIM_QLINEAR_MAX_T (0 is a no-op), n <=
+ * SLIM_Q4_MAX_N.  Products are exact and summed in float32 per group, groups
+ * are scaled and summed in float32, and Y is rounded once; for a given t the
+ * order of the sums is fixed.  Rows of X do not touch each other; a row
+ * with an infinity or a NaN gives infinities or NaN.  Results for different t
+ * agree to float32 rounding, not bit for bit.  Workspace:
+ * slim_q4_linear_workspace(...) bytes, which may be 0 (ws is then ignored).
+ * ---------------------------------------------------------------------- */
+size_t slim_q4_linear_workspace(int64_t t, int64_t n, int64_t m, int group, int xdt);
+int slim_q4_linear(const void *X, int xdt, int64_t t, int64_t m, const uint32_t *packed, int64_t n, int group, void *Y,
+                   int ydt, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Linear layers of a mixture of experts on the 4-bit layout: rows sorted by
+ * expert, ragged.
+ *
+ *   Y[a, :] = w[a] * X[x(a), :] W_hat_j^T   for offsets[j] <= a < offsets[j+1]
+ *
+ * offsets: int32 [e + 1] on the device, nondecreasing within 0 .. r; an expert
+ * may have no rows.  x(a) = rows[a] (int32 [r]: a gather from the tokens'
+ * order, X then has tx rows) or a (rows NULL; tx must equal r).  w = row_scale
+ * (float32 [r], a router's gates) or 1 (NULL).  packed: e matrices of
+ * slim_pack4.  Rows of Y before offsets[0] and from offsets[e] on are left as
+ * they were.  The bounds are read on the device, nothing is copied to the
+ * host.  Offsets that decrease or leave 0 .. r make every row of Y NaN, and a
+ * row whose rows[a] is outside 0 .. tx - 1 is NaN (neither reads out of range).
+ * Numerics as for slim_q4_linear.  1 <= e <= SLIM_Q4_MAX_EXPERTS,
+ * 0 <= r <= SLIM_Q4_MAX_ROWS (0 is a no-op), tx >= 1 unless r = 0.
+ * ---------------------------------------------------------------------- */
+#define SLIM_Q4_MAX_ROWS (1 << 20)
+size_t slim_q4_experts_workspace(int64_t tx, int64_t r, int64_t e, int64_t n, int64_t m, int group, int xdt);
+int slim_q4_experts(const void *X, int xdt, int64_t tx, int64_t m, const int32_t *rows, const float *row_scale,
+                    int64_t r, const int32_t *offsets, int64_t e, const uint32_t *packed, int64_t n, int group,
+                    void *Y, int ydt, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Token log probabilities (rkmt.cn digest, evaluation: perplexity is the mean
+ * of -logprob; scime.ai summary, "Results").
+ *
+ * logits: [t, v] in dtype ldt, row a at logits + a * ld (ld >= v; rows need
+ * only be aligned to an element).  With p = softmax of a row, natural log:
+ *   logprob[a] = ln p[ids[a]]      ids int64 [t]; a negative id gives 0 (no
+ *                                  token: padding), one >= v gives NaN
+ *   entropy[a] = -sum_j p_j ln p_j (a masked entry, -inf, adds 0)
+ *   top_id[a, 0 .. top-1], top_logprob[a, ..]: the top entries by logit,
+ *                                  equal logits by ascending index
+ * float32 results from float32 sums.  A row that has no distribution (a NaN
+ * or +inf among its logits, or nothing but -inf) gives NaN and top_id -1; its
+ * negative id still gives logprob 0.  logprob (then ids may be NULL too) and
+ * entropy may be NULL; top_logprob and top_id are needed if top > 0.
+ * 0 <= t <= SLIM_LOGPROB_MAX_T (0 is a no-op), 1 <= v <= SLIM_LOGPROB_MAX_V,
+ * 0 <= top <= min(v, SLIM_LOGPROB_MAX_TOP).  Workspace:
+ * slim_token_logprobs_workspace(t, v, top) bytes, which may be 0.
+ * ---------------------------------------------------------------------- */
+#define SLIM_LOGPROB_MAX_TOP 64
+#define SLIM_LOGPROB_MAX_T (1 << 23)
+#define SLIM_LOGPROB_MAX_V (1 << 24)
+size_t slim_token_logprobs_workspace(int64_t t, int64_t v, int top);
+int slim_token_logprobs(const void *logits, int ldt, int64_t t, int64_t v, int64_t ld, const int64_t *ids, int top,
+                        float *logprob, float *entropy, float *top_logprob, int32_t *top_id, void *ws,
+                        size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * Kernel timing (instrumentation, not part of the method).  When enabled,

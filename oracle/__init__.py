@@ -38,6 +38,7 @@ from .sba import (rank_groups, allocation, trial_weights, kl_divergence, output_
 from .sqc import mask_3sigma, sqc_calibrate
 from .pack import pack_bitplanes, unpack_bitplanes, packed_words
 from .qlinear import dequant_weights, qlinear
+from .serving import pack4, q4_weight, q4_linear, q4_experts, token_logprobs
 from .gptq import upper_chol_inverse, gptq_quantize
 from .lwc import lwc_calibrate
 from .pipeline import quantize_layer
@@ -48,5 +49,5 @@ __all__ = [
     "fake_quant", "quant_codes", "rank_groups", "allocation", "trial_weights",
     "kl_divergence", "sba_search", "mask_3sigma", "sqc_calibrate", "pack_bitplanes",
     "unpack_bitplanes", "packed_words", "quantize_layer", "dequant_weights", "qlinear",
-    "upper_chol_inverse", "gptq_quantize", "lwc_calibrate",
+    "pack4", "q4_weight", "q4_linear", "q4_experts", "token_logprobs", "upper_chol_inverse", "gptq_quantize", "lwc_calibrate",
 ]

@@ -14,14 +14,21 @@ hand-written HIP kernels:
     qlinear        Y = X W_hat^T read from the planes (decode-sized batches)
                    (qlinear_noalloc: the same with no workspace, for callers that cannot allocate)
 
+    pack4          codes of up to 4 bits with scales and zeros in one streamable buffer
+    q4_linear      Y = X W_hat^T read from it, decode batches to prefill (MFMA bf16)
+    q4_experts     the same grouped by expert over rows sorted by expert
+    token_logprobs log probability of given tokens, entropy and best entries of logits (HBM)
+
 ``quantize_layer`` chains them on the current stream.  PyTorch only provides
 device memory and the stream.
 """
 from ._lib import (SlimError, load_library, hessian, salience, group_salience, sba_search, sba_search_ex, sqc_calibrate, gptq_quantize,
-                   lwc_calibrate, pack, qlinear, qlinear_noalloc, tau_table,
+                   lwc_calibrate, pack, qlinear, qlinear_noalloc, pack4, q4_linear, q4_experts,
+                   token_logprobs, tau_table,
                    timing_enable, timing_select, timing_reset, timing_read, SLIM_F32, SLIM_BF16)
 from .layer import quantize_layer
 
 __all__ = ["SlimError", "load_library", "hessian", "salience", "group_salience", "sba_search", "sba_search_ex", "sqc_calibrate",
-           "gptq_quantize", "lwc_calibrate", "pack", "qlinear", "qlinear_noalloc", "tau_table", "timing_enable", "timing_select", "timing_reset", "timing_read", "quantize_layer", "SLIM_F32",
+           "gptq_quantize", "lwc_calibrate", "pack", "qlinear", "qlinear_noalloc", "pack4", "q4_linear", "q4_experts",
+           "token_logprobs", "tau_table", "timing_enable", "timing_select", "timing_reset", "timing_read", "quantize_layer", "SLIM_F32",
            "SLIM_BF16"]

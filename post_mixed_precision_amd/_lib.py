@@ -16,6 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libslim.so")
 
 SLIM_F32, SLIM_BF16 = 0, 1
+LOGPROB_MAX_TOP = 64    # SLIM_LOGPROB_MAX_TOP
 STATUS = {0: "SLIM_OK", -1: "SLIM_E_NULL", -2: "SLIM_E_SHAPE", -3: "SLIM_E_DTYPE",
           -4: "SLIM_E_PARAM", -5: "SLIM_E_WORKSPACE", -6: "SLIM_E_HIP", -7: "SLIM_E_ALIGN"}
 
@@ -59,6 +60,17 @@ _SIGS = {
     "slim_qlinear_noalloc_scratch_bytes": (_c_sz, []),
     "slim_qlinear_noalloc": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_i64,
                                       _c_int, _c_vp, _c_vp]),
+    "slim_pack4_words": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_int]),
+    "slim_pack4": (_c_int, [_c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp, _c_vp]),
+    "slim_q4_linear_workspace": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_int, _c_int]),
+    "slim_q4_linear": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_i64, _c_int, _c_vp, _c_int, _c_vp, _c_sz,
+                                _c_vp]),
+    "slim_q4_experts_workspace": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_int]),
+    "slim_q4_experts": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64,
+                                 _c_int, _c_vp, _c_int, _c_vp, _c_sz, _c_vp]),
+    "slim_token_logprobs_workspace": (_c_sz, [_c_i64, _c_i64, _c_int]),
+    "slim_token_logprobs": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_int, _c_vp, _c_vp, _c_vp,
+                                     _c_vp, _c_vp, _c_sz, _c_vp]),
     "slim_timing_enable": (_c_int, [_c_int]),
     "slim_timing_select": (_c_int, [ctypes.c_char_p, _c_int]),
     "slim_timing_reset": (_c_int, []),
@@ -486,6 +498,154 @@ def qlinear_noalloc(X, packed, bits, scale, zero, group: int, avg_bits: int, Y=N
                                    _ptr(scale), _ptr(zero), n, group, _ptr(Y), _stream(X.device)),
           "slim_qlinear_noalloc")
     return Y
+
+
+def _out_code(out_dtype) -> int:
+    torch = _torch()
+    if out_dtype not in _float_types():
+        raise SlimError(f"out_dtype {out_dtype}; use bfloat16 or float32")
+    return SLIM_BF16 if out_dtype == torch.bfloat16 else SLIM_F32
+
+
+def pack4(codes, scale, zero, group: int, info=None):
+    """Codes of up to 4 bits with their scales and zeros laid out for q4_linear
+    (codes uint8 [n, m]; scale, zero float32 [n, k]) or, with a leading expert
+    axis on all three, for q4_experts -> int32 words [slim_pack4_words].  Widths
+    above 4 do not fit: info (int32 [1] on the GPU, zeroed by the caller) is set
+    to 1 if a code is above 15."""
+    torch = _torch()
+    lib = load_library()
+    codes = _arg(codes, "codes", None, (torch.uint8,))
+    if codes.dim() not in (2, 3):
+        raise SlimError(f"codes: shape {tuple(codes.shape)}, expected [n, m] or [experts, n, m]")
+    n, m = codes.shape[-2:]
+    e = codes.shape[0] if codes.dim() == 3 else 1
+    k = _group_count(m, group)
+    lead = tuple(codes.shape[:-1])
+    scale = _arg(scale, "scale", (*lead, k), (torch.float32,))
+    zero = _arg(zero, "zero", (*lead, k), (torch.float32,))
+    if info is not None:
+        info = _arg(info, "info", (1,), (torch.int32,))
+    words = lib.slim_pack4_words(e, n, m, group)
+    if words < 0:
+        raise SlimError(f"codes: shape {tuple(codes.shape)} is out of range")
+    _on_gpu(codes, scale, zero, info)
+    with torch.cuda.device(codes.device):
+        packed = torch.empty(words, dtype=torch.int32, device=codes.device)
+        check(lib.slim_pack4(_ptr(codes), _ptr(scale), _ptr(zero), e, n, m, group, _ptr(packed), _ptr(info),
+                             _stream(codes.device)), "slim_pack4")
+    return packed
+
+
+def _packed4(packed, e: int, n: int, m: int, group: int):
+    torch = _torch()
+    _group_count(m, group)
+    words = load_library().slim_pack4_words(e, n, m, group)
+    if words < 0 or n < 1:
+        raise SlimError(f"bad layer shape: {e} experts, n = {n}, m = {m}")
+    return _arg(packed, "packed", (words,), (torch.int32,))
+
+
+def _y4(Y, r: int, n: int, out_dtype, X):
+    """The output tensor: the caller's, or a new one."""
+    torch = _torch()
+    _out_code(out_dtype)
+    if Y is not None:
+        _arg(Y, "Y", (r, n), (out_dtype,))
+    return Y
+
+
+def q4_linear(X, packed, n: int, group: int, out_dtype=None, Y=None):
+    """Y = X W_hat^T from pack4's words: X [t, m] bf16/f32, t <= 65536 -> Y [t, n] in out_dtype
+    (float32 by default; bfloat16 is rounded once at the end).  Y may be given."""
+    torch = _torch()
+    lib = load_library()
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    X = _arg(X, "X", (None, None), _float_types())
+    t, m = X.shape
+    packed = _packed4(packed, 1, n, m, group)
+    Y = _y4(Y, t, n, out_dtype, X)
+    _on_gpu(X, packed, Y)
+    with torch.cuda.device(X.device):
+        if Y is None:
+            Y = torch.empty((t, n), dtype=out_dtype, device=X.device)
+        need = lib.slim_q4_linear_workspace(t, n, m, group, _dtype_code(X))
+        ws = _ws(need, X.device) if need else None
+        check(lib.slim_q4_linear(_ptr(X), _dtype_code(X), t, m, _ptr(packed), n, group, _ptr(Y), _out_code(out_dtype),
+                                 _ptr(ws), need, _stream(X.device)), "slim_q4_linear")
+    return Y
+
+
+def q4_experts(X, offsets, packed, n: int, group: int, rows=None, row_scale=None, out_dtype=None, Y=None):
+    """Rows sorted by expert through their experts' layers: offsets int32 [e + 1] (rows
+    offsets[j] .. offsets[j+1] - 1 belong to expert j; read on the device), packed = pack4 of the e
+    matrices.  rows int32 [r] gathers row a from X's row rows[a]; row_scale float32 [r] scales row a.
+    -> Y [r, n] in out_dtype; rows outside the offsets are not written (a given Y keeps them)."""
+    torch = _torch()
+    lib = load_library()
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    X = _arg(X, "X", (None, None), _float_types())
+    tx, m = X.shape
+    offsets = _arg(offsets, "offsets", (None,), (torch.int32,), min_numel=2)
+    e = offsets.shape[0] - 1
+    r = tx
+    if rows is not None:
+        rows = _arg(rows, "rows", (None,), (torch.int32,))
+        r = rows.shape[0]
+        if r > 0 and tx == 0:
+            raise SlimError("X: no rows to gather from")
+    if row_scale is not None:
+        row_scale = _arg(row_scale, "row_scale", (r,), (torch.float32,))
+    packed = _packed4(packed, e, n, m, group)
+    Y = _y4(Y, r, n, out_dtype, X)
+    _on_gpu(X, offsets, packed, rows, row_scale, Y)
+    with torch.cuda.device(X.device):
+        if Y is None:
+            Y = torch.empty((r, n), dtype=out_dtype, device=X.device)
+        need = lib.slim_q4_experts_workspace(tx, r, e, n, m, group, _dtype_code(X))
+        ws = _ws(need, X.device) if need else None
+        check(lib.slim_q4_experts(_ptr(X), _dtype_code(X), tx, m, _ptr(rows), _ptr(row_scale), r, _ptr(offsets), e,
+                                  _ptr(packed), n, group, _ptr(Y), _out_code(out_dtype), _ptr(ws), need,
+                                  _stream(X.device)), "slim_q4_experts")
+    return Y
+
+
+def token_logprobs(logits, ids, top: int = 0):
+    """logits [t, v] bf16/f32 (rows may be strided), ids int64 [t] -> dict(logprob f32 [t],
+    entropy f32 [t]) and, with top > 0, top_logprob f32 [t, top] and top_id int32 [t, top] (best
+    first, equal logits by ascending index).  A negative id (padding) gives logprob 0."""
+    torch = _torch()
+    lib = load_library()
+    logits = _arg(logits, "logits", (None, None), _float_types())
+    t, v = logits.shape
+    ids = _arg(ids, "ids", (t,), (torch.int64,))
+    top = int(top)
+    if v < 1:
+        raise SlimError("logits: no entries")
+    if not 0 <= top <= min(v, LOGPROB_MAX_TOP):
+        raise SlimError(f"top {top} must lie in 0 .. {min(v, LOGPROB_MAX_TOP)}")
+    ld = logits.stride(0) if t > 1 else v
+    if (v > 1 and logits.stride(1) != 1) or ld < v:
+        raise SlimError("logits: a row's entries must be contiguous and rows must not overlap")
+    if not (logits.is_cuda and ids.is_cuda):
+        raise SlimError("tensors must live in GPU memory")
+    if not ids.is_contiguous():
+        raise SlimError("ids: must be contiguous")
+    if logits.device != ids.device:
+        raise SlimError(f"tensors live on different devices: {logits.device}, {ids.device}")
+    dev = logits.device
+    with torch.cuda.device(dev):
+        out = {"logprob": torch.empty(t, dtype=torch.float32, device=dev),
+               "entropy": torch.empty(t, dtype=torch.float32, device=dev)}
+        if top:
+            out["top_logprob"] = torch.empty((t, top), dtype=torch.float32, device=dev)
+            out["top_id"] = torch.empty((t, top), dtype=torch.int32, device=dev)
+        need = lib.slim_token_logprobs_workspace(t, v, top)
+        ws = _ws(need, dev) if need else None
+        check(lib.slim_token_logprobs(_ptr(logits), _dtype_code(logits), t, v, ld, _ptr(ids), top,
+                                      _ptr(out["logprob"]), _ptr(out["entropy"]), _ptr(out.get("top_logprob")),
+                                      _ptr(out.get("top_id")), _ptr(ws), need, _stream(dev)), "slim_token_logprobs")
+    return out
 
 
 def tau_table(lam: float = 0.1, n_tau: int = 50) -> np.ndarray:

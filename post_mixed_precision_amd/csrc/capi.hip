@@ -9,6 +9,7 @@
 
 #include "slim.h"
 #include "kernels.hpp"
+#include "serve.hpp"
 
 namespace {
 
@@ -353,6 +354,102 @@ int slim_qlinear(const void *X, int xdt, int64_t t, int64_t m, const uint32_t *p
                                       ws, p,
                                       (hipStream_t)stream);
   return e == hipSuccess ? SLIM_OK : hip_fail(e);
+}
+
+// ---------------------------------------------------------------- 4-bit layout and its products
+int64_t slim_pack4_words(int64_t e, int64_t n, int64_t m, int group) {
+  if (e < 0 || e > SLIM_Q4_MAX_EXPERTS || n < 0 || n > SLIM_Q4_MAX_N || m < 1 || m > SLIM_MAX_WIDTH ||
+      !valid_group(group) || m % group)
+    return -1;
+  return e * slim::q4_matrix_words(n, m, group);
+}
+
+int slim_pack4(const uint8_t *codes, const float *scale, const float *zero, int64_t e, int64_t n, int64_t m, int group,
+               uint32_t *packed, int32_t *info, void *stream) {
+  if (slim_pack4_words(e, n, m, group) < 0) return SLIM_E_SHAPE;
+  if (e == 0 || n == 0) return SLIM_OK;
+  if (!codes || !scale || !zero || !packed) return SLIM_E_NULL;
+  if (!aligned16(codes) || !aligned16(packed)) return SLIM_E_ALIGN;
+  hipError_t err = slim::launch_pack4(codes, scale, zero, e, n, m, group, packed, info, (hipStream_t)stream);
+  return err == hipSuccess ? SLIM_OK : hip_fail(err);
+}
+
+size_t slim_q4_linear_workspace(int64_t t, int64_t n, int64_t m, int group, int xdt) {
+  if (t < 0 || t > SLIM_QLINEAR_MAX_T || n < 1 || !valid_dtype(xdt) || slim_pack4_words(1, n, m, group) < 0) return 0;
+  return slim::q4_ws_bytes(t, t, 1, n, m, group, xdt == SLIM_BF16);
+}
+
+int slim_q4_linear(const void *X, int xdt, int64_t t, int64_t m, const uint32_t *packed, int64_t n, int group, void *Y,
+                   int ydt, void *ws, size_t ws_bytes, void *stream) {
+  if (!valid_dtype(xdt) || !valid_dtype(ydt)) return SLIM_E_DTYPE;
+  if (t < 0 || t > SLIM_QLINEAR_MAX_T || n < 1 || slim_pack4_words(1, n, m, group) < 0) return SLIM_E_SHAPE;
+  if (t == 0) return SLIM_OK;
+  if (!X || !packed || !Y) return SLIM_E_NULL;
+  if (!aligned16(X) || !aligned16(packed) || !aligned16(Y)) return SLIM_E_ALIGN;
+  const size_t need = slim::q4_ws_bytes(t, t, 1, n, m, group, xdt == SLIM_BF16);
+  if (need > 0 && (!ws || ws_bytes < need)) return SLIM_E_WORKSPACE;
+  if (need > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
+  slim::Q4Args a = {};
+  a.X = X, a.xrows = t, a.m = m, a.W = packed, a.n = n, a.r = t, a.Y = Y, a.e = 1, a.group = group;
+  a.xbf16 = xdt == SLIM_BF16, a.ybf16 = ydt == SLIM_BF16;
+  hipError_t err = slim::launch_q4(a, ws, (hipStream_t)stream);
+  return err == hipSuccess ? SLIM_OK : hip_fail(err);
+}
+
+static bool experts_shape(int64_t tx, int64_t r, int64_t e, int64_t n, int64_t m, int group) {
+  return e >= 1 && r >= 0 && r <= SLIM_Q4_MAX_ROWS && n >= 1 && tx >= (r > 0 ? 1 : 0) && tx <= SLIM_Q4_MAX_ROWS &&
+         slim_pack4_words(e, n, m, group) >= 0;
+}
+
+size_t slim_q4_experts_workspace(int64_t tx, int64_t r, int64_t e, int64_t n, int64_t m, int group, int xdt) {
+  if (!experts_shape(tx, r, e, n, m, group) || !valid_dtype(xdt)) return 0;
+  return slim::q4_ws_bytes(tx, r, e, n, m, group, xdt == SLIM_BF16);
+}
+
+int slim_q4_experts(const void *X, int xdt, int64_t tx, int64_t m, const int32_t *rows, const float *row_scale,
+                    int64_t r, const int32_t *offsets, int64_t e, const uint32_t *packed, int64_t n, int group,
+                    void *Y, int ydt, void *ws, size_t ws_bytes, void *stream) {
+  if (!valid_dtype(xdt) || !valid_dtype(ydt)) return SLIM_E_DTYPE;
+  if (!experts_shape(tx, r, e, n, m, group) || (!rows && tx != r)) return SLIM_E_SHAPE;
+  if (r == 0) return SLIM_OK;
+  if (!X || !offsets || !packed || !Y) return SLIM_E_NULL;
+  if (!aligned16(X) || !aligned16(packed) || !aligned16(Y)) return SLIM_E_ALIGN;
+  const size_t need = slim::q4_ws_bytes(tx, r, e, n, m, group, xdt == SLIM_BF16);
+  if (need > 0 && (!ws || ws_bytes < need)) return SLIM_E_WORKSPACE;
+  if (need > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
+  slim::Q4Args a = {};
+  a.X = X, a.xrows = tx, a.m = m, a.W = packed, a.n = n, a.r = r, a.offsets = offsets, a.rows = rows;
+  a.row_scale = row_scale, a.Y = Y, a.e = (int)e, a.group = group;
+  a.xbf16 = xdt == SLIM_BF16, a.ybf16 = ydt == SLIM_BF16;
+  hipError_t err = slim::launch_q4(a, ws, (hipStream_t)stream);
+  return err == hipSuccess ? SLIM_OK : hip_fail(err);
+}
+
+// ---------------------------------------------------------------- token log probabilities
+static bool logprob_shape(int64_t t, int64_t v) {
+  return t >= 0 && t <= SLIM_LOGPROB_MAX_T && v >= 1 && v <= SLIM_LOGPROB_MAX_V;
+}
+
+size_t slim_token_logprobs_workspace(int64_t t, int64_t v, int top) {
+  if (!logprob_shape(t, v) || top < 0 || top > SLIM_LOGPROB_MAX_TOP || top > v) return 0;
+  return slim::logprob_plan(t, v, top).ws_bytes;
+}
+
+int slim_token_logprobs(const void *logits, int ldt, int64_t t, int64_t v, int64_t ld, const int64_t *ids, int top,
+                        float *logprob, float *entropy, float *top_logprob, int32_t *top_id, void *ws,
+                        size_t ws_bytes, void *stream) {
+  if (!valid_dtype(ldt)) return SLIM_E_DTYPE;
+  if (!logprob_shape(t, v) || ld < v || ld > ((int64_t)1 << 40)) return SLIM_E_SHAPE;
+  if (top < 0 || top > SLIM_LOGPROB_MAX_TOP || top > v) return SLIM_E_PARAM;
+  if (t == 0) return SLIM_OK;
+  if (!logits || (logprob && !ids) || (top > 0 && (!top_logprob || !top_id))) return SLIM_E_NULL;
+  if ((uintptr_t)logits % (ldt == SLIM_BF16 ? 2 : 4)) return SLIM_E_ALIGN;
+  const slim::LogprobPlan p = slim::logprob_plan(t, v, top);
+  if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes)) return SLIM_E_WORKSPACE;
+  if (p.ws_bytes > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
+  hipError_t err = slim::launch_logprobs(logits, ldt == SLIM_BF16, t, v, ld, ids, top, logprob, entropy, top_logprob,
+                                         top_id, ws, p, (hipStream_t)stream);
+  return err == hipSuccess ? SLIM_OK : hip_fail(err);
 }
 
 // ---------------------------------------------------------------- timing

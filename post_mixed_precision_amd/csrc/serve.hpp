@@ -1,0 +1,47 @@
+// Host-side launchers of the serving kernels: 4-bit products, the same grouped
+// by expert, and token log probabilities (internal to libslim).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace slim {
+
+// ---- 4-bit codes with their scales and zeros, laid out for the products ----
+// A record holds 16 rows x 128 columns: 256 words of codes, then a (scale,
+// zero) pair per row and group.
+inline int64_t q4_row_blocks(int64_t n) { return (n + 15) / 16; }
+inline int64_t q4_chunks(int64_t m) { return (m + 127) / 128; }
+inline int64_t q4_record_words(int group) { return 256 + 32 * (128 / group); }
+inline int64_t q4_matrix_words(int64_t n, int64_t m, int group) {
+  return q4_row_blocks(n) * q4_chunks(m) * q4_record_words(group);
+}
+hipError_t launch_pack4(const uint8_t *codes, const float *scale, const float *zero, int64_t e, int64_t n, int64_t m,
+                        int group, uint32_t *packed, int32_t *info, hipStream_t st);
+
+struct Q4Args {
+  const void *X;             // [xrows, m]
+  int64_t xrows, m;
+  const uint32_t *W;         // e packed matrices
+  int64_t n, r;              // output rows of a matrix; rows of Y
+  const int32_t *offsets;    // e + 1 row bounds, or null: one matrix for all rows
+  const int32_t *rows;       // r rows of X, or null: row i reads X's row i
+  const float *row_scale;    // r factors, or null
+  void *Y;                   // [r, n]
+  int e, group;
+  bool xbf16, ybf16;
+};
+size_t q4_ws_bytes(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16);
+hipError_t launch_q4(const Q4Args &a, void *ws, hipStream_t st);
+
+// ---- Token log probabilities ----
+struct LogprobPlan {
+  int nseg;                  // segments a row is split into
+  size_t ws_bytes;           // their statistics and best entries (0 for one segment)
+};
+LogprobPlan logprob_plan(int64_t t, int64_t v, int top);
+hipError_t launch_logprobs(const void *L, bool bf16, int64_t t, int64_t v, int64_t ld, const int64_t *ids, int top,
+                           float *logprob, float *entropy, float *top_logprob, int32_t *top_id, void *ws,
+                           const LogprobPlan &p, hipStream_t st);
+
+}  // namespace slim

@@ -1,0 +1,479 @@
+"""The 4-bit products (one matrix, or one per expert) and the token log
+probabilities against the float64 oracle, through the binding.
+
+Tolerances, from the arithmetic.  Products: X and the codes enter exactly, so
+an output's error comes from the float32 sums: at most g (3 g for float32 X,
+which enters as three terms) additions inside a group, k over the groups and a
+handful in joining partial sums, each off by at most 2^-23 of a partial sum
+that never exceeds sum_c |x_c| (q_c + |z|) s.  A bfloat16 output adds half a
+step, 2^-8 of the value.  Log probabilities: see _lp_bounds.
+"""
+import numpy as np
+import pytest
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def slim():
+    import post_mixed_precision_amd as s
+    s.load_library()
+    return s
+
+
+def _layer(seed, e, n, m, g):
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 16, size=(e, n, m), dtype=np.uint8)
+    scale = rng.uniform(1e-3, 1e-2, size=(e, n, m // g)).astype(np.float32)
+    zero = rng.uniform(0, 15, size=(e, n, m // g)).astype(np.float32)
+    return codes, scale, zero
+
+
+def _x(seed, t, m, dt):
+    x = torch.from_numpy(np.random.default_rng(seed).standard_normal((t, m)).astype(np.float32))
+    return x.to(DT[dt])
+
+
+def _gpu(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to("cuda:0")
+
+
+def _bound(x, codes, scale, zero, g, xdt, ydt, exact):
+    k = codes.shape[-1] // g
+    mag = np.abs(x) @ ((codes + np.repeat(np.abs(zero), g, -1)) * np.repeat(np.abs(scale), g, -1)).astype(np.float64).T
+    terms = (g if xdt == "bf16" else 3 * g) + k + 24
+    return 2.0 ** -23 * terms * mag + (2.0 ** -8 * np.abs(exact) if ydt == "bf16" else 0) + 1e-30
+
+
+@pytest.mark.parametrize("e,n,m,g", [(1, 16, 128, 128), (1, 1, 32, 32), (3, 37, 96, 32), (2, 130, 320, 64),
+                                     (1, 256, 1152, 128)])
+def test_pack4_layout(slim, e, n, m, g):
+    print(f"pack4 e={e} n={n} m={m} g={g}", flush=True)
+    codes, scale, zero = _layer(n, e, n, m, g)
+    want = oracle.pack4(codes, scale, zero, g)
+    info = torch.zeros(1, dtype=torch.int32, device="cuda:0")
+    got = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g, info=info)
+    np.testing.assert_array_equal(got.cpu().numpy().view(np.uint32), want)
+    assert info.item() == 0
+    if e == 1:
+        got = slim.pack4(_gpu(codes[0]), _gpu(scale[0]), _gpu(zero[0]), g)
+        np.testing.assert_array_equal(got.cpu().numpy().view(np.uint32), want)
+    codes[0, n - 1, m - 1] |= 0x40                          # above 15: flagged, low bits kept
+    got = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g, info=info)
+    np.testing.assert_array_equal(got.cpu().numpy().view(np.uint32), want)
+    assert info.item() == 1
+
+
+LINEAR = [
+    (1, 16, 128, 128, "bf16", "f32"),
+    (1, 1, 32, 32, "f32", "bf16"),           # one output, a quarter of a record
+    (1, 1000, 2048, 128, "bf16", "bf16"),
+    (2, 257, 320, 64, "bf16", "f32"),        # half a record at the end of the row
+    (4, 130, 96, 32, "f32", "f32"),
+    (5, 48, 1088, 64, "bf16", "bf16"),
+    (8, 100, 4224, 128, "f32", "f32"),
+    (9, 31, 160, 32, "bf16", "f32"),
+    (16, 513, 384, 128, "bf16", "bf16"),
+    (17, 64, 256, 64, "bf16", "f32"),
+    (33, 200, 416, 32, "f32", "bf16"),
+    (48, 1040, 640, 128, "bf16", "f32"),
+    (64, 129, 192, 64, "bf16", "bf16"),
+    (65, 300, 512, 128, "bf16", "f32"),
+    (100, 520, 224, 32, "bf16", "bf16"),
+    (128, 256, 256, 128, "f32", "f32"),
+    (129, 272, 2112, 64, "bf16", "f32"),
+    (300, 1003, 1056, 32, "bf16", "bf16"),
+    (257, 385, 1152, 128, "f32", "bf16"),
+    (700, 640, 640, 128, "bf16", "f32"),
+]
+
+
+@pytest.mark.parametrize("t,n,m,g,xdt,ydt", LINEAR)
+def test_q4_linear(slim, t, n, m, g, xdt, ydt):
+    print(f"q4_linear t={t} n={n} m={m} g={g} {xdt} -> {ydt}", flush=True)
+    codes, scale, zero = _layer(t + n + m, 1, n, m, g)
+    X = _x(t * n, t, m, xdt)
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    Y = torch.full((t + 1, n), 7.0, dtype=DT[ydt], device="cuda:0")
+    out = slim.q4_linear(X.to("cuda:0"), packed, n, g, out_dtype=DT[ydt], Y=Y[:t])
+    assert out.data_ptr() == Y.data_ptr()
+    assert torch.all(Y[t] == 7.0)                           # the row behind the last is left alone
+    again = slim.q4_linear(X.to("cuda:0"), packed, n, g, out_dtype=DT[ydt])
+    assert torch.equal(again, out)                          # a fixed order of sums
+    x = X.double().numpy()
+    exact = x @ oracle.q4_weight(codes[0], scale[0], zero[0], g).T
+    err = np.abs(out.double().cpu().numpy() - exact)
+    bound = _bound(x, codes[0], scale[0], zero[0], g, xdt, ydt, exact)
+    assert np.all(err <= bound), float(np.max(err / bound))
+
+
+def test_q4_linear_scales_and_zeros_of_any_sign(slim):
+    # negative, zero and huge scales, zeros far outside the code range
+    n, m, g, t = 40, 256, 64, 3
+    codes, scale, zero = _layer(5, 1, n, m, g)
+    scale[0, ::3] *= -1
+    scale[0, 1::3] = 0
+    scale[0, 2] = 1e6
+    zero[0, ::2] = -40.0
+    X = _x(6, t, m, "f32")
+    Y = slim.q4_linear(X.to("cuda:0"), slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g), n, g)
+    x = X.double().numpy()
+    exact = x @ oracle.q4_weight(codes[0], scale[0], zero[0], g).T
+    err = np.abs(Y.double().cpu().numpy() - exact)
+    assert np.all(err <= _bound(x, codes[0], scale[0], zero[0], g, "f32", "f32", exact))
+
+
+@pytest.mark.parametrize("t", [3, 40, 200])
+def test_q4_linear_nonfinite_row_stays_in_its_row(slim, t):
+    n, m, g = 48, 256, 128
+    codes, scale, zero = _layer(7, 1, n, m, g)
+    X = _x(8, t, m, "bf16").to("cuda:0")
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    clean = slim.q4_linear(X, packed, n, g)
+    X[1, 5] = float("nan")
+    X[2, 9] = float("inf")
+    Y = slim.q4_linear(X, packed, n, g)
+    assert not torch.isfinite(Y[1:3]).any()
+    keep = [a for a in range(t) if a not in (1, 2)]
+    assert torch.equal(Y[keep], clean[keep])
+
+
+def test_q4_linear_no_tokens(slim):
+    codes, scale, zero = _layer(9, 1, 16, 128, 128)
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), 128)
+    assert slim.q4_linear(torch.empty((0, 128), device="cuda:0"), packed, 16, 128).shape == (0, 16)
+
+
+def test_q4_linear_agrees_with_the_planes(slim):
+    # the same 3-bit-average layer through both layouts
+    n, m, g, t = 96, 512, 128, 7
+    rng = np.random.default_rng(10)
+    bits = np.array([2, 3, 4, 3], dtype=np.int8)
+    codes = np.concatenate([rng.integers(0, 2 ** b, size=(n, g), dtype=np.uint8) for b in bits], axis=1)
+    scale = rng.uniform(1e-3, 1e-2, size=(n, 4)).astype(np.float32)
+    zero = rng.uniform(0, 3, size=(n, 4)).astype(np.float32)
+    X = _x(11, t, m, "bf16").to("cuda:0")
+    planes, info = slim.pack(_gpu(codes), _gpu(bits), g, 3)
+    a = slim.qlinear(X, planes, _gpu(bits), _gpu(scale), _gpu(zero), g, 3).double().cpu().numpy()
+    b = slim.q4_linear(X, slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g), n, g).double().cpu().numpy()
+    x = X.double().cpu().numpy()
+    bound = _bound(x, codes, scale, zero, g, "bf16", "f32", b)
+    assert np.all(np.abs(a - b) <= 2 * bound)
+
+
+# ------------------------------------------------------------------ experts
+def _counts_to_offsets(counts, first=0):
+    return np.concatenate([[first], first + np.cumsum(counts)]).astype(np.int32)
+
+
+EXPERTS = [
+    # counts, n, m, g, xdt, ydt, gather, weighted, rows before and behind
+    ([1], 16, 128, 128, "bf16", "f32", False, False, 0, 0),
+    ([2, 0, 1, 1], 100, 256, 64, "bf16", "bf16", True, True, 0, 0),
+    ([0, 0, 5, 0], 33, 96, 32, "f32", "f32", False, True, 2, 3),
+    ([17, 1, 0, 40, 16], 200, 384, 128, "bf16", "f32", True, False, 1, 1),
+    ([300, 0, 7, 65], 130, 320, 64, "bf16", "bf16", True, True, 0, 5),
+    ([129, 128, 127, 0, 260], 272, 640, 128, "bf16", "f32", False, False, 3, 0),
+    ([200, 90], 96, 160, 32, "f32", "bf16", True, True, 0, 0),
+    ([1] * 65, 16, 128, 128, "bf16", "f32", True, False, 0, 0),      # more experts than lanes
+    ([3, 0] * 75, 24, 64, 64, "bf16", "bf16", False, True, 0, 1),
+    ([0, 0, 0], 16, 128, 128, "bf16", "f32", False, False, 0, 4),    # no rows at all
+    ([700, 500, 0, 900], 300, 256, 128, "bf16", "bf16", True, False, 0, 0),
+]
+
+
+@pytest.mark.parametrize("counts,n,m,g,xdt,ydt,gather,weighted,before,behind", EXPERTS)
+def test_q4_experts(slim, counts, n, m, g, xdt, ydt, gather, weighted, before, behind):
+    e, r = len(counts), before + sum(counts) + behind
+    print(f"q4_experts e={e} r={r} n={n} m={m} g={g} {xdt} -> {ydt} gather={gather} weighted={weighted}", flush=True)
+    rng = np.random.default_rng(r + n)
+    off = _counts_to_offsets(counts, before)
+    codes, scale, zero = _layer(r + m, e, n, m, g)
+    tx = max(1, r // 2) if gather else r
+    rows = rng.integers(0, tx, size=r).astype(np.int32) if gather else None
+    gates = rng.uniform(-1, 1, size=r).astype(np.float32) if weighted else None
+    X = _x(r, tx, m, xdt)
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    Y = torch.full((r, n), 7.0, dtype=DT[ydt], device="cuda:0")
+    slim.q4_experts(X.to("cuda:0"), _gpu(off), packed, n, g, rows=None if rows is None else _gpu(rows),
+                    row_scale=None if gates is None else _gpu(gates), out_dtype=DT[ydt], Y=Y)
+    y = Y.double().cpu().numpy()
+    assert np.all(y[:before] == 7.0) and np.all(y[off[-1]:] == 7.0)
+    x = X.double().numpy()
+    for j in range(e):
+        a, b = off[j], off[j + 1]
+        if a == b:
+            continue
+        xs = x[a:b] if rows is None else x[rows[a:b]]
+        w = np.ones(b - a) if gates is None else gates[a:b].astype(np.float64)
+        exact = (xs @ oracle.q4_weight(codes[j], scale[j], zero[j], g).T) * w[:, None]
+        bound = _bound(xs * np.abs(w)[:, None], codes[j], scale[j], zero[j], g, xdt, ydt, exact)
+        bound += 2.0 ** -24 * np.abs(exact)                 # the product with the row's factor
+        err = np.abs(y[a:b] - exact)
+        assert np.all(err <= bound), (j, float(np.max(err / bound)))
+
+
+@pytest.mark.parametrize("per", [3, 150])
+def test_q4_experts_bad_rows_and_offsets(slim, per):
+    # checked by the kernels before anything is read through them
+    e, n, m, g = 3, 32, 128, 128
+    r = e * per
+    codes, scale, zero = _layer(12, e, n, m, g)
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    X = _x(13, 4, m, "bf16").to("cuda:0")
+    rows = np.arange(r, dtype=np.int32) % 4
+    off = _counts_to_offsets([per] * e)
+    good = slim.q4_experts(X, _gpu(off), packed, n, g, rows=_gpu(rows))
+    assert torch.isfinite(good).all()
+    bad = rows.copy()
+    bad[1], bad[r - 1] = -1, 4
+    Y = slim.q4_experts(X, _gpu(off), packed, n, g, rows=_gpu(bad))
+    assert torch.isnan(Y[1]).all() and torch.isnan(Y[r - 1]).all()
+    keep = [a for a in range(r) if a not in (1, r - 1)]
+    assert torch.equal(Y[keep], good[keep])
+    for bounds in ([0, per, per - 1, r], [0, per, 2 * per, r + 1], [-1, per, 2 * per, r],
+                   [0, 2 ** 31 - 1, -2 ** 31, r]):
+        Y = slim.q4_experts(X, _gpu(np.array(bounds, dtype=np.int32)), packed, n, g, rows=_gpu(rows))
+        assert torch.isnan(Y).all(), bounds
+
+
+def test_q4_experts_matches_single_layers(slim):
+    e, n, m, g = 4, 160, 512, 128
+    codes, scale, zero = _layer(14, e, n, m, g)
+    counts = [5, 0, 30, 1]
+    off = _counts_to_offsets(counts)
+    X = _x(15, sum(counts), m, "bf16").to("cuda:0")
+    Y = slim.q4_experts(X, _gpu(off), slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g), n, g)
+    for j in range(e):
+        a, b = int(off[j]), int(off[j + 1])
+        if a < b:
+            one = slim.q4_linear(X[a:b].contiguous(), slim.pack4(_gpu(codes[j]), _gpu(scale[j]), _gpu(zero[j]), g), n, g)
+            torch.testing.assert_close(Y[a:b], one, rtol=1e-4, atol=1e-4)
+
+
+# ------------------------------------------------------------------ log probabilities
+def _lp_bounds(x, out):
+    """Float32 error bounds.  d = x - M is off by 2^-24 |d|; e^d by 3 2^-24 (1 +
+    |d|) relative (the product with log2 e and the power); a lane adds at most
+    V / 64 + 2 terms, the joins some 20 more, each step 2^-24, so ln S is off
+    by rS below (entries with |d| > 104 underflow to 0 and S >= 1).  W's terms
+    e^d d carry |d| / S <= D on top, and the last operations round once more."""
+    eps = 2.0 ** -24
+    v = x.shape[1]
+    fin = np.where(np.isfinite(x), x, 0.0)
+    d = np.minimum(fin.max(axis=1) - fin.min(axis=1), 104.0)
+    rs = eps * (v / 64 + 40 + 4 * (1 + d))
+    lp = rs + eps * 4 * (1 + np.abs(np.nan_to_num(out["logprob"], neginf=0.0)))
+    ent = 2 * rs * (1 + out["entropy"]) + eps * 8 * (1 + np.abs(out["entropy"]) + d)
+    return lp, ent, rs
+
+
+def _check_lp(got, x, ids, top):
+    want = oracle.token_logprobs(x, ids, top)
+    lp_b, ent_b, rs = _lp_bounds(x, want)
+    lp, ent = got["logprob"].double().cpu().numpy(), got["entropy"].double().cpu().numpy()
+    for g, w, b in ((lp, want["logprob"], lp_b), (ent, want["entropy"], ent_b)):
+        same = (g == w) | (np.isnan(g) & np.isnan(w))
+        with np.errstate(invalid="ignore"):
+            ok = same | (np.abs(g - w) <= b)
+        assert ok.all(), (g[~ok], w[~ok], b[~ok])
+    if top:
+        np.testing.assert_array_equal(got["top_id"].cpu().numpy(), want["top_id"])
+        tl, wl = got["top_logprob"].double().cpu().numpy(), want["top_logprob"]
+        same = (tl == wl) | (np.isnan(tl) & np.isnan(wl))
+        with np.errstate(invalid="ignore"):
+            ok = same | (np.abs(tl - wl) <= rs[:, None] + 2.0 ** -22 * (1 + np.abs(wl)))
+        assert ok.all()
+
+
+def _logits(seed, t, v, pad, off, dt, scale=3.0):
+    x = torch.from_numpy((scale * np.random.default_rng(seed).standard_normal((t, off + v + pad))).astype(np.float32))
+    x = x.to(DT[dt])
+    return x[:, off:off + v]
+
+
+@pytest.mark.parametrize("t,v,pad,off,dt,top", [
+    (1, 1, 0, 0, "f32", 1),
+    (1, 7, 0, 0, "bf16", 7),
+    (3, 64, 0, 0, "f32", 64),              # the longest list, the whole row
+    (5, 100, 1, 0, "f32", 5),              # rows not aligned to 16 bytes
+    (4, 255, 3, 1, "bf16", 20),            # the first row neither
+    (2, 4097, 0, 0, "f32", 3),             # two segments
+    (1, 32000, 0, 0, "bf16", 5),
+    (3, 50001, 6, 3, "bf16", 20),          # segments of rows that start anywhere
+    (2, 131072, 0, 0, "f32", 64),
+    (1500, 501, 0, 0, "f32", 2),           # one segment a row
+    (40, 5000, 2, 0, "bf16", 0),
+])
+def test_token_logprobs(slim, t, v, pad, off, dt, top):
+    print(f"token_logprobs t={t} v={v} pad={pad} off={off} {dt} top={top}", flush=True)
+    x = _logits(t + v, t, v, pad, off, dt)
+    ids = np.random.default_rng(v).integers(0, v, size=t)
+    ids[t // 2] = -100 if t > 1 else ids[t // 2]
+    whole = _logits(t + v, t, v, pad, off, dt)._base if pad or off else None
+    base = (x if whole is None else whole).to("cuda:0")
+    g = base if whole is None else base[:, off:off + v]
+    got = slim.token_logprobs(g, _gpu(ids), top=top)
+    assert ("top_id" in got) == (top > 0)
+    _check_lp(got, x.double().numpy(), ids, top)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("v", [300, 9000])
+def test_token_logprobs_masked_and_bad_rows(slim, dt, v):
+    low = torch.finfo(DT[dt]).min
+    x = _logits(3, 12, v, 0, 0, dt).clone()
+    inf = float("inf")
+    x[0] = -inf                              # nothing left
+    x[1] = low                               # everything at the type's lowest value: uniform
+    x[2, 1:] = -inf                          # one entry left: certain
+    x[3, : v // 2] = -inf
+    x[4, ::2] = low
+    x[5, v // 3] = float("nan")
+    x[6, v - 1] = inf
+    x[7] = 0.0                               # ties everywhere
+    x[8, :5] = 50.0                          # ties at the top
+    x[9] = torch.sort(x[9]).values           # rising: every entry is a new maximum
+    x[10, 3:] = -inf                         # fewer entries than asked for
+    x[11, 0], x[11, 1] = -0.0, 0.0           # equal, whatever their bits
+    x[11, 2:] = -1.0
+    ids = np.array([0, v - 1, 0, 0, 0, 0, 0, v, -1, v - 1, 7, 1])
+    got = slim.token_logprobs(x.to("cuda:0"), _gpu(ids), top=8)
+    _check_lp(got, x.double().numpy(), ids, 8)
+    lp = got["logprob"].cpu()
+    assert torch.isnan(lp[[0, 5, 6, 7]]).all() and lp[8] == 0 and lp[2] == 0 and lp[3] == -inf
+    assert got["top_id"][11, 0].item() == 0
+
+
+def test_token_logprobs_large_logits(slim):
+    # differences that overflow float32, and values near its ends
+    x = torch.zeros((3, 600))
+    x[0, 0], x[0, 1] = 3.4e38, -3.4e38
+    x[1] = -3.0e38
+    x[2] = 1e4 + torch.arange(600) * 0.01
+    ids = np.array([0, 3, 599])
+    got = slim.token_logprobs(x.to("cuda:0"), _gpu(ids), top=2)
+    assert got["logprob"][0].item() == 0 and got["entropy"][0].item() == 0
+    _check_lp(got, x.double().numpy(), ids, 2)
+
+
+def test_token_logprobs_no_rows(slim):
+    got = slim.token_logprobs(torch.empty((0, 10), device="cuda:0"), torch.empty(0, dtype=torch.int64, device="cuda:0"),
+                              top=2)
+    assert got["logprob"].shape == (0,) and got["top_id"].shape == (0, 2)
+
+
+# ------------------------------------------------------------------ together
+def test_run_of_the_operators_eager_side_stream_and_graph(slim):
+    """A decode step as a server runs it: experts gathered by token and weighted
+    by the router's gates, summed over the choices, the head, the scores; eager
+    against the float64 chain, then on a side stream and from a replayed graph
+    with new inputs in the same buffers."""
+    t, d, h, v, e, g, top = 6, 256, 384, 1000, 4, 64, 2
+    rng = np.random.default_rng(20)
+    up, head = _layer(21, e, h, d, g), _layer(22, 1, v, h, g)
+    pu = slim.pack4(*[_gpu(a) for a in up], g)
+    ph = slim.pack4(*[_gpu(a) for a in head], g)
+    zc = lambda lay: (lay[0].astype(np.float64) - np.repeat(lay[2], g, -1)) * np.repeat(lay[1], g, -1)  # noqa: E731
+    wu, wh = zc(up), zc(head)[0]
+
+    def inputs(seed):
+        r = np.random.default_rng(seed)
+        x = torch.from_numpy(r.standard_normal((t, d)).astype(np.float32)).to(torch.bfloat16)
+        picks = sorted((int(j), a) for a in range(t) for j in r.choice(e, size=top, replace=False))
+        counts = np.bincount([p[0] for p in picks], minlength=e)
+        rows = np.array([p[1] for p in picks], dtype=np.int32)
+        gates = r.uniform(0.2, 0.8, size=t * top).astype(np.float32)
+        back = np.array([[i for i, p in enumerate(picks) if p[1] == a] for a in range(t)])
+        return (x, torch.from_numpy(_counts_to_offsets(counts)), torch.from_numpy(rows), torch.from_numpy(gates),
+                torch.from_numpy(back), torch.from_numpy(r.integers(0, v, size=t)))
+
+    def step(x, off, rows, gates, back, ids):
+        y = slim.q4_experts(x, off, pu, h, g, rows=rows, row_scale=gates)
+        z = y[back].sum(dim=1).to(torch.bfloat16)
+        logits = slim.q4_linear(z, ph, v, g)
+        return z, logits, slim.token_logprobs(logits, ids, top=5)
+
+    buf = [a.to("cuda:0") for a in inputs(0)]
+    z, logits, s = step(*buf)
+    x, off, rows, gates, back, ids = [a.double().numpy() if a.dtype == torch.bfloat16 else a.numpy() for a in inputs(0)]
+    y = np.zeros((t * top, h))
+    for j in range(e):
+        for a in range(off[j], off[j + 1]):
+            y[a] = wu[j] @ x[rows[a]] * gates[a]
+    zr = y[back].sum(axis=1)
+    np.testing.assert_allclose(z.double().cpu().numpy(), zr, rtol=2.0 ** -7, atol=1e-3)
+    lr = z.double().cpu().numpy() @ wh.T
+    np.testing.assert_allclose(logits.double().cpu().numpy(), lr, rtol=1e-4, atol=1e-4 * np.abs(lr).max())
+    _check_lp(s, logits.double().cpu().numpy(), ids, 5)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        z2, logits2, s2 = step(*buf)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(logits, logits2) and all(torch.equal(s[k], s2[k]) for k in s)
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        zg, lg, sg = step(*buf)
+    for seed in (1, 2, 3):
+        new = inputs(seed)
+        for b, a in zip(buf, new):
+            b.copy_(a)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [lg.clone(), {k: sg[k].clone() for k in sg}]
+        _, le, se = step(*buf)
+        assert torch.equal(got[0], le) and all(torch.equal(got[1][k], se[k]) for k in se), seed
+
+
+def test_two_graphs_share_inputs(slim):
+    # each captured call has its own workspace: replays in any order agree
+    n, m, g, t, v = 256, 512, 128, 150, 40000
+    codes, scale, zero = _layer(30, 1, n, m, g)
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    X = _x(31, t, m, "f32").to("cuda:0")
+    L = _logits(32, 3, v, 0, 0, "f32").to("cuda:0")
+    ids = torch.tensor([1, 2, 3], device="cuda:0")
+    want = slim.q4_linear(X, packed, n, g), slim.token_logprobs(L, ids, top=4)
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = slim.q4_linear(X, packed, n, g), slim.token_logprobs(L, ids, top=4)
+        graphs.append((gr, out))
+    for i in (0, 1, 1, 0, 1):
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        y, s = graphs[i][1]
+        assert torch.equal(y, want[0]) and all(torch.equal(s[k], want[1][k]) for k in s)
+
+
+def test_long_offsets_past_32_bits(slim):
+    # more than 2^31 bytes before the last expert's matrix and the last row's logits
+    e, n, m, g = 40, 16384, 8192, 128           # 75 MB a matrix, 3 GB in all
+    words = slim.load_library().slim_pack4_words(1, n, m, g)
+    packed = torch.zeros(e * words, dtype=torch.int32, device="cuda:0")
+    codes, scale, zero = _layer(40, 1, n, m, g)
+    packed[(e - 1) * words:] = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    X = _x(41, 3, m, "bf16").to("cuda:0")
+    off = torch.tensor([0] * e + [3], dtype=torch.int32, device="cuda:0")
+    Y = slim.q4_experts(X, off, packed, n, g)
+    one = slim.q4_linear(X, packed[(e - 1) * words:].clone(), n, g)
+    assert torch.equal(Y, one)
+    del packed, Y, one
+    t, v = 20000, 60000                          # 2.4 GB of bfloat16
+    L = torch.zeros((t, v), dtype=torch.bfloat16, device="cuda:0")
+    L[t - 1] = _logits(42, 1, v, 0, 0, "bf16").to("cuda:0")[0]
+    ids = torch.full((t,), v - 1, device="cuda:0")
+    got = slim.token_logprobs(L, ids, top=3)
+    last = {k: a[t - 1:] for k, a in got.items()}
+    _check_lp(last, L[t - 1:].double().cpu().numpy(), np.array([v - 1]), 3)
+    assert got["top_id"][:t - 1].eq(torch.arange(3, device="cuda:0")).all()
