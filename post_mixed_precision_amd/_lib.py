@@ -8,6 +8,7 @@ There is no fallback: if the library is missing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -169,7 +170,8 @@ def _arg(t, name: str, shape=None, dtypes=None, min_numel=None):
     if dtypes is not None and t.dtype not in dtypes:
         raise SlimError(f"{name}: dtype {t.dtype}, expected one of {list(dtypes)}")
     if shape is not None:
-        if t.dim() != len(shape) or any(s is not None and int(a) != int(s) for a, s in zip(t.shape, shape)):
+        have = t.shape
+        if len(have) != len(shape) or any(s is not None and a != s for a, s in zip(have, shape)):
             raise SlimError(f"{name}: shape {tuple(t.shape)}, expected {tuple('*' if s is None else s for s in shape)}")
     if min_numel is not None and t.numel() < min_numel:
         raise SlimError(f"{name}: {t.numel()} elements, at least {min_numel} needed")
@@ -537,22 +539,24 @@ def pack4(codes, scale, zero, group: int, info=None):
     return packed
 
 
-def _packed4(packed, e: int, n: int, m: int, group: int):
-    torch = _torch()
+@functools.lru_cache(maxsize=4096)
+def _words4(e: int, n: int, m: int, group: int) -> int:
     _group_count(m, group)
     words = load_library().slim_pack4_words(e, n, m, group)
     if words < 0 or n < 1:
         raise SlimError(f"bad layer shape: {e} experts, n = {n}, m = {m}")
-    return _arg(packed, "packed", (words,), (torch.int32,))
+    return words
 
 
-def _y4(Y, r: int, n: int, out_dtype, X):
-    """The output tensor: the caller's, or a new one."""
-    torch = _torch()
-    _out_code(out_dtype)
-    if Y is not None:
-        _arg(Y, "Y", (r, n), (out_dtype,))
-    return Y
+@functools.lru_cache(maxsize=4096)
+def _need(query: str, *args) -> int:
+    """A workspace size, asked once per set of sizes."""
+    return getattr(load_library(), query)(*args)
+
+
+def _raw_stream(index: int) -> int:
+    """The current stream of a device as an integer (no Stream object)."""
+    return _torch()._C._cuda_getCurrentRawStream(index)
 
 
 def q4_linear(X, packed, n: int, group: int, out_dtype=None, Y=None):
@@ -563,16 +567,24 @@ def q4_linear(X, packed, n: int, group: int, out_dtype=None, Y=None):
     out_dtype = torch.float32 if out_dtype is None else out_dtype
     X = _arg(X, "X", (None, None), _float_types())
     t, m = X.shape
-    packed = _packed4(packed, 1, n, m, group)
-    Y = _y4(Y, t, n, out_dtype, X)
+    ycode = _out_code(out_dtype)
+    packed = _arg(packed, "packed", (_words4(1, n, m, group),), (torch.int32,))
+    if Y is not None:
+        Y = _arg(Y, "Y", (t, n), (out_dtype,))
     _on_gpu(X, packed, Y)
-    with torch.cuda.device(X.device):
-        if Y is None:
-            Y = torch.empty((t, n), dtype=out_dtype, device=X.device)
-        need = lib.slim_q4_linear_workspace(t, n, m, group, _dtype_code(X))
-        ws = _ws(need, X.device) if need else None
-        check(lib.slim_q4_linear(_ptr(X), _dtype_code(X), t, m, _ptr(packed), n, group, _ptr(Y), _out_code(out_dtype),
-                                 _ptr(ws), need, _stream(X.device)), "slim_q4_linear")
+    dev = X.device
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return q4_linear(X, packed, n, group, out_dtype, Y)
+    if Y is None:
+        Y = torch.empty((t, n), dtype=out_dtype, device=dev)
+    xcode = _dtype_code(X)
+    need = _need("slim_q4_linear_workspace", t, n, m, group, xcode)
+    ws = _ws(need, dev) if need else None
+    st = lib.slim_q4_linear(X.data_ptr(), xcode, t, m, packed.data_ptr(), n, group, Y.data_ptr(), ycode,
+                            ws.data_ptr() if need else None, need, _raw_stream(dev.index))
+    if st:
+        check(st, "slim_q4_linear")
     return Y
 
 
@@ -596,17 +608,26 @@ def q4_experts(X, offsets, packed, n: int, group: int, rows=None, row_scale=None
             raise SlimError("X: no rows to gather from")
     if row_scale is not None:
         row_scale = _arg(row_scale, "row_scale", (r,), (torch.float32,))
-    packed = _packed4(packed, e, n, m, group)
-    Y = _y4(Y, r, n, out_dtype, X)
+    ycode = _out_code(out_dtype)
+    packed = _arg(packed, "packed", (_words4(e, n, m, group),), (torch.int32,))
+    if Y is not None:
+        Y = _arg(Y, "Y", (r, n), (out_dtype,))
     _on_gpu(X, offsets, packed, rows, row_scale, Y)
-    with torch.cuda.device(X.device):
-        if Y is None:
-            Y = torch.empty((r, n), dtype=out_dtype, device=X.device)
-        need = lib.slim_q4_experts_workspace(tx, r, e, n, m, group, _dtype_code(X))
-        ws = _ws(need, X.device) if need else None
-        check(lib.slim_q4_experts(_ptr(X), _dtype_code(X), tx, m, _ptr(rows), _ptr(row_scale), r, _ptr(offsets), e,
-                                  _ptr(packed), n, group, _ptr(Y), _out_code(out_dtype), _ptr(ws), need,
-                                  _stream(X.device)), "slim_q4_experts")
+    dev = X.device
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return q4_experts(X, offsets, packed, n, group, rows, row_scale, out_dtype, Y)
+    if Y is None:
+        Y = torch.empty((r, n), dtype=out_dtype, device=dev)
+    xcode = _dtype_code(X)
+    need = _need("slim_q4_experts_workspace", tx, r, e, n, m, group, xcode)
+    ws = _ws(need, dev) if need else None
+    st = lib.slim_q4_experts(X.data_ptr(), xcode, tx, m, None if rows is None else rows.data_ptr(),
+                             None if row_scale is None else row_scale.data_ptr(), r, offsets.data_ptr(), e,
+                             packed.data_ptr(), n, group, Y.data_ptr(), ycode, ws.data_ptr() if need else None, need,
+                             _raw_stream(dev.index))
+    if st:
+        check(st, "slim_q4_experts")
     return Y
 
 
@@ -624,27 +645,35 @@ def token_logprobs(logits, ids, top: int = 0):
         raise SlimError("logits: no entries")
     if not 0 <= top <= min(v, LOGPROB_MAX_TOP):
         raise SlimError(f"top {top} must lie in 0 .. {min(v, LOGPROB_MAX_TOP)}")
-    ld = logits.stride(0) if t > 1 else v
-    if (v > 1 and logits.stride(1) != 1) or ld < v:
+    ld, step = logits.stride()
+    if t <= 1:
+        ld = v
+    if (v > 1 and step != 1) or ld < v:
         raise SlimError("logits: a row's entries must be contiguous and rows must not overlap")
-    if not (logits.is_cuda and ids.is_cuda):
+    dev = logits.device
+    if dev.type != "cuda" or not ids.is_cuda:
         raise SlimError("tensors must live in GPU memory")
     if not ids.is_contiguous():
         raise SlimError("ids: must be contiguous")
-    if logits.device != ids.device:
-        raise SlimError(f"tensors live on different devices: {logits.device}, {ids.device}")
-    dev = logits.device
-    with torch.cuda.device(dev):
-        out = {"logprob": torch.empty(t, dtype=torch.float32, device=dev),
-               "entropy": torch.empty(t, dtype=torch.float32, device=dev)}
-        if top:
-            out["top_logprob"] = torch.empty((t, top), dtype=torch.float32, device=dev)
-            out["top_id"] = torch.empty((t, top), dtype=torch.int32, device=dev)
-        need = lib.slim_token_logprobs_workspace(t, v, top)
-        ws = _ws(need, dev) if need else None
-        check(lib.slim_token_logprobs(_ptr(logits), _dtype_code(logits), t, v, ld, _ptr(ids), top,
-                                      _ptr(out["logprob"]), _ptr(out["entropy"]), _ptr(out.get("top_logprob")),
-                                      _ptr(out.get("top_id")), _ptr(ws), need, _stream(dev)), "slim_token_logprobs")
+    if dev != ids.device:
+        raise SlimError(f"tensors live on different devices: {dev}, {ids.device}")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return token_logprobs(logits, ids, top)
+    logprob, entropy = torch.empty((2, t), dtype=torch.float32, device=dev).unbind()
+    out = {"logprob": logprob, "entropy": entropy}
+    tl = ti = None
+    if top:
+        out["top_logprob"] = tl = torch.empty((t, top), dtype=torch.float32, device=dev)
+        out["top_id"] = ti = torch.empty((t, top), dtype=torch.int32, device=dev)
+    need = _need("slim_token_logprobs_workspace", t, v, top)
+    ws = _ws(need, dev) if need else None
+    st = lib.slim_token_logprobs(logits.data_ptr(), _dtype_code(logits), t, v, ld, ids.data_ptr(), top,
+                                 logprob.data_ptr(), entropy.data_ptr(), tl.data_ptr() if top else None,
+                                 ti.data_ptr() if top else None, ws.data_ptr() if need else None, need,
+                                 _raw_stream(dev.index))
+    if st:
+        check(st, "slim_token_logprobs")
     return out
 
 
