@@ -105,85 +105,84 @@ __device__ __forceinline__ void split3(const float *p, uint4 (&t)[3]) {
 }
 
 // ---------------------------------------------------------------- row tiles
+// The experts' row ranges cut into tiles of TOK rows, in order.  Every wave
+// works this out for itself from the bounds (lane l takes consecutive
+// experts), so no table, extra launch or host copy of the bounds is needed.
+// Bounds out of order make every tile bad; tiles then cut the plain row range.
 struct RowTile {
-  int expert;      // -1: this workgroup has no rows
+  int expert;
   int64_t row0;    // first row of Y
   int cnt;         // rows in the tile
-  bool bad;        // offsets are not nondecreasing inside [0, r]
 };
 
-// The idx-th tile of TOK rows when the experts' row ranges are cut into tiles
-// in order.  Every wave works it out for itself from the bounds (lane l takes
-// per consecutive experts), so no table, extra launch or host copy of the
-// bounds is needed.  Bounds out of order make every tile bad; idx then counts
-// tiles of the plain row range.
 template <int TOK>
-__device__ __forceinline__ RowTile find_tile(const Q4Args &a, int64_t idx) {
-  RowTile t;
-  t.bad = false;
-  t.expert = -1;
-  t.row0 = idx * TOK;
-  t.cnt = 0;
-  if (!a.offsets) {
-    t.expert = 0;
-  } else {
+struct Tiles {
+  int64_t total;   // tiles of this call
+  bool bad;        // offsets are not nondecreasing inside [0, r]
+  int64_t mine, incl;
+
+  __device__ __forceinline__ void scan(const Q4Args &a) {
+    bad = false;
+    mine = incl = 0;
+    total = (a.r + TOK - 1) / TOK;
+    if (!a.offsets) return;
     const int lane = threadIdx.x & 63;
     const int per = (a.e + 63) >> 6;
-    const int e0 = lane * per;
-    int64_t mine = 0;
-    bool bad = false;
+    bool wrong = false;
     for (int i = 0; i < per; ++i) {
-      const int e = e0 + i;
+      const int e = lane * per + i;
       if (e < a.e) {
         const int64_t lo = a.offsets[e], hi = a.offsets[e + 1];
-        if (lo < 0 || hi < lo || hi > a.r) bad = true;
+        if (lo < 0 || hi < lo || hi > a.r) wrong = true;
         else mine += (hi - lo + TOK - 1) / TOK;
       }
     }
-    if (__any(bad)) {
-      t.bad = true;
-      t.expert = 0;
-    } else {
-      int64_t incl = mine;
+    bad = __any(wrong);
+    if (bad) return;
+    incl = mine;
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up(incl, d, 64);
-        if (lane >= d) incl += o;
-      }
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t o = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += o;
+    }
+    total = __shfl(incl, 63, 64);
+  }
+
+  // Tile idx < total.
+  __device__ __forceinline__ RowTile locate(const Q4Args &a, int64_t idx) const {
+    RowTile t;
+    t.expert = 0;
+    t.row0 = idx * TOK;
+    int64_t end = a.r;
+    if (a.offsets && !bad) {
+      const int per = (a.e + 63) >> 6;
       int ex = -1;
-      int64_t row0 = 0, end = 0;
+      int64_t row0 = 0, hi1 = 0;
       int64_t left = idx - (incl - mine);
       if (left >= 0 && left < mine) {
         for (int i = 0; i < per; ++i) {
-          const int e = e0 + i;
+          const int e = (threadIdx.x & 63) * per + i;
           if (e >= a.e) break;
           const int64_t lo = a.offsets[e], hi = a.offsets[e + 1];
           const int64_t tl = (hi - lo + TOK - 1) / TOK;
           if (left < tl) {
             ex = e;
             row0 = lo + left * TOK;
-            end = hi;
+            hi1 = hi;
             break;
           }
           left -= tl;
         }
       }
-      const uint64_t who = __ballot(ex >= 0);
-      if (who) {
-        const int src = __ffsll((unsigned long long)who) - 1;
-        t.expert = __builtin_amdgcn_readfirstlane(__shfl(ex, src, 64));
-        t.row0 = __shfl(row0, src, 64);
-        end = __shfl(end, src, 64);
-        t.cnt = (int)(end - t.row0 < TOK ? end - t.row0 : TOK);
-      }
-      return t;
+      const int src = __ffsll((unsigned long long)__ballot(ex >= 0)) - 1;
+      t.expert = __builtin_amdgcn_readfirstlane(__shfl(ex, src, 64));
+      t.row0 = __shfl(row0, src, 64);
+      end = __shfl(hi1, src, 64);
     }
+    t.cnt = __builtin_amdgcn_readfirstlane((int)(end - t.row0 < TOK ? end - t.row0 : TOK));
+    return t;
   }
-  const int64_t left = a.r - t.row0;
-  if (left <= 0) t.expert = -1;
-  t.cnt = (int)(left < 0 ? 0 : left < TOK ? left : TOK);
-  return t;
-}
+};
 
 __device__ __forceinline__ void store_y(const Q4Args &a, int64_t row, int64_t i, float v) {
   if (a.ybf16) ((uint16_t *)a.Y)[row * a.n + i] = (uint16_t)f32_to_bf16_bits(v);
@@ -209,8 +208,10 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
   __shared__ float part[NW][R * TT * 256];
   const int lane = threadIdx.x & 63, r16 = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const RowTile tl = find_tile<TOK>(a, blockIdx.y);
-  if (tl.expert < 0) return;
+  Tiles<TOK> tiles;
+  tiles.scan(a);
+  if (blockIdx.y >= tiles.total) return;
+  const RowTile tl = tiles.locate(a, blockIdx.y);
   const int rb0 = blockIdx.x * R;
 
   const char *xp[TT];
@@ -233,7 +234,7 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
     for (int u = 0; u < TT; ++u) tot[b][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
 
-  if (!tl.bad) {
+  if (!tiles.bad) {
     for (int ch = wave; ch < nch; ch += NW) {
       uint4 w[R];
 #pragma unroll
@@ -300,7 +301,7 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
 #pragma unroll
     for (int w = 0; w < NW; ++w) v += part[w][idx];
     const int64_t row = tl.row0 + tok;
-    bool ok = !tl.bad;
+    bool ok = !tiles.bad;
     if (a.rows && ok) {
       const int32_t xr = a.rows[row];
       ok = xr >= 0 && xr < a.xrows;
@@ -308,6 +309,287 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
     if (a.row_scale) v *= a.row_scale[row];
     store_y(a, row, i, ok ? v : __uint_as_float(0x7fc00000u));
   }
+}
+
+// ---------------------------------------------------------------- tile kernel
+// Large row tiles.  The zero term -z Xs is formed by the matrix cores too: Xs
+// (float32, from q4_sums_kernel) and z are split into three bfloat16 terms
+// each and eight of their nine products are summed as one more K slice of the
+// group,
+//   A: sh sm sh sl sh sm sl sm    B: -zh -zh -zm -zh -zl -zm -zm -zl
+// (the missing zl sl is below 2^-32 of the product), so a group costs one
+// vector operation per output, the scaling.
+__device__ __forceinline__ void split_sum(float v, uint32_t &h, uint32_t &m, uint32_t &l) {
+  h = __float_as_uint(v) & 0xffff0000u;
+  const float r1 = v - __uint_as_float(h);
+  m = __float_as_uint(r1) & 0xffff0000u;
+  l = __float_as_uint(r1 - __uint_as_float(m));
+}
+__device__ __forceinline__ uint32_t pack_hi(uint32_t lo, uint32_t hi) {
+  return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+}
+
+// Group sums of X as A operands, aug[row][k], and for float32 X its three
+// bfloat16 planes.  With `rows` row i is X's row rows[i].  A thread takes 8
+// columns; a group's G / 8 threads are neighbours.
+template <bool XBF16, int G>
+__global__ __launch_bounds__(256) void q4_sums_kernel(const void *__restrict__ Xv, const int32_t *__restrict__ rows,
+                                                      int64_t xrows, int64_t nrow, int64_t m, uint4 *__restrict__ aug,
+                                                      uint4 *__restrict__ planes) {
+  const int64_t m8 = m / 8, all = nrow * m8;
+  for (int64_t base = (int64_t)blockIdx.x * 256; base < all; base += (int64_t)gridDim.x * 256) {
+    const int64_t id = base + threadIdx.x;
+    const bool has = id < all;
+    float sum = 0.0f;
+    if (has) {
+      int64_t row = id / m8;
+      const int64_t c = id % m8;
+      if (rows) {
+        row = rows[row];
+        if (row < 0 || row >= xrows) row = 0;
+      }
+      const int64_t at = row * m8 + c;
+      float v[8];
+      if constexpr (XBF16) {
+        const uint4 x = ((const uint4 *)Xv)[at];
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[2 * e] = __uint_as_float(u[e] << 16);
+          v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+        }
+      } else {
+        const float4 x = ((const float4 *)Xv)[2 * at], y = ((const float4 *)Xv)[2 * at + 1];
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+        uint4 t[3];
+        split3((const float *)Xv + 8 * at, t);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) planes[p * all + id] = t[p];
+      }
+      sum = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
+#pragma unroll
+    for (int d = 1; d < G / 8; d <<= 1) sum += __shfl_xor(sum, d, 64);
+    if (has && (threadIdx.x & (G / 8 - 1)) == 0) {
+      uint32_t h, mi, l;
+      split_sum(sum, h, mi, l);
+      aug[id / (G / 8)] = make_uint4(pack_hi(h, mi), pack_hi(h, l), pack_hi(h, mi), pack_hi(l, mi));
+    }
+  }
+}
+
+typedef __attribute__((address_space(3))) void q4_lds_t;
+typedef const __attribute__((address_space(1))) void q4_global_t;
+
+// 64 WT rows of Y x 64 WN output rows per workgroup, a 64 x 64 quarter of it
+// per wave (2 x 2 blocks of 32 x 32).  X goes straight to LDS, 128 columns of
+// every row at a time into one of two buffers while the other is multiplied
+// (16-byte slots XOR-swizzled by row, so that 16 rows of a column slice lie in
+// different banks); codes go to registers one record ahead and are expanded
+// there, since each is used by this wave alone (and by the WT - 1 waves beside
+// it, whose reads hit the cache).
+template <int G, int WT, int WN>
+__global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, const uint16_t *__restrict__ X,
+                                                                  int64_t plane, int nt, bool compact,
+                                                                  const uint4 *__restrict__ aug, int nrb, int nch,
+                                                                  int nnb) {
+  constexpr int NW = WT * WN, TOK = 64 * WT;
+  constexpr int GPC = 128 / G, SPG = G / 16;     // groups per record, K steps per group
+  constexpr int RECW = 256 + 32 * GPC;
+  constexpr int XL = 16 / WN;                    // X loads of 1 KB per wave and record
+  constexpr int AL = (WT * GPC + NW - 1) / NW;   // group-sum loads per wave and record
+  __shared__ __align__(16) unsigned char xs0[TOK * 256], xs1[TOK * 256];
+  __shared__ __align__(16) unsigned char au0[GPC * TOK * 16], au1[GPC * TOK * 16];
+  const int lane = threadIdx.x & 63, hi = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wt = wave / WN, wn = wave % WN;
+
+  // Consecutive workgroups go to different XCDs: each XCD takes a contiguous
+  // eighth of the tiles, walked four row tiles at a time over the output
+  // blocks, so the workgroups sharing an L2 share X tiles and codes.
+  Tiles<TOK> tiles;
+  tiles.scan(a);
+  const int64_t all = tiles.total * nnb, per = (all + 7) / 8;
+  const int64_t idx = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int64_t)(blockIdx.x >> 3) >= per || idx >= all) return;
+  const int64_t strip = idx / (4 * nnb), in = idx - strip * 4 * nnb;
+  const int64_t wide = tiles.total - 4 * strip < 4 ? tiles.total - 4 * strip : 4;
+  const int nb = (int)(in / wide);
+  const RowTile tl = tiles.locate(a, 4 * strip + in % wide);
+
+  auto x_row = [&](int tok) __attribute__((always_inline)) {   // row of X (its planes) of row tok of the tile
+    int64_t row = tl.row0 + (tok < tl.cnt ? tok : 0);
+    if (compact && nt > 1) return row;
+    if (a.rows) {
+      row = a.rows[row];
+      if (row < 0 || row >= a.xrows) row = 0;
+    }
+    return row;
+  };
+  const int64_t k = a.m / G;
+  const char *xp[XL];
+  int xc[XL];                                   // column of this lane's 16 bytes
+#pragma unroll
+  for (int i = 0; i < XL; ++i) {
+    const int tok = (wave * XL + i) * 4 + (lane >> 4);
+    xc[i] = ((lane & 15) ^ (tok & 15)) * 8;
+    xp[i] = (const char *)(X + x_row(tok) * a.m);
+  }
+  const uint4 *ap[AL];
+#pragma unroll
+  for (int i = 0; i < AL; ++i) {
+    const int j = wave + i * NW, tok = (j % WT) * 64 + lane;
+    ap[i] = aug + (compact ? tl.row0 + (tok < tl.cnt ? tok : 0) : x_row(tok)) * k + j / WT;
+  }
+  auto issue = [&](int c, unsigned char *xs, unsigned char *au) __attribute__((always_inline)) {
+    const int e = nt > 1 ? c / nch : 0, ch = c - e * nch;
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      // columns past m are not multiplied: read the start of the row instead
+      const int col = ch * 128 + xc[i] < a.m ? ch * 128 + xc[i] : 0;
+      __builtin_amdgcn_global_load_lds((q4_global_t *)(xp[i] + 2 * (e * plane + col)),
+                                       (q4_lds_t *)(xs + (wave * XL + i) * 1024), 16, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < AL; ++i) {
+      const int j = wave + i * NW;
+      if (j < WT * GPC) {
+        const bool in_row = ch * GPC + j / WT < k;
+        __builtin_amdgcn_global_load_lds((q4_global_t *)(ap[i] + (in_row ? ch * GPC : -(j / WT))),
+                                         (q4_lds_t *)(au + (j / WT) * TOK * 16 + (j % WT) * 1024), 16, 0, 0);
+      }
+    }
+  };
+
+  const uint32_t *wp[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    int rb = (nb * WN + wn) * 4 + 2 * b + ((lane >> 4) & 1);
+    if (rb >= nrb) rb = nrb - 1;
+    wp[b] = a.W + ((int64_t)tl.expert * nrb + rb) * nch * RECW;
+  }
+  struct Codes {
+    uint4 w[2][2];
+    float2 sz[2][GPC];
+  };
+  auto fetch = [&](int ch, Codes &c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t *rec = wp[b] + (int64_t)ch * RECW;
+      c.w[b][0] = *(const uint4 *)(rec + 4 * (16 * hi + (lane & 15)));
+      c.w[b][1] = *(const uint4 *)(rec + 4 * (32 + 16 * hi + (lane & 15)));
+#pragma unroll
+      for (int q = 0; q < GPC; ++q) c.sz[b][q] = *(const float2 *)(rec + 256 + 2 * (16 * q + (lane & 15)));
+    }
+  };
+
+  f32x16_t tot[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) tot[i][b][v] = 0.0f;
+
+  const int arow = (wt * 64 + (lane & 31)) * 256 + ((hi ^ (lane & 15)) << 4);
+  auto compute = [&](int c, const unsigned char *xs, const unsigned char *au, const Codes &cd)
+                     __attribute__((always_inline)) {
+    const int e = nt > 1 ? c / nch : 0, ch = c - e * nch;
+#pragma unroll
+    for (int q = 0; q < GPC; ++q) {
+      if (ch * GPC + q >= k) break;
+      f32x16_t acc[2][2];
+      uint4 ba[2], aa[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        aa[i] = *(const uint4 *)(au + (q * TOK + wt * 64 + i * 32 + (lane & 31)) * 16);
+        // K slots 8 .. 15 (the upper lanes) and the later terms of float32 X add nothing
+        if (hi || e) aa[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t h, mi, l;
+        split_sum(-cd.sz[b][q].y, h, mi, l);
+        ba[b] = make_uint4(pack_hi(h, h), pack_hi(mi, h), pack_hi(l, mi), pack_hi(mi, l));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          f32x16_t z;
+#pragma unroll
+          for (int v = 0; v < 16; ++v) z[v] = 0.0f;
+          acc[i][b] = mfma_bf16(aa[i], ba[b], z);
+        }
+#pragma unroll
+      for (int u = 0; u < SPG; ++u) {
+        const int s = q * SPG + u;
+        uint4 x[2], w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x[i] = *(const uint4 *)(xs + (arow ^ (s << 5)) + i * 8192);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint4 &cw = cd.w[b][s & 1];
+          w[b] = q4_codes((s >> 1) == 0 ? cw.x : (s >> 1) == 1 ? cw.y : (s >> 1) == 2 ? cw.z : cw.w);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) acc[i][b] = mfma_bf16(x[i], w[b], acc[i][b]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) tot[i][b][v] = fmaf(cd.sz[b][q].x, acc[i][b][v], tot[i][b][v]);
+    }
+  };
+
+  if (!tiles.bad) {
+    const int n = nt * nch;
+    Codes c0, c1;
+    issue(0, xs0, au0);
+    fetch(0, c0);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    for (int c = 0; c < n; c += 2) {
+      if (c + 1 < n) {
+        issue(c + 1, xs1, au1);
+        fetch((c + 1) % nch, c1);
+      }
+      compute(c, xs0, au0, c0);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if (c + 1 >= n) break;
+      if (c + 2 < n) {
+        issue(c + 2, xs0, au0);
+        fetch((c + 2) % nch, c0);
+      }
+      compute(c + 1, xs1, au1, c1);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int tok = wt * 64 + i * 32 + acc32_row(v, lane);
+      if (tok >= tl.cnt) continue;
+      const int64_t row = tl.row0 + tok;
+      bool ok = !tiles.bad;
+      if (a.rows && ok) {
+        const int32_t xr = a.rows[row];
+        ok = xr >= 0 && xr < a.xrows;
+      }
+      const float f = a.row_scale ? a.row_scale[row] : 1.0f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int64_t col = (int64_t)(nb * WN + wn) * 64 + b * 32 + (lane & 31);
+        if (col < a.n) store_y(a, row, col, ok ? tot[i][b][v] * f : __uint_as_float(0x7fc00000u));
+      }
+    }
 }
 
 // Most tiles of tok rows that e ranges covering at most r rows can be cut into.
@@ -328,11 +610,60 @@ hipError_t stream_go(const Q4Args &a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Workspace of the tile kernel: group sums, then the planes of float32 X, of X's
+// rows or, with a gather of fewer rows than X has, of the gathered rows.
+struct TileWs {
+  bool compact;
+  int64_t nrow;
+  size_t planes, bytes;
+};
+TileWs tile_ws(int64_t xrows, int64_t r, int64_t m, int group, bool xbf16) {
+  TileWs w;
+  w.compact = r < xrows;
+  w.nrow = w.compact ? r : xrows;
+  w.planes = (size_t)w.nrow * (m / group) * 16;
+  w.bytes = w.planes + (xbf16 ? 0 : (size_t)3 * w.nrow * m * 2);
+  return w;
+}
+
+template <int G, int WT, int WN>
+hipError_t tile_go(const Q4Args &a, const TileWs &w, void *ws, hipStream_t st) {
+  const int nrb = (int)q4_row_blocks(a.n), nch = (int)q4_chunks(a.m);
+  const int nnb = (nrb + 4 * WN - 1) / (4 * WN);
+  const int64_t all = max_tiles(a.r, a.offsets ? a.e : 1, 64 * WT) * nnb;
+  const int64_t blocks = (all + 7) / 8 * 8;
+  if (blocks * 64 * WT * WN > 0xffffffffll) return hipErrorInvalidConfiguration;
+  uint4 *aug = (uint4 *)ws, *planes = (uint4 *)((char *)ws + w.planes);
+  const int64_t sum_blocks = (w.nrow * (a.m / 8) + 255) / 256;
+  const uint32_t sb = (uint32_t)(sum_blocks < 16384 ? sum_blocks : 16384);
+  const int32_t *rows = w.compact ? a.rows : nullptr;
+  if (a.xbf16) q4_sums_kernel<true, G><<<sb, 256, 0, st>>>(a.X, rows, a.xrows, w.nrow, a.m, aug, planes);
+  else q4_sums_kernel<false, G><<<sb, 256, 0, st>>>(a.X, rows, a.xrows, w.nrow, a.m, aug, planes);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  q4_tile_kernel<G, WT, WN><<<(uint32_t)blocks, 64 * WT * WN, 0, st>>>(
+      a, a.xbf16 ? (const uint16_t *)a.X : (const uint16_t *)planes, w.nrow * a.m, a.xbf16 ? 1 : 3, w.compact, aug, nrb,
+      nch, nnb);
+  return hipGetLastError();
+}
+
+// Rows per expert, on average: what the tile sizes go by (the bounds are on the device).
+int64_t rows_per_matrix(int64_t r, int64_t e) { return (r + e - 1) / e; }
+bool use_tiles(int64_t r, int64_t e) { return rows_per_matrix(r, e) > 64; }
+
 template <bool XBF16, int G>
 hipError_t stream_pick(const Q4Args &a, hipStream_t st) {
-  const int64_t per = a.offsets ? (a.r + a.e - 1) / a.e : a.r;
-  if (per <= 16) return stream_go<XBF16, G, 1, 1, 8>(a, st);
+  if (rows_per_matrix(a.r, a.e) <= 16) return stream_go<XBF16, G, 1, 1, 8>(a, st);
   return stream_go<XBF16, G, 2, 4, 4>(a, st);
+}
+
+template <int G>
+hipError_t pick(const Q4Args &a, void *ws, hipStream_t st) {
+  if (use_tiles(a.r, a.e)) {
+    const TileWs w = tile_ws(a.xrows, a.r, a.m, G, a.xbf16);
+    return tile_go<G, 2, 4>(a, w, ws, st);
+  }
+  return a.xbf16 ? stream_pick<true, G>(a, st) : stream_pick<false, G>(a, st);
 }
 
 }  // namespace
@@ -345,17 +676,14 @@ hipError_t launch_pack4(const uint8_t *codes, const float *scale, const float *z
   return hipGetLastError();
 }
 
-size_t q4_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int, bool) { return 0; }
+size_t q4_ws_bytes(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16) {
+  return use_tiles(r, e) ? tile_ws(xrows, r, m, group, xbf16).bytes : 0;
+}
 
-hipError_t launch_q4(const Q4Args &a, void *, hipStream_t st) {
-  if (a.xbf16) {
-    if (a.group == 128) return stream_pick<true, 128>(a, st);
-    if (a.group == 64) return stream_pick<true, 64>(a, st);
-    return stream_pick<true, 32>(a, st);
-  }
-  if (a.group == 128) return stream_pick<false, 128>(a, st);
-  if (a.group == 64) return stream_pick<false, 64>(a, st);
-  return stream_pick<false, 32>(a, st);
+hipError_t launch_q4(const Q4Args &a, void *ws, hipStream_t st) {
+  if (a.group == 128) return pick<128>(a, ws, st);
+  if (a.group == 64) return pick<64>(a, ws, st);
+  return pick<32>(a, ws, st);
 }
 
 }  // namespace slim
