@@ -18,6 +18,8 @@
 // a wave reads one record as 64 consecutive 16-byte loads and its pairs with
 // one 8-byte load per group: a pure stream.  Rows past n and columns past m
 // are stored as zeros.
+#include <type_traits>
+
 #include "common.hpp"
 #include "serve.hpp"
 
@@ -137,7 +139,7 @@ struct Tiles {
         else mine += (hi - lo + TOK - 1) / TOK;
       }
     }
-    bad = __any(wrong);
+    bad = __builtin_amdgcn_ballot_w64(wrong) != 0;   // uniform, unlike __any, for the compiler too
     if (bad) return;
     incl = mine;
 #pragma unroll
@@ -145,7 +147,7 @@ struct Tiles {
       const int64_t o = __shfl_up(incl, d, 64);
       if (lane >= d) incl += o;
     }
-    total = __shfl(incl, 63, 64);
+    total = __builtin_amdgcn_readfirstlane((int)__shfl(incl, 63, 64));
   }
 
   // Tile idx < total.
@@ -179,6 +181,7 @@ struct Tiles {
       t.row0 = __shfl(row0, src, 64);
       end = __shfl(hi1, src, 64);
     }
+    t.row0 = __builtin_amdgcn_readfirstlane((int)t.row0);   // uniform, and below 2^20
     t.cnt = __builtin_amdgcn_readfirstlane((int)(end - t.row0 < TOK ? end - t.row0 : TOK));
     return t;
   }
@@ -329,29 +332,32 @@ __device__ __forceinline__ uint32_t pack_hi(uint32_t lo, uint32_t hi) {
   return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
-// Group sums of X as A operands, aug[row][k], and for float32 X its three
-// bfloat16 planes.  With `rows` row i is X's row rows[i].  A thread takes 8
-// columns; a group's G / 8 threads are neighbours.
+// Group sums of X, sums[row][kp] (kp: groups in whole records), and float32 X
+// as three bfloat16 planes side by side, planes[row][3][nch * 128], both zero
+// past m; of bfloat16 X a copy if planes is given.  With `rows` row i is X's
+// row rows[i].  A thread takes 8 columns; a
+// group's G / 8 threads are neighbours.
 template <bool XBF16, int G>
 __global__ __launch_bounds__(256) void q4_sums_kernel(const void *__restrict__ Xv, const int32_t *__restrict__ rows,
-                                                      int64_t xrows, int64_t nrow, int64_t m, uint4 *__restrict__ aug,
-                                                      uint4 *__restrict__ planes) {
-  const int64_t m8 = m / 8, all = nrow * m8;
+                                                      int64_t xrows, int64_t nrow, int64_t m, int nch,
+                                                      float *__restrict__ sums, uint4 *__restrict__ planes) {
+  const int64_t m8 = m / 8, p8 = (int64_t)nch * 16, all = nrow * p8;
   for (int64_t base = (int64_t)blockIdx.x * 256; base < all; base += (int64_t)gridDim.x * 256) {
     const int64_t id = base + threadIdx.x;
-    const bool has = id < all;
+    const int64_t i = id / p8, c = id - i * p8;
+    const bool has = id < all && c < m8;
     float sum = 0.0f;
     if (has) {
-      int64_t row = id / m8;
-      const int64_t c = id % m8;
+      int64_t row = i;
       if (rows) {
-        row = rows[row];
+        row = rows[i];
         if (row < 0 || row >= xrows) row = 0;
       }
       const int64_t at = row * m8 + c;
       float v[8];
       if constexpr (XBF16) {
         const uint4 x = ((const uint4 *)Xv)[at];
+        if (planes) planes[i * p8 + c] = x;
         const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -364,42 +370,88 @@ __global__ __launch_bounds__(256) void q4_sums_kernel(const void *__restrict__ X
         uint4 t[3];
         split3((const float *)Xv + 8 * at, t);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) planes[p * all + id] = t[p];
+        for (int p = 0; p < 3; ++p) planes[(i * 3 + p) * p8 + c] = t[p];
       }
       sum = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    } else if (planes && id < all) {
+#pragma unroll
+      for (int p = 0; p < (XBF16 ? 1 : 3); ++p) planes[(i * (XBF16 ? 1 : 3) + p) * p8 + c] = make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int d = 1; d < G / 8; d <<= 1) sum += __shfl_xor(sum, d, 64);
-    if (has && (threadIdx.x & (G / 8 - 1)) == 0) {
-      uint32_t h, mi, l;
-      split_sum(sum, h, mi, l);
-      aug[id / (G / 8)] = make_uint4(pack_hi(h, mi), pack_hi(h, l), pack_hi(h, mi), pack_hi(l, mi));
-    }
+    if (id < all && (threadIdx.x & (G / 8 - 1)) == 0) sums[i * (nch * (128 / G)) + c / (G / 8)] = sum;
   }
 }
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void q4_lds_t;
 typedef const __attribute__((address_space(1))) void q4_global_t;
 
-// 64 WT rows of Y x 64 WN output rows per workgroup, a 64 x 64 quarter of it
-// per wave (2 x 2 blocks of 32 x 32).  X goes straight to LDS, 128 columns of
-// every row at a time into one of two buffers while the other is multiplied
-// (16-byte slots XOR-swizzled by row, so that 16 rows of a column slice lie in
-// different banks); codes go to registers one record ahead and are expanded
-// there, since each is used by this wave alone (and by the WT - 1 waves beside
-// it, whose reads hit the cache).
+// BYTES (4 or 16) per lane from base + voff + soff straight to LDS, 64 lanes in
+// a row from `to`.
+template <int BYTES>
+__device__ __forceinline__ void load_lds(const void *base, uint32_t limit, void *to, uint32_t voff, int soff) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, (int)limit, 0x00020000);
+  if constexpr (BYTES == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (q4_lds_t *)to, 16, (int)voff, soff, 0, 0);
+  else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (q4_lds_t *)to, 4, (int)voff, soff, 0, 0);
+}
+
+// Waits until at most VM of this wave's loads are in flight (loads complete in
+// order, so what was issued before the last VM is in LDS) and its LDS reads
+// have returned.  The builtin, not inline text: the compiler then knows which
+// LDS loads have landed and adds no full wait before the next stage is read.
+template <int VM>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | 7 << 4 | (VM >> 4) << 14);
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
+
+// 128 rows of Y x 256 output rows per workgroup, a 64 x 64 piece of it per wave
+// (2 x 2 blocks of 32 x 32).  Every operand goes straight to LDS, 128 columns
+// (a record per 16 output rows) to a stage, two stages ahead of the products:
+// X's rows with their 16-byte slots XOR-swizzled by row (16 rows of a column
+// slice then lie in different banks), the records, and the group sums.
+//
+// The two waves of a SIMD take turns.  Half a stage is a load phase (the last
+// group's scaling, LDS reads, expansion of the codes: vector unit) and a
+// product phase (16 MFMAs and the zero term: matrix unit) with a barrier after
+// each, and waves 4 .. 7 run one phase behind waves 0 .. 3, so that at any
+// time one wave of each pair keeps the matrix unit busy while the other
+// prepares.  In slots of one phase, a leading wave works on stage c in slots
+// 4 c (load), 4 c + 1 (products), 4 c + 2, 4 c + 3, a trailing one a slot
+// later.  Stage c + 2 is loaded from slot 4 c (4 c + 1) on into the buffer of
+// stage c - 1, last read in slot 4 c - 1; every wave waits for its own loads
+// of stage c + 1 before the end of its second load phase (4 c + 2, 4 c + 3),
+// and stage c + 1 is first read in slot 4 c + 4.
 template <int G, int WT, int WN>
 __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, const uint16_t *__restrict__ X,
-                                                                  int64_t plane, int nt, bool compact,
-                                                                  const uint4 *__restrict__ aug, int nrb, int nch,
+                                                                  int64_t ldx, int nt, bool gather, bool compact,
+                                                                  const float *__restrict__ sums, int nrb, int nch,
                                                                   int nnb) {
   constexpr int NW = WT * WN, TOK = 64 * WT;
-  constexpr int GPC = 128 / G, SPG = G / 16;     // groups per record, K steps per group
+  static_assert(WT * WN == 8, "the phases pair waves w and w + 4");
+  constexpr int GPC = 128 / G;                   // groups per record
   constexpr int RECW = 256 + 32 * GPC;
-  constexpr int XL = 16 / WN;                    // X loads of 1 KB per wave and record
-  constexpr int AL = (WT * GPC + NW - 1) / NW;   // group-sum loads per wave and record
-  __shared__ __align__(16) unsigned char xs0[TOK * 256], xs1[TOK * 256];
-  __shared__ __align__(16) unsigned char au0[GPC * TOK * 16], au1[GPC * TOK * 16];
+  constexpr int XL = 16 / WN;                    // loads per wave and stage: X (1 KB each),
+  constexpr int RL = 4 / WT;                     //   codes of a record,
+  constexpr int ZL = GPC;                        //   scales and zeros,
+  constexpr int SL = (WT * GPC + NW - 1) / NW;   //   group sums of 64 rows
+  constexpr int LOADS = XL + RL + ZL + SL;
+  constexpr int RST = G == 32 ? 2 : 3;           // stages of records (three of 24 KB do not fit)
+  struct Stage {
+    unsigned char x[TOK * 256];
+    float s[GPC * TOK];
+  };
+  struct Recs {
+    // codes, then scales and zeros
+    unsigned char b[4 * WN * (1024 + 128 * GPC)];
+  };
+  constexpr int ZAT = 4 * WN * 1024;
+  __shared__ __align__(16) Stage st0, st1, st2;
+  __shared__ __align__(16) Recs rc0, rc1;
+  __shared__ __align__(16) typename std::conditional<RST == 3, Recs, uint4>::type rc2;
   const int lane = threadIdx.x & 63, hi = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wt = wave / WN, wn = wave % WN;
@@ -417,70 +469,68 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
   const int nb = (int)(in / wide);
   const RowTile tl = tiles.locate(a, 4 * strip + in % wide);
 
-  auto x_row = [&](int tok) __attribute__((always_inline)) {   // row of X (its planes) of row tok of the tile
-    int64_t row = tl.row0 + (tok < tl.cnt ? tok : 0);
-    if (compact && nt > 1) return row;
-    if (a.rows) {
-      row = a.rows[row];
-      if (row < 0 || row >= a.xrows) row = 0;
-    }
-    return row;
+  // Operands come by buffer loads: one descriptor each with its base at this
+  // tile, a 32-bit offset per lane that stays, and the stage as scalar offset.
+  auto x_row = [&](int tok) __attribute__((always_inline)) {   // row of X, from the tile's base
+    const int64_t row = tok < tl.cnt ? tok : 0;
+    if (!gather) return row;
+    const int64_t g = a.rows[tl.row0 + row];
+    return g < 0 || g >= a.xrows ? 0 : g;
   };
-  const int64_t k = a.m / G;
-  const char *xp[XL];
-  int xc[XL];                                   // column of this lane's 16 bytes
+  const int n = nt * nch;                       // stages: float32 X passes its three planes in turn
+  const uint16_t *xbase = X + (gather ? 0 : tl.row0 * ldx);
+  const float *sbase = sums + (gather && !compact ? 0 : tl.row0 * (nch * GPC));
+  const uint32_t xbytes = (uint32_t)((gather ? a.xrows : tl.cnt) * ldx * 2);
+  const uint32_t sbytes = (uint32_t)((gather && !compact ? a.xrows : tl.cnt) * (nch * GPC) * 4);
+  uint32_t xo[XL];                              // this lane's 16 bytes of each of its rows, stage 0
 #pragma unroll
   for (int i = 0; i < XL; ++i) {
     const int tok = (wave * XL + i) * 4 + (lane >> 4);
-    xc[i] = ((lane & 15) ^ (tok & 15)) * 8;
-    xp[i] = (const char *)(X + x_row(tok) * a.m);
+    xo[i] = (uint32_t)(x_row(tok) * ldx * 2) + ((lane & 15) ^ (tok & 15)) * 16;
   }
-  const uint4 *ap[AL];
+  uint32_t so[SL];                              // waves beyond the rows load a piece again
 #pragma unroll
-  for (int i = 0; i < AL; ++i) {
-    const int j = wave + i * NW, tok = (j % WT) * 64 + lane;
-    ap[i] = aug + (compact ? tl.row0 + (tok < tl.cnt ? tok : 0) : x_row(tok)) * k + j / WT;
+  for (int i = 0; i < SL; ++i) {
+    const int j = (wave + i * NW) % (WT * GPC), tok = (j % WT) * 64 + lane;
+    so[i] = (uint32_t)((compact ? (tok < tl.cnt ? tok : 0) : x_row(tok)) * (nch * GPC) + j / WT) * 4;
   }
-  auto issue = [&](int c, unsigned char *xs, unsigned char *au) __attribute__((always_inline)) {
-    const int e = nt > 1 ? c / nch : 0, ch = c - e * nch;
+  auto load_x = [&](int c, bool end, Stage &st) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
-      // columns past m are not multiplied: read the start of the row instead
-      const int col = ch * 128 + xc[i] < a.m ? ch * 128 + xc[i] : 0;
-      __builtin_amdgcn_global_load_lds((q4_global_t *)(xp[i] + 2 * (e * plane + col)),
-                                       (q4_lds_t *)(xs + (wave * XL + i) * 1024), 16, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < AL; ++i) {
-      const int j = wave + i * NW;
-      if (j < WT * GPC) {
-        const bool in_row = ch * GPC + j / WT < k;
-        __builtin_amdgcn_global_load_lds((q4_global_t *)(ap[i] + (in_row ? ch * GPC : -(j / WT))),
-                                         (q4_lds_t *)(au + (j / WT) * TOK * 16 + (j % WT) * 1024), 16, 0, 0);
+      uint32_t o = xo[i];
+      if (end && nt == 1) {
+        // columns past m meet zero codes: any finite value does, here the start of the row
+        const int col = ((lane & 15) ^ (((wave * XL + i) * 4 + (lane >> 4)) & 15)) * 8;
+        if (c * 128 + col >= a.m) o -= (uint32_t)(c * 256 + col * 2);
       }
+      load_lds<16>(xbase, xbytes, st.x + (wave * XL + i) * 1024, o, c * 256);
+    }
+    const int ch = c < nch ? c : 0;             // used with the first plane only
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      const int j = (wave + i * NW) % (WT * GPC);
+      load_lds<4>(sbase, sbytes, st.s + (j / WT) * TOK + (j % WT) * 64, so[i], ch * GPC * 4);
     }
   };
-
-  const uint32_t *wp[2];
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    int rb = (nb * WN + wn) * 4 + 2 * b + ((lane >> 4) & 1);
-    if (rb >= nrb) rb = nrb - 1;
-    wp[b] = a.W + ((int64_t)tl.expert * nrb + rb) * nch * RECW;
-  }
-  struct Codes {
-    uint4 w[2][2];
-    float2 sz[2][GPC];
+  // Records, as byte offsets from the tile's first; row blocks past the last
+  // repeat it.  A wave loads the codes of records RL wave .. and the scales and
+  // zeros of records j and j + 2, j = 4 (wave / 2) + wave % 2, which one lane
+  // reads together.
+  const int rb0 = nb * WN * 4;
+  auto rec = [&](int j) __attribute__((always_inline)) {
+    return (rb0 + j < nrb ? j : nrb - 1 - rb0) * nch * (RECW * 4);
   };
-  auto fetch = [&](int ch, Codes &c) __attribute__((always_inline)) {
+  const uint32_t *wbase = a.W + ((int64_t)tl.expert * nrb + rb0) * nch * RECW;
+  const uint32_t limit = (uint32_t)(rec(WN * 4 - 1) + nch * (RECW * 4));
+  // scale and zero words in LDS: [4 (wave / 2) + wave % 2][group][row][block][2]
+  const uint32_t zo = (uint32_t)(rec(wave / 2 * 4 + wave % 2 + (lane & 2)) + 1024 + (lane >> 2) * 8 + (lane & 1) * 4);
+  auto load_rec = [&](int c, Recs &rc) __attribute__((always_inline)) {
+    const int at = (nt > 1 ? c % nch : c) * (RECW * 4);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const uint32_t *rec = wp[b] + (int64_t)ch * RECW;
-      c.w[b][0] = *(const uint4 *)(rec + 4 * (16 * hi + (lane & 15)));
-      c.w[b][1] = *(const uint4 *)(rec + 4 * (32 + 16 * hi + (lane & 15)));
+    for (int i = 0; i < RL; ++i)
+      load_lds<16>(wbase, limit, rc.b + (wave * RL + i) * 1024, lane * 16, at + rec(wave * RL + i));
 #pragma unroll
-      for (int q = 0; q < GPC; ++q) c.sz[b][q] = *(const float2 *)(rec + 256 + 2 * (16 * q + (lane & 15)));
-    }
+    for (int q = 0; q < GPC; ++q) load_lds<4>(wbase, limit, rc.b + ZAT + (wave * GPC + q) * 256, zo, at + q * 128);
   };
 
   f32x16_t tot[2][2];
@@ -491,27 +541,97 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
 #pragma unroll
       for (int v = 0; v < 16; ++v) tot[i][b][v] = 0.0f;
 
-  const int arow = (wt * 64 + (lane & 31)) * 256 + ((hi ^ (lane & 15)) << 4);
-  auto compute = [&](int c, const unsigned char *xs, const unsigned char *au, const Codes &cd)
-                     __attribute__((always_inline)) {
-    const int e = nt > 1 ? c / nch : 0, ch = c - e * nch;
+  const int xrow0 = (wt * 64 + (lane & 31)) * 256 + ((hi ^ (lane & 15)) << 4);
+  const int rec0 = wn * 4 + ((lane >> 4) & 1);   // record of this lane's output row in block 0
+  constexpr int GH = G == 32 ? 2 : 1;            // groups that end in a half stage (G = 128: in the second)
+  f32x16_t acc[2][2];                            // sums of the group at hand
+  float sc[GH][2];                               // its scales
 #pragma unroll
-    for (int q = 0; q < GPC; ++q) {
-      if (ch * GPC + q >= k) break;
-      f32x16_t acc[2][2];
-      uint4 ba[2], aa[2];
+  for (int b = 0; b < 2; ++b) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        aa[i] = *(const uint4 *)(au + (q * TOK + wt * 64 + i * 32 + (lane & 31)) * 16);
-        // K slots 8 .. 15 (the upper lanes) and the later terms of float32 X add nothing
-        if (hi || e) aa[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int g = 0; g < GH; ++g) sc[g][b] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][b][v] = 0.0f;
+  }
+  auto scale_group = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) tot[i][b][v] = fmaf(sc[g][b], acc[i][b][v], tot[i][b][v]);
+    // here, and not later, when the next group's sums need the registers
+#pragma unroll
+    for (int i = 0; i < 2; ++i) asm volatile("" : "+v"(tot[i][0]), "+v"(tot[i][1]));
+  };
+
+  u32x4_t x[4][2];                               // X of half a stage, [K step][block]
+  uint2 cw[2][2];                                // its codes, [16 columns of 32][block]
+  u32x4_t w[2][2];                               // and those of one K step, expanded
+  uint4 aa[GH][2], ba[GH][2];                    // and of its zero terms
+  auto expand = [&](int u) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      w[u & 1][b] = __builtin_bit_cast(u32x4_t, q4_codes(u < 2 ? cw[u & 1][b].x : cw[u & 1][b].y));
+  };
+  // Load phase h of stage c.
+  auto prepare = [&](int c, int h, const Stage &st, const Recs &rc) __attribute__((always_inline)) {
+    // addresses formed anew: kept over the loop, those of all stages would
+    // take more registers than there are
+    int arow = xrow0, rrow = rec0;
+    // (an offset the compiler does not know, too, for the scales: seeing that
+    // they cannot be what the first load of the stage writes, it would wait for
+    // every load in flight)
+    int zrow = ZAT + (wn * 2 + ((lane >> 4) & 1)) * GPC * 256 + (lane & 15) * 16;
+    asm volatile("" : "+v"(arow), "+v"(rrow), "+v"(zrow));
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        x[u][i] = *(const u32x4_t *)(st.x + (arow ^ ((4 * h + u) << 5)) + i * 8192);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+        cw[o][b] = *(const uint2 *)(rc.b + (rrow + 2 * b) * 1024 + (16 * (hi + 2 * o) + (lane & 15)) * 16 + 8 * h);
+    expand(0);
+    if (G != 128 || h == 1) {
+      // K slots 8 .. 15 (the upper lanes) and the later planes of float32 X add nothing
+      const uint32_t keep = (uint32_t)(((hi | (c < nch ? 0 : 1)) - 1) >> 31);
+#pragma unroll
+      for (int g = 0; g < GH; ++g) {
+        const int q = G == 128 ? 0 : h * GH + g;
+        uint32_t p, r, l;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          split_sum(st.s[q * TOK + wt * 64 + i * 32 + (lane & 31)], p, r, l);
+          aa[g][i] = make_uint4(pack_hi(p, r) & keep, pack_hi(p, l) & keep, pack_hi(p, r) & keep,
+                                pack_hi(l, r) & keep);
+        }
+        const float4 sz = *(const float4 *)(rc.b + zrow + q * 256);
+        sc[g][0] = sz.x;
+        sc[g][1] = sz.z;
+        split_sum(-sz.y, p, r, l);
+        ba[g][0] = make_uint4(pack_hi(p, p), pack_hi(r, p), pack_hi(l, r), pack_hi(r, l));
+        split_sum(-sz.w, p, r, l);
+        ba[g][1] = make_uint4(pack_hi(p, p), pack_hi(r, p), pack_hi(l, r), pack_hi(r, l));
       }
+    }
+    // keeps this phase's work out of the product phase
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        uint32_t h, mi, l;
-        split_sum(-cd.sz[b][q].y, h, mi, l);
-        ba[b] = make_uint4(pack_hi(h, h), pack_hi(mi, h), pack_hi(l, mi), pack_hi(mi, l));
-      }
+    for (int u = 0; u < 4; ++u) asm volatile("" : "+v"(x[u][0]), "+v"(x[u][1]));
+    asm volatile("" : "+v"(w[0][0]), "+v"(w[0][1]));
+  };
+  // Product phase h.  What lies past m is zero in the codes, and X's part of it
+  // is finite or of a row that is not finite anyway; its sums get scale 0.
+  auto multiply = [&](int h) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (u < 3) expand(u + 1);
+      const bool first = G == 128 ? h == 0 && u == 0 : u % (G / 16) == 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -519,57 +639,90 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
           f32x16_t z;
 #pragma unroll
           for (int v = 0; v < 16; ++v) z[v] = 0.0f;
-          acc[i][b] = mfma_bf16(aa[i], ba[b], z);
+          acc[i][b] = mfma_bf16(__builtin_bit_cast(uint4, x[u][i]), __builtin_bit_cast(uint4, w[u & 1][b]),
+                                first ? z : acc[i][b]);
         }
-#pragma unroll
-      for (int u = 0; u < SPG; ++u) {
-        const int s = q * SPG + u;
-        uint4 x[2], w[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) x[i] = *(const uint4 *)(xs + (arow ^ (s << 5)) + i * 8192);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const uint4 &cw = cd.w[b][s & 1];
-          w[b] = q4_codes((s >> 1) == 0 ? cw.x : (s >> 1) == 1 ? cw.y : (s >> 1) == 2 ? cw.z : cw.w);
-        }
+      if (G == 128 ? h == 1 && u == 3 : u % (G / 16) == G / 16 - 1) {
+        const int g = G == 32 ? u / 2 : 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int b = 0; b < 2; ++b) acc[i][b] = mfma_bf16(x[i], w[b], acc[i][b]);
+          for (int b = 0; b < 2; ++b) acc[i][b] = mfma_bf16(aa[g][i], ba[g][b], acc[i][b]);
+        if (G == 32 && u == 1) scale_group(0);
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) tot[i][b][v] = fmaf(cd.sz[b][q].x, acc[i][b][v], tot[i][b][v]);
     }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {                // the next step's expansion among this step's MFMAs
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+    }
+    __builtin_amdgcn_s_setprio(0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]));
+    __builtin_amdgcn_sched_barrier(0);
+    meet();
   };
 
   if (!tiles.bad) {
-    const int n = nt * nch;
-    Codes c0, c1;
-    issue(0, xs0, au0);
-    fetch(0, c0);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    for (int c = 0; c < n; c += 2) {
-      if (c + 1 < n) {
-        issue(c + 1, xs1, au1);
-        fetch((c + 1) % nch, c1);
-      }
-      compute(c, xs0, au0, c0);
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      if (c + 1 >= n) break;
-      if (c + 2 < n) {
-        issue(c + 2, xs0, au0);
-        fetch((c + 2) % nch, c0);
-      }
-      compute(c + 1, xs1, au1, c1);
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
+    constexpr int AHEAD = RST == 3 ? LOADS : XL + SL;   // loads that may still fly at the end of a stage
+    auto stage = [&](int c, bool steady, Stage &st, Stage &nxt, Recs &rc, Recs &rnxt) __attribute__((always_inline)) {
+      if (steady || c + RST - 1 < n) load_rec(c + RST - 1, rnxt);
+      if (steady || c + 2 < n) load_x(c + 2, !steady, nxt);
+      scale_group(GH - 1);
+      prepare(c, 0, st, rc);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      meet();
+      multiply(0);
+      if (G != 128) scale_group(GH - 1);
+      prepare(c, 1, st, rc);
+      if (steady) wait_loads<AHEAD>();
+      else wait_loads<0>();
+      __builtin_amdgcn_sched_barrier(0);
+      meet();
+      multiply(1);
+    };
+    load_rec(0, rc0);
+    load_x(0, true, st0);
+    if (n > 1) {
+      if (RST == 3) load_rec(1, rc1);
+      load_x(1, true, st1);
     }
+    wait_loads<0>();
+    meet();
+    if (wave >= 4) meet();
+    int c = 0;
+    if constexpr (RST == 3) {
+      for (; c + 6 <= n; c += 3) {
+        stage(c, true, st0, st2, rc0, rc2);
+        stage(c + 1, true, st1, st0, rc1, rc0);
+        stage(c + 2, true, st2, st1, rc2, rc1);
+      }
+      for (; c < n; c += 3) {
+        stage(c, false, st0, st2, rc0, rc2);
+        if (c + 1 < n) stage(c + 1, false, st1, st0, rc1, rc0);
+        if (c + 2 < n) stage(c + 2, false, st2, st1, rc2, rc1);
+      }
+    } else {
+      for (; c + 9 <= n; c += 6) {
+        stage(c, true, st0, st2, rc0, rc1);
+        stage(c + 1, true, st1, st0, rc1, rc0);
+        stage(c + 2, true, st2, st1, rc0, rc1);
+        stage(c + 3, true, st0, st2, rc1, rc0);
+        stage(c + 4, true, st1, st0, rc0, rc1);
+        stage(c + 5, true, st2, st1, rc1, rc0);
+      }
+      for (; c < n; c += 6) {
+        stage(c, false, st0, st2, rc0, rc1);
+        if (c + 1 < n) stage(c + 1, false, st1, st0, rc1, rc0);
+        if (c + 2 < n) stage(c + 2, false, st2, st1, rc0, rc1);
+        if (c + 3 < n) stage(c + 3, false, st0, st2, rc1, rc0);
+        if (c + 4 < n) stage(c + 4, false, st1, st0, rc0, rc1);
+        if (c + 5 < n) stage(c + 5, false, st2, st1, rc1, rc0);
+      }
+    }
+    if (wave < 4) meet();
+    scale_group(GH - 1);
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -610,19 +763,25 @@ hipError_t stream_go(const Q4Args &a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Workspace of the tile kernel: group sums, then the planes of float32 X, of X's
-// rows or, with a gather of fewer rows than X has, of the gathered rows.
+// Workspace of the tile kernel: group sums, then what of X it cannot read in
+// place, of X's rows or, with a gather of fewer rows than X has, of the
+// gathered rows (compact): the planes of float32 X, or a copy of gathered
+// bfloat16 rows that lie more than 32-bit offsets apart.
 struct TileWs {
-  bool compact;
+  bool compact, copy;
   int64_t nrow;
   size_t planes, bytes;
 };
 TileWs tile_ws(int64_t xrows, int64_t r, int64_t m, int group, bool xbf16) {
   TileWs w;
-  w.compact = r < xrows;
+  const size_t nch = (size_t)q4_chunks(m);
+  const bool far = (uint64_t)xrows * (xbf16 ? 2 * (uint64_t)m : 768 * (uint64_t)nch) >= 0xfff00000ull;
+  // a gather is known only by r != xrows here; far X is always taken row by row
+  w.compact = r < xrows || far;
+  w.copy = xbf16 && far;
   w.nrow = w.compact ? r : xrows;
-  w.planes = (size_t)w.nrow * (m / group) * 16;
-  w.bytes = w.planes + (xbf16 ? 0 : (size_t)3 * w.nrow * m * 2);
+  w.planes = ((size_t)w.nrow * nch * (128 / group) * 4 + 15) / 16 * 16;
+  w.bytes = w.planes + (!xbf16 ? (size_t)w.nrow * 3 * nch * 256 : w.copy ? (size_t)w.nrow * nch * 256 : 0);
   return w;
 }
 
@@ -633,17 +792,20 @@ hipError_t tile_go(const Q4Args &a, const TileWs &w, void *ws, hipStream_t st) {
   const int64_t all = max_tiles(a.r, a.offsets ? a.e : 1, 64 * WT) * nnb;
   const int64_t blocks = (all + 7) / 8 * 8;
   if (blocks * 64 * WT * WN > 0xffffffffll) return hipErrorInvalidConfiguration;
-  uint4 *aug = (uint4 *)ws, *planes = (uint4 *)((char *)ws + w.planes);
-  const int64_t sum_blocks = (w.nrow * (a.m / 8) + 255) / 256;
+  float *sums = (float *)ws;
+  const bool own = !a.xbf16 || w.copy;            // X is read from the workspace
+  uint4 *planes = own ? (uint4 *)((char *)ws + w.planes) : nullptr;
+  const int64_t sum_blocks = (w.nrow * nch * 16 + 255) / 256;
   const uint32_t sb = (uint32_t)(sum_blocks < 16384 ? sum_blocks : 16384);
   const int32_t *rows = w.compact ? a.rows : nullptr;
-  if (a.xbf16) q4_sums_kernel<true, G><<<sb, 256, 0, st>>>(a.X, rows, a.xrows, w.nrow, a.m, aug, planes);
-  else q4_sums_kernel<false, G><<<sb, 256, 0, st>>>(a.X, rows, a.xrows, w.nrow, a.m, aug, planes);
+  if (a.xbf16) q4_sums_kernel<true, G><<<sb, 256, 0, st>>>(a.X, rows, a.xrows, w.nrow, a.m, nch, sums, planes);
+  else q4_sums_kernel<false, G><<<sb, 256, 0, st>>>(a.X, rows, a.xrows, w.nrow, a.m, nch, sums, planes);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   q4_tile_kernel<G, WT, WN><<<(uint32_t)blocks, 64 * WT * WN, 0, st>>>(
-      a, a.xbf16 ? (const uint16_t *)a.X : (const uint16_t *)planes, w.nrow * a.m, a.xbf16 ? 1 : 3, w.compact, aug, nrb,
-      nch, nnb);
+      a, own ? (const uint16_t *)planes : (const uint16_t *)a.X,
+      !own ? a.m : (a.xbf16 ? 1 : 3) * (int64_t)nch * 128, a.xbf16 ? 1 : 3, a.rows && !(own && w.compact), w.compact,
+      sums, nrb, nch, nnb);
   return hipGetLastError();
 }
 
