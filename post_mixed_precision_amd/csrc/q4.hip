@@ -422,9 +422,10 @@ __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory");
 // prepares.  In slots of one phase, a leading wave works on stage c in slots
 // 4 c (load), 4 c + 1 (products), 4 c + 2, 4 c + 3, a trailing one a slot
 // later.  Stage c + 2 is loaded from slot 4 c (4 c + 1) on into the buffer of
-// stage c - 1, last read in slot 4 c - 1; every wave waits for its own loads
-// of stage c + 1 before the end of its second load phase (4 c + 2, 4 c + 3),
-// and stage c + 1 is first read in slot 4 c + 4.
+// stage c - 1, last read in slot 4 c - 1 (4 c for its own); every wave waits for
+// its own loads of stage c + 1 at the end of its first product phase (4 c + 1,
+// 4 c + 2), and stage c + 1 is first read in slot 4 c + 3: X is read into
+// registers during the product phase before its own.
 template <int G, int WT, int WN>
 __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, const uint16_t *__restrict__ X,
                                                                   int64_t ldx, int nt, bool gather, bool compact,
@@ -494,17 +495,9 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
     const int j = (wave + i * NW) % (WT * GPC), tok = (j % WT) * 64 + lane;
     so[i] = (uint32_t)((compact ? (tok < tl.cnt ? tok : 0) : x_row(tok)) * (nch * GPC) + j / WT) * 4;
   }
-  auto load_x = [&](int c, bool end, Stage &st) __attribute__((always_inline)) {
+  auto load_x = [&](int c, Stage &st) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < XL; ++i) {
-      uint32_t o = xo[i];
-      if (end && nt == 1) {
-        // columns past m meet zero codes: any finite value does, here the start of the row
-        const int col = ((lane & 15) ^ (((wave * XL + i) * 4 + (lane >> 4)) & 15)) * 8;
-        if (c * 128 + col >= a.m) o -= (uint32_t)(c * 256 + col * 2);
-      }
-      load_lds<16>(xbase, xbytes, st.x + (wave * XL + i) * 1024, o, c * 256);
-    }
+    for (int i = 0; i < XL; ++i) load_lds<16>(xbase, xbytes, st.x + (wave * XL + i) * 1024, xo[i], c * 256);
     const int ch = c < nch ? c : 0;             // used with the first plane only
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
@@ -576,57 +569,70 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
     for (int b = 0; b < 2; ++b)
       w[u & 1][b] = __builtin_bit_cast(u32x4_t, q4_codes(u < 2 ? cw[u & 1][b].x : cw[u & 1][b].y));
   };
-  // Load phase h of stage c.
-  auto prepare = [&](int c, int h, const Stage &st, const Recs &rc) __attribute__((always_inline)) {
+  float su[GH][2];                               // sums of X, scales and zeros as read
+  float4 sz[GH];
+  constexpr bool BOTH = G != 128;                // a group ends in either half of a stage
+  // Load phase h of stage c: its reads, issued before anything else of the phase,
+  auto read = [&](int h, const Stage &st, const Recs &rc) __attribute__((always_inline)) {
     // addresses formed anew: kept over the loop, those of all stages would
     // take more registers than there are
-    int arow = xrow0, rrow = rec0;
+    int rrow = rec0;
     // (an offset the compiler does not know, too, for the scales: seeing that
     // they cannot be what the first load of the stage writes, it would wait for
     // every load in flight)
     int zrow = ZAT + (wn * 2 + ((lane >> 4) & 1)) * GPC * 256 + (lane & 15) * 16;
-    asm volatile("" : "+v"(arow), "+v"(rrow), "+v"(zrow));
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        x[u][i] = *(const u32x4_t *)(st.x + (arow ^ ((4 * h + u) << 5)) + i * 8192);
+    asm volatile("" : "+v"(rrow), "+v"(zrow));
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int o = 0; o < 2; ++o)
         cw[o][b] = *(const uint2 *)(rc.b + (rrow + 2 * b) * 1024 + (16 * (hi + 2 * o) + (lane & 15)) * 16 + 8 * h);
+    if (BOTH || h == 1) {
+#pragma unroll
+      for (int g = 0; g < GH; ++g) {
+        const int q = BOTH ? h * GH + g : 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) su[g][i] = st.s[q * TOK + wt * 64 + i * 32 + (lane & 31)];
+        sz[g] = *(const float4 *)(rc.b + zrow + q * 256);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto read_x = [&](int h, int u, const Stage &st) __attribute__((always_inline)) {
+    int arow = xrow0;
+    asm volatile("" : "+v"(arow));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[u][i] = *(const u32x4_t *)(st.x + (arow ^ ((4 * h + u) << 5)) + i * 8192);
+  };
+  // and what is computed from them.
+  auto prepare = [&](int c, int h) __attribute__((always_inline)) {
     expand(0);
-    if (G != 128 || h == 1) {
+    if (BOTH || h == 1) {
       // K slots 8 .. 15 (the upper lanes) and the later planes of float32 X add nothing
       const uint32_t keep = (uint32_t)(((hi | (c < nch ? 0 : 1)) - 1) >> 31);
 #pragma unroll
       for (int g = 0; g < GH; ++g) {
-        const int q = G == 128 ? 0 : h * GH + g;
         uint32_t p, r, l;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          split_sum(st.s[q * TOK + wt * 64 + i * 32 + (lane & 31)], p, r, l);
+          split_sum(su[g][i], p, r, l);
           aa[g][i] = make_uint4(pack_hi(p, r) & keep, pack_hi(p, l) & keep, pack_hi(p, r) & keep,
                                 pack_hi(l, r) & keep);
         }
-        const float4 sz = *(const float4 *)(rc.b + zrow + q * 256);
-        sc[g][0] = sz.x;
-        sc[g][1] = sz.z;
-        split_sum(-sz.y, p, r, l);
+        sc[g][0] = sz[g].x;
+        sc[g][1] = sz[g].z;
+        split_sum(-sz[g].y, p, r, l);
         ba[g][0] = make_uint4(pack_hi(p, p), pack_hi(r, p), pack_hi(l, r), pack_hi(r, l));
-        split_sum(-sz.w, p, r, l);
+        split_sum(-sz[g].w, p, r, l);
         ba[g][1] = make_uint4(pack_hi(p, p), pack_hi(r, p), pack_hi(l, r), pack_hi(r, l));
       }
     }
     // keeps this phase's work out of the product phase
-#pragma unroll
-    for (int u = 0; u < 4; ++u) asm volatile("" : "+v"(x[u][0]), "+v"(x[u][1]));
     asm volatile("" : "+v"(w[0][0]), "+v"(w[0][1]));
   };
-  // Product phase h.  What lies past m is zero in the codes, and X's part of it
-  // is finite or of a row that is not finite anyway; its sums get scale 0.
-  auto multiply = [&](int h) __attribute__((always_inline)) {
+  // Product phase h.  X of the next half stage is read into the registers that a
+  // K step has used.
+  auto multiply = [&](int h, const Stage &nst) __attribute__((always_inline)) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -642,6 +648,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
           acc[i][b] = mfma_bf16(__builtin_bit_cast(uint4, x[u][i]), __builtin_bit_cast(uint4, w[u & 1][b]),
                                 first ? z : acc[i][b]);
         }
+      read_x(1 - h, u, nst);
       if (G == 128 ? h == 1 && u == 3 : u % (G / 16) == G / 16 - 1) {
         const int g = G == 32 ? u / 2 : 0;
 #pragma unroll
@@ -652,77 +659,80 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
       }
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {                // the next step's expansion among this step's MFMAs
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {               // the next step's expansion among this step's MFMAs
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
     }
     __builtin_amdgcn_s_setprio(0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]));
-    __builtin_amdgcn_sched_barrier(0);
-    meet();
   };
 
   if (!tiles.bad) {
     constexpr int AHEAD = RST == 3 ? LOADS : XL + SL;   // loads that may still fly at the end of a stage
-    auto stage = [&](int c, bool steady, Stage &st, Stage &nxt, Recs &rc, Recs &rnxt) __attribute__((always_inline)) {
-      if (steady || c + RST - 1 < n) load_rec(c + RST - 1, rnxt);
-      if (steady || c + 2 < n) load_x(c + 2, !steady, nxt);
+    // The last stages load the last one again: no stage differs from the others.
+    auto stage = [&](int c, Stage &st, Stage &st1, Stage &st2, Recs &rc, Recs &rnxt) __attribute__((always_inline)) {
+      read(0, st, rc);
+      load_rec(c + RST - 1 < n ? c + RST - 1 : n - 1, rnxt);
+      load_x(c + 2 < n ? c + 2 : n - 1, st2);
       scale_group(GH - 1);
-      prepare(c, 0, st, rc);
+      prepare(c, 0);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
       meet();
-      multiply(0);
-      if (G != 128) scale_group(GH - 1);
-      prepare(c, 1, st, rc);
-      if (steady) wait_loads<AHEAD>();
-      else wait_loads<0>();
+      multiply(0, st);
+      wait_loads<AHEAD>();
       __builtin_amdgcn_sched_barrier(0);
       meet();
-      multiply(1);
+      read(1, st, rc);
+      if (BOTH) scale_group(GH - 1);
+      prepare(c, 1);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      meet();
+      multiply(1, st1);
+      __builtin_amdgcn_sched_barrier(0);
+      meet();
     };
     load_rec(0, rc0);
-    load_x(0, true, st0);
-    if (n > 1) {
-      if (RST == 3) load_rec(1, rc1);
-      load_x(1, true, st1);
-    }
+    load_x(0, st0);
+    if (RST == 3) load_rec(n > 1 ? 1 : 0, rc1);
+    load_x(n > 1 ? 1 : 0, st1);
     wait_loads<0>();
     meet();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) read_x(0, u, st0);
     if (wave >= 4) meet();
-    int c = 0;
     if constexpr (RST == 3) {
-      for (; c + 6 <= n; c += 3) {
-        stage(c, true, st0, st2, rc0, rc2);
-        stage(c + 1, true, st1, st0, rc1, rc0);
-        stage(c + 2, true, st2, st1, rc2, rc1);
-      }
-      for (; c < n; c += 3) {
-        stage(c, false, st0, st2, rc0, rc2);
-        if (c + 1 < n) stage(c + 1, false, st1, st0, rc1, rc0);
-        if (c + 2 < n) stage(c + 2, false, st2, st1, rc2, rc1);
+      for (int c = 0;;) {
+        stage(c, st0, st1, st2, rc0, rc2);
+        if (++c == n) break;
+        stage(c, st1, st2, st0, rc1, rc0);
+        if (++c == n) break;
+        stage(c, st2, st0, st1, rc2, rc1);
+        if (++c == n) break;
       }
     } else {
-      for (; c + 9 <= n; c += 6) {
-        stage(c, true, st0, st2, rc0, rc1);
-        stage(c + 1, true, st1, st0, rc1, rc0);
-        stage(c + 2, true, st2, st1, rc0, rc1);
-        stage(c + 3, true, st0, st2, rc1, rc0);
-        stage(c + 4, true, st1, st0, rc0, rc1);
-        stage(c + 5, true, st2, st1, rc1, rc0);
-      }
-      for (; c < n; c += 6) {
-        stage(c, false, st0, st2, rc0, rc1);
-        if (c + 1 < n) stage(c + 1, false, st1, st0, rc1, rc0);
-        if (c + 2 < n) stage(c + 2, false, st2, st1, rc0, rc1);
-        if (c + 3 < n) stage(c + 3, false, st0, st2, rc1, rc0);
-        if (c + 4 < n) stage(c + 4, false, st1, st0, rc0, rc1);
-        if (c + 5 < n) stage(c + 5, false, st2, st1, rc1, rc0);
+      for (int c = 0;;) {
+        stage(c, st0, st1, st2, rc0, rc1);
+        if (++c == n) break;
+        stage(c, st1, st2, st0, rc1, rc0);
+        if (++c == n) break;
+        stage(c, st2, st0, st1, rc0, rc1);
+        if (++c == n) break;
+        stage(c, st0, st1, st2, rc1, rc0);
+        if (++c == n) break;
+        stage(c, st1, st2, st0, rc0, rc1);
+        if (++c == n) break;
+        stage(c, st2, st0, st1, rc1, rc0);
+        if (++c == n) break;
       }
     }
     if (wave < 4) meet();
     scale_group(GH - 1);
+    wait_loads<0>();                             // nothing may still write to this workgroup's LDS
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -765,8 +775,8 @@ hipError_t stream_go(const Q4Args &a, hipStream_t st) {
 
 // Workspace of the tile kernel: group sums, then what of X it cannot read in
 // place, of X's rows or, with a gather of fewer rows than X has, of the
-// gathered rows (compact): the planes of float32 X, or a copy of gathered
-// bfloat16 rows that lie more than 32-bit offsets apart.
+// gathered rows (compact): the planes of float32 X, or a copy of bfloat16 X
+// whose rows do not end with a record or may lie more than 32-bit offsets apart.
 struct TileWs {
   bool compact, copy;
   int64_t nrow;
@@ -778,7 +788,7 @@ TileWs tile_ws(int64_t xrows, int64_t r, int64_t m, int group, bool xbf16) {
   const bool far = (uint64_t)xrows * (xbf16 ? 2 * (uint64_t)m : 768 * (uint64_t)nch) >= 0xfff00000ull;
   // a gather is known only by r != xrows here; far X is always taken row by row
   w.compact = r < xrows || far;
-  w.copy = xbf16 && far;
+  w.copy = xbf16 && (far || m % 128 != 0);
   w.nrow = w.compact ? r : xrows;
   w.planes = ((size_t)w.nrow * nch * (128 / group) * 4 + 15) / 16 * 16;
   w.bytes = w.planes + (!xbf16 ? (size_t)w.nrow * 3 * nch * 256 : w.copy ? (size_t)w.nrow * nch * 256 : 0);
