@@ -194,15 +194,15 @@ __device__ __forceinline__ void store_y(const Q4Args &a, int64_t row, int64_t i,
 
 // ---------------------------------------------------------------- streaming kernel
 // A workgroup owns 16 R output rows of one matrix and a tile of 16 TT rows of
-// Y; its NW waves take the 128-column records in turn (wave w: w, w + NW, ...)
-// and their sums are joined through LDS in wave order, so the result does not
-// depend on timing.
+// Y; its NW waves take the 128-column records in turn (wave w: w, w + NW, ...;
+// U of them at a time, whose loads are all in flight together) and their sums
+// are joined through LDS in wave order, so the result does not depend on timing.
 // MFMA operands (v_mfma_f32_16x16x32_bf16): A = X (row l % 16, columns
 // 8 (l / 16) .. +7), B = codes (column l % 16 = output row), D element j =
 // (row 4 (l / 16) + j, output row l % 16): one lane keeps one output row, so a
 // group's scale and zero are one pair per lane.  Row a of A is token
 // 4 (a % 4) + a / 4 of its 16, which puts the first four tokens in element 0.
-template <bool XBF16, int G, int R, int TT, int NW>
+template <bool XBF16, int G, int R, int TT, int NW, int U>
 __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, int nch) {
   constexpr int GPC = 128 / G, SPG = G / 32;     // groups per record, K slices per group
   constexpr int RECW = 256 + 32 * GPC;
@@ -228,7 +228,10 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
     }
     xp[u] = (const char *)a.X + (row * a.m + 8 * lg) * (XBF16 ? 2 : 4);
   }
-  const uint32_t *wp = a.W + (int64_t)tl.expert * nrb * nch * RECW + 4 * lane;
+  const uint32_t *wp[R];                         // row blocks past the last repeat it
+#pragma unroll
+  for (int b = 0; b < R; ++b)
+    wp[b] = a.W + ((int64_t)tl.expert * nrb + (rb0 + b < nrb ? rb0 + b : nrb - 1)) * nch * RECW;
 
   f32x4_t tot[R][TT];
 #pragma unroll
@@ -237,14 +240,33 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
     for (int u = 0; u < TT; ++u) tot[b][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
 
-  if (!tiles.bad) {
-    for (int ch = wave; ch < nch; ch += NW) {
-      uint4 w[R];
+  // U records of the wave at a time, all their loads first.
+  auto records = [&](int ch0, auto count) __attribute__((always_inline)) {
+    constexpr int N = decltype(count)::value;
+    uint4 w[N][R];
+    float2 sz[N][R][GPC];
+    uint4 x[XBF16 ? N : 1][TT][4];
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      const int ch = ch0 + v * NW;
 #pragma unroll
       for (int b = 0; b < R; ++b) {
-        const int rb = rb0 + b < nrb ? rb0 + b : nrb - 1;
-        w[b] = *(const uint4 *)(wp + ((int64_t)rb * nch + ch) * RECW);
+        const uint32_t *rec = wp[b] + (int64_t)ch * RECW;
+        w[v][b] = *(const uint4 *)(rec + 4 * lane);
+#pragma unroll
+        for (int q = 0; q < GPC; ++q) sz[v][b][q] = *(const float2 *)(rec + 256 + 2 * (16 * q + r16));
       }
+      if constexpr (XBF16) {
+#pragma unroll
+        for (int u = 0; u < TT; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)            // a record past m holds zeros there: any finite X will do
+            x[v][u][i] = *(const uint4 *)(xp[u] + (ch * 128 + 32 * i < a.m ? ch * 256 + 64 * i : 0));
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      const int ch = ch0 + v * NW;
 #pragma unroll
       for (int q = 0; q < GPC; ++q) {
         if (ch * 128 + q * G >= a.m) break;
@@ -260,46 +282,51 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
           const int i = q * SPG + s;
           uint4 c[R];
 #pragma unroll
-          for (int b = 0; b < R; ++b) c[b] = q4_codes(i == 0 ? w[b].x : i == 1 ? w[b].y : i == 2 ? w[b].z : w[b].w);
+          for (int b = 0; b < R; ++b)
+            c[b] = q4_codes(i == 0 ? w[v][b].x : i == 1 ? w[v][b].y : i == 2 ? w[v][b].z : w[v][b].w);
 #pragma unroll
           for (int u = 0; u < TT; ++u) {
-            uint4 x[NT];
-            const char *p = xp[u] + (int64_t)(ch * 128 + 32 * i) * (XBF16 ? 2 : 4);
-            if constexpr (XBF16) x[0] = *(const uint4 *)p;
-            else split3((const float *)p, x);
+            uint4 xt[NT];
+            if constexpr (XBF16) xt[0] = x[v][u][i];
+            else split3((const float *)(xp[u] + (int64_t)(ch * 128 + 32 * i) * 4), xt);
 #pragma unroll
             for (int e = 0; e < NT; ++e) {
-              sx[u] = mfma16(x[e], ones, sx[u]);
+              sx[u] = mfma16(xt[e], ones, sx[u]);
 #pragma unroll
-              for (int b = 0; b < R; ++b) acc[b][u] = mfma16(x[e], c[b], acc[b][u]);
+              for (int b = 0; b < R; ++b) acc[b][u] = mfma16(xt[e], c[b], acc[b][u]);
             }
           }
         }
 #pragma unroll
-        for (int b = 0; b < R; ++b) {
-          const int rb = rb0 + b < nrb ? rb0 + b : nrb - 1;
-          const float2 sz = *(const float2 *)(wp - 4 * lane + ((int64_t)rb * nch + ch) * RECW + 256 + 2 * (16 * q + r16));
+        for (int b = 0; b < R; ++b)
 #pragma unroll
           for (int u = 0; u < TT; ++u)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              tot[b][u][j] = fmaf(sz.x, fmaf(-sz.y, sx[u][j], acc[b][u][j]), tot[b][u][j]);
-        }
+              tot[b][u][j] = fmaf(sz[v][b][q].x, fmaf(-sz[v][b][q].y, sx[u][j], acc[b][u][j]), tot[b][u][j]);
       }
     }
+  };
+  if (!tiles.bad) {
+    int ch = wave;
+    for (; ch + (U - 1) * NW < nch; ch += U * NW) records(ch, std::integral_constant<int, U>());
+    if constexpr (U > 1)
+      for (; ch < nch; ch += NW) records(ch, std::integral_constant<int, 1>());
   }
   // part[wave][(u * 4 + j) * 4 + lg][b][r16]: token 16 u + 4 j + lg, output row 16 b + r16
 #pragma unroll
   for (int u = 0; u < TT; ++u)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j) {
+      if (16 * u + 4 * j >= tl.cnt) break;       // no such token in the tile
 #pragma unroll
       for (int b = 0; b < R; ++b) part[wave][((16 * u + 4 * j + lg) * R + b) * 16 + r16] = tot[b][u][j];
+    }
   __syncthreads();
-  for (int idx = threadIdx.x; idx < R * TT * 256; idx += 64 * NW) {
+  for (int idx = threadIdx.x; idx < tl.cnt * R * 16; idx += 64 * NW) {
     const int tok = idx / (16 * R), col = idx % (16 * R);
     const int64_t i = (int64_t)rb0 * 16 + col;
-    if (tok >= tl.cnt || i >= a.n) continue;
+    if (i >= a.n) continue;
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) v += part[w][idx];
@@ -319,7 +346,7 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
 // (float32, from q4_sums_kernel) and z are split into three bfloat16 terms
 // each and eight of their nine products are summed as one more K slice of the
 // group,
-//   A: sh sm sh sl sh sm sl sm    B: -zh -zh -zm -zh -zl -zm -zm -zl
+//   A: sh sm sh sm sh sl sm sl    B: -zh -zh -zm -zm -zl -zh -zl -zm
 // (the missing zl sl is below 2^-32 of the product), so a group costs one
 // vector operation per output, the scaling.
 __device__ __forceinline__ void split_sum(float v, uint32_t &h, uint32_t &m, uint32_t &l) {
@@ -495,9 +522,11 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
     const int j = (wave + i * NW) % (WT * GPC), tok = (j % WT) * 64 + lane;
     so[i] = (uint32_t)((compact ? (tok < tl.cnt ? tok : 0) : x_row(tok)) * (nch * GPC) + j / WT) * 4;
   }
-  auto load_x = [&](int c, Stage &st) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < XL; ++i) load_lds<16>(xbase, xbytes, st.x + (wave * XL + i) * 1024, xo[i], c * 256);
+  // A quarter of the loads of X's stage c, the sums with the last.
+  static_assert(XL == 4, "a load for each K step of a product phase");
+  auto load_x = [&](int c, int part, Stage &st) __attribute__((always_inline)) {
+    load_lds<16>(xbase, xbytes, st.x + (wave * XL + part) * 1024, xo[part], c * 256);
+    if (part < 3) return;
     const int ch = c < nch ? c : 0;             // used with the first plane only
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
@@ -615,16 +644,15 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
         uint32_t p, r, l;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          split_sum(su[g][i], p, r, l);
-          aa[g][i] = make_uint4(pack_hi(p, r) & keep, pack_hi(p, l) & keep, pack_hi(p, r) & keep,
-                                pack_hi(l, r) & keep);
+          split_sum(__uint_as_float(__float_as_uint(su[g][i]) & keep), p, r, l);
+          aa[g][i] = make_uint4(pack_hi(p, r), pack_hi(p, r), pack_hi(p, l), pack_hi(r, l));
         }
         sc[g][0] = sz[g].x;
         sc[g][1] = sz[g].z;
         split_sum(-sz[g].y, p, r, l);
-        ba[g][0] = make_uint4(pack_hi(p, p), pack_hi(r, p), pack_hi(l, r), pack_hi(r, l));
+        ba[g][0] = make_uint4(pack_hi(p, p), pack_hi(r, r), pack_hi(l, p), pack_hi(l, r));
         split_sum(-sz[g].w, p, r, l);
-        ba[g][1] = make_uint4(pack_hi(p, p), pack_hi(r, p), pack_hi(l, r), pack_hi(r, l));
+        ba[g][1] = make_uint4(pack_hi(p, p), pack_hi(r, r), pack_hi(l, p), pack_hi(l, r));
       }
     }
     // keeps this phase's work out of the product phase
@@ -632,7 +660,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
   };
   // Product phase h.  X of the next half stage is read into the registers that a
   // K step has used.
-  auto multiply = [&](int h, const Stage &nst) __attribute__((always_inline)) {
+  auto multiply = [&](int h, const Stage &nst, int cl, Stage &lst) __attribute__((always_inline)) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -649,6 +677,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
                                 first ? z : acc[i][b]);
         }
       read_x(1 - h, u, nst);
+      if (h == 0) load_x(cl, u, lst);
       if (G == 128 ? h == 1 && u == 3 : u % (G / 16) == G / 16 - 1) {
         const int g = G == 32 ? u / 2 : 0;
 #pragma unroll
@@ -663,6 +692,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
 #pragma unroll
       for (int j = 0; j < 4; ++j) {               // the next step's expansion among this step's MFMAs
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (h == 0 && j == 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
       }
       __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
@@ -676,13 +706,12 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
     auto stage = [&](int c, Stage &st, Stage &st1, Stage &st2, Recs &rc, Recs &rnxt) __attribute__((always_inline)) {
       read(0, st, rc);
       load_rec(c + RST - 1 < n ? c + RST - 1 : n - 1, rnxt);
-      load_x(c + 2 < n ? c + 2 : n - 1, st2);
       scale_group(GH - 1);
       prepare(c, 0);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
       meet();
-      multiply(0, st);
+      multiply(0, st, c + 2 < n ? c + 2 : n - 1, st2);
       wait_loads<AHEAD>();
       __builtin_amdgcn_sched_barrier(0);
       meet();
@@ -692,14 +721,16 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
       meet();
-      multiply(1, st1);
+      multiply(1, st1, 0, st1);
       __builtin_amdgcn_sched_barrier(0);
       meet();
     };
     load_rec(0, rc0);
-    load_x(0, st0);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_x(0, u, st0);
     if (RST == 3) load_rec(n > 1 ? 1 : 0, rc1);
-    load_x(n > 1 ? 1 : 0, st1);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_x(n > 1 ? 1 : 0, u, st1);
     wait_loads<0>();
     meet();
 #pragma unroll
@@ -764,12 +795,12 @@ int64_t max_tiles(int64_t r, int64_t e, int64_t tok) {
   return most > whole ? most : whole;
 }
 
-template <bool XBF16, int G, int R, int TT, int NW>
+template <bool XBF16, int G, int R, int TT, int NW, int U>
 hipError_t stream_go(const Q4Args &a, hipStream_t st) {
   const int nrb = (int)q4_row_blocks(a.n), nch = (int)q4_chunks(a.m);
   const int64_t tiles = max_tiles(a.r, a.offsets ? a.e : 1, 16 * TT);
   if (tiles > 65535) return hipErrorInvalidConfiguration;
-  q4_stream_kernel<XBF16, G, R, TT, NW><<<dim3((nrb + R - 1) / R, (uint32_t)tiles), 64 * NW, 0, st>>>(a, nrb, nch);
+  q4_stream_kernel<XBF16, G, R, TT, NW, U><<<dim3((nrb + R - 1) / R, (uint32_t)tiles), 64 * NW, 0, st>>>(a, nrb, nch);
   return hipGetLastError();
 }
 
@@ -819,19 +850,36 @@ hipError_t tile_go(const Q4Args &a, const TileWs &w, void *ws, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Rows per expert, on average: what the tile sizes go by (the bounds are on the device).
+// Which kernel, by what fills the 256 CUs (the experts' bounds are on the
+// device, so their rows count by the average).  Measured, us:
+//  - tile kernel against streaming: t = 2048, 4096 x 11008: 188 against 737; at
+//    t = 256, 4096 x 4096 its 32 workgroups leave most CUs idle: 38 against 27.
+//  - 64 rows at a time against 16 (large n only: fewer workgroups): t = 64, 28672
+//    x 8192: 86 against 99; t = 256, 4096 x 4096: 28 against 27.
+//  - 4, 2 or 1 row blocks a workgroup (X is read once for all of them): t = 16,
+//    13824 x 5120: 15.4, 17.4, 25; t = 32, 4096 x 4096: 9.7, 8.0, 11.2; t = 1,
+//    4096 x 4096: 8.5, 5.2, 4.7.
+//  - 4 waves instead of 8 where a row has few records: 64 experts of 1024 x
+//    2048, 1024 rows: 33 against 38; 13824 x 5120: 17.0 against 15.4.
 int64_t rows_per_matrix(int64_t r, int64_t e) { return (r + e - 1) / e; }
-bool use_tiles(int64_t r, int64_t e) { return rows_per_matrix(r, e) > 64; }
+bool use_tiles(int64_t r, int64_t e, int64_t n) {
+  return rows_per_matrix(r, e) > 64 && (r + 127) / 128 * ((n + 255) / 256) >= 96;
+}
 
 template <bool XBF16, int G>
 hipError_t stream_pick(const Q4Args &a, hipStream_t st) {
-  if (rows_per_matrix(a.r, a.e) <= 16) return stream_go<XBF16, G, 1, 1, 8>(a, st);
-  return stream_go<XBF16, G, 2, 4, 4>(a, st);
+  const int64_t nrb = q4_row_blocks(a.n), nch = q4_chunks(a.m), r4 = (nrb + 3) / 4;
+  if (rows_per_matrix(a.r, a.e) >= 48 && r4 * ((a.r + 63) / 64) >= 384) return stream_go<XBF16, G, 4, 4, 4, 1>(a, st);
+  const int64_t tiles = max_tiles(a.r, a.e, 16);
+  if (r4 * tiles >= 192)
+    return nch <= 16 ? stream_go<XBF16, G, 4, 1, 4, 2>(a, st) : stream_go<XBF16, G, 4, 1, 8, 1>(a, st);
+  if ((nrb + 1) / 2 * tiles >= 144) return stream_go<XBF16, G, 2, 1, 8, 2>(a, st);
+  return stream_go<XBF16, G, 1, 1, 8, 2>(a, st);
 }
 
 template <int G>
 hipError_t pick(const Q4Args &a, void *ws, hipStream_t st) {
-  if (use_tiles(a.r, a.e)) {
+  if (use_tiles(a.r, a.e, a.n)) {
     const TileWs w = tile_ws(a.xrows, a.r, a.m, G, a.xbf16);
     return tile_go<G, 2, 4>(a, w, ws, st);
   }
@@ -849,7 +897,7 @@ hipError_t launch_pack4(const uint8_t *codes, const float *scale, const float *z
 }
 
 size_t q4_ws_bytes(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16) {
-  return use_tiles(r, e) ? tile_ws(xrows, r, m, group, xbf16).bytes : 0;
+  return use_tiles(r, e, n) ? tile_ws(xrows, r, m, group, xbf16).bytes : 0;
 }
 
 hipError_t launch_q4(const Q4Args &a, void *ws, hipStream_t st) {
