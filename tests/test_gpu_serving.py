@@ -90,6 +90,19 @@ LINEAR = [
     (300, 1003, 1056, 32, "bf16", "bf16"),
     (257, 385, 1152, 128, "f32", "bf16"),
     (700, 640, 640, 128, "bf16", "f32"),
+    # enough rows and outputs for the tile kernel: 1, 2, 3, 4, 5, 7 stages
+    (1537, 2100, 128, 128, "bf16", "f32"),
+    (1700, 1800, 256, 64, "bf16", "bf16"),
+    (1600, 2048, 384, 32, "bf16", "f32"),
+    (1300, 2570, 512, 128, "bf16", "bf16"),
+    (1410, 2310, 576, 64, "bf16", "f32"),     # a row that ends inside a record: X is copied
+    (3000, 1033, 800, 32, "bf16", "bf16"),
+    (1290, 2320, 128, 128, "f32", "f32"),     # float32 X: three planes
+    (1665, 1793, 160, 32, "f32", "bf16"),
+    (2049, 1500, 320, 64, "f32", "f32"),
+    # 64 rows at a time
+    (64, 25000, 128, 128, "bf16", "bf16"),
+    (100, 13000, 96, 32, "f32", "f32"),
 ]
 
 
@@ -128,9 +141,9 @@ def test_q4_linear_scales_and_zeros_of_any_sign(slim):
     assert np.all(err <= _bound(x, codes[0], scale[0], zero[0], g, "f32", "f32", exact))
 
 
-@pytest.mark.parametrize("t", [3, 40, 200])
-def test_q4_linear_nonfinite_row_stays_in_its_row(slim, t):
-    n, m, g = 48, 256, 128
+@pytest.mark.parametrize("t,n,m,g", [(3, 48, 256, 128), (40, 48, 96, 32), (200, 48, 256, 128), (1500, 2100, 256, 128),
+                                     (1500, 2100, 192, 64)])
+def test_q4_linear_nonfinite_row_stays_in_its_row(slim, t, n, m, g):
     codes, scale, zero = _layer(7, 1, n, m, g)
     X = _x(8, t, m, "bf16").to("cuda:0")
     packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
@@ -184,6 +197,12 @@ EXPERTS = [
     ([3, 0] * 75, 24, 64, 64, "bf16", "bf16", False, True, 0, 1),
     ([0, 0, 0], 16, 128, 128, "bf16", "f32", False, False, 0, 4),    # no rows at all
     ([700, 500, 0, 900], 300, 256, 128, "bf16", "bf16", True, False, 0, 0),
+    # the tile kernel
+    ([700, 500, 0, 900], 1600, 256, 128, "bf16", "bf16", True, False, 0, 0),
+    ([129, 0, 1, 1400, 128, 0, 300], 1700, 192, 64, "bf16", "f32", False, True, 5, 7),
+    ([900, 333, 700], 1610, 384, 32, "bf16", "bf16", True, True, 0, 130),
+    ([400, 0, 1100, 513], 1550, 160, 32, "f32", "f32", True, True, 1, 0),
+    ([1000, 1000], 1540, 256, 128, "f32", "bf16", False, False, 0, 3),
 ]
 
 
@@ -218,14 +237,14 @@ def test_q4_experts(slim, counts, n, m, g, xdt, ydt, gather, weighted, before, b
         assert np.all(err <= bound), (j, float(np.max(err / bound)))
 
 
-@pytest.mark.parametrize("per", [3, 150])
-def test_q4_experts_bad_rows_and_offsets(slim, per):
+@pytest.mark.parametrize("per,n,xdt", [(3, 32, "bf16"), (150, 32, "f32"), (700, 1600, "bf16"), (700, 1600, "f32")])
+def test_q4_experts_bad_rows_and_offsets(slim, per, n, xdt):
     # checked by the kernels before anything is read through them
-    e, n, m, g = 3, 32, 128, 128
+    e, m, g = 3, 128, 128
     r = e * per
     codes, scale, zero = _layer(12, e, n, m, g)
     packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
-    X = _x(13, 4, m, "bf16").to("cuda:0")
+    X = _x(13, 4, m, xdt).to("cuda:0")
     rows = np.arange(r, dtype=np.int32) % 4
     off = _counts_to_offsets([per] * e)
     good = slim.q4_experts(X, _gpu(off), packed, n, g, rows=_gpu(rows))
@@ -436,7 +455,7 @@ def test_run_of_the_operators_eager_side_stream_and_graph(slim):
 
 def test_two_graphs_share_inputs(slim):
     # each captured call has its own workspace: replays in any order agree
-    n, m, g, t, v = 256, 512, 128, 150, 40000
+    n, m, g, t, v = 2100, 512, 128, 1500, 40000
     codes, scale, zero = _layer(30, 1, n, m, g)
     packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
     X = _x(31, t, m, "f32").to("cuda:0")
