@@ -660,7 +660,7 @@ def token_logprobs(logits, ids, top: int = 0):
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return token_logprobs(logits, ids, top)
-    logprob, entropy = torch.empty((2, t), dtype=torch.float32, device=dev).unbind()
+    logprob, entropy = torch.empty((2, t), dtype=torch.float32, device=dev)
     out = {"logprob": logprob, "entropy": entropy}
     tl = ti = None
     if top:

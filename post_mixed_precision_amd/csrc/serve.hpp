@@ -36,6 +36,7 @@ hipError_t launch_q4(const Q4Args &a, void *ws, hipStream_t st);
 
 // ---- Token log probabilities ----
 struct LogprobPlan {
+  bool wide;                 // one workgroup of 16 waves a row
   int nseg;                  // segments a row is split into
   size_t ws_bytes;           // their statistics and best entries (0 for one segment)
 };
