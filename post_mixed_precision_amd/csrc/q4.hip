@@ -87,14 +87,13 @@ __device__ __forceinline__ uint4 q4_codes(uint32_t w) {
 
 // 8 columns of a float32 row as three bfloat16 terms whose sum is exact
 // (truncation leaves 16, then 8 significant bits).
-__device__ __forceinline__ void split3(const float *p, uint4 (&t)[3]) {
-  const float4 a = *(const float4 *)p, b = *(const float4 *)(p + 4);
-  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void split3(const uint4 &a, const uint4 &b, uint4 (&t)[3]) {
+  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t h[8], m[8], l[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    h[e] = __float_as_uint(v[e]) & 0xffff0000u;
-    const float r1 = v[e] - __uint_as_float(h[e]);
+    h[e] = u[e] & 0xffff0000u;
+    const float r1 = __uint_as_float(u[e]) - __uint_as_float(h[e]);
     m[e] = __float_as_uint(r1) & 0xffff0000u;
     l[e] = __float_as_uint(r1 - __uint_as_float(m[e]));
   }
@@ -206,7 +205,8 @@ template <bool XBF16, int G, int R, int TT, int NW, int U>
 __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, int nch) {
   constexpr int GPC = 128 / G, SPG = G / 32;     // groups per record, K slices per group
   constexpr int RECW = 256 + 32 * GPC;
-  constexpr int NT = XBF16 ? 1 : 3;
+  constexpr int NT = XBF16 ? 1 : 3;              // bfloat16 terms of X
+  constexpr int XL = XBF16 ? 1 : 2;              // 16-byte loads for 8 columns of X
   constexpr int TOK = 16 * TT;
   __shared__ float part[NW][R * TT * 256];
   const int lane = threadIdx.x & 63, r16 = lane & 15, lg = lane >> 4;
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
     constexpr int N = decltype(count)::value;
     uint4 w[N][R];
     float2 sz[N][R][GPC];
-    uint4 x[XBF16 ? N : 1][TT][4];
+    uint4 x[N][TT][4][XL];
 #pragma unroll
     for (int v = 0; v < N; ++v) {
       const int ch = ch0 + v * NW;
@@ -256,13 +256,13 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
 #pragma unroll
         for (int q = 0; q < GPC; ++q) sz[v][b][q] = *(const float2 *)(rec + 256 + 2 * (16 * q + r16));
       }
-      if constexpr (XBF16) {
 #pragma unroll
-        for (int u = 0; u < TT; ++u)
+      for (int u = 0; u < TT; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)            // a record past m holds zeros there: any finite X will do
-            x[v][u][i] = *(const uint4 *)(xp[u] + (ch * 128 + 32 * i < a.m ? ch * 256 + 64 * i : 0));
-      }
+        for (int i = 0; i < 4; ++i)              // a record past m holds zeros there: any finite X will do
+#pragma unroll
+          for (int e = 0; e < XL; ++e)
+            x[v][u][i][e] = *(const uint4 *)(xp[u] + (ch * 128 + 32 * i < a.m ? (ch * 128 + 32 * i) * (2 * XL) : 0) + 16 * e);
     }
 #pragma unroll
     for (int v = 0; v < N; ++v) {
@@ -287,8 +287,8 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
 #pragma unroll
           for (int u = 0; u < TT; ++u) {
             uint4 xt[NT];
-            if constexpr (XBF16) xt[0] = x[v][u][i];
-            else split3((const float *)(xp[u] + (int64_t)(ch * 128 + 32 * i) * 4), xt);
+            if constexpr (XBF16) xt[0] = x[v][u][i][0];
+            else split3(x[v][u][i][0], x[v][u][i][1], xt);
 #pragma unroll
             for (int e = 0; e < NT; ++e) {
               sx[u] = mfma16(xt[e], ones, sx[u]);
@@ -392,10 +392,12 @@ __global__ __launch_bounds__(256) void q4_sums_kernel(const void *__restrict__ X
           v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
         }
       } else {
-        const float4 x = ((const float4 *)Xv)[2 * at], y = ((const float4 *)Xv)[2 * at + 1];
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+        const uint4 x = ((const uint4 *)Xv)[2 * at], y = ((const uint4 *)Xv)[2 * at + 1];
+        const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[e]);
         uint4 t[3];
-        split3((const float *)Xv + 8 * at, t);
+        split3(x, y, t);
 #pragma unroll
         for (int p = 0; p < 3; ++p) planes[(i * 3 + p) * p8 + c] = t[p];
       }
@@ -457,7 +459,7 @@ template <int G, int WT, int WN>
 __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, const uint16_t *__restrict__ X,
                                                                   int64_t ldx, int nt, bool gather, bool compact,
                                                                   const float *__restrict__ sums, int nrb, int nch,
-                                                                  int nnb) {
+                                                                  int nnb, float *__restrict__ partial) {
   constexpr int NW = WT * WN, TOK = 64 * WT;
   static_assert(WT * WN == 8, "the phases pair waves w and w + 4");
   constexpr int GPC = 128 / G;                   // groups per record
@@ -505,7 +507,10 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
     const int64_t g = a.rows[tl.row0 + row];
     return g < 0 || g >= a.xrows ? 0 : g;
   };
-  const int n = nt * nch;                       // stages: float32 X passes its three planes in turn
+  // Stages of this workgroup (blockIdx.y takes a run of them, and its sums go to
+  // `partial`, where the columns are split); float32 X passes its three planes in turn.
+  const int c0 = nt * nch * (int)blockIdx.y / (int)gridDim.y;
+  const int n = nt * nch * ((int)blockIdx.y + 1) / (int)gridDim.y;
   const uint16_t *xbase = X + (gather ? 0 : tl.row0 * ldx);
   const float *sbase = sums + (gather && !compact ? 0 : tl.row0 * (nch * GPC));
   const uint32_t xbytes = (uint32_t)((gather ? a.xrows : tl.cnt) * ldx * 2);
@@ -725,19 +730,19 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
       __builtin_amdgcn_sched_barrier(0);
       meet();
     };
-    load_rec(0, rc0);
+    load_rec(c0, rc0);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) load_x(0, u, st0);
-    if (RST == 3) load_rec(n > 1 ? 1 : 0, rc1);
+    for (int u = 0; u < 4; ++u) load_x(c0, u, st0);
+    if (RST == 3) load_rec(c0 + 1 < n ? c0 + 1 : c0, rc1);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) load_x(n > 1 ? 1 : 0, u, st1);
+    for (int u = 0; u < 4; ++u) load_x(c0 + 1 < n ? c0 + 1 : c0, u, st1);
     wait_loads<0>();
     meet();
 #pragma unroll
     for (int u = 0; u < 4; ++u) read_x(0, u, st0);
     if (wave >= 4) meet();
     if constexpr (RST == 3) {
-      for (int c = 0;;) {
+      for (int c = c0;;) {
         stage(c, st0, st1, st2, rc0, rc2);
         if (++c == n) break;
         stage(c, st1, st2, st0, rc1, rc0);
@@ -746,7 +751,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
         if (++c == n) break;
       }
     } else {
-      for (int c = 0;;) {
+      for (int c = c0;;) {
         stage(c, st0, st1, st2, rc0, rc1);
         if (++c == n) break;
         stage(c, st1, st2, st0, rc1, rc0);
@@ -772,6 +777,14 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
       const int tok = wt * 64 + i * 32 + acc32_row(v, lane);
       if (tok >= tl.cnt) continue;
       const int64_t row = tl.row0 + tok;
+      if (partial) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int64_t col = (int64_t)(nb * WN + wn) * 64 + b * 32 + (lane & 31);
+          if (col < a.n) partial[((int64_t)blockIdx.y * a.r + row) * a.n + col] = tot[i][b][v];
+        }
+        continue;
+      }
       bool ok = !tiles.bad;
       if (a.rows && ok) {
         const int32_t xr = a.rows[row];
@@ -784,6 +797,30 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
         if (col < a.n) store_y(a, row, col, ok ? tot[i][b][v] * f : __uint_as_float(0x7fc00000u));
       }
     }
+}
+
+// Sums of a tile kernel whose columns were split, added in order, to Y.  A
+// workgroup takes 1024 outputs of one row; rows outside the experts' ranges are
+// left alone.
+__global__ __launch_bounds__(256) void q4_join_kernel(Q4Args a, const float *__restrict__ partial, int parts) {
+  Tiles<128> tiles;
+  tiles.scan(a);
+  const int64_t row = blockIdx.x;
+  if (a.offsets && !tiles.bad && (row < a.offsets[0] || row >= a.offsets[a.e])) return;
+  bool ok = !tiles.bad;
+  if (a.rows && ok) {
+    const int32_t xr = a.rows[row];
+    ok = xr >= 0 && xr < a.xrows;
+  }
+  const float f = a.row_scale ? a.row_scale[row] : 1.0f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int64_t i = (int64_t)blockIdx.y * 1024 + u * 256 + threadIdx.x;
+    if (i >= a.n) return;
+    float v = 0.0f;
+    for (int p = 0; p < parts; ++p) v += partial[(p * a.r + row) * a.n + i];
+    store_y(a, row, i, ok ? v * f : __uint_as_float(0x7fc00000u));
+  }
 }
 
 // Most tiles of tok rows that e ranges covering at most r rows can be cut into.
@@ -808,12 +845,17 @@ hipError_t stream_go(const Q4Args &a, hipStream_t st) {
 // place, of X's rows or, with a gather of fewer rows than X has, of the
 // gathered rows (compact): the planes of float32 X, or a copy of bfloat16 X
 // whose rows do not end with a record or may lie more than 32-bit offsets apart.
+// With fewer workgroups than CUs the columns are split over up to four, whose
+// sums follow: t = 500, 5000 x 4096 (80 workgroups): 46 us, unsplit 70; t = 1024,
+// 4096 x 4096 (128 workgroups, halves): 55 us.
 struct TileWs {
   bool compact, copy;
+  int parts;
   int64_t nrow;
-  size_t planes, bytes;
+  size_t planes, partial, bytes;
 };
-TileWs tile_ws(int64_t xrows, int64_t r, int64_t m, int group, bool xbf16) {
+int64_t tile_count(int64_t r, int64_t n) { return (r + 127) / 128 * ((n + 255) / 256); }
+TileWs tile_ws(int64_t xrows, int64_t r, int64_t n, int64_t m, int group, bool xbf16) {
   TileWs w;
   const size_t nch = (size_t)q4_chunks(m);
   const bool far = (uint64_t)xrows * (xbf16 ? 2 * (uint64_t)m : 768 * (uint64_t)nch) >= 0xfff00000ull;
@@ -822,7 +864,11 @@ TileWs tile_ws(int64_t xrows, int64_t r, int64_t m, int group, bool xbf16) {
   w.copy = xbf16 && (far || m % 128 != 0);
   w.nrow = w.compact ? r : xrows;
   w.planes = ((size_t)w.nrow * nch * (128 / group) * 4 + 15) / 16 * 16;
-  w.bytes = w.planes + (!xbf16 ? (size_t)w.nrow * 3 * nch * 256 : w.copy ? (size_t)w.nrow * nch * 256 : 0);
+  w.partial = w.planes + (!xbf16 ? (size_t)w.nrow * 3 * nch * 256 : w.copy ? (size_t)w.nrow * nch * 256 : 0);
+  const int64_t most = (int64_t)nch / 4 < 4 ? (int64_t)nch / 4 : 4;     // four records at least to a part
+  const int64_t parts = 256 / tile_count(r, n) < most ? 256 / tile_count(r, n) : most;
+  w.parts = parts < 1 ? 1 : (int)parts;
+  w.bytes = w.partial + (w.parts > 1 ? (size_t)w.parts * r * n * 4 : 0);
   return w;
 }
 
@@ -843,17 +889,25 @@ hipError_t tile_go(const Q4Args &a, const TileWs &w, void *ws, hipStream_t st) {
   else q4_sums_kernel<false, G><<<sb, 256, 0, st>>>(a.X, rows, a.xrows, w.nrow, a.m, nch, sums, planes);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  q4_tile_kernel<G, WT, WN><<<(uint32_t)blocks, 64 * WT * WN, 0, st>>>(
+  float *partial = w.parts > 1 ? (float *)((char *)ws + w.partial) : nullptr;
+  q4_tile_kernel<G, WT, WN><<<dim3((uint32_t)blocks, w.parts), 64 * WT * WN, 0, st>>>(
       a, own ? (const uint16_t *)planes : (const uint16_t *)a.X,
       !own ? a.m : (a.xbf16 ? 1 : 3) * (int64_t)nch * 128, a.xbf16 ? 1 : 3, a.rows && !(own && w.compact), w.compact,
-      sums, nrb, nch, nnb);
+      sums, nrb, nch, nnb, partial);
+  e = hipGetLastError();
+  if (e != hipSuccess || !partial) return e;
+  q4_join_kernel<<<dim3((uint32_t)a.r, (uint32_t)((a.n + 1023) / 1024)), 256, 0, st>>>(a, partial, w.parts);
   return hipGetLastError();
 }
 
 // Which kernel, by what fills the 256 CUs (the experts' bounds are on the
 // device, so their rows count by the average).  Measured, us:
-//  - tile kernel against streaming: t = 2048, 4096 x 11008: 188 against 737; at
-//    t = 256, 4096 x 4096 its 32 workgroups leave most CUs idle: 38 against 27.
+//  - tile kernel against streaming: t = 2048, 4096 x 11008: 188 against 737; t =
+//    500, 5000 x 4096 (its columns split, see tile_ws): 46 against 72; at t = 256,
+//    4096 x 4096 its 32 tiles are too few either way: 38 against 27.
+//    With one or two records to a row its start (the group sums, three stages
+//    of loads) outweighs them: three experts of 5346 x 128 over 602 rows: 26
+//    against 22; t = 2000, 4096 x 512 the other way: 28 against 38.
 //  - 64 rows at a time against 16 (large n only: fewer workgroups): t = 64, 28672
 //    x 8192: 86 against 99; t = 256, 4096 x 4096: 28 against 27.
 //  - 4, 2 or 1 row blocks a workgroup (X is read once for all of them): t = 16,
@@ -862,8 +916,8 @@ hipError_t tile_go(const Q4Args &a, const TileWs &w, void *ws, hipStream_t st) {
 //  - 4 waves instead of 8 where a row has few records: 64 experts of 1024 x
 //    2048, 1024 rows: 33 against 38; 13824 x 5120: 17.0 against 15.4.
 int64_t rows_per_matrix(int64_t r, int64_t e) { return (r + e - 1) / e; }
-bool use_tiles(int64_t r, int64_t e, int64_t n) {
-  return rows_per_matrix(r, e) > 64 && (r + 127) / 128 * ((n + 255) / 256) >= 96;
+bool use_tiles(int64_t r, int64_t e, int64_t n, int64_t m) {
+  return rows_per_matrix(r, e) > 64 && m > 256 && tile_count(r, n) >= 36;
 }
 
 template <bool XBF16, int G>
@@ -879,8 +933,8 @@ hipError_t stream_pick(const Q4Args &a, hipStream_t st) {
 
 template <int G>
 hipError_t pick(const Q4Args &a, void *ws, hipStream_t st) {
-  if (use_tiles(a.r, a.e, a.n)) {
-    const TileWs w = tile_ws(a.xrows, a.r, a.m, G, a.xbf16);
+  if (use_tiles(a.r, a.e, a.n, a.m)) {
+    const TileWs w = tile_ws(a.xrows, a.r, a.n, a.m, G, a.xbf16);
     return tile_go<G, 2, 4>(a, w, ws, st);
   }
   return a.xbf16 ? stream_pick<true, G>(a, st) : stream_pick<false, G>(a, st);
@@ -897,7 +951,7 @@ hipError_t launch_pack4(const uint8_t *codes, const float *scale, const float *z
 }
 
 size_t q4_ws_bytes(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16) {
-  return use_tiles(r, e, n) ? tile_ws(xrows, r, m, group, xbf16).bytes : 0;
+  return use_tiles(r, e, n, m) ? tile_ws(xrows, r, n, m, group, xbf16).bytes : 0;
 }
 
 hipError_t launch_q4(const Q4Args &a, void *ws, hipStream_t st) {

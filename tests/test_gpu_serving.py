@@ -90,16 +90,21 @@ LINEAR = [
     (300, 1003, 1056, 32, "bf16", "bf16"),
     (257, 385, 1152, 128, "f32", "bf16"),
     (700, 640, 640, 128, "bf16", "f32"),
-    # enough rows and outputs for the tile kernel: 1, 2, 3, 4, 5, 7 stages
-    (1537, 2100, 128, 128, "bf16", "f32"),
-    (1700, 1800, 256, 64, "bf16", "bf16"),
-    (1600, 2048, 384, 32, "bf16", "f32"),
-    (1300, 2570, 512, 128, "bf16", "bf16"),
+    # enough rows and outputs for the tile kernel: 3, 4, 5, 6, 7 stages
+    (1537, 2100, 384, 128, "bf16", "f32"),
+    (1700, 1800, 512, 64, "bf16", "bf16"),
+    (1600, 2048, 640, 32, "bf16", "f32"),
+    (1300, 2570, 768, 128, "bf16", "bf16"),
     (1410, 2310, 576, 64, "bf16", "f32"),     # a row that ends inside a record: X is copied
     (3000, 1033, 800, 32, "bf16", "bf16"),
-    (1290, 2320, 128, 128, "f32", "f32"),     # float32 X: three planes
-    (1665, 1793, 160, 32, "f32", "bf16"),
+    (1290, 2320, 384, 128, "f32", "f32"),     # float32 X: three planes
+    (1665, 1793, 288, 32, "f32", "bf16"),
     (2049, 1500, 320, 64, "f32", "f32"),
+    # and its columns split over two, three and four workgroups
+    (500, 2600, 1024, 128, "bf16", "bf16"),
+    (700, 3000, 1536, 64, "bf16", "f32"),
+    (400, 2500, 2080, 32, "bf16", "bf16"),
+    (385, 2309, 1152, 128, "f32", "f32"),
     # 64 rows at a time
     (64, 25000, 128, 128, "bf16", "bf16"),
     (100, 13000, 96, 32, "f32", "f32"),
@@ -141,8 +146,8 @@ def test_q4_linear_scales_and_zeros_of_any_sign(slim):
     assert np.all(err <= _bound(x, codes[0], scale[0], zero[0], g, "f32", "f32", exact))
 
 
-@pytest.mark.parametrize("t,n,m,g", [(3, 48, 256, 128), (40, 48, 96, 32), (200, 48, 256, 128), (1500, 2100, 256, 128),
-                                     (1500, 2100, 192, 64)])
+@pytest.mark.parametrize("t,n,m,g", [(3, 48, 256, 128), (40, 48, 96, 32), (200, 48, 256, 128), (1500, 2100, 384, 128),
+                                     (1500, 2100, 320, 64), (500, 2600, 1024, 128)])
 def test_q4_linear_nonfinite_row_stays_in_its_row(slim, t, n, m, g):
     codes, scale, zero = _layer(7, 1, n, m, g)
     X = _x(8, t, m, "bf16").to("cuda:0")
@@ -198,11 +203,14 @@ EXPERTS = [
     ([0, 0, 0], 16, 128, 128, "bf16", "f32", False, False, 0, 4),    # no rows at all
     ([700, 500, 0, 900], 300, 256, 128, "bf16", "bf16", True, False, 0, 0),
     # the tile kernel
-    ([700, 500, 0, 900], 1600, 256, 128, "bf16", "bf16", True, False, 0, 0),
-    ([129, 0, 1, 1400, 128, 0, 300], 1700, 192, 64, "bf16", "f32", False, True, 5, 7),
-    ([900, 333, 700], 1610, 384, 32, "bf16", "bf16", True, True, 0, 130),
-    ([400, 0, 1100, 513], 1550, 160, 32, "f32", "f32", True, True, 1, 0),
-    ([1000, 1000], 1540, 256, 128, "f32", "bf16", False, False, 0, 3),
+    ([700, 500, 0, 900], 1600, 384, 128, "bf16", "bf16", True, False, 0, 0),
+    ([129, 0, 1, 1400, 128, 0, 300], 1700, 320, 64, "bf16", "f32", False, True, 5, 7),
+    ([900, 333, 700], 1610, 640, 32, "bf16", "bf16", True, True, 0, 130),
+    ([400, 0, 1100, 513], 1550, 288, 32, "f32", "f32", True, True, 1, 0),
+    ([1000, 1000], 1540, 512, 128, "f32", "bf16", False, False, 0, 3),
+    # with its columns split
+    ([300, 0, 7, 200], 2600, 1024, 128, "bf16", "bf16", True, True, 2, 9),
+    ([0, 290, 410], 2100, 1216, 64, "f32", "f32", False, True, 3, 1),
 ]
 
 
@@ -237,10 +245,11 @@ def test_q4_experts(slim, counts, n, m, g, xdt, ydt, gather, weighted, before, b
         assert np.all(err <= bound), (j, float(np.max(err / bound)))
 
 
-@pytest.mark.parametrize("per,n,xdt", [(3, 32, "bf16"), (150, 32, "f32"), (700, 1600, "bf16"), (700, 1600, "f32")])
-def test_q4_experts_bad_rows_and_offsets(slim, per, n, xdt):
+@pytest.mark.parametrize("per,n,m,xdt", [(3, 32, 128, "bf16"), (150, 32, 128, "f32"), (700, 1600, 384, "bf16"),
+                                         (700, 1600, 384, "f32"), (200, 2600, 1024, "bf16")])
+def test_q4_experts_bad_rows_and_offsets(slim, per, n, m, xdt):
     # checked by the kernels before anything is read through them
-    e, m, g = 3, 128, 128
+    e, g = 3, 128
     r = e * per
     codes, scale, zero = _layer(12, e, n, m, g)
     packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
@@ -455,7 +464,7 @@ def test_run_of_the_operators_eager_side_stream_and_graph(slim):
 
 def test_two_graphs_share_inputs(slim):
     # each captured call has its own workspace: replays in any order agree
-    n, m, g, t, v = 2100, 512, 128, 1500, 40000
+    n, m, g, t, v = 2600, 1024, 128, 500, 40000
     codes, scale, zero = _layer(30, 1, n, m, g)
     packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
     X = _x(31, t, m, "f32").to("cuda:0")
