@@ -385,7 +385,7 @@ int slim_q4_linear(const void *X, int xdt, int64_t t, int64_t m, const uint32_t 
   if (t < 0 || t > SLIM_QLINEAR_MAX_T || n < 1 || slim_pack4_words(1, n, m, group) < 0) return SLIM_E_SHAPE;
   if (t == 0) return SLIM_OK;
   if (!X || !packed || !Y) return SLIM_E_NULL;
-  if (!aligned16(X) || !aligned16(packed) || !aligned16(Y)) return SLIM_E_ALIGN;
+  if (!aligned16(X) || !aligned16(packed) || (uintptr_t)Y % (ydt == SLIM_BF16 ? 2 : 4)) return SLIM_E_ALIGN;
   const size_t need = slim::q4_ws_bytes(t, t, 1, n, m, group, xdt == SLIM_BF16);
   if (need > 0 && (!ws || ws_bytes < need)) return SLIM_E_WORKSPACE;
   if (need > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
@@ -413,7 +413,7 @@ int slim_q4_experts(const void *X, int xdt, int64_t tx, int64_t m, const int32_t
   if (!experts_shape(tx, r, e, n, m, group) || (!rows && tx != r)) return SLIM_E_SHAPE;
   if (r == 0) return SLIM_OK;
   if (!X || !offsets || !packed || !Y) return SLIM_E_NULL;
-  if (!aligned16(X) || !aligned16(packed) || !aligned16(Y)) return SLIM_E_ALIGN;
+  if (!aligned16(X) || !aligned16(packed) || (uintptr_t)Y % (ydt == SLIM_BF16 ? 2 : 4)) return SLIM_E_ALIGN;
   const size_t need = slim::q4_ws_bytes(tx, r, e, n, m, group, xdt == SLIM_BF16);
   if (need > 0 && (!ws || ws_bytes < need)) return SLIM_E_WORKSPACE;
   if (need > 0 && !aligned16(ws)) return SLIM_E_ALIGN;

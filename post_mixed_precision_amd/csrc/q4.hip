@@ -213,8 +213,9 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   Tiles<TOK> tiles;
   tiles.scan(a);
-  if (blockIdx.y >= tiles.total) return;
-  const RowTile tl = tiles.locate(a, blockIdx.y);
+  const int64_t tile = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+  if (tile >= tiles.total) return;
+  const RowTile tl = tiles.locate(a, tile);
   const int rb0 = blockIdx.x * R;
 
   const char *xp[TT];
@@ -836,8 +837,9 @@ template <bool XBF16, int G, int R, int TT, int NW, int U>
 hipError_t stream_go(const Q4Args &a, hipStream_t st) {
   const int nrb = (int)q4_row_blocks(a.n), nch = (int)q4_chunks(a.m);
   const int64_t tiles = max_tiles(a.r, a.offsets ? a.e : 1, 16 * TT);
-  if (tiles > 65535) return hipErrorInvalidConfiguration;
-  q4_stream_kernel<XBF16, G, R, TT, NW, U><<<dim3((nrb + R - 1) / R, (uint32_t)tiles), 64 * NW, 0, st>>>(a, nrb, nch);
+  const int64_t gz = (tiles + 65534) / 65535, gy = (tiles + gz - 1) / gz;   // grid limits of 65535
+  q4_stream_kernel<XBF16, G, R, TT, NW, U>
+      <<<dim3((nrb + R - 1) / R, (uint32_t)gy, (uint32_t)gz), 64 * NW, 0, st>>>(a, nrb, nch);
   return hipGetLastError();
 }
 

@@ -462,6 +462,34 @@ def test_run_of_the_operators_eager_side_stream_and_graph(slim):
         assert torch.equal(got[0], le) and all(torch.equal(got[1][k], se[k]) for k in se), seed
 
 
+@pytest.mark.parametrize("avg", [2, 3])
+def test_quantized_layer_served_and_scored(slim, avg):
+    """quantize_layer's codes through both layouts, and the layer as an output
+    layer: the scores of its logits, formed in blocks."""
+    n, m, g, T = 300, 512, 128, 70
+    W = (0.02 * _x(50, n, m, "f32")).to(torch.bfloat16).to("cuda:0")
+    X = _x(51, 256, m, "bf16").to("cuda:0")
+    q = slim.quantize_layer(X, W, g, avg, nibbles=True)
+    assert int(q["info"]) == 0 and int(q["pack_info"]) == 0
+    codes, scale, zero = (q[k].cpu().numpy() for k in ("codes", "scale", "zero"))
+    Xt = X[:T].contiguous()
+    a = slim.qlinear(Xt, q["packed"], q["bits"], q["scale"], q["zero"], g, avg).double().cpu().numpy()
+    b = slim.q4_linear(Xt, q["packed4"], n, g)
+    x = Xt.double().cpu().numpy()
+    exact = x @ oracle.q4_weight(codes, scale, zero, g).T
+    bound = _bound(x, codes, scale, zero, g, "bf16", "f32", exact)
+    assert np.all(np.abs(b.double().cpu().numpy() - exact) <= bound) and np.all(np.abs(a - exact) <= 2 * bound)
+    ids = torch.arange(T, device="cuda:0") * 4
+    ids[3] = -1
+    whole = slim.score_tokens(Xt, ids, q["packed4"], n, g, top=3)
+    _check_lp(whole, b.double().cpu().numpy(), ids.cpu().numpy(), 3)
+    cut = slim.score_tokens(Xt, ids, q["packed4"], n, g, top=3, block=32)
+    for a0 in range(0, T, 32):                  # a block's product may take another order of sums
+        lg = slim.q4_linear(Xt[a0:a0 + 32].contiguous(), q["packed4"], n, g)
+        part = {k: v[a0:a0 + 32] for k, v in cut.items()}
+        _check_lp(part, lg.double().cpu().numpy(), ids[a0:a0 + 32].cpu().numpy(), 3)
+
+
 def test_two_graphs_share_inputs(slim):
     # each captured call has its own workspace: replays in any order agree
     n, m, g, t, v = 2600, 1024, 128, 500, 40000
@@ -482,6 +510,29 @@ def test_two_graphs_share_inputs(slim):
         torch.cuda.synchronize()
         y, s = graphs[i][1]
         assert torch.equal(y, want[0]) and all(torch.equal(s[k], want[1][k]) for k in s)
+
+
+def test_most_rows_and_unaligned_outputs(slim):
+    # 2^20 rows of 16: more tiles than one grid axis takes; then an output that starts anywhere
+    e, n, m, g, r = 2, 16, 32, 32, 1 << 20
+    codes, scale, zero = _layer(60, e, n, m, g)
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    X = _x(61, 50, m, "bf16").to("cuda:0")
+    rows = (torch.arange(r, device="cuda:0") % 50).to(torch.int32)
+    off = torch.tensor([0, r // 2 + 3, r], dtype=torch.int32, device="cuda:0")
+    Y = slim.q4_experts(X, off, packed, n, g, rows=rows)
+    for j, (a, b) in enumerate(((0, r // 2 + 3), (r // 2 + 3, r))):
+        exact = X.double().cpu().numpy() @ oracle.q4_weight(codes[j], scale[j], zero[j], g).T
+        one = Y[a:a + 50][torch.argsort(rows[a:a + 50])]
+        bound = _bound(X.double().cpu().numpy(), codes[j], scale[j], zero[j], g, "bf16", "f32", exact)
+        assert np.all(np.abs(one.double().cpu().numpy() - exact) <= bound)
+        whole = Y[a:a + (b - a) // 50 * 50].view(-1, 50, n)
+        assert torch.equal(whole, whole[:1].expand_as(whole))
+    p1 = slim.pack4(_gpu(codes[0]), _gpu(scale[0]), _gpu(zero[0]), g)
+    flat = torch.full((50 * n + 3,), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    out = slim.q4_linear(X, p1, n, g, out_dtype=torch.bfloat16, Y=flat[1:1 + 50 * n].view(50, n))
+    assert torch.equal(out, slim.q4_linear(X, p1, n, g, out_dtype=torch.bfloat16))
+    assert flat[0] == 7 and torch.all(flat[1 + 50 * n:] == 7)
 
 
 def test_long_offsets_past_32_bits(slim):

@@ -64,9 +64,11 @@ def test_q4_linear_abi(lib):
     assert call(xdt=2) == -3 and call(ydt=-1) == -3
     assert call(t=-1) == -2 and call(t=65537) == -2 and call(m=200) == -2 and call(n=0) == -2 and call(g=256) == -2
     assert call(n=(1 << 20) + 1) == -2
-    assert call(X=ODD) == -7 and call(W=ODD) == -7 and call(Y=ODD) == -7
+    assert call(X=ODD) == -7 and call(W=ODD) == -7
+    assert call(Y=ctypes.c_void_p(4097)) == -7 and call(ydt=0, Y=ctypes.c_void_p(4098)) == -7
     assert call(t=0, X=None, Y=None) == 0
     need = lib.slim_q4_linear_workspace(2048, 4096, 4096, 128, 1)
+    assert need > 0
     if need:
         assert call(t=2048, n=4096, m=4096, wsb=need - 1) == -5
         assert call(t=2048, n=4096, m=4096, ws=None) == -5
@@ -164,3 +166,12 @@ def test_token_logprobs_binding(L):
     raises(L, lambda: L.token_logprobs(_f(8, 3).t(), ids), "contiguous")
     raises(L, lambda: L.token_logprobs(_f(1, 8).expand(3, 8), ids), "overlap")
     raises(L, lambda: L.token_logprobs(_f(3, 8), ids), "GPU")
+
+
+def test_layer_paths(L):
+    import post_mixed_precision_amd as slim
+    raises(L, lambda: slim.quantize_layer(_bf(8, 256), _bf(8, 256), avg_bits=4, nibbles=True), "nibbles")
+    ids = torch.zeros(4, dtype=torch.int64)
+    raises(L, lambda: slim.score_tokens(_bf(3, 128), ids, _i(288), 16, 128), "ids")
+    raises(L, lambda: slim.score_tokens(_bf(4, 128), ids, _i(288), 16, 128, block=0), "block")
+    raises(L, lambda: slim.score_tokens(_bf(4, 128), ids, _i(287), 16, 128), "packed")
