@@ -171,7 +171,13 @@ def _arg(t, name: str, shape=None, dtypes=None, min_numel=None):
         raise SlimError(f"{name}: dtype {t.dtype}, expected one of {list(dtypes)}")
     if shape is not None:
         have = t.shape
-        if len(have) != len(shape) or any(s is not None and a != s for a, s in zip(have, shape)):
+        same = len(have) == len(shape)
+        if same:
+            for a, s in zip(have, shape):
+                if s is not None and a != s:
+                    same = False
+                    break
+        if not same:
             raise SlimError(f"{name}: shape {tuple(t.shape)}, expected {tuple('*' if s is None else s for s in shape)}")
     if min_numel is not None and t.numel() < min_numel:
         raise SlimError(f"{name}: {t.numel()} elements, at least {min_numel} needed")
@@ -554,6 +560,14 @@ def _need(query: str, *args) -> int:
     return getattr(load_library(), query)(*args)
 
 
+def _ready(dev, *ts):
+    """_on_gpu for tensors that are all on dev, the usual case, without its sets."""
+    for t in ts:
+        if t is not None and not (t.is_cuda and t.is_contiguous() and t.device == dev):
+            _on_gpu(*ts)
+            raise SlimError("tensors must live in GPU memory")
+
+
 def _raw_stream(index: int) -> int:
     """The current stream of a device as an integer (no Stream object)."""
     return _torch()._C._cuda_getCurrentRawStream(index)
@@ -571,8 +585,8 @@ def q4_linear(X, packed, n: int, group: int, out_dtype=None, Y=None):
     packed = _arg(packed, "packed", (_words4(1, n, m, group),), (torch.int32,))
     if Y is not None:
         Y = _arg(Y, "Y", (t, n), (out_dtype,))
-    _on_gpu(X, packed, Y)
     dev = X.device
+    _ready(dev, X, packed, Y)
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return q4_linear(X, packed, n, group, out_dtype, Y)
@@ -612,8 +626,8 @@ def q4_experts(X, offsets, packed, n: int, group: int, rows=None, row_scale=None
     packed = _arg(packed, "packed", (_words4(e, n, m, group),), (torch.int32,))
     if Y is not None:
         Y = _arg(Y, "Y", (r, n), (out_dtype,))
-    _on_gpu(X, offsets, packed, rows, row_scale, Y)
     dev = X.device
+    _ready(dev, X, offsets, packed, rows, row_scale, Y)
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return q4_experts(X, offsets, packed, n, group, rows, row_scale, out_dtype, Y)

@@ -270,6 +270,48 @@ def test_q4_experts_bad_rows_and_offsets(slim, per, n, m, xdt):
         assert torch.isnan(Y).all(), bounds
 
 
+@pytest.mark.parametrize("tx,n,m,g,xdt", [(5000, 1600, 384, 128, "bf16"), (3000, 1700, 320, 64, "bf16"),
+                                          (2500, 1600, 288, 32, "f32"), (3000, 2600, 1024, 128, "f32"),
+                                          (900, 40, 96, 32, "bf16")])
+def test_q4_experts_gather_of_few_rows(slim, tx, n, m, g, xdt):
+    # X has more rows than are asked for, some of them twice
+    e, counts = 2, [400, 300]
+    r = sum(counts)
+    codes, scale, zero = _layer(70, e, n, m, g)
+    rows = np.random.default_rng(71).integers(0, tx, size=r).astype(np.int32)
+    rows[:3] = rows[5], 0, tx - 1
+    X = _x(72, tx, m, xdt)
+    Y = slim.q4_experts(X.to("cuda:0"), _gpu(_counts_to_offsets(counts)),
+                        slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g), n, g, rows=_gpu(rows))
+    x = X.double().numpy()[rows]
+    for j, (a, b) in enumerate(((0, counts[0]), (counts[0], r))):
+        exact = x[a:b] @ oracle.q4_weight(codes[j], scale[j], zero[j], g).T
+        err = np.abs(Y[a:b].double().cpu().numpy() - exact)
+        bound = _bound(x[a:b], codes[j], scale[j], zero[j], g, xdt, "f32", exact)
+        assert np.all(err <= bound), float(np.max(err / bound))
+
+
+def test_q4_experts_gather_over_4_gib(slim):
+    # rows of X further apart than a 32-bit offset, in the tile kernel; the same rows in order agree
+    tx, n, m, g, r = 40000, 9216, 65536, 128, 128
+    X = torch.zeros((tx, m), dtype=torch.bfloat16, device="cuda:0")
+    rows = torch.cat([torch.arange(64), torch.arange(tx - 64, tx)]).to(torch.int32).to("cuda:0")
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(80)
+    X[:64] = torch.randn((64, m), generator=gen, device="cuda:0")
+    X[tx - 64:] = torch.randn((64, m), generator=gen, device="cuda:0")
+    codes = torch.randint(0, 16, (1, n, m), generator=gen, device="cuda:0").to(torch.uint8)
+    scale = torch.rand((1, n, m // g), generator=gen, device="cuda:0") * 0.01
+    zero = 7.5 + torch.rand((1, n, m // g), generator=gen, device="cuda:0")
+    packed = slim.pack4(codes, scale, zero, g)
+    off = torch.tensor([0, r], dtype=torch.int32, device="cuda:0")
+    lib = slim.load_library()
+    assert lib.slim_q4_experts_workspace(tx, r, 1, n, m, g, 1) > 2 * r * m      # the copy of the gathered rows
+    Y = slim.q4_experts(X, off, packed, n, g, rows=rows)
+    one = slim.q4_linear(X[rows.long()].contiguous(), packed, n, g)
+    torch.testing.assert_close(Y, one, rtol=1e-4, atol=1e-3)
+
+
 def test_q4_experts_matches_single_layers(slim):
     e, n, m, g = 4, 160, 512, 128
     codes, scale, zero = _layer(14, e, n, m, g)
