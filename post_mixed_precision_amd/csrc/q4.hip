@@ -916,7 +916,9 @@ hipError_t tile_go(const Q4Args &a, const TileWs &w, void *ws, hipStream_t st) {
 //    13824 x 5120: 15.4, 17.4, 25; t = 32, 4096 x 4096: 9.7, 8.0, 11.2; t = 1,
 //    4096 x 4096: 8.5, 5.2, 4.7.
 //  - 4 waves instead of 8 where a row has few records: 64 experts of 1024 x
-//    2048, 1024 rows: 33 against 38; 13824 x 5120: 17.0 against 15.4.
+//    2048, 1024 rows: 34 against 38; 13824 x 5120: 16.9 against 15.8.  16 where
+//    a workgroup has a CU to itself: t = 16, 13824 x 5120 (216 workgroups): 13.9
+//    against 15.8; t = 1, 28672 x 8192 (448): 31.7 against 30.1.
 int64_t rows_per_matrix(int64_t r, int64_t e) { return (r + e - 1) / e; }
 bool use_tiles(int64_t r, int64_t e, int64_t n, int64_t m) {
   return rows_per_matrix(r, e) > 64 && m > 256 && tile_count(r, n) >= 36;
@@ -927,8 +929,10 @@ hipError_t stream_pick(const Q4Args &a, hipStream_t st) {
   const int64_t nrb = q4_row_blocks(a.n), nch = q4_chunks(a.m), r4 = (nrb + 3) / 4;
   if (rows_per_matrix(a.r, a.e) >= 48 && r4 * ((a.r + 63) / 64) >= 384) return stream_go<XBF16, G, 4, 4, 4, 1>(a, st);
   const int64_t tiles = max_tiles(a.r, a.e, 16);
-  if (r4 * tiles >= 192)
-    return nch <= 16 ? stream_go<XBF16, G, 4, 1, 4, 2>(a, st) : stream_go<XBF16, G, 4, 1, 8, 1>(a, st);
+  if (r4 * tiles >= 192) {
+    if (nch <= 16) return stream_go<XBF16, G, 4, 1, 4, 2>(a, st);
+    return r4 * tiles < 320 ? stream_go<XBF16, G, 4, 1, 16, 1>(a, st) : stream_go<XBF16, G, 4, 1, 8, 1>(a, st);
+  }
   if ((nrb + 1) / 2 * tiles >= 144) return stream_go<XBF16, G, 2, 1, 8, 2>(a, st);
   return stream_go<XBF16, G, 1, 1, 8, 2>(a, st);
 }

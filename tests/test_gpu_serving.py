@@ -588,7 +588,15 @@ def test_long_offsets_past_32_bits(slim):
     off = torch.tensor([0] * e + [3], dtype=torch.int32, device="cuda:0")
     Y = slim.q4_experts(X, off, packed, n, g)
     one = slim.q4_linear(X, packed[(e - 1) * words:].clone(), n, g)
-    assert torch.equal(Y, one)
+    # the two calls may join their partial sums in different orders: each is
+    # within the bound of the exact value, so they are within twice of each other
+    x = X.double().cpu().numpy()
+    part = slice(n - 256, n)
+    exact = x @ oracle.q4_weight(codes[0][part], scale[0][part], zero[0][part], g).T
+    bound = _bound(x, codes[0][part], scale[0][part], zero[0][part], g, "bf16", "f32", exact)
+    assert np.all(np.abs(Y[:, part].double().cpu().numpy() - exact) <= bound)
+    assert np.all(np.abs((Y - one)[:, part].double().cpu().numpy()) <= 2 * bound)
+    torch.testing.assert_close(Y, one, rtol=1e-4, atol=1e-3)
     del packed, Y, one
     t, v = 20000, 60000                          # 2.4 GB of bfloat16
     L = torch.zeros((t, v), dtype=torch.bfloat16, device="cuda:0")
