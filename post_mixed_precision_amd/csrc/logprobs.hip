@@ -20,6 +20,14 @@
 // exchanges, all by DPP and lane swaps).  Of N values in random order only
 // about top ln(N / top) get that far.  Waves and segments are joined by the
 // same merge.  The set and its order depend on the keys alone.
+//
+// Bound by reading the logits where there are many: 2048 rows of 32000 float32
+// 41.7 us (262 MB, 6.3 TB/s), 333 rows of 100003 30 us (133 MB, 4.4 TB/s) and 4
+// for the join.  bfloat16 halves the bytes but not the work of an entry (seven
+// vector operations and a power, which costs four): 2048 rows of 32000 34 us.
+// The best entries add the first threshold of every wave (a sort, 0.8 us) and
+// the joins: +4 us for one entry and +20 for 20 at 2048 x 32000.  Few rows are
+// latency: 16 rows of 131072 bfloat16 with 20 entries 10.8 + 5.6 us.
 #include <algorithm>
 
 #include "common.hpp"
