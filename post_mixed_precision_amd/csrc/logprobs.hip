@@ -14,7 +14,8 @@
 //
 // Best entries: every wave keeps the largest 64 keys (ordered value bits, then
 // the inverted index, so that a larger key is a better entry) sorted over its
-// lanes.  Values above the top-th key are offered a register at a time: a few
+// lanes.  The first threshold is the top-th of the lanes' largest entries;
+// what passes the threshold is collected in LDS and offered together: a few keys
 // are broadcast and inserted one by one, shifting the lanes below; more are
 // sorted over the lanes and merged (a bitonic network of 21 and 7 lane
 // exchanges, all by DPP and lane swaps).  Of N values in random order only
@@ -80,7 +81,7 @@ __device__ __forceinline__ key_t64 lane_key(key_t64 k, int lane) {
 // Lane exchanges: the value of lane l ^ X.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
 }
 template <int X>
 __device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
@@ -210,15 +211,13 @@ __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
 }
 
 // N entries of every lane: e is entry idx(e) of the row, rising with e, and one
-// that does not exist is -inf and idx(e) >= v.  The lanes' largest entries are
-// offered, then their next ones, until no lane's passes the threshold: at the
-// start the first 64 set one that few of the others pass.  shared: a
-// threshold of the workgroup's other waves; s_thr: where this one's goes.  The
-// waves see each other's at different times, but it only spares work: what it
-// keeps out has top larger keys in some wave's list.
+// that does not exist is -inf and idx(e) >= v.  shared: a threshold of the
+// workgroup's other waves; s_thr: where this one's goes.  The waves see each
+// other's at different times, but it only spares work: what it keeps out has
+// top larger keys in some wave's list.
 template <int N, class Idx>
 __device__ __forceinline__ void take(const float (&x)[N], Idx idx, uint32_t v, int top, uint32_t shared, Stats &st,
-                                     Best &best, uint32_t *s_thr) {
+                                     Best &best, uint32_t *s_thr, key_t64 *room) {
   float b = x[0];
 #pragma unroll
   for (int e = 1; e < N; ++e) b = fmaxf(b, x[e]);
@@ -243,26 +242,55 @@ __device__ __forceinline__ void take(const float (&x)[N], Idx idx, uint32_t v, i
   if (shared > (uint32_t)(best.thr >> 32)) best.thr = (key_t64)shared << 32;
   float thr = from_order_bits((uint32_t)(best.thr >> 32));   // NaN while no list is full
   if (!__ballot(!(b < thr))) return;
-  float y[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) y[e] = x[e];
-  for (;;) {
-    int at = 0;                                              // of equal entries the lowest: largest key
+  auto key = [&](float val, int e) __attribute__((always_inline)) {
+    const uint32_t i = idx(e);
+    return val == val && i < v ? make_key(val, i) : (key_t64)0;
+  };
+  auto largest = [&](const float (&y)[N]) __attribute__((always_inline)) {   // where y is b, the lowest of equals
+    int at = 0;
 #pragma unroll
     for (int e = 0; e < N; ++e) at = y[N - 1 - e] == b ? N - 1 - e : at;
-    const uint32_t i = idx(at);
-    const key_t64 k = b == b && i < v ? make_key(b, i) : 0;
-    if (!__ballot(k > best.thr)) break;
-    best.offer(k, top);
-    if constexpr (N == 1) {
-      break;
-    } else {                                                 // the lanes' next largest
+    return at;
+  };
+  key_t64 first = 0;
+  if (N > 1 && !best.thr) {                                  // no threshold yet: the lanes' largest set one
+    first = key(b, largest(x));
+    best.offer(first, top);
+    thr = from_order_bits((uint32_t)(best.thr >> 32));
+  }
+  // The entries that pass it, side by side in `room`, 64 keys of LDS.
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if (!__ballot(!(x[e] < thr))) continue;
+    const key_t64 k = key(x[e], e);
+    const bool in = k > best.thr && k != first;
+    const uint64_t who = __ballot(in);
+    const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+    if (in && at < 64) room[at] = k;
+    n += __popcll(who);
+  }
+  if (n > 0 && n <= 64) {
+    __builtin_amdgcn_wave_barrier();
+    best.offer(lane < n ? room[lane] : 0, top);
+    __builtin_amdgcn_wave_barrier();
+  } else if (n > 64) {
+    // More than fit (rising rows, ties, or no threshold): the lanes' largest,
+    // then their next ones, until no lane's passes.
+    float y[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) y[e] = first && key(x[e], e) == first ? __uint_as_float(0x7fc00000u) : x[e];
+    for (int round = 0; round < N; ++round) {
       b = __uint_as_float(0x7fc00000u);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        y[e] = e == at ? __uint_as_float(0x7fc00000u) : y[e];
-        b = fmaxf(b, y[e]);
-      }
+      for (int e = 0; e < N; ++e) b = fmaxf(b, y[e]);
+      const int at = largest(y);
+      const key_t64 k = key(b, at);
+      if (!__ballot(k > best.thr)) break;
+      best.offer(k, top);
+#pragma unroll
+      for (int e = 0; e < N; ++e) y[e] = e == at ? __uint_as_float(0x7fc00000u) : y[e];
     }
   }
   if ((threadIdx.x & 63) == 0) atomicMax(s_thr, (uint32_t)(best.thr >> 32));
@@ -389,7 +417,7 @@ __global__ __launch_bounds__(64 * LP_WAVES) void logprob_kernel(const void *__re
           const int at = j + e / VEC * STEP;
           return at < v1 ? (uint32_t)(head + at * VEC + e % VEC) : 0xffffffffu;
         },
-        (uint32_t)v, top, shared, st, best, &s_thr);
+        (uint32_t)v, top, shared, st, best, &s_thr, s_keys[wave]);
   };
   if (v0 < v1) {
     fetch(j, cur);
@@ -409,7 +437,7 @@ __global__ __launch_bounds__(64 * LP_WAVES) void logprob_kernel(const void *__re
     float x[1] = {-__builtin_inff()};
     if (has) x[0] = load_one<BF16>(row + at * ES);
     take<1>(x, [&](int) __attribute__((always_inline)) { return has ? (uint32_t)at : 0xffffffffu; }, (uint32_t)v, top,
-            0u, st, best, &s_thr);
+            0u, st, best, &s_thr, s_keys[wave]);
   }
   st = wave_join(st);
   if (lane == 0) s_stats[wave] = st;
