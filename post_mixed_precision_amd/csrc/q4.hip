@@ -192,6 +192,34 @@ __device__ __forceinline__ void store_y(const Q4Args &a, int64_t row, int64_t i,
   else ((float *)a.Y)[row * a.n + i] = v;
 }
 
+// A record's scale and zero pairs of row l % 16, for lanes that loaded group
+// (l / 16) % GPC's: one load and a few lane swaps in place of a load per group.
+// A value swapped with itself leaves both rows' (halves') values in every lane.
+template <int GPC>
+__device__ __forceinline__ void spread(float2 v, float2 (&o)[GPC]) {
+  if constexpr (GPC == 1) {
+    o[0] = v;
+  } else {
+    float2 half[GPC / 2];
+    if constexpr (GPC == 2) {
+      half[0] = v;
+    } else {
+      const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v.x), __float_as_uint(v.x), false, false);
+      const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(v.y), __float_as_uint(v.y), false, false);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) half[h] = make_float2(__uint_as_float(x[h]), __uint_as_float(y[h]));
+    }
+#pragma unroll
+    for (int h = 0; h < GPC / 2; ++h) {
+      const uint32_t s = __float_as_uint(half[h].x), z = __float_as_uint(half[h].y);
+      const auto x = __builtin_amdgcn_permlane16_swap(s, s, false, false);
+      const auto y = __builtin_amdgcn_permlane16_swap(z, z, false, false);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) o[2 * h + q] = make_float2(__uint_as_float(x[q]), __uint_as_float(y[q]));
+    }
+  }
+}
+
 // ---------------------------------------------------------------- streaming kernel
 // A workgroup owns 16 R output rows of one matrix and a tile of 16 TT rows of
 // Y; its NW waves take the 128-column records in turn (wave w: w, w + NW, ...;
@@ -253,7 +281,7 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
   auto records = [&](int ch0, auto count) __attribute__((always_inline)) {
     constexpr int N = decltype(count)::value;
     uint4 w[N][R];
-    float2 sz[N][R][GPC];
+    float2 pair[N][R];
     uint4 x[N][TT][4][XL];
 #pragma unroll
     for (int v = 0; v < N; ++v) {
@@ -262,8 +290,7 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
       for (int b = 0; b < R; ++b) {
         const uint32_t *rec = wp[b] + (int64_t)ch * RECW;
         w[v][b] = *(const uint4 *)(rec + 4 * lane);
-#pragma unroll
-        for (int q = 0; q < GPC; ++q) sz[v][b][q] = *(const float2 *)(rec + 256 + 2 * (16 * q + r16));
+        pair[v][b] = *(const float2 *)(rec + 256 + 2 * (16 * (lg & (GPC - 1)) + r16));
       }
 #pragma unroll
       for (int u = 0; u < TT; ++u)
@@ -276,6 +303,9 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
 #pragma unroll
     for (int v = 0; v < N; ++v) {
       const int ch = ch0 + v * NW;
+      float2 sz[R][GPC];
+#pragma unroll
+      for (int b = 0; b < R; ++b) spread<GPC>(pair[v][b], sz[b]);
 #pragma unroll
       for (int q = 0; q < GPC; ++q) {
         if (ch * 128 + q * G >= a.m) break;
@@ -306,13 +336,21 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
             }
           }
         }
+        auto add = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
-        for (int b = 0; b < R; ++b)
+          for (int b = 0; b < R; ++b)
 #pragma unroll
-          for (int u = 0; u < TT; ++u)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tot[b][u][j] = fmaf(sz[v][b][q].x, fmaf(-sz[v][b][q].y, sx[u][j], acc[b][u][j]), tot[b][u][j]);
+            for (int u = 0; u < TT; ++u)
+              tot[b][u][j] = fmaf(sz[b][q].x, fmaf(-sz[b][q].y, sx[u][j], acc[b][u][j]), tot[b][u][j]);
+        };
+        // up to four tokens have no more than element 0 (the branch costs the other
+        // variants more than it saves: 64 experts over 1024 rows, g = 64, 34 against 31 us)
+        add(0);
+        if (TT > 1 || U > 1 || G == 32 || tl.cnt > 4) {
+          add(1);
+          add(2);
+          add(3);
+        }
       }
     }
   };
