@@ -432,7 +432,8 @@ static bool logprob_shape(int64_t t, int64_t v) {
 
 size_t slim_token_logprobs_workspace(int64_t t, int64_t v, int top) {
   if (!logprob_shape(t, v) || top < 0 || top > SLIM_LOGPROB_MAX_TOP || top > v) return 0;
-  return slim::logprob_plan(t, v, top).ws_bytes;
+  const size_t f = slim::logprob_plan(t, v, top, false).ws_bytes, b = slim::logprob_plan(t, v, top, true).ws_bytes;
+  return f > b ? f : b;   // of either dtype
 }
 
 int slim_token_logprobs(const void *logits, int ldt, int64_t t, int64_t v, int64_t ld, const int64_t *ids, int top,
@@ -444,9 +445,10 @@ int slim_token_logprobs(const void *logits, int ldt, int64_t t, int64_t v, int64
   if (t == 0) return SLIM_OK;
   if (!logits || (logprob && !ids) || (top > 0 && (!top_logprob || !top_id))) return SLIM_E_NULL;
   if ((uintptr_t)logits % (ldt == SLIM_BF16 ? 2 : 4)) return SLIM_E_ALIGN;
-  const slim::LogprobPlan p = slim::logprob_plan(t, v, top);
-  if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes)) return SLIM_E_WORKSPACE;
-  if (p.ws_bytes > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
+  const slim::LogprobPlan p = slim::logprob_plan(t, v, top, ldt == SLIM_BF16);
+  const size_t need = slim_token_logprobs_workspace(t, v, top);
+  if (need > 0 && (!ws || ws_bytes < need)) return SLIM_E_WORKSPACE;
+  if (need > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
   hipError_t err = slim::launch_logprobs(logits, ldt == SLIM_BF16, t, v, ld, ids, top, logprob, entropy, top_logprob,
                                          top_id, ws, p, (hipStream_t)stream);
   return err == hipSuccess ? SLIM_OK : hip_fail(err);

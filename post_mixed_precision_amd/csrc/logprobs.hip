@@ -501,21 +501,22 @@ __global__ __launch_bounds__(64 * LP_WAVES) void logprob_join_kernel(
 
 }  // namespace
 
-LogprobPlan logprob_plan(int64_t t, int64_t v, int top) {
+LogprobPlan logprob_plan(int64_t t, int64_t v, int top, bool bf16) {
   LogprobPlan p;
   const int64_t rows = t > 0 ? t : 1;
-  // A few short rows: one workgroup of 16 waves each and a single launch takes as
-  // long on the device as 16 pieces and their joining (one token of 32000, top 1:
-  // 10.8 against 10.3 us) and spares the host a launch; 131072 entries keep one
-  // CU busy for longer than that (19.9 against 13.7 us).
-  p.wide = rows <= 64 && v <= 32768;
-  // Else few rows are cut until 512 workgroups share them, down to 2048 entries
-  // each, and long rows, in pieces of 16384, until 1536 do, so that the last
-  // workgroups of the card end together (333 rows of 100003: 5 segments 31.4 us,
-  // 2 segments 35).
+  // Few rows: workgroups of 16 waves, whose lists are joined by halves, each with
+  // 16384 entries or a short row to itself, which then takes a single launch (one
+  // float32 row of 131072, top 5: 12.8 us, by 4 waves 16.7).  More rows, and long
+  // bfloat16 ones (16 rows of 131072: 15.1 against 12.9: 16 waves read 32768 of
+  // its entries at once), are cut for workgroups of 4 waves.
+  p.wide = (rows <= 32 && !bf16) || (rows <= 64 && v <= 32768);
+  const int64_t wide = v <= 32768 ? 1 : std::min((256 + rows - 1) / rows, (v + 16383) / 16384);
+  // Those pieces: 2048 entries at least until 512 workgroups share the rows, and
+  // of 16384 until 1536 do, so that the last workgroups of the card end together
+  // (333 rows of 100003: 5 segments 31.4 us, 2 segments 35).
   const int64_t few = std::min((512 + rows - 1) / rows, (v + 2047) / 2048);
   const int64_t even = std::min((1536 + rows - 1) / rows, (v + 16383) / 16384);
-  const int64_t seg = p.wide ? 1 : std::min<int64_t>(64, std::max(few, even));
+  const int64_t seg = std::min<int64_t>(64, p.wide ? wide : std::max(few, even));
   p.nseg = (int)seg;
   p.ws_bytes = seg > 1 ? (((size_t)t * seg * 12 + 15) & ~(size_t)15) + (size_t)t * seg * top * 8 : 0;
   return p;
@@ -525,15 +526,15 @@ template <bool BF16>
 static hipError_t go(const void *L, int64_t t, int64_t v, int64_t ld, const int64_t *ids, int top, float *logprob,
                      float *entropy, float *top_logprob, int32_t *top_id, void *ws, const LogprobPlan &p,
                      hipStream_t st) {
-  if (p.wide) {
-    logprob_kernel<BF16, 16><<<(uint32_t)t, 64 * 16, 0, st>>>(L, v, ld, ids, top, 1, logprob, entropy, top_logprob,
-                                                              top_id, nullptr, nullptr);
-    return hipGetLastError();
-  }
   float *stats = (float *)ws;
   key_t64 *keys = (key_t64 *)((char *)ws + (((size_t)t * p.nseg * 12 + 15) & ~(size_t)15));
-  logprob_kernel<BF16, 4><<<dim3((uint32_t)t, p.nseg), 64 * 4, 0, st>>>(L, v, ld, ids, top, p.nseg, logprob, entropy,
-                                                                       top_logprob, top_id, stats, keys);
+  const dim3 grid((uint32_t)t, p.nseg);
+  if (p.wide)
+    logprob_kernel<BF16, 16><<<grid, 64 * 16, 0, st>>>(L, v, ld, ids, top, p.nseg, logprob, entropy, top_logprob, top_id,
+                                                       stats, keys);
+  else
+    logprob_kernel<BF16, 4><<<grid, 64 * 4, 0, st>>>(L, v, ld, ids, top, p.nseg, logprob, entropy, top_logprob, top_id,
+                                                     stats, keys);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.nseg == 1) return e;
   logprob_join_kernel<BF16, 4><<<(uint32_t)t, 64 * 4, 0, st>>>(L, v, ld, ids, top, p.nseg, logprob, entropy,

@@ -36,11 +36,11 @@ hipError_t launch_q4(const Q4Args &a, void *ws, hipStream_t st);
 
 // ---- Token log probabilities ----
 struct LogprobPlan {
-  bool wide;                 // one workgroup of 16 waves a row
+  bool wide;                 // workgroups of 16 waves, not 4
   int nseg;                  // segments a row is split into
   size_t ws_bytes;           // their statistics and best entries (0 for one segment)
 };
-LogprobPlan logprob_plan(int64_t t, int64_t v, int top);
+LogprobPlan logprob_plan(int64_t t, int64_t v, int top, bool bf16);
 hipError_t launch_logprobs(const void *L, bool bf16, int64_t t, int64_t v, int64_t ld, const int64_t *ids, int top,
                            float *logprob, float *entropy, float *top_logprob, int32_t *top_id, void *ws,
                            const LogprobPlan &p, hipStream_t st);
