@@ -225,11 +225,11 @@ __device__ __forceinline__ void spread(float2 v, float2 (&o)[GPC]) {
 // Y; its NW waves take the 128-column records in turn (wave w: w, w + NW, ...;
 // U of them at a time, whose loads are all in flight together) and their sums
 // are joined through LDS in wave order, so the result does not depend on timing.
-// Bound by the stream of records: one token through 28672 x 8192 takes 25 us
-// (132 MB, 5.2 TB/s; 28 us with cold caches), 16 tokens through 13824 x 5120
-// 13.8 us (45 MB, 3.2 TB/s: X is read by every workgroup and 216 workgroups of
-// 4 row blocks leave 40 CUs idle), 1024 rows over 64 experts of 1024 x 2048
-// 31.6 us (84 MB once; an expert with more than 16 rows is read again for each
+// Bound by the stream of records: one token through 28672 x 8192 takes 23 us
+// (132 MB, 5.7 TB/s; 28 us where other weights pass between calls), 16 tokens
+// through 13824 x 5120, g = 64, 12.0 us (45 MB, 3.7 TB/s: 216 workgroups leave 40
+// CUs idle), 1024 rows over 64 experts of 1024 x 2048, g = 64, 31 us (84 MB once;
+// an expert with more than 16 rows is read again for each
 // 16).  Splitting the columns over the waves of a workgroup rather than over
 // workgroups keeps it one launch without partial sums in memory.
 // MFMA operands (v_mfma_f32_16x16x32_bf16): A = X (row l % 16, columns
