@@ -113,20 +113,22 @@ __device__ __forceinline__ void split3(const uint4 &a, const uint4 &b, uint4 (&t
 // Bounds out of order make every tile bad; tiles then cut the plain row range.
 struct RowTile {
   int expert;
-  int64_t row0;    // first row of Y
+  int row0;        // first row of Y (rows are below 2^20)
   int cnt;         // rows in the tile
 };
 
 template <int TOK>
 struct Tiles {
-  int64_t total;   // tiles of this call
+  int total;       // tiles of this call
   bool bad;        // offsets are not nondecreasing inside [0, r]
-  int64_t mine, incl;
+  int mine, incl;
+  int lo0, hi0;    // bounds of this lane's first expert
 
   __device__ __forceinline__ void scan(const Q4Args &a) {
+    const int r = (int)a.r;
     bad = false;
-    mine = incl = 0;
-    total = (a.r + TOK - 1) / TOK;
+    mine = incl = lo0 = hi0 = 0;
+    total = (r + TOK - 1) / TOK;
     if (!a.offsets) return;
     const int lane = threadIdx.x & 63;
     const int per = (a.e + 63) >> 6;
@@ -134,9 +136,10 @@ struct Tiles {
     for (int i = 0; i < per; ++i) {
       const int e = lane * per + i;
       if (e < a.e) {
-        const int64_t lo = a.offsets[e], hi = a.offsets[e + 1];
-        if (lo < 0 || hi < lo || hi > a.r) wrong = true;
-        else mine += (hi - lo + TOK - 1) / TOK;
+        const int lo = a.offsets[e], hi = a.offsets[e + 1];
+        if (i == 0) lo0 = lo, hi0 = hi;
+        if (lo < 0 || hi < lo || hi > r) wrong = true;
+        else mine += (int)((uint32_t)(hi - lo + TOK - 1) / TOK);
       }
     }
     bad = __builtin_amdgcn_ballot_w64(wrong) != 0;   // uniform, unlike __any, for the compiler too
@@ -144,29 +147,29 @@ struct Tiles {
     incl = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int64_t o = __shfl_up(incl, d, 64);
+      const int o = __shfl_up(incl, d, 64);
       if (lane >= d) incl += o;
     }
-    total = __builtin_amdgcn_readfirstlane((int)__shfl(incl, 63, 64));
+    total = __builtin_amdgcn_readlane(incl, 63);
   }
 
   // Tile idx < total.
-  __device__ __forceinline__ RowTile locate(const Q4Args &a, int64_t idx) const {
+  __device__ __forceinline__ RowTile locate(const Q4Args &a, int idx) const {
     RowTile t;
     t.expert = 0;
     t.row0 = idx * TOK;
-    int64_t end = a.r;
+    int end = (int)a.r;
     if (a.offsets && !bad) {
       const int per = (a.e + 63) >> 6;
       int ex = -1;
-      int64_t row0 = 0, hi1 = 0;
-      int64_t left = idx - (incl - mine);
+      int row0 = 0, hi1 = 0;
+      int left = idx - (incl - mine);
       if (left >= 0 && left < mine) {
         for (int i = 0; i < per; ++i) {
           const int e = (threadIdx.x & 63) * per + i;
           if (e >= a.e) break;
-          const int64_t lo = a.offsets[e], hi = a.offsets[e + 1];
-          const int64_t tl = (hi - lo + TOK - 1) / TOK;
+          const int lo = i ? a.offsets[e] : lo0, hi = i ? a.offsets[e + 1] : hi0;
+          const int tl = (int)((uint32_t)(hi - lo + TOK - 1) / TOK);
           if (left < tl) {
             ex = e;
             row0 = lo + left * TOK;
@@ -176,13 +179,13 @@ struct Tiles {
           left -= tl;
         }
       }
-      const int src = __ffsll((unsigned long long)__ballot(ex >= 0)) - 1;
-      t.expert = __builtin_amdgcn_readfirstlane(__shfl(ex, src, 64));
-      t.row0 = __shfl(row0, src, 64);
-      end = __shfl(hi1, src, 64);
+      const int src = __ffsll((unsigned long long)__builtin_amdgcn_ballot_w64(ex >= 0)) - 1;
+      t.expert = __builtin_amdgcn_readlane(ex, src);
+      t.row0 = __builtin_amdgcn_readlane(row0, src);
+      end = __builtin_amdgcn_readlane(hi1, src);
     }
-    t.row0 = __builtin_amdgcn_readfirstlane((int)t.row0);   // uniform, and below 2^20
-    t.cnt = __builtin_amdgcn_readfirstlane((int)(end - t.row0 < TOK ? end - t.row0 : TOK));
+    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    t.cnt = __builtin_amdgcn_readfirstlane(end - t.row0 < TOK ? end - t.row0 : TOK);
     return t;
   }
 };
@@ -190,6 +193,18 @@ struct Tiles {
 __device__ __forceinline__ void store_y(const Q4Args &a, int64_t row, int64_t i, float v) {
   if (a.ybf16) ((uint16_t *)a.Y)[row * a.n + i] = (uint16_t)f32_to_bf16_bits(v);
   else ((float *)a.Y)[row * a.n + i] = v;
+}
+
+// What row `row` of Y is multiplied by: NaN where its row of X is out of range, or
+// the bounds are.
+__device__ __forceinline__ float row_factor(const Q4Args &a, bool bad, int64_t row) {
+  float f = a.row_scale ? a.row_scale[row] : 1.0f;
+  bool ok = !bad;
+  if (a.rows) {
+    const int32_t xr = a.rows[row];
+    ok = ok && xr >= 0 && xr < a.xrows;
+  }
+  return ok ? f : __uint_as_float(0x7fc00000u);
 }
 
 // A record's scale and zero pairs of row l % 16, for lanes that loaded group
@@ -245,11 +260,12 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
   constexpr int XL = XBF16 ? 1 : 2;              // 16-byte loads for 8 columns of X
   constexpr int TOK = 16 * TT;
   __shared__ float part[NW][R * TT * 256];
+  __shared__ float factor[TOK];
   const int lane = threadIdx.x & 63, r16 = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   Tiles<TOK> tiles;
   tiles.scan(a);
-  const int64_t tile = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+  const int tile = (int)(blockIdx.z * gridDim.y + blockIdx.y);
   if (tile >= tiles.total) return;
   const RowTile tl = tiles.locate(a, tile);
   const int rb0 = blockIdx.x * R;
@@ -265,6 +281,7 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
     }
     xp[u] = (const char *)a.X + (row * a.m + 8 * lg) * (XBF16 ? 2 : 4);
   }
+  if ((int)threadIdx.x < tl.cnt) factor[threadIdx.x] = row_factor(a, tiles.bad, tl.row0 + threadIdx.x);
   const uint32_t *wp[R];                         // row blocks past the last repeat it
 #pragma unroll
   for (int b = 0; b < R; ++b)
@@ -377,14 +394,7 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) v += part[w][idx];
-    const int64_t row = tl.row0 + tok;
-    bool ok = !tiles.bad;
-    if (a.rows && ok) {
-      const int32_t xr = a.rows[row];
-      ok = xr >= 0 && xr < a.xrows;
-    }
-    if (a.row_scale) v *= a.row_scale[row];
-    store_y(a, row, i, ok ? v : __uint_as_float(0x7fc00000u));
+    store_y(a, tl.row0 + tok, i, v * factor[tok]);
   }
 }
 
@@ -473,6 +483,21 @@ __device__ __forceinline__ void load_lds(const void *base, uint32_t limit, void 
   else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (q4_lds_t *)to, 4, (int)voff, soff, 0, 0);
 }
 
+// Stores that drop what lies past `limit` bytes from `base`.
+__device__ __forceinline__ void store_pair(void *base, uint32_t limit, bool half, uint32_t at0, uint32_t at1, float y0,
+                                           float y1) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)limit, 0x00020000);
+  if (half) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    const uint32_t p = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)y0, (__bf16)y1});
+    __builtin_amdgcn_raw_buffer_store_b16((short)p, r, (int)at0, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b16((short)(p >> 16), r, (int)at1, 0, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(y0), r, (int)at0, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(y1), r, (int)at1, 0, 0);
+  }
+}
+
 // Waits until at most VM of this wave's loads are in flight (loads complete in
 // order, so what was issued before the last VM is in LDS) and its LDS reads
 // have returned.  The builtin, not inline text: the compiler then knows which
@@ -485,8 +510,8 @@ __device__ __forceinline__ void wait_loads() {
 }
 __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
 
-// 128 rows of Y x 256 output rows per workgroup, a 64 x 64 piece of it per wave
-// (2 x 2 blocks of 32 x 32).  Every operand goes straight to LDS, 128 columns
+// 128 rows of Y x 256 output rows per workgroup (WT = 2, WN = 4) or 64 x 512 (1, 8),
+// a 64 x 64 piece of it per wave (2 x 2 blocks of 32 x 32).  Every operand goes straight to LDS, 128 columns
 // (a record per 16 output rows) to a stage, two stages ahead of the products:
 // X's rows with their 16-byte slots XOR-swizzled by row (16 rows of a column
 // slice then lie in different banks), the records, and the group sums.
@@ -511,21 +536,24 @@ __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory");
 // load phases (the scaling's 256 cycles, LDS latency) are as long as the
 // products.  Without the phases, both waves of a SIMD alike, it was 218 us; one
 // load and one product phase a stage (g = 128) measured the same 178 us.
+// A workgroup's start and end run beside no product, so they are kept short: tile
+// arithmetic in 32 bits, the rows' factors fetched at the start, stores whose bounds
+// the buffer descriptor checks (8 experts of 11008 x 4096 over 4096 rows: 472 -> 418 us).
 template <int G, int WT, int WN>
 __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, const uint16_t *__restrict__ X,
                                                                   int64_t ldx, int nt, bool gather, bool compact,
                                                                   const float *__restrict__ sums, int nrb, int nch,
                                                                   int nnb, float *__restrict__ partial) {
   constexpr int NW = WT * WN, TOK = 64 * WT;
-  static_assert(WT * WN == 8, "the phases pair waves w and w + 4");
+  static_assert(WT * WN == 8 && WN >= 4, "the phases pair waves w and w + 4");
   constexpr int GPC = 128 / G;                   // groups per record
   constexpr int RECW = 256 + 32 * GPC;
   constexpr int XL = 16 / WN;                    // loads per wave and stage: X (1 KB each),
   constexpr int RL = 4 / WT;                     //   codes of a record,
-  constexpr int ZL = GPC;                        //   scales and zeros,
+  constexpr int ZP = WN / 4, ZL = ZP * GPC;      //   scales and zeros,
   constexpr int SL = (WT * GPC + NW - 1) / NW;   //   group sums of 64 rows
   constexpr int LOADS = XL + RL + ZL + SL;
-  constexpr int RST = G == 32 ? 2 : 3;           // stages of records (three of 24 KB do not fit)
+  constexpr int RST = (G == 32 || (G == 64 && WN == 8)) ? 2 : 3;   // stages of records, as many as fit
   struct Stage {
     unsigned char x[TOK * 256];
     float s[GPC * TOK];
@@ -537,6 +565,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
   constexpr int ZAT = 4 * WN * 1024;
   __shared__ __align__(16) Stage st0, st1, st2;
   __shared__ __align__(16) Recs rc0, rc1;
+  __shared__ float factor[TOK];
   __shared__ __align__(16) typename std::conditional<RST == 3, Recs, uint4>::type rc2;
   const int lane = threadIdx.x & 63, hi = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -547,13 +576,13 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
   // blocks, so the workgroups sharing an L2 share X tiles and codes.
   Tiles<TOK> tiles;
   tiles.scan(a);
-  const int64_t all = tiles.total * nnb, per = (all + 7) / 8;
-  const int64_t idx = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((int64_t)(blockIdx.x >> 3) >= per || idx >= all) return;
-  const int64_t strip = idx / (4 * nnb), in = idx - strip * 4 * nnb;
-  const int64_t wide = tiles.total - 4 * strip < 4 ? tiles.total - 4 * strip : 4;
+  const uint32_t all = (uint32_t)tiles.total * nnb, per = (all + 7) / 8;   // below 2^27
+  const uint32_t idx = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (blockIdx.x >> 3 >= per || idx >= all) return;
+  const uint32_t strip = idx / (4 * nnb), in = idx - strip * 4 * nnb;
+  const uint32_t wide = tiles.total - 4 * strip < 4 ? tiles.total - 4 * strip : 4;
   const int nb = (int)(in / wide);
-  const RowTile tl = tiles.locate(a, 4 * strip + in % wide);
+  const RowTile tl = tiles.locate(a, (int)(4 * strip + in % wide));
 
   // Operands come by buffer loads: one descriptor each with its base at this
   // tile, a 32-bit offset per lane that stays, and the stage as scalar offset.
@@ -567,8 +596,8 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
   // `partial`, where the columns are split); float32 X passes its three planes in turn.
   const int c0 = nt * nch * (int)blockIdx.y / (int)gridDim.y;
   const int n = nt * nch * ((int)blockIdx.y + 1) / (int)gridDim.y;
-  const uint16_t *xbase = X + (gather ? 0 : tl.row0 * ldx);
-  const float *sbase = sums + (gather && !compact ? 0 : tl.row0 * (nch * GPC));
+  const uint16_t *xbase = X + (gather ? 0 : (int64_t)tl.row0 * ldx);
+  const float *sbase = sums + (gather && !compact ? 0 : (int64_t)tl.row0 * (nch * GPC));
   const uint32_t xbytes = (uint32_t)((gather ? a.xrows : tl.cnt) * ldx * 2);
   const uint32_t sbytes = (uint32_t)((gather && !compact ? a.xrows : tl.cnt) * (nch * GPC) * 4);
   uint32_t xo[XL];                              // this lane's 16 bytes of each of its rows, stage 0
@@ -583,11 +612,11 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
     const int j = (wave + i * NW) % (WT * GPC), tok = (j % WT) * 64 + lane;
     so[i] = (uint32_t)((compact ? (tok < tl.cnt ? tok : 0) : x_row(tok)) * (nch * GPC) + j / WT) * 4;
   }
-  // A quarter of the loads of X's stage c, the sums with the last.
-  static_assert(XL == 4, "a load for each K step of a product phase");
+  // One of the loads of X's stage c, the sums with the last.
+  static_assert(XL <= 4, "one load to a K step of a product phase at most");
   auto load_x = [&](int c, int part, Stage &st) __attribute__((always_inline)) {
     load_lds<16>(xbase, xbytes, st.x + (wave * XL + part) * 1024, xo[part], c * 256);
-    if (part < 3) return;
+    if (part < XL - 1) return;
     const int ch = c < nch ? c : 0;             // used with the first plane only
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
@@ -597,24 +626,36 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
   };
   // Records, as byte offsets from the tile's first; row blocks past the last
   // repeat it.  A wave loads the codes of records RL wave .. and the scales and
-  // zeros of records j and j + 2, j = 4 (wave / 2) + wave % 2, which one lane
-  // reads together.
+  // zeros of the pairs p = wave (and wave + 8): records j and j + 2, j = 4 (p / 2)
+  // + p % 2, which one lane reads together.
   const int rb0 = nb * WN * 4;
   auto rec = [&](int j) __attribute__((always_inline)) {
     return (rb0 + j < nrb ? j : nrb - 1 - rb0) * nch * (RECW * 4);
   };
   const uint32_t *wbase = a.W + ((int64_t)tl.expert * nrb + rb0) * nch * RECW;
   const uint32_t limit = (uint32_t)(rec(WN * 4 - 1) + nch * (RECW * 4));
-  // scale and zero words in LDS: [4 (wave / 2) + wave % 2][group][row][block][2]
-  const uint32_t zo = (uint32_t)(rec(wave / 2 * 4 + wave % 2 + (lane & 2)) + 1024 + (lane >> 2) * 8 + (lane & 1) * 4);
+  // scale and zero words in LDS: [pair][group][row][record][2]
+  uint32_t zo[ZP];
+#pragma unroll
+  for (int i = 0; i < ZP; ++i) {
+    const int p = wave + 8 * i;
+    zo[i] = (uint32_t)(rec(p / 2 * 4 + p % 2 + (lane & 2)) + 1024 + (lane >> 2) * 8 + (lane & 1) * 4);
+  }
   auto load_rec = [&](int c, Recs &rc) __attribute__((always_inline)) {
     const int at = (nt > 1 ? c % nch : c) * (RECW * 4);
 #pragma unroll
     for (int i = 0; i < RL; ++i)
       load_lds<16>(wbase, limit, rc.b + (wave * RL + i) * 1024, lane * 16, at + rec(wave * RL + i));
 #pragma unroll
-    for (int q = 0; q < GPC; ++q) load_lds<4>(wbase, limit, rc.b + ZAT + (wave * GPC + q) * 256, zo, at + q * 128);
+    for (int i = 0; i < ZP; ++i)
+#pragma unroll
+      for (int q = 0; q < GPC; ++q)
+        load_lds<4>(wbase, limit, rc.b + ZAT + ((wave + 8 * i) * GPC + q) * 256, zo[i], at + q * 128);
   };
+
+  // of this wave's 64 rows, for the end (the waves with the same rows write the same)
+  factor[wt * 64 + lane] =
+      partial ? 1.0f : row_factor(a, tiles.bad, tl.row0 + (wt * 64 + lane < tl.cnt ? wt * 64 + lane : 0));
 
   f32x16_t tot[2][2];
 #pragma unroll
@@ -738,7 +779,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
                                 first ? z : acc[i][b]);
         }
       read_x(1 - h, u, nst);
-      if (h == 0) load_x(cl, u, lst);
+      if (h == 0 && u < XL) load_x(cl, u, lst);
       if (G == 128 ? h == 1 && u == 3 : u % (G / 16) == G / 16 - 1) {
         const int g = G == 32 ? u / 2 : 0;
 #pragma unroll
@@ -753,7 +794,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
 #pragma unroll
       for (int j = 0; j < 4; ++j) {               // the next step's expansion among this step's MFMAs
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (h == 0 && j == 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        if (h == 0 && u < XL && j == 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
       }
       __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
@@ -788,10 +829,10 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
     };
     load_rec(c0, rc0);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) load_x(c0, u, st0);
+    for (int u = 0; u < XL; ++u) load_x(c0, u, st0);
     if (RST == 3) load_rec(c0 + 1 < n ? c0 + 1 : c0, rc1);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) load_x(c0 + 1 < n ? c0 + 1 : c0, u, st1);
+    for (int u = 0; u < XL; ++u) load_x(c0 + 1 < n ? c0 + 1 : c0, u, st1);
     wait_loads<0>();
     meet();
 #pragma unroll
@@ -826,32 +867,27 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, cons
     scale_group(GH - 1);
     wait_loads<0>();                             // nothing may still write to this workgroup's LDS
   }
+  // The tile's rows of Y (or of the split columns' sums): rows past it lie past the
+  // limit, and so does the offset of a column past n (the rows are below 2^30 bytes).
+  const bool half = !partial && a.ybf16;
+  const uint32_t line = (uint32_t)a.n * (half ? 2 : 4);
+  char *to = partial ? (char *)(partial + ((int64_t)blockIdx.y * a.r + tl.row0) * a.n)
+                     : (char *)a.Y + tl.row0 * (int64_t)line;
+  uint32_t at[2];
+  int l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0));   // `lane` anew: the loop needs its registers
+  asm volatile("" : "+v"(l));
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int64_t col = (int64_t)(nb * WN + wn) * 64 + b * 32 + (l & 31);
+    at[b] = col < a.n ? (uint32_t)(wt * 64 + acc32_row(0, l)) * line + (uint32_t)col * (half ? 2 : 4) : 0x80000000u;
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
-      const int tok = wt * 64 + i * 32 + acc32_row(v, lane);
-      if (tok >= tl.cnt) continue;
-      const int64_t row = tl.row0 + tok;
-      if (partial) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int64_t col = (int64_t)(nb * WN + wn) * 64 + b * 32 + (lane & 31);
-          if (col < a.n) partial[((int64_t)blockIdx.y * a.r + row) * a.n + col] = tot[i][b][v];
-        }
-        continue;
-      }
-      bool ok = !tiles.bad;
-      if (a.rows && ok) {
-        const int32_t xr = a.rows[row];
-        ok = xr >= 0 && xr < a.xrows;
-      }
-      const float f = a.row_scale ? a.row_scale[row] : 1.0f;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int64_t col = (int64_t)(nb * WN + wn) * 64 + b * 32 + (lane & 31);
-        if (col < a.n) store_y(a, row, col, ok ? tot[i][b][v] * f : __uint_as_float(0x7fc00000u));
-      }
+      const uint32_t down = (uint32_t)(i * 32 + acc32_row(v, 0)) * line;
+      const float f = factor[wt * 64 + i * 32 + acc32_row(v, l)];
+      store_pair(to, tl.cnt * line, half, at[0] + down, at[1] + down, tot[i][0][v] * f, tot[i][1][v] * f);
     }
 }
 
@@ -863,19 +899,14 @@ __global__ __launch_bounds__(256) void q4_join_kernel(Q4Args a, const float *__r
   tiles.scan(a);
   const int64_t row = blockIdx.x;
   if (a.offsets && !tiles.bad && (row < a.offsets[0] || row >= a.offsets[a.e])) return;
-  bool ok = !tiles.bad;
-  if (a.rows && ok) {
-    const int32_t xr = a.rows[row];
-    ok = xr >= 0 && xr < a.xrows;
-  }
-  const float f = a.row_scale ? a.row_scale[row] : 1.0f;
+  const float f = row_factor(a, tiles.bad, row);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int64_t i = (int64_t)blockIdx.y * 1024 + u * 256 + threadIdx.x;
     if (i >= a.n) return;
     float v = 0.0f;
     for (int p = 0; p < parts; ++p) v += partial[(p * a.r + row) * a.n + i];
-    store_y(a, row, i, ok ? v * f : __uint_as_float(0x7fc00000u));
+    store_y(a, row, i, v * f);
   }
 }
 
@@ -979,6 +1010,19 @@ bool use_tiles(int64_t r, int64_t e, int64_t n, int64_t m) {
   return rows_per_matrix(r, e) > 64 && m > 256 && tile_count(r, n) >= 36;
 }
 
+// 64 rows of Y x 512 output rows in place of 128 x 256 (the same work) where that
+// takes fewer rounds of 256 workgroups; an expert's last tile counts as half.
+// 8 experts of 11008 x 4096 over 4096 rows, 6 rounds for 7: 472 us against 523; 64
+// of 4096 x 2048 over 8192, 5 for 6: 286 against 331; with as many rounds the two
+// are alike (8 of 4096 x 4096 over 2048: 142, 141; 8 of 4096 x 11008 over 4096: 509, 501).
+bool narrow_tiles(int64_t r, int64_t e, int64_t n) {
+  auto rounds = [&](int64_t tok, int64_t out) {
+    const int64_t tiles = e == 1 ? (r + tok - 1) / tok : (2 * r + e * tok) / (2 * tok);
+    return (tiles * ((n + out - 1) / out) + 255) / 256;
+  };
+  return rounds(64, 512) < rounds(128, 256);
+}
+
 template <bool XBF16, int G>
 hipError_t stream_pick(const Q4Args &a, hipStream_t st) {
   const int64_t nrb = q4_row_blocks(a.n), nch = q4_chunks(a.m), r4 = (nrb + 3) / 4;
@@ -996,6 +1040,7 @@ template <int G>
 hipError_t pick(const Q4Args &a, void *ws, hipStream_t st) {
   if (use_tiles(a.r, a.e, a.n, a.m)) {
     const TileWs w = tile_ws(a.xrows, a.r, a.n, a.m, G, a.xbf16);
+    if (w.parts == 1 && narrow_tiles(a.r, a.e, a.n)) return tile_go<G, 1, 8>(a, w, ws, st);
     return tile_go<G, 2, 4>(a, w, ws, st);
   }
   return a.xbf16 ? stream_pick<true, G>(a, st) : stream_pick<false, G>(a, st);

@@ -105,7 +105,13 @@ LINEAR = [
     (700, 3000, 1536, 64, "bf16", "f32"),
     (400, 2500, 2080, 32, "bf16", "bf16"),
     (385, 2309, 1152, 128, "f32", "f32"),
-    # 64 rows at a time
+    # tiles of 64 rows by 512 outputs: 255 of them for 261 of 128 by 256
+    (1088, 7300, 384, 128, "bf16", "bf16"),
+    (1085, 7200, 576, 64, "bf16", "f32"),
+    (1088, 7300, 416, 32, "bf16", "f32"),
+    (1030, 7425, 640, 128, "f32", "f32"),
+    (1088, 7171, 288, 32, "f32", "bf16"),
+    # streaming, 64 rows at a time
     (64, 25000, 128, 128, "bf16", "bf16"),
     (100, 13000, 96, 32, "f32", "f32"),
 ]
@@ -147,7 +153,7 @@ def test_q4_linear_scales_and_zeros_of_any_sign(slim):
 
 
 @pytest.mark.parametrize("t,n,m,g", [(3, 48, 256, 128), (40, 48, 96, 32), (200, 48, 256, 128), (1500, 2100, 384, 128),
-                                     (1500, 2100, 320, 64), (500, 2600, 1024, 128)])
+                                     (1500, 2100, 320, 64), (500, 2600, 1024, 128), (1088, 7300, 384, 128)])
 def test_q4_linear_nonfinite_row_stays_in_its_row(slim, t, n, m, g):
     codes, scale, zero = _layer(7, 1, n, m, g)
     X = _x(8, t, m, "bf16").to("cuda:0")
@@ -208,6 +214,12 @@ EXPERTS = [
     ([900, 333, 700], 1610, 640, 32, "bf16", "bf16", True, True, 0, 130),
     ([400, 0, 1100, 513], 1550, 288, 32, "f32", "f32", True, True, 1, 0),
     ([1000, 1000], 1540, 512, 128, "f32", "bf16", False, False, 0, 3),
+    # with tiles of 64 rows by 512 outputs
+    ([66] * 30 + [0, 132] * 17, 1000, 320, 64, "bf16", "bf16", True, True, 0, 0),
+    ([1400, 1332, 1300], 2000, 640, 32, "bf16", "bf16", False, True, 0, 0),
+    ([1, 2630, 1397], 1800, 384, 128, "bf16", "f32", True, False, 1, 3),
+    ([64, 2567, 1400], 2048, 288, 32, "f32", "f32", True, True, 1, 0),
+    ([1000, 0, 3032], 1793, 512, 128, "f32", "bf16", False, False, 0, 0),
     # with its columns split
     ([300, 0, 7, 200], 2600, 1024, 128, "bf16", "bf16", True, True, 2, 9),
     ([0, 290, 410], 2100, 1216, 64, "f32", "f32", False, True, 3, 1),
@@ -246,7 +258,8 @@ def test_q4_experts(slim, counts, n, m, g, xdt, ydt, gather, weighted, before, b
 
 
 @pytest.mark.parametrize("per,n,m,xdt", [(3, 32, 128, "bf16"), (150, 32, 128, "f32"), (700, 1600, 384, "bf16"),
-                                         (700, 1600, 384, "f32"), (200, 2600, 1024, "bf16")])
+                                         (700, 1600, 384, "f32"), (200, 2600, 1024, "bf16"),
+                                         (1344, 2000, 384, "bf16"), (1344, 2000, 384, "f32")])
 def test_q4_experts_bad_rows_and_offsets(slim, per, n, m, xdt):
     # checked by the kernels before anything is read through them
     e, g = 3, 128
