@@ -18,6 +18,8 @@
 // a wave reads one record as 64 consecutive 16-byte loads and its pairs with
 // one 8-byte load per group: a pure stream.  Rows past n and columns past m
 // are stored as zeros.
+#include <math.h>
+
 #include <type_traits>
 
 #include "common.hpp"
@@ -238,12 +240,13 @@ __device__ __forceinline__ void spread(float2 v, float2 (&o)[GPC]) {
 // ---------------------------------------------------------------- streaming kernel
 // A workgroup owns 16 R output rows of one matrix and a tile of 16 TT rows of
 // Y; its NW waves take the 128-column records in turn (wave w: w, w + NW, ...;
-// U of them at a time, whose loads are all in flight together) and their sums
+// U of them at a time, whose loads are all in flight together, or AHEAD: the next
+// one's while this one is multiplied) and their sums
 // are joined through LDS in wave order, so the result does not depend on timing.
-// Bound by the stream of records: one token through 28672 x 8192 takes 23 us
-// (132 MB, 5.7 TB/s; 28 us where other weights pass between calls), 16 tokens
+// Bound by the stream of records: one token through 28672 x 8192 takes 22.4 us
+// (132 MB, 5.9 TB/s; 28 us where other weights pass between calls), 16 tokens
 // through 13824 x 5120, g = 64, 12.0 us (45 MB, 3.7 TB/s: 216 workgroups leave 40
-// CUs idle), 1024 rows over 64 experts of 1024 x 2048, g = 64, 31 us (84 MB once;
+// CUs idle), 1024 rows over 64 experts of 1024 x 2048, g = 64, 28.5 us (84 MB once;
 // an expert with more than 16 rows is read again for each
 // 16).  Splitting the columns over the waves of a workgroup rather than over
 // workgroups keeps it one launch without partial sums in memory.
@@ -252,7 +255,7 @@ __device__ __forceinline__ void spread(float2 v, float2 (&o)[GPC]) {
 // (row 4 (l / 16) + j, output row l % 16): one lane keeps one output row, so a
 // group's scale and zero are one pair per lane.  Row a of A is token
 // 4 (a % 4) + a / 4 of its 16, which puts the first four tokens in element 0.
-template <bool XBF16, int G, int R, int TT, int NW, int U>
+template <bool XBF16, int G, int R, int TT, int NW, int U, bool AHEAD>
 __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, int nch) {
   constexpr int GPC = 128 / G, SPG = G / 32;     // groups per record, K slices per group
   constexpr int RECW = 256 + 32 * GPC;
@@ -294,12 +297,17 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
     for (int u = 0; u < TT; ++u) tot[b][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
 
-  // U records of the wave at a time, all their loads first.
-  auto records = [&](int ch0, auto count) __attribute__((always_inline)) {
+  // N records of the wave.
+  struct Regs {
+    uint4 w[U][R];
+    float2 pair[U][R];
+    uint4 x[U][TT][4][XL];
+  };
+  auto fetch = [&](int ch0, auto count, Regs &rg) __attribute__((always_inline)) {
     constexpr int N = decltype(count)::value;
-    uint4 w[N][R];
-    float2 pair[N][R];
-    uint4 x[N][TT][4][XL];
+    auto &w = rg.w;
+    auto &pair = rg.pair;
+    auto &x = rg.x;
 #pragma unroll
     for (int v = 0; v < N; ++v) {
       const int ch = ch0 + v * NW;
@@ -317,6 +325,12 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
           for (int e = 0; e < XL; ++e)
             x[v][u][i][e] = *(const uint4 *)(xp[u] + (ch * 128 + 32 * i < a.m ? (ch * 128 + 32 * i) * (2 * XL) : 0) + 16 * e);
     }
+  };
+  auto compute = [&](int ch0, auto count, const Regs &rg) __attribute__((always_inline)) {
+    constexpr int N = decltype(count)::value;
+    auto &w = rg.w;
+    auto &pair = rg.pair;
+    auto &x = rg.x;
 #pragma unroll
     for (int v = 0; v < N; ++v) {
       const int ch = ch0 + v * NW;
@@ -360,8 +374,8 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
             for (int u = 0; u < TT; ++u)
               tot[b][u][j] = fmaf(sz[b][q].x, fmaf(-sz[b][q].y, sx[u][j], acc[b][u][j]), tot[b][u][j]);
         };
-        // up to four tokens have no more than element 0 (the branch costs the other
-        // variants more than it saves: 64 experts over 1024 rows, g = 64, 34 against 31 us)
+        // up to four tokens have no more than element 0 (t = 1, 28672 x 8192: 28.1 against
+        // 28.7 us; where two records are taken at a time the branch costs more than it saves)
         add(0);
         if (TT > 1 || U > 1 || G == 32 || tl.cnt > 4) {
           add(1);
@@ -373,9 +387,38 @@ __global__ __launch_bounds__(64 * NW) void q4_stream_kernel(Q4Args a, int nrb, i
   };
   if (!tiles.bad) {
     int ch = wave;
-    for (; ch + (U - 1) * NW < nch; ch += U * NW) records(ch, std::integral_constant<int, U>());
-    if constexpr (U > 1)
-      for (; ch < nch; ch += NW) records(ch, std::integral_constant<int, 1>());
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, U> all;
+    Regs p, q;
+    if constexpr (AHEAD) {
+      if (ch < nch) {
+        fetch(ch, one, p);
+        for (;;) {
+          bool more = ch + NW < nch;
+          if (more) fetch(ch + NW, one, q);
+          __builtin_amdgcn_sched_barrier(0);     // these loads before the products
+          compute(ch, one, p);
+          if (!more) break;
+          ch += NW;
+          more = ch + NW < nch;
+          if (more) fetch(ch + NW, one, p);
+          __builtin_amdgcn_sched_barrier(0);
+          compute(ch, one, q);
+          if (!more) break;
+          ch += NW;
+        }
+      }
+    } else {
+      for (; ch + (U - 1) * NW < nch; ch += U * NW) {
+        fetch(ch, all, p);
+        compute(ch, all, p);
+      }
+      if constexpr (U > 1)
+        for (; ch < nch; ch += NW) {
+          fetch(ch, one, p);
+          compute(ch, one, p);
+        }
+    }
   }
   // part[wave][(u * 4 + j) * 4 + lg][b][r16]: token 16 u + 4 j + lg, output row 16 b + r16
 #pragma unroll
@@ -529,8 +572,8 @@ __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory");
 // 4 c + 2), and stage c + 1 is first read in slot 4 c + 3: X is read into
 // registers during the product phase before its own.
 //
-// 2048 rows through 4096 x 11008, g = 128: 177 us, 1.04 PFLOP/s of the product
-// (1.17 with the zero term), the matrix unit busy 60% of the cycles at 1.87 GHz;
+// 2048 rows through 4096 x 11008, g = 128: 173 us, 1.07 PFLOP/s of the product
+// (1.20 with the zero term), the matrix unit busy 60% of the cycles at 1.87 GHz;
 // a plain bfloat16 library product of that shape takes 151 us.  A phase takes
 // 700 to 850 cycles where its products need 512 (640 with the zero term): the
 // load phases (the scaling's 256 cycles, LDS latency) are as long as the
@@ -919,14 +962,44 @@ int64_t max_tiles(int64_t r, int64_t e, int64_t tok) {
   return most > whole ? most : whole;
 }
 
-template <bool XBF16, int G, int R, int TT, int NW, int U>
+template <bool XBF16, int G, int R, int TT, int NW, int U, bool AHEAD>
 hipError_t stream_go(const Q4Args &a, hipStream_t st) {
   const int nrb = (int)q4_row_blocks(a.n), nch = (int)q4_chunks(a.m);
   const int64_t tiles = max_tiles(a.r, a.offsets ? a.e : 1, 16 * TT);
   const int64_t gz = (tiles + 65534) / 65535, gy = (tiles + gz - 1) / gz;   // grid limits of 65535
-  q4_stream_kernel<XBF16, G, R, TT, NW, U>
+  q4_stream_kernel<XBF16, G, R, TT, NW, U, AHEAD>
       <<<dim3((nrb + R - 1) / R, (uint32_t)gy, (uint32_t)gz), 64 * NW, 0, st>>>(a, nrb, nch);
   return hipGetLastError();
+}
+
+// Row tiles to expect: the bounds are on the device, so an expert's last tile
+// counts as half, with one standard deviation of their sum (e / 12 is its variance)
+// so that a round filled to the last workgroup counts as two; an expert that may
+// have rows has one tile at least.
+double likely_tiles(int64_t r, int64_t e, int64_t tok) {
+  if (e == 1) return (double)((r + tok - 1) / tok);
+  const double some = (double)(e < r ? e : r), t = (double)r / tok + some / 2 + 0.3 * sqrt(some);
+  return t > some ? t : some;
+}
+// Workgroups of the tile kernel with tiles of tok rows and out outputs.
+int64_t likely_blocks(int64_t r, int64_t e, int64_t n, int64_t tok, int64_t out) {
+  return (int64_t)ceil(likely_tiles(r, e, tok) * (double)((n + out - 1) / out));
+}
+// 64 rows of Y x 512 output rows in place of 128 x 256 (the same work) where that
+// takes fewer rounds of 256 workgroups.
+// 8 experts of 11008 x 4096 over 4096 rows, 6 rounds for 7: 472 us against 523; 64
+// of 4096 x 2048 over 8192, 5 for 6: 286 against 331; with as many rounds the two
+// are alike (8 of 4096 x 4096 over 2048: 142, 141; 8 of 4096 x 11008 over 4096: 509, 501).
+bool narrow_tiles(int64_t r, int64_t e, int64_t n) {
+  return (likely_blocks(r, e, n, 64, 512) + 255) / 256 < (likely_blocks(r, e, n, 128, 256) + 255) / 256;
+}
+// Workgroups over which the columns are split, four records at least to each and
+// all of them in one round.
+int column_parts(int64_t r, int64_t e, int64_t n, int64_t m) {
+  const int64_t blocks = narrow_tiles(r, e, n) ? likely_blocks(r, e, n, 64, 512) : likely_blocks(r, e, n, 128, 256);
+  const int64_t most = q4_chunks(m) / 4 < 4 ? q4_chunks(m) / 4 : 4;
+  const int64_t parts = 256 / blocks < most ? 256 / blocks : most;
+  return parts < 1 ? 1 : (int)parts;
 }
 
 // Workspace of the tile kernel: group sums, then what of X it cannot read in
@@ -934,7 +1007,7 @@ hipError_t stream_go(const Q4Args &a, hipStream_t st) {
 // gathered rows (compact): the planes of float32 X, or a copy of bfloat16 X
 // whose rows do not end with a record or may lie more than 32-bit offsets apart.
 // With fewer workgroups than CUs the columns are split over up to four, whose
-// sums follow: t = 500, 5000 x 4096 (80 workgroups): 46 us, unsplit 70; t = 1024,
+// sums follow: t = 500, 5000 x 4096 (80 workgroups): 44 us, unsplit 70; t = 1024,
 // 4096 x 4096 (128 workgroups, halves): 55 us.
 struct TileWs {
   bool compact, copy;
@@ -942,8 +1015,7 @@ struct TileWs {
   int64_t nrow;
   size_t planes, partial, bytes;
 };
-int64_t tile_count(int64_t r, int64_t n) { return (r + 127) / 128 * ((n + 255) / 256); }
-TileWs tile_ws(int64_t xrows, int64_t r, int64_t n, int64_t m, int group, bool xbf16) {
+TileWs tile_ws(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16) {
   TileWs w;
   const size_t nch = (size_t)q4_chunks(m);
   const bool far = (uint64_t)xrows * (xbf16 ? 2 * (uint64_t)m : 768 * (uint64_t)nch) >= 0xfff00000ull;
@@ -953,9 +1025,7 @@ TileWs tile_ws(int64_t xrows, int64_t r, int64_t n, int64_t m, int group, bool x
   w.nrow = w.compact ? r : xrows;
   w.planes = ((size_t)w.nrow * nch * (128 / group) * 4 + 15) / 16 * 16;
   w.partial = w.planes + (!xbf16 ? (size_t)w.nrow * 3 * nch * 256 : w.copy ? (size_t)w.nrow * nch * 256 : 0);
-  const int64_t most = (int64_t)nch / 4 < 4 ? (int64_t)nch / 4 : 4;     // four records at least to a part
-  const int64_t parts = 256 / tile_count(r, n) < most ? 256 / tile_count(r, n) : most;
-  w.parts = parts < 1 ? 1 : (int)parts;
+  w.parts = column_parts(r, e, n, m);
   w.bytes = w.partial + (w.parts > 1 ? (size_t)w.parts * r * n * 4 : 0);
   return w;
 }
@@ -988,59 +1058,67 @@ hipError_t tile_go(const Q4Args &a, const TileWs &w, void *ws, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Which kernel, by what fills the 256 CUs (the experts' bounds are on the
-// device, so their rows count by the average).  Measured, us:
-//  - tile kernel against streaming: t = 2048, 4096 x 11008: 188 against 737; t =
-//    500, 5000 x 4096 (its columns split, see tile_ws): 46 against 72; at t = 256,
-//    4096 x 4096 its 32 tiles are too few either way: 38 against 27.
-//    With one or two records to a row its start (the group sums, three stages
-//    of loads) outweighs them: three experts of 5346 x 128 over 602 rows: 26
-//    against 22; t = 2000, 4096 x 512 the other way: 28 against 38.
-//  - 64 rows at a time against 16 (large n only: fewer workgroups): t = 64, 28672
-//    x 8192: 86 against 99; t = 256, 4096 x 4096: 28 against 27.
+// Which kernel.  Where there are plainly enough rows and outputs the tile kernel
+// (t = 2048, 4096 x 11008: 184 us against 737 streaming; with one or two records to
+// a row its start outweighs them: three experts of 5346 x 128 over 602 rows: 26
+// against 22, t = 2000, 4096 x 512 the other way: 28 against 38), elsewhere the
+// shorter of two estimates in us, fitted to measurements: a stage of 128 columns
+// takes a round of tiles 1.9 (float32 X, three planes: 5.3), and 5300 (2900)
+// records are multiplied by 16 rows in one us.  bfloat16, g = 128, tiles against
+// streaming: 8 experts of 11008 x 4096 over 192 rows 69 - 70, over 256 68 - 90, over
+// 384 73 - 111; 64 of 1024 x 2048 over 3840 rows 51 - 63; 16 of 4096 x 4096 over 512
+// rows 74 - 64 (streamed); t = 64, 28672 x 8192 71 - 82; t = 64, 13824 x 5120 34 - 29
+// (streamed); t = 256, 4096 x 4096 31 - 24 (streamed), 4096 x 11008 48 - 54.
+int64_t rows_per_matrix(int64_t r, int64_t e) { return (r + e - 1) / e; }
+bool use_tiles(int64_t r, int64_t e, int64_t n, int64_t m, bool xbf16) {
+  const int64_t nch = q4_chunks(m), blocks = (r + 127) / 128 * ((n + 255) / 256);
+  if (rows_per_matrix(r, e) > 64 && m > 256 && blocks >= 36) return true;
+  const bool narrow = narrow_tiles(r, e, n);
+  const int64_t parts = column_parts(r, e, n, m);
+  const int64_t rounds = (likely_blocks(r, e, n, narrow ? 64 : 128, narrow ? 512 : 256) * parts + 255) / 256;
+  const double stages = (double)(rounds * ((nch + parts - 1) / parts));
+  const double tile = 10.0 + stages * (xbf16 ? 1.9 : 5.3) + (parts > 1 ? 4.0 + (double)(parts * r) * n * 1.6e-6 : 0.0);
+  const double stream = 3.0 + likely_tiles(r, e, 16) * q4_row_blocks(n) * nch / (xbf16 ? 5300.0 : 2900.0);
+  return tile < stream;
+}
+
+// Shape of the streaming kernel, by what fills the 256 CUs.  Measured, us:
+//  - 32 rows at a time, bfloat16 only (float32 has not the registers: t = 64, 28672
+//    x 8192: 172 against 150 with 16): t = 24, 28672 x 8192: 44.7 against 54; t = 64: 82
+//    against 90; t = 256, 4096 x 4096: 23.6 against 25.5; with 128 workgroups (t = 64,
+//    4096 x 4096) 13.7 against 9.4 with two row blocks.  An expert's second half tile
+//    is mostly empty: 64 of 1024 x 2048 over 2048 rows 42.7 against 40, 8 of 11008 x
+//    4096 over 384 110 against 113.
 //  - 4, 2 or 1 row blocks a workgroup (X is read once for all of them): t = 16,
 //    13824 x 5120: 15.4, 17.4, 25; t = 32, 4096 x 4096: 9.7, 8.0, 11.2; t = 1,
 //    4096 x 4096: 8.5, 5.2, 4.7.
-//  - 4 waves instead of 8 where a row has few records: 64 experts of 1024 x
-//    2048, 1024 rows: 34 against 38; 13824 x 5120: 16.9 against 15.8.  16 where
-//    a workgroup has a CU to itself: t = 16, 13824 x 5120 (216 workgroups): 13.9
-//    against 15.8; t = 1, 28672 x 8192 (448): 31.7 against 30.1.
-int64_t rows_per_matrix(int64_t r, int64_t e) { return (r + e - 1) / e; }
-bool use_tiles(int64_t r, int64_t e, int64_t n, int64_t m) {
-  return rows_per_matrix(r, e) > 64 && m > 256 && tile_count(r, n) >= 36;
-}
-
-// 64 rows of Y x 512 output rows in place of 128 x 256 (the same work) where that
-// takes fewer rounds of 256 workgroups; an expert's last tile counts as half.
-// 8 experts of 11008 x 4096 over 4096 rows, 6 rounds for 7: 472 us against 523; 64
-// of 4096 x 2048 over 8192, 5 for 6: 286 against 331; with as many rounds the two
-// are alike (8 of 4096 x 4096 over 2048: 142, 141; 8 of 4096 x 11008 over 4096: 509, 501).
-bool narrow_tiles(int64_t r, int64_t e, int64_t n) {
-  auto rounds = [&](int64_t tok, int64_t out) {
-    const int64_t tiles = e == 1 ? (r + tok - 1) / tok : (2 * r + e * tok) / (2 * tok);
-    return (tiles * ((n + out - 1) / out) + 255) / 256;
-  };
-  return rounds(64, 512) < rounds(128, 256);
-}
-
+//  - 4 waves that load a record ahead; against 8 waves: t = 1, 28672 x 8192, 28.1
+//    against 29.5 (g = 32: 39 - 44; float32, 16 rows, g = 32: 61 - 73); against 4 waves
+//    with two records at a time: 64 experts of 1024 x 2048, 1024 rows: 27 - 29.
+//    (float32, t = 256, 4096 x 4096 loses: 45 - 41.)
+//  - 16 waves where a workgroup has a CU to itself: t = 16, 13824 x 5120 (216
+//    workgroups): 11.7 against 14.5 with 4 a record ahead; t = 1, 28672 x 8192 (448):
+//    31.7 against 28.1.
 template <bool XBF16, int G>
 hipError_t stream_pick(const Q4Args &a, hipStream_t st) {
   const int64_t nrb = q4_row_blocks(a.n), nch = q4_chunks(a.m), r4 = (nrb + 3) / 4;
-  if (rows_per_matrix(a.r, a.e) >= 48 && r4 * ((a.r + 63) / 64) >= 384) return stream_go<XBF16, G, 4, 4, 4, 1>(a, st);
+  if constexpr (XBF16)
+    if (rows_per_matrix(a.r, a.e) > (a.e == 1 ? 16 : 40) && r4 * ((a.r + 31) / 32) >= 192)
+      return stream_go<XBF16, G, 4, 2, 4, 1, true>(a, st);
   const int64_t tiles = max_tiles(a.r, a.e, 16);
   if (r4 * tiles >= 192) {
-    if (nch <= 16) return stream_go<XBF16, G, 4, 1, 4, 2>(a, st);
-    return r4 * tiles < 320 ? stream_go<XBF16, G, 4, 1, 16, 1>(a, st) : stream_go<XBF16, G, 4, 1, 8, 1>(a, st);
+    if (nch > 16 && r4 * tiles < 320) return stream_go<XBF16, G, 4, 1, 16, 1, false>(a, st);
+    return stream_go<XBF16, G, 4, 1, 4, 1, true>(a, st);
   }
-  if ((nrb + 1) / 2 * tiles >= 144) return stream_go<XBF16, G, 2, 1, 8, 2>(a, st);
-  return stream_go<XBF16, G, 1, 1, 8, 2>(a, st);
+  if ((nrb + 1) / 2 * tiles >= 144) return stream_go<XBF16, G, 2, 1, 8, 2, false>(a, st);
+  return stream_go<XBF16, G, 1, 1, 8, 2, false>(a, st);
 }
 
 template <int G>
 hipError_t pick(const Q4Args &a, void *ws, hipStream_t st) {
-  if (use_tiles(a.r, a.e, a.n, a.m)) {
-    const TileWs w = tile_ws(a.xrows, a.r, a.n, a.m, G, a.xbf16);
-    if (w.parts == 1 && narrow_tiles(a.r, a.e, a.n)) return tile_go<G, 1, 8>(a, w, ws, st);
+  if (use_tiles(a.r, a.e, a.n, a.m, a.xbf16)) {
+    const TileWs w = tile_ws(a.xrows, a.r, a.e, a.n, a.m, G, a.xbf16);
+    if (narrow_tiles(a.r, a.e, a.n)) return tile_go<G, 1, 8>(a, w, ws, st);
     return tile_go<G, 2, 4>(a, w, ws, st);
   }
   return a.xbf16 ? stream_pick<true, G>(a, st) : stream_pick<false, G>(a, st);
@@ -1057,7 +1135,7 @@ hipError_t launch_pack4(const uint8_t *codes, const float *scale, const float *z
 }
 
 size_t q4_ws_bytes(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16) {
-  return use_tiles(r, e, n, m) ? tile_ws(xrows, r, n, m, group, xbf16).bytes : 0;
+  return r > 0 && use_tiles(r, e, n, m, xbf16) ? tile_ws(xrows, r, e, n, m, group, xbf16).bytes : 0;
 }
 
 hipError_t launch_q4(const Q4Args &a, void *ws, hipStream_t st) {

@@ -111,7 +111,16 @@ LINEAR = [
     (1088, 7300, 416, 32, "bf16", "f32"),
     (1030, 7425, 640, 128, "f32", "f32"),
     (1088, 7171, 288, 32, "f32", "bf16"),
-    # streaming, 64 rows at a time
+    # few rows of a long and wide matrix, in tiles with the columns split, and streamed
+    (64, 7000, 8192, 128, "bf16", "bf16"),
+    (30, 6200, 384, 128, "bf16", "f32"),
+    (33, 12300, 640, 64, "bf16", "bf16"),
+    (5, 20500, 1408, 32, "bf16", "f32"),
+    (40, 12400, 416, 32, "bf16", "f32"),
+    (18, 10300, 1184, 32, "f32", "bf16"),
+    (1, 20480, 2176, 128, "bf16", "f32"),
+    (1, 13000, 2304, 64, "f32", "f32"),
+    # streaming, 32 rows at a time
     (64, 25000, 128, 128, "bf16", "bf16"),
     (100, 13000, 96, 32, "f32", "f32"),
 ]
@@ -220,6 +229,14 @@ EXPERTS = [
     ([1, 2630, 1397], 1800, 384, 128, "bf16", "f32", True, False, 1, 3),
     ([64, 2567, 1400], 2048, 288, 32, "f32", "f32", True, True, 1, 0),
     ([1000, 0, 3032], 1793, 512, 128, "f32", "bf16", False, False, 0, 0),
+    ([1600, 1500, 2200], 1450, 384, 128, "bf16", "f32", True, True, 0, 0),
+    ([2100, 1, 3199], 1400, 352, 32, "bf16", "bf16", False, True, 0, 0),
+    ([5000, 150, 147], 1500, 320, 64, "f32", "bf16", True, False, 1, 2),
+    ([1750, 1850, 1700], 1290, 288, 32, "f32", "f32", False, False, 0, 0),
+    # experts of some 50 rows, streamed 32 rows at a time, and of some 40, long enough for tiles
+    ([50, 0, 90, 33, 64, 45, 61, 57], 1100, 256, 64, "bf16", "bf16", True, True, 0, 0),
+    ([40, 64, 0, 65, 3, 30, 70, 48], 5700, 2048, 128, "bf16", "bf16", True, True, 0, 0),
+    ([41, 0, 20, 77], 4200, 2112, 64, "bf16", "f32", False, False, 0, 1),
     # with its columns split
     ([300, 0, 7, 200], 2600, 1024, 128, "bf16", "bf16", True, True, 2, 9),
     ([0, 290, 410], 2100, 1216, 64, "f32", "f32", False, True, 3, 1),
@@ -259,7 +276,8 @@ def test_q4_experts(slim, counts, n, m, g, xdt, ydt, gather, weighted, before, b
 
 @pytest.mark.parametrize("per,n,m,xdt", [(3, 32, 128, "bf16"), (150, 32, 128, "f32"), (700, 1600, 384, "bf16"),
                                          (700, 1600, 384, "f32"), (200, 2600, 1024, "bf16"),
-                                         (1344, 2000, 384, "bf16"), (1344, 2000, 384, "f32")])
+                                         (1344, 2000, 384, "bf16"), (1344, 2000, 384, "f32"),
+                                         (1768, 1400, 384, "bf16"), (1768, 1400, 384, "f32")])
 def test_q4_experts_bad_rows_and_offsets(slim, per, n, m, xdt):
     # checked by the kernels before anything is read through them
     e, g = 3, 128
