@@ -1058,27 +1058,29 @@ hipError_t tile_go(const Q4Args &a, const TileWs &w, void *ws, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Which kernel.  Where there are plainly enough rows and outputs the tile kernel
-// (t = 2048, 4096 x 11008: 184 us against 737 streaming; with one or two records to
-// a row its start outweighs them: three experts of 5346 x 128 over 602 rows: 26
-// against 22, t = 2000, 4096 x 512 the other way: 28 against 38), elsewhere the
-// shorter of two estimates in us, fitted to measurements: a stage of 128 columns
-// takes a round of tiles 1.9 (float32 X, three planes: 5.3), and 5300 (2900)
-// records are multiplied by 16 rows in one us.  bfloat16, g = 128, tiles against
-// streaming: 8 experts of 11008 x 4096 over 192 rows 69 - 70, over 256 68 - 90, over
-// 384 73 - 111; 64 of 1024 x 2048 over 3840 rows 51 - 63; 16 of 4096 x 4096 over 512
-// rows 74 - 64 (streamed); t = 64, 28672 x 8192 71 - 82; t = 64, 13824 x 5120 34 - 29
-// (streamed); t = 256, 4096 x 4096 31 - 24 (streamed), 4096 x 11008 48 - 54.
+// Which kernel: the shorter of two estimates in us, fitted to measurements (g = 64
+// and 128; both are slower alike at 32).  Tiles: 9.5 for the group sums, the first
+// loads and the stores, 1.85 for a stage of 128 columns in a round (float32 X, three
+// planes: 5.3), and where columns are split 4 and the traffic of the partial sums.
+// Streaming: 8, and 6600 (float32 3200) records by 16 rows in one us, the sums' join
+// and stores counting as two records.  Measured, tiles - streaming:
+//  - t = 2048, 4096 x 11008: 184 - 737; 1537, 2100 x 384: 14 - 17; 1000, 4096 x 2048: 38 -
+//    44; 500, 2600 x 1024: 24 - 14; 256, 4096 x 4096: 31 - 24; 256, 4096 x 11008: 48 - 54;
+//    130, 4747 x 1088: 25 - 12; 64, 28672 x 8192: 71 - 82; 64, 13824 x 5120: 34 - 29;
+//    float32: 1030, 7425 x 640: 42 - 91; 385, 2309 x 1152: 37 - 20.
+//  - 8 experts of 11008 x 4096 over 192 rows 69 - 70, over 256 68 - 90, over 384 73 -
+//    111; 64 of 1024 x 2048 over 3840 rows 51 - 63; 16 of 4096 x 4096 over 512 rows 74 -
+//    64; 18 of 391 x 1152 over 2222 rows 29 - 21.
 int64_t rows_per_matrix(int64_t r, int64_t e) { return (r + e - 1) / e; }
 bool use_tiles(int64_t r, int64_t e, int64_t n, int64_t m, bool xbf16) {
-  const int64_t nch = q4_chunks(m), blocks = (r + 127) / 128 * ((n + 255) / 256);
-  if (rows_per_matrix(r, e) > 64 && m > 256 && blocks >= 36) return true;
+  const int64_t nch = q4_chunks(m);
   const bool narrow = narrow_tiles(r, e, n);
   const int64_t parts = column_parts(r, e, n, m);
   const int64_t rounds = (likely_blocks(r, e, n, narrow ? 64 : 128, narrow ? 512 : 256) * parts + 255) / 256;
   const double stages = (double)(rounds * ((nch + parts - 1) / parts));
-  const double tile = 10.0 + stages * (xbf16 ? 1.9 : 5.3) + (parts > 1 ? 4.0 + (double)(parts * r) * n * 1.6e-6 : 0.0);
-  const double stream = 3.0 + likely_tiles(r, e, 16) * q4_row_blocks(n) * nch / (xbf16 ? 5300.0 : 2900.0);
+  const double tile = 9.5 + stages * (xbf16 ? 1.85 : 5.3) + (parts > 1 ? 4.0 + (double)(parts * r) * n * 1.6e-6 : 0.0);
+  const double records = likely_tiles(r, e, 16) * (double)(q4_row_blocks(n) * (nch + 2));
+  const double stream = 8.0 + records / (xbf16 ? 6600.0 : 3200.0);
   return tile < stream;
 }
 

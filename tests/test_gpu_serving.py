@@ -111,6 +111,18 @@ LINEAR = [
     (1088, 7300, 416, 32, "bf16", "f32"),
     (1030, 7425, 640, 128, "f32", "f32"),
     (1088, 7171, 288, 32, "f32", "bf16"),
+    # one and two stages
+    (2000, 2100, 128, 128, "bf16", "bf16"),
+    (2000, 2100, 96, 32, "f32", "f32"),
+    (1900, 2300, 256, 64, "bf16", "f32"),
+    (1700, 2200, 192, 64, "bf16", "bf16"),
+    (1600, 7000, 160, 32, "bf16", "bf16"),
+    # columns split over two, three and four workgroups
+    (1000, 4096, 2048, 128, "bf16", "bf16"),
+    (600, 4000, 4128, 32, "bf16", "f32"),
+    (640, 2400, 6080, 64, "bf16", "bf16"),
+    (640, 2411, 6144, 128, "bf16", "f32"),
+    (484, 4873, 1920, 128, "f32", "f32"),
     # few rows of a long and wide matrix, in tiles with the columns split, and streamed
     (64, 7000, 8192, 128, "bf16", "bf16"),
     (30, 6200, 384, 128, "bf16", "f32"),
@@ -162,7 +174,8 @@ def test_q4_linear_scales_and_zeros_of_any_sign(slim):
 
 
 @pytest.mark.parametrize("t,n,m,g", [(3, 48, 256, 128), (40, 48, 96, 32), (200, 48, 256, 128), (1500, 2100, 384, 128),
-                                     (1500, 2100, 320, 64), (500, 2600, 1024, 128), (1088, 7300, 384, 128)])
+                                     (1500, 2100, 320, 64), (500, 2600, 1024, 128), (1088, 7300, 384, 128),
+                                     (640, 2400, 6144, 128)])
 def test_q4_linear_nonfinite_row_stays_in_its_row(slim, t, n, m, g):
     codes, scale, zero = _layer(7, 1, n, m, g)
     X = _x(8, t, m, "bf16").to("cuda:0")
@@ -240,6 +253,8 @@ EXPERTS = [
     # with its columns split
     ([300, 0, 7, 200], 2600, 1024, 128, "bf16", "bf16", True, True, 2, 9),
     ([0, 290, 410], 2100, 1216, 64, "f32", "f32", False, True, 3, 1),
+    ([300, 0, 7, 200], 4100, 6144, 128, "bf16", "bf16", True, True, 2, 9),
+    ([0, 380, 380], 4000, 4160, 64, "f32", "f32", False, True, 3, 1),
 ]
 
 
@@ -277,7 +292,8 @@ def test_q4_experts(slim, counts, n, m, g, xdt, ydt, gather, weighted, before, b
 @pytest.mark.parametrize("per,n,m,xdt", [(3, 32, 128, "bf16"), (150, 32, 128, "f32"), (700, 1600, 384, "bf16"),
                                          (700, 1600, 384, "f32"), (200, 2600, 1024, "bf16"),
                                          (1344, 2000, 384, "bf16"), (1344, 2000, 384, "f32"),
-                                         (1768, 1400, 384, "bf16"), (1768, 1400, 384, "f32")])
+                                         (1768, 1400, 384, "bf16"), (1768, 1400, 384, "f32"),
+                                         (200, 4100, 6144, "bf16")])
 def test_q4_experts_bad_rows_and_offsets(slim, per, n, m, xdt):
     # checked by the kernels before anything is read through them
     e, g = 3, 128
@@ -303,7 +319,9 @@ def test_q4_experts_bad_rows_and_offsets(slim, per, n, m, xdt):
 
 @pytest.mark.parametrize("tx,n,m,g,xdt", [(5000, 1600, 384, 128, "bf16"), (3000, 1700, 320, 64, "bf16"),
                                           (2500, 1600, 288, 32, "f32"), (3000, 2600, 1024, 128, "f32"),
-                                          (900, 40, 96, 32, "bf16")])
+                                          (900, 40, 96, 32, "bf16"), (5000, 9000, 384, 128, "bf16"),
+                                          (3000, 9000, 320, 64, "bf16"), (2500, 9000, 288, 32, "f32"),
+                                          (3000, 4000, 4096, 128, "f32")])
 def test_q4_experts_gather_of_few_rows(slim, tx, n, m, g, xdt):
     # X has more rows than are asked for, some of them twice
     e, counts = 2, [400, 300]
