@@ -175,3 +175,20 @@ def test_layer_paths(L):
     raises(L, lambda: slim.score_tokens(_bf(3, 128), ids, _i(288), 16, 128), "ids")
     raises(L, lambda: slim.score_tokens(_bf(4, 128), ids, _i(288), 16, 128, block=0), "block")
     raises(L, lambda: slim.score_tokens(_bf(4, 128), ids, _i(287), 16, 128), "packed")
+
+
+def test_workspace_sizes_of_extreme_shapes(lib):
+    # no rows, one row, the most rows, experts and outputs: sizes that fit what they describe
+    assert lib.slim_q4_linear_workspace(0, 4096, 4096, 128, 1) == 0
+    assert lib.slim_q4_experts_workspace(0, 0, 8, 4096, 4096, 128, 1) == 0
+    assert lib.slim_q4_experts_workspace(5, 0, 1024, 1 << 20, 65536, 32, 0) == 0
+    for xdt in (0, 1):
+        assert lib.slim_q4_linear_workspace(1, 1, 32, 32, xdt) == 0
+        assert lib.slim_q4_experts_workspace(1, 1, 1024, 1, 32, 32, xdt) == 0
+        for e in (1, 7, 1024):
+            for tx, r in ((1, 1), (1 << 20, 1), (1, 1 << 20), (1 << 20, 1 << 20)):
+                for n in (1, 1 << 20):
+                    need = lib.slim_q4_experts_workspace(tx, r, e, n, 65536, 32, xdt)
+                    rows = min(tx, r)
+                    assert need == 0 or need >= rows * (65536 // 32) * 4
+                    assert need < 1 << 48
