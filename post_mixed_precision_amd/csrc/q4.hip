@@ -1018,10 +1018,13 @@ struct TileWs {
 TileWs tile_ws(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16) {
   TileWs w;
   const size_t nch = (size_t)q4_chunks(m);
-  const bool far = (uint64_t)xrows * (xbf16 ? 2 * (uint64_t)m : 768 * (uint64_t)nch) >= 0xfff00000ull;
+  // bytes of a row as the kernel reads it: in place, of the padded copy or of the planes
+  const bool padded = m % 128 != 0;
+  const uint64_t row = !xbf16 ? 768 * (uint64_t)nch : padded ? 256 * (uint64_t)nch : 2 * (uint64_t)m;
+  const bool far = (uint64_t)xrows * row >= 0xfff00000ull;
   // a gather is known only by r != xrows here; far X is always taken row by row
   w.compact = r < xrows || far;
-  w.copy = xbf16 && (far || m % 128 != 0);
+  w.copy = xbf16 && (far || padded);
   w.nrow = w.compact ? r : xrows;
   w.planes = ((size_t)w.nrow * nch * (128 / group) * 4 + 15) / 16 * 16;
   w.partial = w.planes + (!xbf16 ? (size_t)w.nrow * 3 * nch * 256 : w.copy ? (size_t)w.nrow * nch * 256 : 0);

@@ -361,6 +361,35 @@ def test_q4_experts_gather_over_4_gib(slim):
     torch.testing.assert_close(Y, one, rtol=1e-4, atol=1e-3)
 
 
+@pytest.mark.parametrize("tx,n,m,g", [(32768, 256, 65504, 32), (520000, 200, 4128, 32)])
+def test_q4_experts_gather_with_a_copy_over_4_gib(slim, tx, n, m, g):
+    # X itself is within a 32-bit offset, its copy with rows padded to whole records is not
+    print(f"q4_experts gather tx=r={tx} n={n} m={m} g={g}", flush=True)
+    nch = -(-m // 128)
+    assert 2 * m * tx < 0xfff00000 < 1 << 32 <= 256 * nch * tx
+    lib = slim.load_library()
+    assert lib.slim_q4_experts_workspace(tx, tx, 2, n, m, g, 1) >= 256 * nch * tx    # the tile kernel, with the copy
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(81)
+    X = torch.randn((tx, m), generator=gen, device="cuda:0", dtype=torch.bfloat16)
+    codes, scale, zero = _layer(82, 2, n, m, g)
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    rows = torch.randperm(tx, generator=gen, device="cuda:0").to(torch.int32)
+    wrap = min((1 << 32) // (256 * nch), tx - 1)             # rows on both sides of where an offset would wrap
+    rows[:5] = torch.tensor([0, 1, tx - 1, wrap - 1, wrap], device="cuda:0")
+    cut = tx // 2 + 3
+    Y = slim.q4_experts(X, torch.tensor([0, cut, tx], dtype=torch.int32, device="cuda:0"), packed, n, g, rows=rows)
+    at = torch.cat([torch.arange(24), torch.arange(cut - 4, cut + 4), torch.arange(tx - 24, tx)]).to("cuda:0")
+    x = X[rows[at].long()].double().cpu().numpy()
+    y, at = Y[at].double().cpu().numpy(), at.cpu().numpy()
+    for j in range(2):
+        mine = (at >= cut) == (j == 1)
+        exact = x[mine] @ oracle.q4_weight(codes[j], scale[j], zero[j], g).T
+        bound = _bound(x[mine], codes[j], scale[j], zero[j], g, "bf16", "f32", exact)
+        err = np.abs(y[mine] - exact)
+        assert np.all(err <= bound), float(np.max(err / bound))
+
+
 def test_q4_experts_matches_single_layers(slim):
     e, n, m, g = 4, 160, 512, 128
     codes, scale, zero = _layer(14, e, n, m, g)

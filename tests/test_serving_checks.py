@@ -192,3 +192,39 @@ def test_workspace_sizes_of_extreme_shapes(lib):
                     rows = min(tx, r)
                     assert need == 0 or need >= rows * (65536 // 32) * 4
                     assert need < 1 << 48
+
+
+# ------------------------------------------------------------------ how far X reaches
+# The tile kernel reads gathered rows by 32-bit offsets from X's first row, or, where they would
+# not reach the last row, from a copy of the gathered rows in their order (compact).  What it
+# reads is a row of m bfloat16 values in place, of whole records where m does not end with one
+# (then always a copy), or of three bfloat16 planes.
+REACH = 0xfff00000
+
+
+def _up(v, k):
+    return -(-v // k)
+
+
+def _row_bytes(m, xdt):
+    return 768 * _up(m, 128) if xdt == 0 else 2 * m if m % 128 == 0 else 256 * _up(m, 128)
+
+
+def _tile_bytes(nrow, m, g, xdt, copy):
+    sums = _up(nrow * _up(m, 128) * (128 // g) * 4, 16) * 16
+    return sums + (nrow * 256 * _up(m, 128) * (3 if xdt == 0 else 1) if copy else 0)
+
+
+@pytest.mark.parametrize("m,g,xdt", [(4128, 32, 1), (2112, 64, 1), (65504, 32, 1), (4096, 128, 1), (8192, 32, 1),
+                                     (4096, 128, 0), (2016, 32, 0), (65536, 64, 0)])
+def test_gather_workspace_around_32_bit_reach(lib, m, g, xdt):
+    # more rows of Y than X has, so that the size tells a compact workspace (r rows) from X's own tx rows
+    r, e, n = 1 << 20, 8, 1024
+    last = (REACH - 1) // _row_bytes(m, xdt)             # the most rows of X within reach
+    assert last < r
+    for tx in (last - 1, last, last + 1, last + 2, (1 << 32) // _row_bytes(m, xdt)):
+        near = tx * _row_bytes(m, xdt) < REACH
+        assert near == (tx <= last)
+        need = lib.slim_q4_experts_workspace(tx, r, e, n, m, g, xdt)
+        copy = xdt == 0 or m % 128 != 0 or not near
+        assert need == _tile_bytes(tx if near else r, m, g, xdt, copy), (tx, need)
