@@ -424,7 +424,9 @@ __global__ __launch_bounds__(64 * LP_WAVES) void logprob_kernel(const void *__re
     fetch(j, cur);
     while (j - lane < v1) {
       fetch(j + LP_UN * STEP, nxt);
-      if (top) shared = *(volatile uint32_t *)&s_thr;
+      // one value for all lanes, whatever other waves do to it meanwhile: it decides
+      // branches around the lane exchanges
+      if (top) shared = __builtin_amdgcn_readfirstlane(*(volatile uint32_t *)&s_thr);
       batch();
       j += LP_UN * STEP;
 #pragma unroll

@@ -510,6 +510,29 @@ def test_token_logprobs_large_logits(slim):
     _check_lp(got, x.double().numpy(), ids, 2)
 
 
+@pytest.mark.parametrize("t,v,dt,top", [(7, 60000, "f32", 20), (5, 30000, "bf16", 64), (300, 26000, "f32", 5),
+                                        (80, 70000, "bf16", 20)])
+def test_token_logprobs_thresholds_that_keep_moving(slim, t, v, dt, top):
+    # rows in which every wave finds better entries again and again, at its own time
+    print(f"token_logprobs t={t} v={v} {dt} top={top}", flush=True)
+    j = torch.arange(v, dtype=torch.float64)
+    rng = np.random.default_rng(v)
+    kinds = [j / v * 9,                                  # rising: the last entries win
+             -j / v * 9,                                 # falling: the first do
+             (j % 1024) / 100 + j / v,                   # a saw that rises
+             torch.floor(j / v * 40),                    # steps of ties
+             (j // 1024 % 4 * 7 + j % 1024 / 200) + j / v,   # one wave after another ahead
+             torch.from_numpy(3 * rng.standard_normal(v))]
+    x = torch.stack([kinds[a % len(kinds)] for a in range(t)]).to(DT[dt])
+    ids = rng.integers(0, v, size=t)
+    got = slim.token_logprobs(x.to("cuda:0"), _gpu(ids), top=top)
+    n = min(t, 2 * len(kinds))                           # rows of a kind are alike: the oracle sorts some
+    _check_lp({k: a[:n] for k, a in got.items()}, x[:n].double().numpy(), ids[:n], top)
+    for a in range(len(kinds), t):
+        assert torch.equal(got["top_id"][a], got["top_id"][a % len(kinds)]), a
+        assert torch.equal(got["top_logprob"][a], got["top_logprob"][a % len(kinds)]), a
+
+
 def test_token_logprobs_no_rows(slim):
     got = slim.token_logprobs(torch.empty((0, 10), device="cuda:0"), torch.empty(0, dtype=torch.int64, device="cuda:0"),
                               top=2)
