@@ -460,7 +460,8 @@ int slim_q4_linear(const void *X, int xdt, int64_t t, int64_t m, const uint32_t 
  * host.  Offsets that decrease or leave 0 .. r make every row of Y NaN, and a
  * row whose rows[a] is outside 0 .. tx - 1 is NaN (neither reads out of range).
  * Numerics as for slim_q4_linear.  1 <= e <= SLIM_Q4_MAX_EXPERTS,
- * 0 <= r <= SLIM_Q4_MAX_ROWS (0 is a no-op), tx >= 1 unless r = 0.
+ * 0 <= r <= SLIM_Q4_MAX_ROWS (0 is a no-op), tx >= 1 unless r = 0.  The
+ * workspace's size does not know whether rows is NULL: it is what a gather needs.
  * ---------------------------------------------------------------------- */
 #define SLIM_Q4_MAX_ROWS (1 << 20)
 size_t slim_q4_experts_workspace(int64_t tx, int64_t r, int64_t e, int64_t n, int64_t m, int group, int xdt);

@@ -376,7 +376,7 @@ int slim_pack4(const uint8_t *codes, const float *scale, const float *zero, int6
 
 size_t slim_q4_linear_workspace(int64_t t, int64_t n, int64_t m, int group, int xdt) {
   if (t < 0 || t > SLIM_QLINEAR_MAX_T || n < 1 || !valid_dtype(xdt) || slim_pack4_words(1, n, m, group) < 0) return 0;
-  return slim::q4_ws_bytes(t, t, 1, n, m, group, xdt == SLIM_BF16);
+  return slim::q4_ws_bytes(t, t, 1, n, m, group, xdt == SLIM_BF16, false);
 }
 
 int slim_q4_linear(const void *X, int xdt, int64_t t, int64_t m, const uint32_t *packed, int64_t n, int group, void *Y,
@@ -386,7 +386,7 @@ int slim_q4_linear(const void *X, int xdt, int64_t t, int64_t m, const uint32_t 
   if (t == 0) return SLIM_OK;
   if (!X || !packed || !Y) return SLIM_E_NULL;
   if (!aligned16(X) || !aligned16(packed) || (uintptr_t)Y % (ydt == SLIM_BF16 ? 2 : 4)) return SLIM_E_ALIGN;
-  const size_t need = slim::q4_ws_bytes(t, t, 1, n, m, group, xdt == SLIM_BF16);
+  const size_t need = slim::q4_ws_bytes(t, t, 1, n, m, group, xdt == SLIM_BF16, false);
   if (need > 0 && (!ws || ws_bytes < need)) return SLIM_E_WORKSPACE;
   if (need > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
   slim::Q4Args a = {};
@@ -403,7 +403,7 @@ static bool experts_shape(int64_t tx, int64_t r, int64_t e, int64_t n, int64_t m
 
 size_t slim_q4_experts_workspace(int64_t tx, int64_t r, int64_t e, int64_t n, int64_t m, int group, int xdt) {
   if (!experts_shape(tx, r, e, n, m, group) || !valid_dtype(xdt)) return 0;
-  return slim::q4_ws_bytes(tx, r, e, n, m, group, xdt == SLIM_BF16);
+  return slim::q4_ws_bytes(tx, r, e, n, m, group, xdt == SLIM_BF16, true);
 }
 
 int slim_q4_experts(const void *X, int xdt, int64_t tx, int64_t m, const int32_t *rows, const float *row_scale,
@@ -414,7 +414,7 @@ int slim_q4_experts(const void *X, int xdt, int64_t tx, int64_t m, const int32_t
   if (r == 0) return SLIM_OK;
   if (!X || !offsets || !packed || !Y) return SLIM_E_NULL;
   if (!aligned16(X) || !aligned16(packed) || (uintptr_t)Y % (ydt == SLIM_BF16 ? 2 : 4)) return SLIM_E_ALIGN;
-  const size_t need = slim::q4_ws_bytes(tx, r, e, n, m, group, xdt == SLIM_BF16);
+  const size_t need = slim::q4_ws_bytes(tx, r, e, n, m, group, xdt == SLIM_BF16, true);
   if (need > 0 && (!ws || ws_bytes < need)) return SLIM_E_WORKSPACE;
   if (need > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
   slim::Q4Args a = {};

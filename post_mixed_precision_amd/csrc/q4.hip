@@ -1003,9 +1003,10 @@ int column_parts(int64_t r, int64_t e, int64_t n, int64_t m) {
 }
 
 // Workspace of the tile kernel: group sums, then what of X it cannot read in
-// place, of X's rows or, with a gather of fewer rows than X has, of the
-// gathered rows (compact): the planes of float32 X, or a copy of bfloat16 X
-// whose rows do not end with a record or may lie more than 32-bit offsets apart.
+// place, of X's rows or, with a gather of fewer rows than X has or past 32-bit
+// offsets, of the gathered rows (compact): the planes of float32 X, or a copy of
+// bfloat16 X whose rows do not end with a record or are gathered from too far.
+// Without a gather a tile's rows lie together, at any distance from X's first.
 // With fewer workgroups than CUs the columns are split over up to four, whose
 // sums follow: t = 500, 5000 x 4096 (80 workgroups): 44 us, unsplit 70; t = 1024,
 // 4096 x 4096 (128 workgroups, halves): 55 us.
@@ -1015,15 +1016,14 @@ struct TileWs {
   int64_t nrow;
   size_t planes, partial, bytes;
 };
-TileWs tile_ws(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16) {
+TileWs tile_ws(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16, bool gather) {
   TileWs w;
   const size_t nch = (size_t)q4_chunks(m);
   // bytes of a row as the kernel reads it: in place, of the padded copy or of the planes
   const bool padded = m % 128 != 0;
   const uint64_t row = !xbf16 ? 768 * (uint64_t)nch : padded ? 256 * (uint64_t)nch : 2 * (uint64_t)m;
-  const bool far = (uint64_t)xrows * row >= 0xfff00000ull;
-  // a gather is known only by r != xrows here; far X is always taken row by row
-  w.compact = r < xrows || far;
+  const bool far = gather && (uint64_t)xrows * row >= 0xfff00000ull;
+  w.compact = gather && (r < xrows || far);
   w.copy = xbf16 && (far || padded);
   w.nrow = w.compact ? r : xrows;
   w.planes = ((size_t)w.nrow * nch * (128 / group) * 4 + 15) / 16 * 16;
@@ -1122,7 +1122,7 @@ hipError_t stream_pick(const Q4Args &a, hipStream_t st) {
 template <int G>
 hipError_t pick(const Q4Args &a, void *ws, hipStream_t st) {
   if (use_tiles(a.r, a.e, a.n, a.m, a.xbf16)) {
-    const TileWs w = tile_ws(a.xrows, a.r, a.e, a.n, a.m, G, a.xbf16);
+    const TileWs w = tile_ws(a.xrows, a.r, a.e, a.n, a.m, G, a.xbf16, a.rows != nullptr);
     if (narrow_tiles(a.r, a.e, a.n)) return tile_go<G, 1, 8>(a, w, ws, st);
     return tile_go<G, 2, 4>(a, w, ws, st);
   }
@@ -1139,8 +1139,8 @@ hipError_t launch_pack4(const uint8_t *codes, const float *scale, const float *z
   return hipGetLastError();
 }
 
-size_t q4_ws_bytes(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16) {
-  return r > 0 && use_tiles(r, e, n, m, xbf16) ? tile_ws(xrows, r, e, n, m, group, xbf16).bytes : 0;
+size_t q4_ws_bytes(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16, bool gather) {
+  return r > 0 && use_tiles(r, e, n, m, xbf16) ? tile_ws(xrows, r, e, n, m, group, xbf16, gather).bytes : 0;
 }
 
 hipError_t launch_q4(const Q4Args &a, void *ws, hipStream_t st) {

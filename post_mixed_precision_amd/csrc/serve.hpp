@@ -31,7 +31,8 @@ struct Q4Args {
   int e, group;
   bool xbf16, ybf16;
 };
-size_t q4_ws_bytes(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16);
+// gather: `rows` may be given (the workspace then does for calls without it as well)
+size_t q4_ws_bytes(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16, bool gather);
 hipError_t launch_q4(const Q4Args &a, void *ws, hipStream_t st);
 
 // ---- Token log probabilities ----

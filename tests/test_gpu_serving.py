@@ -390,6 +390,32 @@ def test_q4_experts_gather_with_a_copy_over_4_gib(slim, tx, n, m, g):
         assert np.all(err <= bound), float(np.max(err / bound))
 
 
+@pytest.mark.parametrize("t,n,m,g", [(65536, 200, 32896, 128), (33400, 256, 64480, 32)])
+def test_rows_in_order_over_4_gib(slim, t, n, m, g):
+    # no gather: the tile kernel reads X where it is (or a copy with padded rows), past 32-bit offsets
+    print(f"q4_linear t={t} n={n} m={m} g={g}", flush=True)
+    assert 2 * m * t >= 1 << 32
+    copy = 0 if m % 128 == 0 else t * -(-m // 128) * 256
+    lib = slim.load_library()
+    assert copy < lib.slim_q4_linear_workspace(t, n, m, g, 1) < copy + 2 * m * t
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(83)
+    X = torch.randn((t, m), generator=gen, device="cuda:0", dtype=torch.bfloat16)
+    codes, scale, zero = _layer(84, 1, n, m, g)
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    wrap = min((1 << 32) // (2 * m), t - 2)
+    at = torch.tensor([0, 1, 127, 128, wrap - 1, wrap, wrap + 1, t - 2, t - 1], device="cuda:0")
+    Y = slim.q4_linear(X, packed, n, g)
+    off = torch.tensor([5, t], dtype=torch.int32, device="cuda:0")
+    E = slim.q4_experts(X, off, packed, n, g, Y=torch.full((t, n), 7.0, device="cuda:0"))
+    assert torch.all(E[:5] == 7.0)
+    x = X[at].double().cpu().numpy()
+    exact = x @ oracle.q4_weight(codes[0], scale[0], zero[0], g).T
+    bound = _bound(x, codes[0], scale[0], zero[0], g, "bf16", "f32", exact)
+    assert np.all(np.abs(Y[at].double().cpu().numpy() - exact) <= bound)
+    assert np.all(np.abs(E[at].double().cpu().numpy() - exact)[2:] <= bound[2:])
+
+
 def test_q4_experts_matches_single_layers(slim):
     e, n, m, g = 4, 160, 512, 128
     codes, scale, zero = _layer(14, e, n, m, g)

@@ -228,3 +228,13 @@ def test_gather_workspace_around_32_bit_reach(lib, m, g, xdt):
         need = lib.slim_q4_experts_workspace(tx, r, e, n, m, g, xdt)
         copy = xdt == 0 or m % 128 != 0 or not near
         assert need == _tile_bytes(tx if near else r, m, g, xdt, copy), (tx, need)
+
+
+def test_workspace_of_far_rows_in_order(lib):
+    # without a gather a tile's rows lie together, so that X of any size is read in place
+    t, m = 65536, 32768
+    assert t * _row_bytes(m, 1) >= REACH
+    assert lib.slim_q4_linear_workspace(t, 4096, m, 128, 1) == _tile_bytes(t, m, 128, 1, False)
+    for m in (32768 + 32, 65536 - 64):                   # but for rows that end inside a record
+        assert lib.slim_q4_linear_workspace(t, 4096, m, 32, 1) == _tile_bytes(t, m, 32, 1, True)
+    assert lib.slim_q4_linear_workspace(t, 4096, m, 32, 0) == _tile_bytes(t, m, 32, 0, True)
