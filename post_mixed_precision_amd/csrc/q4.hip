@@ -18,8 +18,6 @@
 // a wave reads one record as 64 consecutive 16-byte loads and its pairs with
 // one 8-byte load per group: a pure stream.  Rows past n and columns past m
 // are stored as zeros.
-#include <math.h>
-
 #include <type_traits>
 
 #include "common.hpp"
@@ -953,15 +951,6 @@ __global__ __launch_bounds__(256) void q4_join_kernel(Q4Args a, const float *__r
   }
 }
 
-// Most tiles of tok rows that e ranges covering at most r rows can be cut into.
-int64_t max_tiles(int64_t r, int64_t e, int64_t tok) {
-  const int64_t whole = (r + tok - 1) / tok;
-  if (e <= 1) return whole;
-  const int64_t ragged = (r + e * (tok - 1)) / tok;
-  const int64_t most = ragged < r ? ragged : r;
-  return most > whole ? most : whole;
-}
-
 template <bool XBF16, int G, int R, int TT, int NW, int U, bool AHEAD>
 hipError_t stream_go(const Q4Args &a, hipStream_t st) {
   const int nrb = (int)q4_row_blocks(a.n), nch = (int)q4_chunks(a.m);
@@ -970,67 +959,6 @@ hipError_t stream_go(const Q4Args &a, hipStream_t st) {
   q4_stream_kernel<XBF16, G, R, TT, NW, U, AHEAD>
       <<<dim3((nrb + R - 1) / R, (uint32_t)gy, (uint32_t)gz), 64 * NW, 0, st>>>(a, nrb, nch);
   return hipGetLastError();
-}
-
-// Row tiles to expect: the bounds are on the device, so an expert's last tile
-// counts as half, with one standard deviation of their sum (e / 12 is its variance)
-// so that a round filled to the last workgroup counts as two; an expert that may
-// have rows has one tile at least.
-double likely_tiles(int64_t r, int64_t e, int64_t tok) {
-  if (e == 1) return (double)((r + tok - 1) / tok);
-  const double some = (double)(e < r ? e : r), t = (double)r / tok + some / 2 + 0.3 * sqrt(some);
-  return t > some ? t : some;
-}
-// Workgroups of the tile kernel with tiles of tok rows and out outputs.
-int64_t likely_blocks(int64_t r, int64_t e, int64_t n, int64_t tok, int64_t out) {
-  return (int64_t)ceil(likely_tiles(r, e, tok) * (double)((n + out - 1) / out));
-}
-// 64 rows of Y x 512 output rows in place of 128 x 256 (the same work) where that
-// takes fewer rounds of 256 workgroups.
-// 8 experts of 11008 x 4096 over 4096 rows, 6 rounds for 7: 472 us against 523; 64
-// of 4096 x 2048 over 8192, 5 for 6: 286 against 331; with as many rounds the two
-// are alike (8 of 4096 x 4096 over 2048: 142, 141; 8 of 4096 x 11008 over 4096: 509, 501).
-bool narrow_tiles(int64_t r, int64_t e, int64_t n) {
-  return (likely_blocks(r, e, n, 64, 512) + 255) / 256 < (likely_blocks(r, e, n, 128, 256) + 255) / 256;
-}
-// Workgroups over which the columns are split, four records at least to each and
-// all of them in one round.
-int column_parts(int64_t r, int64_t e, int64_t n, int64_t m) {
-  const int64_t blocks = narrow_tiles(r, e, n) ? likely_blocks(r, e, n, 64, 512) : likely_blocks(r, e, n, 128, 256);
-  const int64_t most = q4_chunks(m) / 4 < 4 ? q4_chunks(m) / 4 : 4;
-  const int64_t parts = 256 / blocks < most ? 256 / blocks : most;
-  return parts < 1 ? 1 : (int)parts;
-}
-
-// Workspace of the tile kernel: group sums, then what of X it cannot read in
-// place, of X's rows or, with a gather of fewer rows than X has or past 32-bit
-// offsets, of the gathered rows (compact): the planes of float32 X, or a copy of
-// bfloat16 X whose rows do not end with a record or are gathered from too far.
-// Without a gather a tile's rows lie together, at any distance from X's first.
-// With fewer workgroups than CUs the columns are split over up to four, whose
-// sums follow: t = 500, 5000 x 4096 (80 workgroups): 44 us, unsplit 70; t = 1024,
-// 4096 x 4096 (128 workgroups, halves): 55 us.
-struct TileWs {
-  bool compact, copy;
-  int parts;
-  int64_t nrow;
-  size_t planes, partial, bytes;
-};
-TileWs tile_ws(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16, bool gather) {
-  TileWs w;
-  const size_t nch = (size_t)q4_chunks(m);
-  // bytes of a row as the kernel reads it: in place, of the padded copy or of the planes
-  const bool padded = m % 128 != 0;
-  const uint64_t row = !xbf16 ? 768 * (uint64_t)nch : padded ? 256 * (uint64_t)nch : 2 * (uint64_t)m;
-  const bool far = gather && (uint64_t)xrows * row >= 0xfff00000ull;
-  w.compact = gather && (r < xrows || far);
-  w.copy = xbf16 && (far || padded);
-  w.nrow = w.compact ? r : xrows;
-  w.planes = ((size_t)w.nrow * nch * (128 / group) * 4 + 15) / 16 * 16;
-  w.partial = w.planes + (!xbf16 ? (size_t)w.nrow * 3 * nch * 256 : w.copy ? (size_t)w.nrow * nch * 256 : 0);
-  w.parts = column_parts(r, e, n, m);
-  w.bytes = w.partial + (w.parts > 1 ? (size_t)w.parts * r * n * 4 : 0);
-  return w;
 }
 
 template <int G, int WT, int WN>
@@ -1061,62 +989,14 @@ hipError_t tile_go(const Q4Args &a, const TileWs &w, void *ws, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Which kernel: the shorter of two estimates in us, fitted to measurements (g = 64
-// and 128; both are slower alike at 32).  Tiles: 9.5 for the group sums, the first
-// loads and the stores, 1.85 for a stage of 128 columns in a round (float32 X, three
-// planes: 5.3), and where columns are split 4 and the traffic of the partial sums.
-// Streaming: 8, and 6600 (float32 3200) records by 16 rows in one us, the sums' join
-// and stores counting as two records.  Measured, tiles - streaming:
-//  - t = 2048, 4096 x 11008: 184 - 737; 1537, 2100 x 384: 14 - 17; 1000, 4096 x 2048: 38 -
-//    44; 500, 2600 x 1024: 24 - 14; 256, 4096 x 4096: 31 - 24; 256, 4096 x 11008: 48 - 54;
-//    130, 4747 x 1088: 25 - 12; 64, 28672 x 8192: 71 - 82; 64, 13824 x 5120: 34 - 29;
-//    float32: 1030, 7425 x 640: 42 - 91; 385, 2309 x 1152: 37 - 20.
-//  - 8 experts of 11008 x 4096 over 192 rows 69 - 70, over 256 68 - 90, over 384 73 -
-//    111; 64 of 1024 x 2048 over 3840 rows 51 - 63; 16 of 4096 x 4096 over 512 rows 74 -
-//    64; 18 of 391 x 1152 over 2222 rows 29 - 21.
-int64_t rows_per_matrix(int64_t r, int64_t e) { return (r + e - 1) / e; }
-bool use_tiles(int64_t r, int64_t e, int64_t n, int64_t m, bool xbf16) {
-  const int64_t nch = q4_chunks(m);
-  const bool narrow = narrow_tiles(r, e, n);
-  const int64_t parts = column_parts(r, e, n, m);
-  const int64_t rounds = (likely_blocks(r, e, n, narrow ? 64 : 128, narrow ? 512 : 256) * parts + 255) / 256;
-  const double stages = (double)(rounds * ((nch + parts - 1) / parts));
-  const double tile = 9.5 + stages * (xbf16 ? 1.85 : 5.3) + (parts > 1 ? 4.0 + (double)(parts * r) * n * 1.6e-6 : 0.0);
-  const double records = likely_tiles(r, e, 16) * (double)(q4_row_blocks(n) * (nch + 2));
-  const double stream = 8.0 + records / (xbf16 ? 6600.0 : 3200.0);
-  return tile < stream;
-}
-
-// Shape of the streaming kernel, by what fills the 256 CUs.  Measured, us:
-//  - 32 rows at a time, bfloat16 only (float32 has not the registers: t = 64, 28672
-//    x 8192: 172 against 150 with 16): t = 24, 28672 x 8192: 44.7 against 54; t = 64: 82
-//    against 90; t = 256, 4096 x 4096: 23.6 against 25.5; with 128 workgroups (t = 64,
-//    4096 x 4096) 13.7 against 9.4 with two row blocks.  An expert's second half tile
-//    is mostly empty: 64 of 1024 x 2048 over 2048 rows 42.7 against 40, 8 of 11008 x
-//    4096 over 384 110 against 113.
-//  - 4, 2 or 1 row blocks a workgroup (X is read once for all of them): t = 16,
-//    13824 x 5120: 15.4, 17.4, 25; t = 32, 4096 x 4096: 9.7, 8.0, 11.2; t = 1,
-//    4096 x 4096: 8.5, 5.2, 4.7.
-//  - 4 waves that load a record ahead; against 8 waves: t = 1, 28672 x 8192, 28.1
-//    against 29.5 (g = 32: 39 - 44; float32, 16 rows, g = 32: 61 - 73); against 4 waves
-//    with two records at a time: 64 experts of 1024 x 2048, 1024 rows: 27 - 29.
-//    (float32, t = 256, 4096 x 4096 loses: 45 - 41.)
-//  - 16 waves where a workgroup has a CU to itself: t = 16, 13824 x 5120 (216
-//    workgroups): 11.7 against 14.5 with 4 a record ahead; t = 1, 28672 x 8192 (448):
-//    31.7 against 28.1.
 template <bool XBF16, int G>
 hipError_t stream_pick(const Q4Args &a, hipStream_t st) {
-  const int64_t nrb = q4_row_blocks(a.n), nch = q4_chunks(a.m), r4 = (nrb + 3) / 4;
+  const StreamShape s = stream_shape(a.r, a.e, a.n, a.m, XBF16);
   if constexpr (XBF16)
-    if (rows_per_matrix(a.r, a.e) > (a.e == 1 ? 16 : 40) && r4 * ((a.r + 31) / 32) >= 192)
-      return stream_go<XBF16, G, 4, 2, 4, 1, true>(a, st);
-  const int64_t tiles = max_tiles(a.r, a.e, 16);
-  if (r4 * tiles >= 192) {
-    if (nch > 16 && r4 * tiles < 320) return stream_go<XBF16, G, 4, 1, 16, 1, false>(a, st);
-    return stream_go<XBF16, G, 4, 1, 4, 1, true>(a, st);
-  }
-  if ((nrb + 1) / 2 * tiles >= 144) return stream_go<XBF16, G, 2, 1, 8, 2, false>(a, st);
-  return stream_go<XBF16, G, 1, 1, 8, 2, false>(a, st);
+    if (s.tiles == 2) return stream_go<XBF16, G, 4, 2, 4, 1, true>(a, st);
+  if (s.blocks == 4)
+    return s.waves == 16 ? stream_go<XBF16, G, 4, 1, 16, 1, false>(a, st) : stream_go<XBF16, G, 4, 1, 4, 1, true>(a, st);
+  return s.blocks == 2 ? stream_go<XBF16, G, 2, 1, 8, 2, false>(a, st) : stream_go<XBF16, G, 1, 1, 8, 2, false>(a, st);
 }
 
 template <int G>

@@ -5,17 +5,11 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "q4_plan.hpp"
+
 namespace slim {
 
-// ---- 4-bit codes with their scales and zeros, laid out for the products ----
-// A record holds 16 rows x 128 columns: 256 words of codes, then a (scale,
-// zero) pair per row and group.
-inline int64_t q4_row_blocks(int64_t n) { return (n + 15) / 16; }
-inline int64_t q4_chunks(int64_t m) { return (m + 127) / 128; }
-inline int64_t q4_record_words(int group) { return 256 + 32 * (128 / group); }
-inline int64_t q4_matrix_words(int64_t n, int64_t m, int group) {
-  return q4_row_blocks(n) * q4_chunks(m) * q4_record_words(group);
-}
+// ---- 4-bit products ----
 hipError_t launch_pack4(const uint8_t *codes, const float *scale, const float *zero, int64_t e, int64_t n, int64_t m,
                         int group, uint32_t *packed, int32_t *info, hipStream_t st);
 

@@ -430,6 +430,139 @@ def test_q4_experts_matches_single_layers(slim):
             torch.testing.assert_close(Y[a:b], one, rtol=1e-4, atol=1e-4)
 
 
+# ------------------------------------------------------------------ every kernel that can be chosen
+# What runs is chosen by estimates from the sizes; each case names the kernel it is for (row blocks x
+# row tiles x waves x records; rows x outputs), which test_serving_plan.py holds against the rules.
+LINEAR_KERNELS = [
+    # 16 waves: a batch of 16 (and less) through a wide layer, and many rows through a small one
+    ("stream 4x1x16x1", 16, 12400, 2240, 64, "bf16", "bf16"),
+    ("stream 4x1x16x1", 3, 12900, 2144, 32, "bf16", "f32"),
+    ("stream 4x1x16x1", 530, 337, 2176, 128, "bf16", "f32"),
+    ("stream 4x1x16x1", 400, 475, 2208, 32, "f32", "bf16"),
+    ("stream 4x1x16x1", 61, 3100, 2304, 128, "f32", "f32"),
+    ("stream 4x1x16x1", 16, 12400, 2112, 64, "f32", "f32"),
+    # two row blocks
+    ("stream 2x1x8x2", 16, 5000, 2080, 32, "bf16", "f32"),
+    ("stream 2x1x8x2", 40, 1650, 320, 64, "bf16", "bf16"),
+    ("stream 2x1x8x2", 12, 5001, 1152, 128, "bf16", "f32"),
+    ("stream 2x1x8x2", 7, 4700, 416, 32, "f32", "bf16"),
+    ("stream 2x1x8x2", 33, 1700, 1088, 64, "f32", "f32"),
+    # one
+    ("stream 1x1x8x2", 5, 300, 1984, 64, "f32", "f32"),
+    # four, a record ahead
+    ("stream 4x1x4x1 ahead", 9, 12700, 1088, 64, "bf16", "bf16"),
+    ("stream 4x1x4x1 ahead", 30, 7000, 960, 64, "f32", "bf16"),
+    # tiles that few rows leave part empty
+    ("tile 128x256 split 4", 127, 13492, 3392, 64, "bf16", "f32"),
+    ("tile 128x256 split 4", 100, 14716, 2016, 32, "f32", "bf16"),
+    ("tile 128x256", 123, 15004, 32, 32, "bf16", "bf16"),
+    # columns split over two, three and four workgroups
+    ("tile 128x256 split 2", 2521, 1490, 1280, 128, "bf16", "f32"),
+    ("tile 128x256 split 3", 1066, 2255, 2208, 32, "bf16", "bf16"),
+    ("tile 128x256 split 2", 2243, 1310, 992, 32, "f32", "f32"),
+    ("tile 128x256 split 3", 2185, 988, 1472, 32, "f32", "bf16"),
+    ("tile 128x256 split 4", 1179, 1504, 1984, 64, "f32", "f32"),
+    ("tile 64x512", 1034, 7235, 320, 64, "f32", "f32"),
+]
+
+
+@pytest.mark.parametrize("kernel,t,n,m,g,xdt,ydt", LINEAR_KERNELS)
+def test_q4_linear_of_every_kernel(slim, kernel, t, n, m, g, xdt, ydt):
+    need = slim.load_library().slim_q4_linear_workspace(t, n, m, g, xdt == "bf16")
+    assert (need > 0) == kernel.startswith("tile")
+    test_q4_linear(slim, t, n, m, g, xdt, ydt)
+
+
+_FEW = [5, 0, 1, 3, 0, 2, 4, 1]
+EXPERT_KERNELS = [
+    ("stream 1x1x8x2", [2, 0, 3], 100, 224, 32, "bf16", "bf16", True, False, 1, 0),
+    ("stream 1x1x8x2", [2, 0, 3], 100, 192, 64, "f32", "f32", False, True, 0, 2),
+    ("stream 1x1x8x2", [18, 1, 30], 70, 2304, 128, "f32", "f32", True, True, 0, 0),
+    ("stream 2x1x8x2", _FEW, 700, 2080, 32, "bf16", "f32", True, True, 0, 0),
+    ("stream 2x1x8x2", _FEW, 690, 1152, 128, "bf16", "bf16", False, True, 0, 0),
+    ("stream 2x1x8x2", _FEW, 705, 288, 32, "f32", "f32", True, False, 0, 0),
+    ("stream 2x1x8x2", _FEW, 700, 960, 64, "f32", "bf16", False, False, 0, 0),
+    ("stream 2x1x8x2", _FEW, 700, 2432, 128, "f32", "f32", True, True, 0, 0),
+    ("stream 4x1x16x1", _FEW, 1700, 2144, 32, "bf16", "bf16", True, True, 0, 0),
+    ("stream 4x1x16x1", _FEW, 1690, 2240, 64, "bf16", "f32", False, True, 0, 0),
+    ("stream 4x1x16x1", _FEW, 1700, 2432, 128, "bf16", "bf16", True, False, 0, 0),
+    ("stream 4x1x16x1", _FEW, 1710, 2336, 32, "f32", "f32", False, False, 0, 0),
+    ("stream 4x1x16x1", _FEW, 1700, 2112, 64, "f32", "bf16", True, True, 0, 0),
+    ("stream 4x1x16x1", _FEW, 1700, 2176, 128, "f32", "f32", True, True, 0, 0),
+    ("stream 4x1x4x1 ahead", _FEW, 1700, 1952, 32, "bf16", "f32", True, True, 0, 0),
+    ("stream 4x1x4x1 ahead", [20, 40, 0, 17, 33], 1900, 608, 32, "f32", "bf16", True, False, 1, 1),
+    ("stream 4x1x4x1 ahead", _FEW, 1700, 1152, 128, "f32", "f32", False, True, 0, 0),
+    ("stream 4x2x4x1 ahead", [50, 0, 90, 33, 64, 45, 61, 57], 1100, 224, 32, "bf16", "f32", True, True, 0, 0),
+    ("tile 128x256", [900, 0, 517, 1, 700, 599], 1700, 192, 64, "f32", "bf16", True, True, 1, 2),
+    ("tile 128x256 split 2", [1000, 795], 1951, 1472, 32, "bf16", "f32", True, False, 0, 3),
+    ("tile 128x256 split 3", [600, 743], 1571, 2688, 64, "bf16", "bf16", False, True, 2, 0),
+    ("tile 128x256 split 2", [1000, 710], 1761, 992, 32, "f32", "f32", True, True, 0, 0),
+    ("tile 128x256 split 4", [1700, 0, 2031], 412, 2560, 128, "f32", "bf16", False, False, 1, 1),
+    ("tile 64x512", [30, 0, 1, 60, 3, 20, 64, 7, 8, 9, 10], 6027, 128, 128, "f32", "f32", True, True, 0, 0),
+]
+
+
+@pytest.mark.parametrize("kernel,counts,n,m,g,xdt,ydt,gather,weighted,before,behind", EXPERT_KERNELS)
+def test_q4_experts_of_every_kernel(slim, kernel, counts, n, m, g, xdt, ydt, gather, weighted, before, behind):
+    r = before + sum(counts) + behind
+    need = slim.load_library().slim_q4_experts_workspace(r, r, len(counts), n, m, g, xdt == "bf16")
+    assert (need > 0) == kernel.startswith("tile")
+    test_q4_experts(slim, counts, n, m, g, xdt, ydt, gather, weighted, before, behind)
+
+
+# tiles; with planes of float32 X; with a copy of X; columns split
+TILED = [(1537, 2100, 384, 128, "bf16"), (1290, 2320, 384, 128, "f32"), (1410, 2310, 576, 64, "bf16"),
+         (1066, 2255, 2208, 32, "bf16"), (2243, 1310, 992, 32, "f32")]
+
+
+@pytest.mark.parametrize("ydt", ["bf16", "f32"])
+@pytest.mark.parametrize("t,n,m,g,xdt", TILED)
+def test_q4_tiles_to_outputs_that_start_anywhere(slim, t, n, m, g, xdt, ydt):
+    print(f"q4_linear t={t} n={n} m={m} g={g} {xdt} -> {ydt}, one element off", flush=True)
+    assert slim.load_library().slim_q4_linear_workspace(t, n, m, g, xdt == "bf16") > 0
+    codes, scale, zero = _layer(90, 1, n, m, g)
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    X = _x(91, t, m, xdt).to("cuda:0")
+    flat = torch.full((t * n + 3,), 7.0, dtype=DT[ydt], device="cuda:0")
+    out = slim.q4_linear(X, packed, n, g, out_dtype=DT[ydt], Y=flat[1:1 + t * n].view(t, n))
+    assert torch.equal(out, slim.q4_linear(X, packed, n, g, out_dtype=DT[ydt]))
+    assert flat[0] == 7 and torch.all(flat[1 + t * n:] == 7)
+
+
+@pytest.mark.parametrize("t,n,m,g,xdt", TILED)
+def test_tiles_in_two_graphs(slim, t, n, m, g, xdt):
+    # each captured call has a workspace of its own (sums, planes or a copy of X, partial sums): replays in
+    # any order agree with eager calls between them, also after X has changed
+    print(f"graphs of q4_linear and q4_experts t={t} n={n} m={m} g={g} {xdt}", flush=True)
+    assert slim.load_library().slim_q4_linear_workspace(t, n, m, g, xdt == "bf16") > 0
+    codes, scale, zero = _layer(92, 2, n, m, g)
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    first = slim.pack4(_gpu(codes[0]), _gpu(scale[0]), _gpu(zero[0]), g)
+    X = _x(93, t, m, xdt).to("cuda:0")
+    off = torch.tensor([0, t // 3, t], dtype=torch.int32, device="cuda:0")
+    rows = torch.arange(t - 1, -1, -1, device="cuda:0").to(torch.int32)
+
+    def calls():
+        return slim.q4_linear(X, first, n, g), slim.q4_experts(X, off, packed, n, g, rows=rows)
+    eager = calls()
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = calls()
+        graphs.append((gr, out))
+    for turn, i in enumerate((0, 1, 1, 0, 1)):
+        if turn == 2:
+            X.neg_()
+            off[1] = t // 2
+            eager = calls()
+        graphs[i][0].replay()
+        again = calls()
+        torch.cuda.synchronize()
+        for a, b, c in zip(graphs[i][1], again, eager):
+            assert torch.equal(a, b) and torch.equal(b, c), turn
+
+
 # ------------------------------------------------------------------ log probabilities
 def _lp_bounds(x, out):
     """Float32 error bounds.  d = x - M is off by 2^-24 |d|; e^d by 3 2^-24 (1 +
