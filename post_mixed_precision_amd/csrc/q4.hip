@@ -991,9 +991,11 @@ hipError_t tile_go(const Q4Args &a, const TileWs &w, void *ws, hipStream_t st) {
 
 template <bool XBF16, int G>
 hipError_t stream_pick(const Q4Args &a, hipStream_t st) {
-  const StreamShape s = stream_shape(a.r, a.e, a.n, a.m, XBF16);
+  const StreamShape s = stream_shape(a.r, a.e, a.n, a.m, G, XBF16);
   if constexpr (XBF16)
     if (s.tiles == 2) return stream_go<XBF16, G, 4, 2, 4, 1, true>(a, st);
+  if constexpr (!XBF16 && G == 128)
+    if (s.blocks == 4 && s.waves == 8) return stream_go<XBF16, G, 4, 1, 8, 1, false>(a, st);
   if (s.blocks == 4)
     return s.waves == 16 ? stream_go<XBF16, G, 4, 1, 16, 1, false>(a, st) : stream_go<XBF16, G, 4, 1, 4, 1, true>(a, st);
   return s.blocks == 2 ? stream_go<XBF16, G, 2, 1, 8, 2, false>(a, st) : stream_go<XBF16, G, 1, 1, 8, 2, false>(a, st);

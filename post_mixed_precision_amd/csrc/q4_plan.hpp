@@ -127,7 +127,13 @@ inline bool use_tiles(int64_t r, int64_t e, int64_t n, int64_t m, bool xbf16) {
 //  - 4 waves that load a record ahead; against 8 waves: t = 1, 28672 x 8192, 28.1
 //    against 29.5 (g = 32: 39 - 44; float32, 16 rows, g = 32: 61 - 73); against 4 waves
 //    with two records at a time: 64 experts of 1024 x 2048, 1024 rows: 27 - 29.
-//    (float32, t = 256, 4096 x 4096 loses: 45 - 41.)
+//  - but 8 waves, none ahead, for float32 X with a group to a record, where the records
+//    pass more than once (up to 16 rows the stream bounds it) and a wave has two at
+//    least; other weights between calls: t = 256, 4096 x 4096: 41.8 against 4 waves' 45.4
+//    (g = 64 50.3 - 48.4, g = 32 59.3 - 56.5); t = 48, 13824 x 5120: 42.9 - 45.0; t = 48,
+//    22016 x 4096: 53.2 - 57.2 (t = 32 42.4 - 38.0); t = 64, 28672 x 8192: 152.6 - 149.9;
+//    t = 1, 28672 x 8192: 46.8 - 43.0; 64 experts of 1024 x 2048, 2048 rows: 65 - 67.7; rows
+//    of 12 records, t = 130, 8000 x 1536: 27.4 - 25.5.
 //  - 16 waves where a workgroup has a CU to itself: t = 16, 13824 x 5120 (216
 //    workgroups): 11.7 against 14.5 with 4 a record ahead; t = 1, 28672 x 8192 (448):
 //    31.7 against 28.1.
@@ -138,13 +144,14 @@ struct StreamShape {
   int records;               // taken by a wave at a time
   bool ahead;                // the next one's loads beside the products
 };
-inline StreamShape stream_shape(int64_t r, int64_t e, int64_t n, int64_t m, bool xbf16) {
+inline StreamShape stream_shape(int64_t r, int64_t e, int64_t n, int64_t m, int group, bool xbf16) {
   const int64_t nrb = q4_row_blocks(n), nch = q4_chunks(m), r4 = (nrb + 3) / 4;
   const int64_t rows_per_matrix = (r + e - 1) / e;
   if (xbf16 && rows_per_matrix > (e == 1 ? 16 : 40) && r4 * ((r + 31) / 32) >= 192) return {4, 2, 4, 1, true};
   const int64_t tiles = max_tiles(r, e, 16);
   if (r4 * tiles >= 192) {
     if (nch > 16 && r4 * tiles < 320) return {4, 1, 16, 1, false};
+    if (!xbf16 && group == 128 && nch >= 16 && rows_per_matrix > 16) return {4, 1, 8, 1, false};
     return {4, 1, 4, 1, true};
   }
   if ((nrb + 1) / 2 * tiles >= 144) return {2, 1, 8, 2, false};

@@ -452,6 +452,10 @@ LINEAR_KERNELS = [
     # four, a record ahead
     ("stream 4x1x4x1 ahead", 9, 12700, 1088, 64, "bf16", "bf16"),
     ("stream 4x1x4x1 ahead", 30, 7000, 960, 64, "f32", "bf16"),
+    ("stream 4x1x4x1 ahead", 100, 4000, 1920, 128, "f32", "bf16"),
+    # by 8 waves
+    ("stream 4x1x8x1", 100, 4000, 2048, 128, "f32", "f32"),
+    ("stream 4x1x8x1", 17, 10300, 2432, 128, "f32", "bf16"),
     # tiles that few rows leave part empty
     ("tile 128x256 split 4", 127, 13492, 3392, 64, "bf16", "f32"),
     ("tile 128x256 split 4", 100, 14716, 2016, 32, "f32", "bf16"),
@@ -492,6 +496,7 @@ EXPERT_KERNELS = [
     ("stream 4x1x4x1 ahead", _FEW, 1700, 1952, 32, "bf16", "f32", True, True, 0, 0),
     ("stream 4x1x4x1 ahead", [20, 40, 0, 17, 33], 1900, 608, 32, "f32", "bf16", True, False, 1, 1),
     ("stream 4x1x4x1 ahead", _FEW, 1700, 1152, 128, "f32", "f32", False, True, 0, 0),
+    ("stream 4x1x8x1", [40, 3, 0, 50, 20, 31], 1710, 2432, 128, "f32", "bf16", True, True, 1, 2),
     ("stream 4x2x4x1 ahead", [50, 0, 90, 33, 64, 45, 61, 57], 1100, 224, 32, "bf16", "f32", True, True, 0, 0),
     ("tile 128x256", [900, 0, 517, 1, 700, 599], 1700, 192, 64, "f32", "bf16", True, True, 1, 2),
     ("tile 128x256 split 2", [1000, 795], 1951, 1472, 32, "bf16", "f32", True, False, 0, 3),

@@ -22,12 +22,12 @@ REACH = 0xfff00000          # bytes that 32-bit offsets may span
 SOURCE = """
 #include "q4_plan.hpp"
 using namespace slim;
-extern "C" void choose(int64_t r, int64_t e, int64_t n, int64_t m, int xbf16, int *out) {
+extern "C" void choose(int64_t r, int64_t e, int64_t n, int64_t m, int g, int xbf16, int *out) {
   out[0] = use_tiles(r, e, n, m, xbf16);
   if (out[0]) {
     out[1] = narrow_tiles(r, e, n), out[2] = column_parts(r, e, n, m);
   } else {
-    const StreamShape s = stream_shape(r, e, n, m, xbf16);
+    const StreamShape s = stream_shape(r, e, n, m, g, xbf16);
     out[1] = s.blocks, out[2] = s.tiles, out[3] = s.waves, out[4] = s.records, out[5] = s.ahead;
   }
 }
@@ -53,17 +53,17 @@ def plan(tmp_path_factory):
     assert r.returncode == 0, r.stderr
     lib = ctypes.CDLL(str(so))
     i64 = ctypes.c_int64
-    lib.choose.argtypes = [i64] * 4 + [ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
+    lib.choose.argtypes = [i64] * 4 + [ctypes.c_int] * 2 + [ctypes.POINTER(ctypes.c_int)]
     lib.sizes.argtypes = [i64] * 5 + [ctypes.c_int] * 3 + [ctypes.POINTER(i64)]
     lib.most_tiles.argtypes, lib.most_tiles.restype = [i64] * 3, i64
     return lib
 
 
-def choose(plan, r, e, n, m, xdt):
+def choose(plan, r, e, n, m, g, xdt):
     """The kernel as GPU cases name it: "tile 128x256", with " split 3" where the columns are, or
     "stream 4x1x16x1": row blocks x row tiles x waves x records, with " ahead"."""
     out = (ctypes.c_int * 6)()
-    plan.choose(r, e, n, m, xdt == "bf16", out)
+    plan.choose(r, e, n, m, g, xdt == "bf16", out)
     if out[0]:
         return ("tile 64x512" if out[1] else "tile 128x256") + (f" split {out[2]}" if out[2] > 1 else "")
     return "stream " + "x".join(map(str, out[1:5])) + (" ahead" if out[5] else "")
@@ -93,16 +93,16 @@ def _shapes(count, seed=0):
 
 def test_gpu_cases_run_on_the_kernel_they_name(plan):
     for kernel, t, n, m, g, xdt, ydt in gpu.LINEAR_KERNELS:
-        assert choose(plan, t, 1, n, m, xdt) == kernel, (t, n, m, g, xdt)
+        assert choose(plan, t, 1, n, m, g, xdt) == kernel, (t, n, m, g, xdt)
     for kernel, counts, n, m, g, xdt, ydt, gather, weighted, before, behind in gpu.EXPERT_KERNELS:
         r = before + sum(counts) + behind
-        assert choose(plan, r, len(counts), n, m, xdt) == kernel, (r, len(counts), n, m, g, xdt)
+        assert choose(plan, r, len(counts), n, m, g, xdt) == kernel, (r, len(counts), n, m, g, xdt)
 
 
 def test_every_kernel_that_can_be_chosen_has_a_gpu_case(plan):
     def keys(r, e, n, m, g, xdt):
         """What is compiled for it, and over how many workgroups its columns are split."""
-        kernel, _, parts = choose(plan, r, e, n, m, xdt).partition(" split ")
+        kernel, _, parts = choose(plan, r, e, n, m, g, xdt).partition(" split ")
         return {(kernel, g, xdt, bool(parts)), ("parts", parts, xdt)}
     have = set()
     for t, n, m, g, xdt, _ in [*gpu.LINEAR, *(c[1:] for c in gpu.LINEAR_KERNELS)]:
@@ -174,7 +174,7 @@ def test_library_asks_for_these_sizes(plan):
     lib = slim.load_library()
     for r, e, n, m, g, xdt in _shapes(2000, 5):
         bf = xdt == "bf16"
-        tile = choose(plan, r, e, n, m, xdt).startswith("tile")
+        tile = choose(plan, r, e, n, m, g, xdt).startswith("tile")
         for tx in (r, max(1, r // 3), min(1 << 20, 2 * r)):
             want = sizes(plan, tx, r, e, n, m, g, xdt, 1)["bytes"] if tile else 0
             assert lib.slim_q4_experts_workspace(tx, r, e, n, m, g, bf) == want
