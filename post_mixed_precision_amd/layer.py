@@ -59,7 +59,13 @@ def score_tokens(X, ids, packed4, n: int, group: int, top: int = 0, block: int =
     if not isinstance(X, torch.Tensor) or not isinstance(ids, torch.Tensor) or X.dim() != 2 or ids.dim() != 1 \
             or ids.shape[0] != X.shape[0]:
         raise _lib.SlimError("X: expected [T, m] and ids: expected [T]")
-    T = X.shape[0]
+    T, m = X.shape
+    # what can be refused, before the buffer of a block's logits is made
+    packed4 = _lib._arg(packed4, "packed", (_lib._words4(1, n, m, group),), (torch.int32,))
+    if not 0 <= top <= min(n, _lib.LOGPROB_MAX_TOP):
+        raise _lib.SlimError(f"top {top} must lie in 0 .. {min(n, _lib.LOGPROB_MAX_TOP)}")
+    if not (X.is_cuda and packed4.is_cuda and ids.is_cuda):
+        raise _lib.SlimError("tensors must live in GPU memory")
     if T <= block:
         return _lib.token_logprobs(_lib.q4_linear(X, packed4, n, group), ids, top)
     buf = torch.empty((block, n), dtype=torch.float32, device=X.device)

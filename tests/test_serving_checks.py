@@ -238,3 +238,20 @@ def test_workspace_of_far_rows_in_order(lib):
     for m in (32768 + 32, 65536 - 64):                   # but for rows that end inside a record
         assert lib.slim_q4_linear_workspace(t, 4096, m, 32, 1) == _tile_bytes(t, m, 32, 1, True)
     assert lib.slim_q4_linear_workspace(t, 4096, m, 32, 0) == _tile_bytes(t, m, 32, 0, True)
+
+
+def test_score_tokens_refuses_before_it_allocates(L):
+    import post_mixed_precision_amd as slim
+    X, ids, W = _bf(4, 128), torch.zeros(4, dtype=torch.int64), _i(288)
+    for n in (-1, 0, 1 << 50, (1 << 20) + 1):
+        raises(L, lambda: slim.score_tokens(X, ids, W, n, 128, block=2), "layer shape")
+        raises(L, lambda: slim.score_tokens(X, ids, W, n, 128), "layer shape")
+    raises(L, lambda: slim.score_tokens(X, ids, W, 17, 128, block=2), "packed")
+    raises(L, lambda: slim.score_tokens(X, ids, W, 16, 100, block=2), "group")
+    raises(L, lambda: slim.score_tokens(X, ids, W, 16, 128, top=17, block=2), "top")
+    raises(L, lambda: slim.score_tokens(X, ids, W, 16, 128, top=-1, block=2), "top")
+    # a million outputs by 65536 rows: no buffer of that size is made for tensors that are not on a GPU
+    words = L.load_library().slim_pack4_words(1, 1 << 20, 32, 32)
+    big = torch.zeros(1, dtype=torch.int32).expand(words)
+    raises(L, lambda: slim.score_tokens(_bf(70000, 32), torch.zeros(70000, dtype=torch.int64), big, 1 << 20, 32,
+                                        block=65536), "GPU")
