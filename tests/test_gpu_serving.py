@@ -871,3 +871,96 @@ def test_long_offsets_past_32_bits(slim):
     last = {k: a[t - 1:] for k, a in got.items()}
     _check_lp(last, L[t - 1:].double().cpu().numpy(), np.array([v - 1]), 3)
     assert got["top_id"][:t - 1].eq(torch.arange(3, device="cuda:0")).all()
+
+
+# ------------------------------------------------------------------ the largest sizes
+def _check_rows(got, x, codes, scale, zero, g, xdt):
+    """Rows of Y, float64 rows of X and one matrix's codes."""
+    exact = x @ oracle.q4_weight(codes, scale, zero, g).T
+    bound = _bound(x, codes, scale, zero, g, xdt, "f32", exact)
+    err = np.abs(got.double().cpu().numpy() - exact)
+    assert np.all(err <= bound), float(np.max(err / bound))
+
+
+@pytest.mark.parametrize("t,m,tiles", [(3, 640, False), (200, 32, True)])
+def test_q4_linear_of_the_most_outputs(slim, t, m, tiles):
+    n, g = 1 << 20, 32
+    print(f"q4_linear t={t} n={n} m={m}", flush=True)
+    assert (slim.load_library().slim_q4_linear_workspace(t, n, m, g, 1) > 0) == tiles
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(100)
+    codes = torch.randint(0, 16, (n, m), generator=gen, device="cuda:0", dtype=torch.uint8)
+    scale = 1e-3 + 0.01 * torch.rand((n, m // g), generator=gen, device="cuda:0")
+    zero = 15 * torch.rand((n, m // g), generator=gen, device="cuda:0")
+    X = _x(101, t, m, "bf16")
+    Y = slim.q4_linear(X.to("cuda:0"), slim.pack4(codes, scale, zero, g), n, g)
+    x = X.double().numpy()
+    at = [0, 1, 2] if t < 100 else [0, 63, 64, 127, 128, 199]
+    for a, b in ((0, 700), (n // 2 - 300, n // 2 + 300), (n - 700, n)):
+        _check_rows(Y[at, a:b], x[at], *(w[a:b].cpu().numpy() for w in (codes, scale, zero)), g, "bf16")
+
+
+@pytest.mark.parametrize("r,n,m,tiles", [(3000, 48, 160, False), (100000, 256, 128, True)])
+def test_q4_experts_of_the_most_experts(slim, r, n, m, tiles):
+    e, g = 1024, 32
+    print(f"q4_experts e={e} r={r} n={n} m={m}", flush=True)
+    assert (slim.load_library().slim_q4_experts_workspace(r, r, e, n, m, g, 1) > 0) == tiles
+    rng = np.random.default_rng(102)
+    off = np.sort(rng.integers(0, r + 1, size=e + 1)).astype(np.int32)
+    off[1:1 + e // 4] = off[1]                               # a quarter of them have no rows
+    off[0], off[-1] = 2, r - 3
+    off = np.clip(off, 2, r - 3)
+    codes, scale, zero = _layer(103, e, n, m, g)
+    X = _x(104, r, m, "bf16")
+    Y = torch.full((r, n), 7.0, device="cuda:0")
+    slim.q4_experts(X.to("cuda:0"), _gpu(off), slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g), n, g, Y=Y)
+    assert torch.all(Y[:2] == 7.0) and torch.all(Y[r - 3:] == 7.0)
+    x = X.double().numpy()
+    for j in (0, 1, e // 4, e // 4 + 1, *range(300, e, 37), e - 1):
+        a, b = off[j], off[j + 1]
+        if a < b:
+            _check_rows(Y[a:b], x[a:b], codes[j], scale[j], zero[j], g, "bf16")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_token_logprobs_of_the_longest_rows(slim, dt):
+    v, top = 1 << 24, 64
+    print(f"token_logprobs v={v} {dt} top={top}", flush=True)
+    x = _logits(105, 2, v, 0, 0, dt)
+    x[1, v - 1] = 30.0
+    ids = np.array([v - 1, v - 1])
+    got = slim.token_logprobs(x.to("cuda:0"), _gpu(ids), top=top)
+    # _check_lp, with numpy's sort in place of Python's
+    xd = x.double().numpy()
+    order = np.stack([np.argsort(-row, kind="stable")[:top] for row in xd])
+    np.testing.assert_array_equal(got["top_id"].cpu().numpy(), order)
+    mx = xd.max(axis=1, keepdims=True)
+    lp = (xd - mx) - np.log(np.exp(xd - mx).sum(axis=1, keepdims=True))
+    want = {"logprob": lp[:, v - 1], "entropy": -(np.exp(lp) * lp).sum(axis=1)}
+    lp_b, ent_b, rs = _lp_bounds(xd, want)
+    assert np.all(np.abs(got["logprob"].double().cpu().numpy() - want["logprob"]) <= lp_b)
+    assert np.all(np.abs(got["entropy"].double().cpu().numpy() - want["entropy"]) <= ent_b)
+    wl = np.take_along_axis(lp, order, axis=1)
+    err = np.abs(got["top_logprob"].double().cpu().numpy() - wl)
+    assert np.all(err <= rs[:, None] + 2.0 ** -22 * (1 + np.abs(wl)))
+
+
+def test_token_logprobs_of_the_most_rows(slim):
+    t, v = 1 << 23, 3
+    print(f"token_logprobs t={t} v={v}", flush=True)
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(106)
+    x = 3 * torch.randn((t, v), generator=gen, device="cuda:0")
+    ids = torch.randint(0, v, (t,), generator=gen, device="cuda:0")
+    got = slim.token_logprobs(x, ids, top=2)
+    d = x.double() - x.double().amax(dim=1, keepdim=True)
+    lp = d - d.exp().sum(dim=1, keepdim=True).log()
+    # the bounds of _lp_bounds with the spread of all rows
+    spread = float((-d).max())
+    rs = 2.0 ** -24 * (v / 64 + 40 + 4 * (1 + spread))
+    want = lp.gather(1, ids[:, None])[:, 0]
+    assert ((got["logprob"].double() - want).abs() <= rs + 2.0 ** -22 * (1 + want.abs())).all()
+    ent = -(lp.exp() * lp).sum(dim=1)
+    assert ((got["entropy"].double() - ent).abs() <= 2 * rs * (1 + ent) + 2.0 ** -21 * (1 + ent + spread)).all()
+    order = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :2]
+    assert torch.equal(got["top_id"].long(), order)
