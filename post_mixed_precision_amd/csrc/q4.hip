@@ -5,7 +5,7 @@
 //   P[a, i, j] = sum_{c in group j} X[a, c] q[i, c],   Xs[a, j] = sum_{c in group j} X[a, c].
 //
 // A code below 16 is exact in bfloat16, X enters as stored (float32 X as three
-// bfloat16 terms whose sum is exact), and P and Xs come from the bfloat16 MFMA
+// bfloat16 terms whose sum is exact from 2^-110 on), and P and Xs come from the bfloat16 MFMA
 // with float32 sums, so nothing is rounded before the float32 group sums; Y is
 // rounded once at the end.  Folding s into a bfloat16 weight would save the
 // per-group scaling but round every weight to 8 bits.
@@ -87,7 +87,8 @@ __device__ __forceinline__ uint4 q4_codes(uint32_t w) {
 }
 
 // 8 columns of a float32 row as three bfloat16 terms whose sum is exact
-// (truncation leaves 16, then 8 significant bits).
+// (truncation leaves 16, then 8 significant bits), but for what lies below
+// bfloat16's least value of 2^-133.
 __device__ __forceinline__ void split3(const uint4 &a, const uint4 &b, uint4 (&t)[3]) {
   const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t h[8], m[8], l[8];

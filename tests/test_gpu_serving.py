@@ -964,3 +964,23 @@ def test_token_logprobs_of_the_most_rows(slim):
     assert ((got["entropy"].double() - ent).abs() <= 2 * rs * (1 + ent) + 2.0 ** -21 * (1 + ent + spread)).all()
     order = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :2]
     assert torch.equal(got["top_id"].long(), order)
+
+
+@pytest.mark.parametrize("t,n,m,g", [(3, 64, 256, 128), (20, 96, 160, 32), (1290, 2320, 384, 128)])
+@pytest.mark.parametrize("xdt", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -115, 2.0 ** -125, 2.0 ** -130])
+def test_q4_linear_of_tiny_rows(slim, t, n, m, g, xdt, size):
+    # bfloat16 X is exact down to its least value, float32 X enters to its multiples, 2^-133 (truncated)
+    codes, scale, zero = _layer(110, 1, n, m, g)
+    scale *= np.float32(2.0 ** 90)
+    X = (size * _x(111, t, m, "f32").double()).to(DT[xdt])
+    Y = slim.q4_linear(X.to("cuda:0"), slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g), n, g)
+    x = X.double().numpy()
+    exact = x @ oracle.q4_weight(codes[0], scale[0], zero[0], g).T
+    bound = _bound(x, codes[0], scale[0], zero[0], g, xdt, "f32", exact)
+    if xdt == "f32":
+        bound += 2.0 ** -133 * (codes[0] * np.repeat(scale[0], g, -1).astype(np.float64)).sum(axis=1)
+    # what is below float32's normal range before the scale: a group's sums, to half of 2^-149 a term
+    bound += 2.0 ** -149 * (3 * g + 32 * 2) * np.abs(scale[0].astype(np.float64)).sum(axis=1)
+    err = np.abs(Y.double().cpu().numpy() - exact)
+    assert np.all(err <= bound), float(np.max(err / bound))
