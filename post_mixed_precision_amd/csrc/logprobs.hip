@@ -23,13 +23,14 @@
 // same merge.  The set and its order depend on the keys alone.
 //
 // Bound by reading the logits where there are many: 2048 rows of 32000 float32
-// 42.2 us (262 MB, 6.2 TB/s), 333 rows of 100003 29.4 us (133 MB, 4.5 TB/s) and 4
-// for the join.  bfloat16 halves the bytes but not the work of an entry (seven
-// vector operations and a power, which costs four): 2048 rows of 32000 34 us.
+// 48.2 us where other logits pass between calls (262 MB, 5.4 TB/s; 41.4 again and
+// again, part of them in the last-level cache), 333 rows of 100003 32 us (133 MB, 4.2
+// TB/s) and 4.6 for the join.  bfloat16 halves the bytes but not the work of an entry
+// (seven vector operations and a power, which costs four): 2048 rows of 32000 30 to 33 us.
 // The best entries add the first threshold of every wave (a sort, 0.8 us) and
-// the joins: at 2048 x 32000, float32 +2.5 us for one entry and +18 for 20,
-// bfloat16 +8.5 and +26.  Few rows are latency: 16 rows of 131072 bfloat16 with 20
-// entries 10.5 + 5.4 us, one row of 32000 float32 with five 11.2.
+// the joins: at 2048 x 32000, float32 +4 us for one entry and +20 for 20,
+// bfloat16 +9 and +28.  Few rows are latency: 16 rows of 131072 bfloat16 with 20
+// entries 10.4 + 5.1 us, one row of 32000 float32 with five 11.2.
 #include <algorithm>
 
 #include "common.hpp"

@@ -242,10 +242,11 @@ __device__ __forceinline__ void spread(float2 v, float2 (&o)[GPC]) {
 // U of them at a time, whose loads are all in flight together, or AHEAD: the next
 // one's while this one is multiplied) and their sums
 // are joined through LDS in wave order, so the result does not depend on timing.
-// Bound by the stream of records: one token through 28672 x 8192 takes 22.4 us
-// (132 MB, 5.9 TB/s; 28 us where other weights pass between calls), 16 tokens
-// through 13824 x 5120, g = 64, 12.0 us (45 MB, 3.7 TB/s: 216 workgroups leave 40
-// CUs idle), 1024 rows over 64 experts of 1024 x 2048, g = 64, 28.5 us (84 MB once;
+// Bound by the stream of records: one token through 28672 x 8192 takes 26.2 us
+// where other weights pass between calls (132 MB, 5.1 TB/s; 22.6 us again and again, half
+// of it in the last-level cache), 16 tokens through 13824 x 5120, g = 64, 11.5 us (45 MB,
+// 3.9 TB/s: 216 workgroups leave 40 CUs idle), 1024 rows over 64 experts of 1024 x 2048,
+// g = 64, 28.4 us (84 MB once;
 // an expert with more than 16 rows is read again for each
 // 16).  Splitting the columns over the waves of a workgroup rather than over
 // workgroups keeps it one launch without partial sums in memory.
@@ -458,7 +459,7 @@ __device__ __forceinline__ uint32_t pack_hi(uint32_t lo, uint32_t hi) {
   return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
-// 2048 x 11008 bfloat16: 10.6 us, 4.3 TB/s.
+// 2048 x 11008 bfloat16: 12.3 us, 3.7 TB/s.
 // Group sums of X, sums[row][kp] (kp: groups in whole records), and float32 X
 // as three bfloat16 planes side by side, planes[row][3][nch * 128], both zero
 // past m; of bfloat16 X a copy if planes is given.  With `rows` row i is X's
@@ -571,8 +572,8 @@ __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory");
 // 4 c + 2), and stage c + 1 is first read in slot 4 c + 3: X is read into
 // registers during the product phase before its own.
 //
-// 2048 rows through 4096 x 11008, g = 128: 173 us, 1.07 PFLOP/s of the product
-// (1.20 with the zero term), the matrix unit busy 60% of the cycles at 1.87 GHz;
+// 2048 rows through 4096 x 11008, g = 128: 171 us, 1.08 PFLOP/s of the product
+// (1.21 with the zero term), the matrix unit busy 65% of the cycles at 1.8 GHz;
 // a plain bfloat16 library product of that shape takes 151 us.  A phase takes
 // 700 to 850 cycles where its products need 512 (640 with the zero term): the
 // load phases (the scaling's 256 cycles, LDS latency) are as long as the
@@ -580,7 +581,8 @@ __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory");
 // load and one product phase a stage (g = 128) measured the same 178 us.
 // A workgroup's start and end run beside no product, so they are kept short: tile
 // arithmetic in 32 bits, the rows' factors fetched at the start, stores whose bounds
-// the buffer descriptor checks (8 experts of 11008 x 4096 over 4096 rows: 472 -> 418 us).
+// the buffer descriptor checks (8 experts of 11008 x 4096 over 4096 rows: 472 -> 418 us
+// when that was done, 392 to 412 by card with the group sums now).
 template <int G, int WT, int WN>
 __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, const uint16_t *__restrict__ X,
                                                                   int64_t ldx, int nt, bool gather, bool compact,

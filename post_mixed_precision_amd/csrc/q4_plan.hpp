@@ -42,9 +42,9 @@ inline int64_t likely_blocks(int64_t r, int64_t e, int64_t n, int64_t tok, int64
 }
 // 64 rows of Y x 512 output rows in place of 128 x 256 (the same work) where that
 // takes fewer rounds of 256 workgroups.
-// 8 experts of 11008 x 4096 over 4096 rows, 6 rounds for 7: 472 us against 523; 64
-// of 4096 x 2048 over 8192, 5 for 6: 286 against 331; with as many rounds the two
-// are alike (8 of 4096 x 4096 over 2048: 142, 141; 8 of 4096 x 11008 over 4096: 509, 501).
+// 8 experts of 11008 x 4096 over 4096 rows, 6 rounds for 7: 390 us against 426; 64
+// of 4096 x 2048 over 8192, 5 for 6: 212 against 240; with as many rounds the two
+// are alike (8 of 4096 x 4096 over 2048: 120, 118; 8 of 4096 x 11008 over 4096: 453, 444).
 inline bool narrow_tiles(int64_t r, int64_t e, int64_t n) {
   return (likely_blocks(r, e, n, 64, 512) + 255) / 256 < (likely_blocks(r, e, n, 128, 256) + 255) / 256;
 }
@@ -95,13 +95,16 @@ inline TileWs tile_ws(int64_t xrows, int64_t r, int64_t e, int64_t n, int64_t m,
 // planes: 5.3), and where columns are split 4 and the traffic of the partial sums.
 // Streaming: 8, and 6600 (float32 3200) records by 16 rows in one us, the sums' join
 // and stores counting as two records.  Measured, tiles - streaming:
-//  - t = 2048, 4096 x 11008: 184 - 737; 1537, 2100 x 384: 14 - 17; 1000, 4096 x 2048: 38 -
-//    44; 500, 2600 x 1024: 24 - 14; 256, 4096 x 4096: 31 - 24; 256, 4096 x 11008: 48 - 54;
-//    130, 4747 x 1088: 25 - 12; 64, 28672 x 8192: 71 - 82; 64, 13824 x 5120: 34 - 29;
-//    float32: 1030, 7425 x 640: 42 - 91; 385, 2309 x 1152: 37 - 20.
-//  - 8 experts of 11008 x 4096 over 192 rows 69 - 70, over 256 68 - 90, over 384 73 -
-//    111; 64 of 1024 x 2048 over 3840 rows 51 - 63; 16 of 4096 x 4096 over 512 rows 74 -
-//    64; 18 of 391 x 1152 over 2222 rows 29 - 21.
+//  - t = 2048, 4096 x 11008: 172 - 388; 1537, 2100 x 384: 14 - 17; 1000, 4096 x 2048: 36 -
+//    43; 500, 2600 x 1024: 24 - 14; 256, 4096 x 4096: 31 - 24; 256, 4096 x 11008: 48 - 54;
+//    130, 4747 x 1088: 25 - 12; 64, 28672 x 8192: 71 - 82; 64, 13824 x 5120: 33 - 28;
+//    float32: 1030, 7425 x 640: 40 - 90; 385, 2309 x 1152: 37 - 20.
+//  - 8 experts of 11008 x 4096 over 256 rows 68 - 87, over 384 72 - 110; 64 of 1024 x
+//    2048 over 3840 rows 40 - 61; 16 of 4096 x 4096 over 512 rows 66 - 65; 18 of 391 x
+//    1152 over 2222 rows 27 - 20.
+//  - Where they choose the slower: streaming, t = 100, 11008 x 4096: 31 - 33; t = 320, 4096 x
+//    4096: 31.7 - 32.5; 8 experts of 11008 x 4096 over 192 rows 64 - 67; and tiles, by more,
+//    for float32 t = 2049, 1500 x 320, g = 64: 29 - 24.
 inline bool use_tiles(int64_t r, int64_t e, int64_t n, int64_t m, bool xbf16) {
   const int64_t nch = q4_chunks(m);
   const bool narrow = narrow_tiles(r, e, n);
