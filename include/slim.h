@@ -437,9 +437,10 @@ int slim_pack4(const uint8_t *codes, const float *scale, const float *zero, int6
  * SLIM_Q4_MAX_N.  Products are exact and summed in float32 per group, groups
  * are scaled and summed in float32, and Y is rounded once; for a given t the
  * order of the sums is fixed.  float32 X enters as three bfloat16 terms: what
- * an entry has below 2^-133 is dropped (entries of 2^-110 or more have none).  Rows of X do not touch each other; a row
- * with an infinity or a NaN gives infinities or NaN.  Results for different t
- * agree to float32 rounding, not bit for bit.  Workspace:
+ * an entry has below 2^-133 is dropped (entries of 2^-110 or more have none).
+ * Rows of X do not touch each other; a row with an infinity or a NaN gives
+ * infinities or NaN.  Results for different t agree to float32 rounding, not
+ * bit for bit.  Workspace:
  * slim_q4_linear_workspace(...) bytes, which may be 0 (ws is then ignored).
  * ---------------------------------------------------------------------- */
 size_t slim_q4_linear_workspace(int64_t t, int64_t n, int64_t m, int group, int xdt);

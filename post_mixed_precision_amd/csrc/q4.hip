@@ -5,9 +5,9 @@
 //   P[a, i, j] = sum_{c in group j} X[a, c] q[i, c],   Xs[a, j] = sum_{c in group j} X[a, c].
 //
 // A code below 16 is exact in bfloat16, X enters as stored (float32 X as three
-// bfloat16 terms whose sum is exact from 2^-110 on), and P and Xs come from the bfloat16 MFMA
-// with float32 sums, so nothing is rounded before the float32 group sums; Y is
-// rounded once at the end.  Folding s into a bfloat16 weight would save the
+// bfloat16 terms whose sum is exact from 2^-110 on), and P and Xs come from the
+// bfloat16 MFMA with float32 sums, so nothing is rounded before the float32 group
+// sums; Y is rounded once at the end.  Folding s into a bfloat16 weight would save the
 // per-group scaling but round every weight to 8 bits.
 //
 // Layout (pack4_kernel).  A record holds 16 rows x 128 columns: word 4 l + i
@@ -243,12 +243,11 @@ __device__ __forceinline__ void spread(float2 v, float2 (&o)[GPC]) {
 // one's while this one is multiplied) and their sums
 // are joined through LDS in wave order, so the result does not depend on timing.
 // Bound by the stream of records: one token through 28672 x 8192 takes 26.2 us
-// where other weights pass between calls (132 MB, 5.1 TB/s; 22.6 us again and again, half
-// of it in the last-level cache), 16 tokens through 13824 x 5120, g = 64, 11.5 us (45 MB,
-// 3.9 TB/s: 216 workgroups leave 40 CUs idle), 1024 rows over 64 experts of 1024 x 2048,
-// g = 64, 28.4 us (84 MB once;
-// an expert with more than 16 rows is read again for each
-// 16).  Splitting the columns over the waves of a workgroup rather than over
+// where other weights pass between calls (132 MB, 5.1 TB/s; 22.6 us with the same
+// ones, from the last-level cache), 16 tokens through 13824 x 5120, g = 64, 11.5 us
+// (45 MB, 3.9 TB/s: 216 workgroups leave 40 CUs idle), 1024 rows over 64 experts of
+// 1024 x 2048, g = 64, 28.4 us (84 MB once; an expert with more than 16 rows is read
+// again for each 16).  Splitting the columns over the waves of a workgroup rather than over
 // workgroups keeps it one launch without partial sums in memory.
 // MFMA operands (v_mfma_f32_16x16x32_bf16): A = X (row l % 16, columns
 // 8 (l / 16) .. +7), B = codes (column l % 16 = output row), D element j =
@@ -582,7 +581,7 @@ __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory");
 // A workgroup's start and end run beside no product, so they are kept short: tile
 // arithmetic in 32 bits, the rows' factors fetched at the start, stores whose bounds
 // the buffer descriptor checks (8 experts of 11008 x 4096 over 4096 rows: 472 -> 418 us
-// when that was done, 392 to 412 by card with the group sums now).
+// when that was done; 390 to 412 by card, group sums included).
 template <int G, int WT, int WN>
 __global__ __launch_bounds__(64 * WT * WN, 2) void q4_tile_kernel(Q4Args a, const uint16_t *__restrict__ X,
                                                                   int64_t ldx, int nt, bool gather, bool compact,
@@ -995,13 +994,18 @@ hipError_t tile_go(const Q4Args &a, const TileWs &w, void *ws, hipStream_t st) {
 template <bool XBF16, int G>
 hipError_t stream_pick(const Q4Args &a, hipStream_t st) {
   const StreamShape s = stream_shape(a.r, a.e, a.n, a.m, G, XBF16);
+  const auto is = [&s](int blocks, int tiles, int waves, int records, bool ahead) {
+    return s.blocks == blocks && s.tiles == tiles && s.waves == waves && s.records == records && s.ahead == ahead;
+  };
   if constexpr (XBF16)
-    if (s.tiles == 2) return stream_go<XBF16, G, 4, 2, 4, 1, true>(a, st);
+    if (is(4, 2, 4, 1, true)) return stream_go<XBF16, G, 4, 2, 4, 1, true>(a, st);
   if constexpr (!XBF16 && G == 128)
-    if (s.blocks == 4 && s.waves == 8) return stream_go<XBF16, G, 4, 1, 8, 1, false>(a, st);
-  if (s.blocks == 4)
-    return s.waves == 16 ? stream_go<XBF16, G, 4, 1, 16, 1, false>(a, st) : stream_go<XBF16, G, 4, 1, 4, 1, true>(a, st);
-  return s.blocks == 2 ? stream_go<XBF16, G, 2, 1, 8, 2, false>(a, st) : stream_go<XBF16, G, 1, 1, 8, 2, false>(a, st);
+    if (is(4, 1, 8, 1, false)) return stream_go<XBF16, G, 4, 1, 8, 1, false>(a, st);
+  if (is(4, 1, 16, 1, false)) return stream_go<XBF16, G, 4, 1, 16, 1, false>(a, st);
+  if (is(4, 1, 4, 1, true)) return stream_go<XBF16, G, 4, 1, 4, 1, true>(a, st);
+  if (is(2, 1, 8, 2, false)) return stream_go<XBF16, G, 2, 1, 8, 2, false>(a, st);
+  if (is(1, 1, 8, 2, false)) return stream_go<XBF16, G, 1, 1, 8, 2, false>(a, st);
+  return hipErrorInvalidDeviceFunction;            // a shape of the rules that is not compiled here
 }
 
 template <int G>
