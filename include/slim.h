@@ -440,7 +440,7 @@ int slim_pack4(const uint8_t *codes, const float *scale, const float *zero, int6
  * an entry has below 2^-133 is dropped (entries of 2^-110 or more have none).
  * Rows of X do not touch each other; a row with an infinity or a NaN gives
  * infinities or NaN.  Results for different t agree to float32 rounding, not
- * bit for bit.  Workspace:
+ * bit for bit.  Y must not overlap an input.  Workspace:
  * slim_q4_linear_workspace(...) bytes, which may be 0 (ws is then ignored).
  * ---------------------------------------------------------------------- */
 size_t slim_q4_linear_workspace(int64_t t, int64_t n, int64_t m, int group, int xdt);
@@ -461,7 +461,7 @@ int slim_q4_linear(const void *X, int xdt, int64_t t, int64_t m, const uint32_t 
  * they were.  The bounds are read on the device, nothing is copied to the
  * host.  Offsets that decrease or leave 0 .. r make every row of Y NaN, and a
  * row whose rows[a] is outside 0 .. tx - 1 is NaN (neither reads out of range).
- * Numerics as for slim_q4_linear.  1 <= e <= SLIM_Q4_MAX_EXPERTS,
+ * Numerics as for slim_q4_linear; Y must not overlap an input.  1 <= e <= SLIM_Q4_MAX_EXPERTS,
  * 0 <= r <= SLIM_Q4_MAX_ROWS (0 is a no-op), tx >= 1 unless r = 0.  The
  * workspace's size does not know whether rows is NULL: it is what a gather needs.
  * ---------------------------------------------------------------------- */

@@ -568,6 +568,14 @@ def _ready(dev, *ts):
             raise SlimError("tensors must live in GPU memory")
 
 
+def _apart(Y, **ins):
+    """Y, which is written while other workgroups still read, shares no byte with an input."""
+    a, b = Y.data_ptr(), Y.data_ptr() + Y.numel() * Y.element_size()
+    for name, t in ins.items():
+        if t is not None and a < b and a < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < b:
+            raise SlimError(f"Y: overlaps {name}")
+
+
 def _raw_stream(index: int) -> int:
     """The current stream of a device as an integer (no Stream object)."""
     return _torch()._C._cuda_getCurrentRawStream(index)
@@ -575,7 +583,7 @@ def _raw_stream(index: int) -> int:
 
 def q4_linear(X, packed, n: int, group: int, out_dtype=None, Y=None):
     """Y = X W_hat^T from pack4's words: X [t, m] bf16/f32, t <= 65536 -> Y [t, n] in out_dtype
-    (float32 by default; bfloat16 is rounded once at the end).  Y may be given."""
+    (float32 by default; bfloat16 is rounded once at the end).  Y may be given, apart from X."""
     torch = _torch()
     lib = load_library()
     out_dtype = torch.float32 if out_dtype is None else out_dtype
@@ -585,6 +593,7 @@ def q4_linear(X, packed, n: int, group: int, out_dtype=None, Y=None):
     packed = _arg(packed, "packed", (_words4(1, n, m, group),), (torch.int32,))
     if Y is not None:
         Y = _arg(Y, "Y", (t, n), (out_dtype,))
+        _apart(Y, X=X, packed=packed)
     dev = X.device
     _ready(dev, X, packed, Y)
     if dev.index != torch.cuda.current_device():
@@ -606,7 +615,8 @@ def q4_experts(X, offsets, packed, n: int, group: int, rows=None, row_scale=None
     """Rows sorted by expert through their experts' layers: offsets int32 [e + 1] (rows
     offsets[j] .. offsets[j+1] - 1 belong to expert j; read on the device), packed = pack4 of the e
     matrices.  rows int32 [r] gathers row a from X's row rows[a]; row_scale float32 [r] scales row a.
-    -> Y [r, n] in out_dtype; rows outside the offsets are not written (a given Y keeps them)."""
+    -> Y [r, n] in out_dtype; rows outside the offsets are not written (a given Y, apart from
+    the inputs, keeps them)."""
     torch = _torch()
     lib = load_library()
     out_dtype = torch.float32 if out_dtype is None else out_dtype
@@ -626,6 +636,7 @@ def q4_experts(X, offsets, packed, n: int, group: int, rows=None, row_scale=None
     packed = _arg(packed, "packed", (_words4(e, n, m, group),), (torch.int32,))
     if Y is not None:
         Y = _arg(Y, "Y", (r, n), (out_dtype,))
+        _apart(Y, X=X, offsets=offsets, packed=packed, rows=rows, row_scale=row_scale)
     dev = X.device
     _ready(dev, X, offsets, packed, rows, row_scale, Y)
     if dev.index != torch.cuda.current_device():

@@ -240,6 +240,19 @@ def test_workspace_of_far_rows_in_order(lib):
     assert lib.slim_q4_linear_workspace(t, 4096, m, 32, 0) == _tile_bytes(t, m, 32, 0, True)
 
 
+def test_outputs_over_inputs_are_refused(L):
+    X, W = _f(16, 128), _i(288)
+    raises(L, lambda: L.q4_linear(X[:, :].view(16, 128), _i(288 * 8), 128, 128, Y=X), "Y", "overlaps X")
+    raises(L, lambda: L.q4_linear(X[:4], _i(288 * 8), 128, 128, Y=X[3:7]), "Y", "overlaps X")
+    raises(L, lambda: L.q4_linear(X[:4], _i(288 * 8), 128, 128, Y=X[4:8]), "GPU")        # side by side
+    raises(L, lambda: L.q4_linear(X[4:], _i(288 * 8), 128, 128, Y=X[:12]), "Y", "overlaps X")
+    raises(L, lambda: L.q4_linear(_f(2, 128), W, 16, 128, Y=W[:32].view(torch.float32).view(2, 16)), "Y", "packed")
+    off, gates = _i(2), _f(32)
+    raises(L, lambda: L.q4_experts(X[:2], off, _i(288 * 8), 128, 128, Y=X[1:3]), "Y", "overlaps X")
+    raises(L, lambda: L.q4_experts(X[:2], off, W, 16, 128, row_scale=gates[:2], Y=gates.view(2, 16)), "Y", "row_scale")
+    raises(L, lambda: L.q4_experts(_f(0, 128), off, W, 16, 128, Y=_f(0, 16)), "GPU")     # nothing overlaps nothing
+
+
 def test_score_tokens_refuses_before_it_allocates(L):
     import post_mixed_precision_amd as slim
     X, ids, W = _bf(4, 128), torch.zeros(4, dtype=torch.int64), _i(288)
