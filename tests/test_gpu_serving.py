@@ -984,3 +984,62 @@ def test_q4_linear_of_tiny_rows(slim, t, n, m, g, xdt, size):
     bound += 2.0 ** -149 * (3 * g + 32 * 2) * np.abs(scale[0].astype(np.float64)).sum(axis=1)
     err = np.abs(Y.double().cpu().numpy() - exact)
     assert np.all(err <= bound), float(np.max(err / bound))
+
+
+# ------------------------------------------------------------------ two calls at once
+def test_two_threads_on_two_streams(slim):
+    """Every operator from two host threads, each on a stream of its own, against what it gives alone."""
+    import threading
+    n, m, g = 1410, 576, 64
+    codes, scale, zero = _layer(120, 2, n, m, g)
+    packed = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), g)
+    one = slim.pack4(_gpu(codes[0]), _gpu(scale[0]), _gpu(zero[0]), g)
+    big, small = _x(121, 2310, m, "bf16").to("cuda:0"), _x(122, 5, m, "f32").to("cuda:0")
+    off = torch.tensor([0, 1000, 2310], dtype=torch.int32, device="cuda:0")
+    ids = torch.arange(2310, device="cuda:0") % n
+    logits = _logits(123, 3, 40000, 0, 0, "f32").to("cuda:0")
+    assert slim.load_library().slim_q4_linear_workspace(2310, n, m, g, 1) > 0       # a tile kernel
+    assert slim.load_library().slim_token_logprobs_workspace(3, 40000, 4) > 0       # rows in segments
+
+    def calls():
+        s = slim.score_tokens(big, ids, one, n, g, top=3, block=1000)
+        p = slim.token_logprobs(logits, ids[:3], top=4)
+        return [slim.q4_linear(big, one, n, g), slim.q4_linear(small, one, n, g),
+                slim.q4_experts(big, off, packed, n, g), *s.values(), *p.values()]
+    want = calls()
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(5):
+                got = calls()
+                stream.synchronize()
+                bad.extend(i for i, (a, b) in enumerate(zip(got, want)) if not torch.equal(a, b))
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not bad, bad
+
+
+@pytest.mark.parametrize("how", ["gptq", "hinv"])
+def test_nibbles_of_every_way_to_quantize(slim, how):
+    n, m, g, avg = 96, 512, 128, 3
+    W = (0.02 * _x(130, n, m, "f32")).to(torch.bfloat16).to("cuda:0")
+    X = _x(131, 300, m, "bf16").to("cuda:0")
+    if how == "gptq":
+        q = slim.quantize_layer(X, W, g, avg, gptq=True, nibbles=True)
+    else:
+        first = slim.quantize_layer(X, W, g, avg)
+        q = slim.quantize_layer(X, W, g, avg, H=first["H"], hinv=first["hinv"], nibbles=True)
+    assert int(q["info"]) == 0 and int(q["pack_info"]) == 0 and int(q["codes"].max()) < 16
+    codes, scale, zero = (q[k].cpu().numpy() for k in ("codes", "scale", "zero"))
+    np.testing.assert_array_equal(q["packed4"].cpu().numpy().view(np.uint32),
+                                  oracle.pack4(codes[None], scale[None], zero[None], g))
+    x = X[:9].double().cpu().numpy()
+    exact = x @ oracle.q4_weight(codes, scale, zero, g).T
+    Y = slim.q4_linear(X[:9].contiguous(), q["packed4"], n, g).double().cpu().numpy()
+    assert np.all(np.abs(Y - exact) <= _bound(x, codes, scale, zero, g, "bf16", "f32", exact))
