@@ -69,6 +69,8 @@ def test_pack4_layout(slim, e, n, m, g):
     assert info.item() == 1
 
 
+# Sizes of all kinds.  The headings say what the cases were written for; the choice of kernel has moved
+# some of them since, and LINEAR_KERNELS and EXPERT_KERNELS below name the kernel that runs.
 LINEAR = [
     (1, 16, 128, 128, "bf16", "f32"),
     (1, 1, 32, 32, "f32", "bf16"),           # one output, a quarter of a record
