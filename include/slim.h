@@ -23,6 +23,10 @@
  *   slim_q4_linear      Y = X W_hat^T read from that buffer                    (FAQ: deployment)
  *   slim_q4_experts     the same grouped by expert over sorted rows            (evaluation: Mixtral)
  *   slim_token_logprobs log probabilities, entropy and best entries of logits  (evaluation: perplexity)
+ *   slim_kv4_append     keys and values into a paged 4-bit cache, rotated on the way
+ *   slim_kv4_read       the values given slots of it stand for
+ *   slim_kv4_attention  attention over it, single tokens to prompts
+ *   slim_verify_draft   drafted tokens against the target's probabilities
  *
  * Conventions shared by every call:
  *  - Pointers are DEVICE pointers unless the parameter says "host".  Arrays
@@ -497,6 +501,126 @@ size_t slim_token_logprobs_workspace(int64_t t, int64_t v, int top);
 int slim_token_logprobs(const void *logits, int ldt, int64_t t, int64_t v, int64_t ld, const int64_t *ids, int top,
                         float *logprob, float *entropy, float *top_logprob, int32_t *top_id, void *ws,
                         size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Keys and values in four bits: a paged cache of what the layers' quantizer
+ * leaves of a context (the asymmetric uniform quantizer of the weights, per
+ * token, head and group of g channels).
+ *
+ *   low  = min x rounded down to bfloat16
+ *   step = fl((max x - low) / 15) rounded up to bfloat16, at least 2^-126 unless it is 0
+ *   code = clamp(rint(fl(fl(x - low) fl(1 / step))), 0, 15)    (0 if step is 0)
+ *   a slot stands for fl(code step + low)
+ *
+ * in float32.  A group with an infinity or a NaN, or whose step or low would
+ * be infinite, stands for NaN throughout.
+ *
+ * cache: uint32 [pages, heads, slim_kv4_words(page, dim, g)], 16-byte aligned;
+ * page (tokens a page) is 16, 32, 64, 128 or 256, dim 64, 128 or 256, g 32, 64
+ * or 128, at most dim.  Slot s is token s % page of page s / page; pages
+ * * page <= SLIM_KV4_MAX_SLOTS, heads <= SLIM_KV4_MAX_HEADS.  Record x of a
+ * head's page holds its tokens 16 x .. +15 in 4 dim + 32 (dim / g) words:
+ *   word (16 lg + t) (dim / 32) + j (lg < 4, t < 16, j < dim / 32): token t's key, channels c = 32 j + 8 lg:
+ *     byte b is the code of channel c + b plus 16 times that of c + 4 + b
+ *   words 2 dim + (16 lg + r) (dim / 32) + a: byte b has token 4 lg + b's value, the code of channel
+ *     32 a + 2 r plus 16 times that of 32 a + 2 r + 1
+ *   words 4 dim + 16 q + t: the key's step (low half) and low (high half) of group q, bfloat16 bits;
+ *   16 (dim / g) words further the value's
+ *
+ * slim_kv4_append: k, v [t, heads, dim] in dtype xdt, strides in elements
+ * (channels are adjacent).  Token i goes to slots[i] (int32); a negative slot
+ * and one past the cache is skipped, and the slots of a call must differ (else
+ * what the shared slot holds is undefined).  Nothing else of the cache is
+ * written.  With rotary (float32 [npos, rot], dense: cosines of the rot / 2
+ * pairs, then sines; rot even, 2 <= rot <= dim) the first rot channels of
+ * every key are turned by row positions[i] (int32):
+ *   (x, y) -> (x cos - y sin, y cos + x sin),
+ * a pair being channels (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved.
+ * In float64, rounded to float32 once; a position outside 0 .. npos - 1 makes
+ * the key NaN.  q (may be NULL, with hq = 0): [t, hq, dim], turned alike into
+ * q_out (dense, xdt, 16-byte aligned), whatever its slot; q_out must not
+ * overlap an input.  0 <= t <= SLIM_KV4_MAX_T.
+ *
+ * slim_kv4_read: k_out, v_out [t, heads, dim] dense in dtype odt, 16-byte
+ * aligned (bfloat16: rounded to nearest): what slots[i] stands for; 0 for a
+ * negative slot, NaN for one past the cache.
+ * ---------------------------------------------------------------------- */
+#define SLIM_KV4_MAX_SLOTS (1 << 30)
+#define SLIM_KV4_MAX_HEADS 1024
+#define SLIM_KV4_MAX_T (1 << 20)
+int64_t slim_kv4_words(int page, int dim, int group);   /* of one head's page; -1: out of range */
+int slim_kv4_append(const void *k, int64_t k_row, int64_t k_head, const void *v, int64_t v_row, int64_t v_head,
+                    int xdt, int64_t t, int64_t heads, int dim, int group, const int32_t *slots, uint32_t *cache,
+                    int64_t pages, int page, const float *rotary, int64_t npos, int rot, int interleaved,
+                    const int32_t *positions, const void *q, int64_t hq, int64_t q_row, int64_t q_head, void *q_out,
+                    void *stream);
+int slim_kv4_read(const int32_t *slots, int64_t t, const uint32_t *cache, int64_t pages, int page, int64_t heads,
+                  int dim, int group, void *k_out, void *v_out, int odt, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over the 4-bit cache.
+ *
+ *   out[i, h, :] = sum_s softmax_s(scale q[i, h, :] . k[s, h', :]) v[s, h', :],   h' = h / (hq / heads)
+ *
+ * over the tokens s of query token i's sequence.  Sequence x has lengths[x]
+ * tokens (int32), the query tokens being its last: causal, the j-th of its n
+ * query tokens attends to s <= lengths[x] - n + j, otherwise to all.  Token s
+ * is token s % page of page table[x, s / page] (int32 [b, per]).  q, out: [tq,
+ * hq, dim] dense, 16-byte aligned, in dtypes qdt and odt; hq a multiple of
+ * heads.  Sequence x has query tokens offsets[x] .. offsets[x+1] - 1 (int32
+ * [b + 1], read on the device), or tq / b each if offsets is NULL.  Rows
+ * outside the offsets are left as they were; offsets that decrease or leave 0
+ * .. tq make every row NaN.  A row that attends to nothing (length 0 or less,
+ * more query tokens than tokens) is 0; a length past per * page makes the
+ * sequence's rows NaN, and a page outside 0 .. pages - 1 the rows that reach it.
+ * What lies past a length, or after a row's last token, does not matter, NaN included.
+ *
+ * Codes enter exactly, steps and low ends are applied in float32, sums and
+ * the softmax are float32.  The weights of the second product (probability
+ * times step) are rounded to bfloat16 if q is bfloat16; float32 q and those
+ * weights enter as three bfloat16 terms otherwise (what lies below 2^-133 is
+ * dropped).  The result is rounded once.  For given sizes the order of the
+ * sums is fixed.  out must not overlap an input.  1 <= b <= tq unless tq = 0
+ * (a no-op), tq <= SLIM_KV4_MAX_T, hq <= SLIM_KV4_MAX_HEADS, scale finite.
+ * Workspace: slim_kv4_attention_workspace(...) bytes, which may be 0.
+ * ---------------------------------------------------------------------- */
+#define SLIM_KV4_MAX_SEQS 65536
+size_t slim_kv4_attention_workspace(int64_t b, int64_t tq, int uneven, int64_t hq, int64_t heads, int dim,
+                                    int64_t per, int page, int qdt);
+int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uint32_t *cache, int64_t pages, int page,
+                       int64_t heads, int dim, int group, const int32_t *table, int64_t b, int64_t per,
+                       const int32_t *lengths, const int32_t *offsets, double scale, int causal, void *out, int odt,
+                       void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Drafted tokens against the target's probabilities (speculative sampling),
+ * from given random numbers.
+ *
+ * target: [b, k + 1, v] logits, draft: [b, k, v] logits or NULL (then the
+ * draft's probability of its token is 1), dtype ldt, strides in elements (row
+ * >= v, entries adjacent, aligned to an element).  tokens: int64 [b, k], the
+ * drafted tokens; the first negative one ends a sequence's draft.  uniform:
+ * float32 [b, k + 1] in [0, 1).  With p_j, q_j the softmax of target[j] /
+ * temperature and draft[j] / temperature:
+ *   token j is accepted while uniform[j] q_j(token) < p_j(token);
+ *   after the accepted ones comes a token drawn from max(p_j - q_j, 0) (the j-th was refused) or from p_j (none
+ *   was): the least index whose running sum exceeds uniform[k] times the sum
+ * accepted: int32 [b]; ids: int64 [b, k + 1]: the accepted tokens, the drawn
+ * one, then -1.  Everything is computed in float64.  A token >= v is refused.
+ * A row without a distribution (a NaN or +inf among its logits, or nothing but
+ * -inf) accepts nothing; if there is nothing to draw from (such a row, or p_j
+ * nowhere above q_j) the drawn id is -1.
+ * 0 <= b <= SLIM_DRAFT_MAX_B (0 is a no-op), 1 <= k <= SLIM_DRAFT_MAX_K,
+ * 1 <= v <= SLIM_LOGPROB_MAX_V, b (2 k + 1) v <= 2^40, temperature > 0.  Workspace:
+ * slim_verify_draft_workspace(b, k, v) bytes.
+ * ---------------------------------------------------------------------- */
+#define SLIM_DRAFT_MAX_B 65536
+#define SLIM_DRAFT_MAX_K 32
+size_t slim_verify_draft_workspace(int64_t b, int k, int64_t v);
+int slim_verify_draft(const void *target, int64_t t_seq, int64_t t_row, const void *draft, int64_t d_seq,
+                      int64_t d_row, int ldt, int64_t b, int k, int64_t v, const int64_t *tokens,
+                      const float *uniform, double temperature, int32_t *accepted, int64_t *ids, void *ws,
+                      size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * Kernel timing (instrumentation, not part of the method).  When enabled,

@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(HERE, "libslim.so")
 
 SLIM_F32, SLIM_BF16 = 0, 1
 LOGPROB_MAX_TOP = 64    # SLIM_LOGPROB_MAX_TOP
+KV4_MAX_SLOTS, KV4_MAX_HEADS, KV4_MAX_T, KV4_MAX_SEQS = 1 << 30, 1024, 1 << 20, 65536    # SLIM_KV4_MAX_*
+DRAFT_MAX_K = 32        # SLIM_DRAFT_MAX_K
 STATUS = {0: "SLIM_OK", -1: "SLIM_E_NULL", -2: "SLIM_E_SHAPE", -3: "SLIM_E_DTYPE",
           -4: "SLIM_E_PARAM", -5: "SLIM_E_WORKSPACE", -6: "SLIM_E_HIP", -7: "SLIM_E_ALIGN"}
 
@@ -72,6 +74,19 @@ _SIGS = {
     "slim_token_logprobs_workspace": (_c_sz, [_c_i64, _c_i64, _c_int]),
     "slim_token_logprobs": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_int, _c_vp, _c_vp, _c_vp,
                                      _c_vp, _c_vp, _c_sz, _c_vp]),
+    "slim_kv4_words": (_c_i64, [_c_int, _c_int, _c_int]),
+    "slim_kv4_append": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _c_int,
+                                 _c_vp, _c_vp, _c_i64, _c_int, _c_vp, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_i64,
+                                 _c_i64, _c_i64, _c_vp, _c_vp]),
+    "slim_kv4_read": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_int,
+                               _c_vp]),
+    "slim_kv4_attention_workspace": (_c_sz, [_c_i64, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _c_i64, _c_int, _c_int]),
+    "slim_kv4_attention": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_int, _c_int,
+                                    _c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_dbl, _c_int, _c_vp, _c_int, _c_vp, _c_sz,
+                                    _c_vp]),
+    "slim_verify_draft_workspace": (_c_sz, [_c_i64, _c_int, _c_i64]),
+    "slim_verify_draft": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_int, _c_i64, _c_int, _c_i64,
+                                   _c_vp, _c_vp, _c_dbl, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
     "slim_timing_enable": (_c_int, [_c_int]),
     "slim_timing_select": (_c_int, [ctypes.c_char_p, _c_int]),
     "slim_timing_reset": (_c_int, []),
@@ -700,6 +715,263 @@ def token_logprobs(logits, ids, top: int = 0):
     if st:
         check(st, "slim_token_logprobs")
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv4_page(words: int, dim: int, group: int) -> int:
+    """Tokens a page, from the words of one head's page."""
+    lib = load_library()
+    for page in (16, 32, 64, 128, 256):
+        if words == lib.slim_kv4_words(page, dim, group):
+            return page
+    raise SlimError(f"cache: {words} words a head are no page of {dim} channels in groups of {group} "
+                    "(channels: 64, 128 or 256; groups: 32, 64 or 128, at most the channels)")
+
+
+def kv4_cache(pages: int, heads: int, dim: int, group: int, page: int = 64, device="cuda"):
+    """An empty 4-bit cache: int32 words [pages, heads, slim_kv4_words] for kv4_append and
+    kv4_attention.  A page holds `page` tokens (16, 32, 64, 128 or 256) of `heads` key and value
+    heads of dim channels (64, 128 or 256) in groups of 32, 64 or 128."""
+    torch = _torch()
+    words = load_library().slim_kv4_words(page, dim, group)
+    if words < 0:
+        raise SlimError(f"no cache of pages of {page} tokens, {dim} channels and groups of {group}")
+    if not (1 <= heads <= KV4_MAX_HEADS and 1 <= pages <= KV4_MAX_SLOTS // page):
+        raise SlimError(f"{pages} pages of {page} tokens and {heads} heads are out of range")
+    return torch.zeros((pages, heads, words), dtype=torch.int32, device=device)
+
+
+def _kv4_heads(t, name: str, shape, dtype):
+    """[tokens, heads, dim] rows, strided but for the channels -> their strides."""
+    t = _arg(t, name, shape, (dtype,))
+    row, head, step = t.stride()
+    if t.numel() == 0:
+        return 0, 0
+    if step != 1 or row < 0 or head < 0:
+        raise SlimError(f"{name}: a head's channels must be contiguous")
+    return (0 if t.shape[0] == 1 else row), (0 if t.shape[1] == 1 else head)
+
+
+def _span(t):
+    """First and last byte of a tensor with nonnegative strides."""
+    a = t.data_ptr()
+    n = 1
+    for size, step in zip(t.shape, t.stride()):
+        if size == 0:
+            return a, a
+        n += (size - 1) * step
+    return a, a + n * t.element_size()
+
+
+def _outside(Y, yname: str, **ins):
+    """Y, which is written while other workgroups still read, shares no byte with an input."""
+    a, b = _span(Y)
+    for name, t in ins.items():
+        if t is not None:
+            lo, hi = _span(t)
+            if a < hi and lo < b:
+                raise SlimError(f"{yname}: overlaps {name}")
+
+
+def kv4_append(k, v, slots, cache, group: int, rotary=None, positions=None, interleaved: bool = False, q=None):
+    """Keys and values of new tokens into a kv4_cache: k, v [t, heads, dim] bf16/f32 (views of a fused
+    projection will do: channels adjacent, any other strides), slots int32 [t] (page * tokens a page
+    + place, all different; negative ones are skipped).  With rotary (float32 [positions, rot]: cosines, then
+    sines) the first rot channels of the keys are turned by rows positions (int32 [t]), pairs half
+    of rot apart, or adjacent if interleaved, and so are q's [t, query heads, dim], which are returned
+    (in q's dtype).  Writes the slots given and nothing else."""
+    torch = _torch()
+    lib = load_library()
+    k = _arg(k, "k", (None, None, None), _float_types())
+    t, heads, dim = k.shape
+    cache = _arg(cache, "cache", (None, heads, None), (torch.int32,))
+    page = _kv4_page(cache.shape[2], dim, group)
+    krow, khead = _kv4_heads(k, "k", None, k.dtype)
+    vrow, vhead = _kv4_heads(v, "v", (t, heads, dim), k.dtype)
+    slots = _arg(slots, "slots", (t,), (torch.int32,))
+    rot = npos = qrow = qhead = hq = 0
+    if (rotary is None) != (positions is None):
+        raise SlimError("rotary and positions are given together")
+    if rotary is not None:
+        rotary = _arg(rotary, "rotary", (None, None), (torch.float32,))
+        npos, rot = rotary.shape
+        if npos < 1 or rot < 2 or rot > dim or rot % 2:
+            raise SlimError(f"rotary: shape {tuple(rotary.shape)}, expected [positions, an even number up to {dim}]")
+        positions = _arg(positions, "positions", (t,), (torch.int32,))
+    if q is not None:
+        qrow, qhead = _kv4_heads(q, "q", (t, None, dim), k.dtype)
+        hq = q.shape[1]
+        if hq > KV4_MAX_HEADS:
+            raise SlimError(f"q: {hq} heads, at most {KV4_MAX_HEADS}")
+    if t > KV4_MAX_T:
+        raise SlimError(f"k: {t} tokens, at most {KV4_MAX_T}")
+    dev = k.device
+    _ready(dev, slots, cache, rotary, positions)
+    for x in (k, v, q):
+        if x is not None and x.device != dev:
+            raise SlimError(f"tensors live on different devices: {dev}, {x.device}")
+    if dev.type != "cuda":
+        raise SlimError("tensors must live in GPU memory")
+    _outside(cache, "cache", k=k, v=v, q=q, slots=slots, rotary=rotary, positions=positions)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv4_append(k, v, slots, cache, group, rotary, positions, interleaved, q)
+    out = None if q is None else torch.empty((t, hq, dim), dtype=k.dtype, device=dev)
+    st = lib.slim_kv4_append(k.data_ptr(), krow, khead, v.data_ptr(), vrow, vhead, _dtype_code(k), t, heads, dim, group,
+                             slots.data_ptr(), cache.data_ptr(), cache.shape[0], page,
+                             None if rotary is None else rotary.data_ptr(), npos, rot, 1 if interleaved else 0,
+                             None if rotary is None else positions.data_ptr(), q.data_ptr() if hq else None, hq, qrow,
+                             qhead, out.data_ptr() if hq else None, _raw_stream(dev.index))
+    if st:
+        check(st, "slim_kv4_append")
+    return out
+
+
+def kv4_read(slots, cache, dim: int, group: int, out_dtype=None):
+    """What slots (int32 [t]) of a kv4_cache stand for -> (k, v) [t, heads, dim] in out_dtype (float32
+    by default, exact; bfloat16 is rounded): 0 for a negative slot, NaN for one past the cache."""
+    torch = _torch()
+    lib = load_library()
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    code = _out_code(out_dtype)
+    slots = _arg(slots, "slots", (None,), (torch.int32,))
+    cache = _arg(cache, "cache", (None, None, None), (torch.int32,))
+    page = _kv4_page(cache.shape[2], dim, group)
+    t, heads = slots.shape[0], cache.shape[1]
+    if t > KV4_MAX_T:
+        raise SlimError(f"slots: {t} of them, at most {KV4_MAX_T}")
+    dev = cache.device
+    _ready(dev, slots, cache)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv4_read(slots, cache, dim, group, out_dtype)
+    k, v = torch.empty((2, t, heads, dim), dtype=out_dtype, device=dev)
+    st = lib.slim_kv4_read(slots.data_ptr(), t, cache.data_ptr(), cache.shape[0], page, heads, dim, group, k.data_ptr(),
+                           v.data_ptr(), code, _raw_stream(dev.index))
+    if st:
+        check(st, "slim_kv4_read")
+    return k, v
+
+
+def kv4_attention(q, cache, table, lengths, group: int, offsets=None, scale=None, causal: bool = True, out_dtype=None,
+                  out=None):
+    """Attention over a kv4_cache.  table int32 [b, pages a sequence]: the pages of each sequence in
+    order; lengths int32 [b]: its tokens, the queries' own among them.  q bf16/f32 [b, n, query heads,
+    dim]: the last n tokens of each sequence; or [tokens, query heads, dim] with offsets int32 [b + 1]
+    (sequence x has the query tokens offsets[x] .. offsets[x+1] - 1; read on the device).  Query heads: a multiple
+    of the cache's heads, each of which serves as many neighbours.  A query attends to its token and
+    those before it, or to all if not causal; scale: dim ** -0.5 by default.  -> out, shaped as q, in
+    out_dtype (q's by default).  Rows that attend to nothing are 0; rows outside the offsets are
+    not written (a given out, apart from the inputs, keeps them)."""
+    torch = _torch()
+    lib = load_library()
+    q = _arg(q, "q", (None, None, None, None) if offsets is None else (None, None, None), _float_types())
+    hq, dim = q.shape[-2:]
+    cache = _arg(cache, "cache", (None, None, None), (torch.int32,))
+    pages, heads = cache.shape[:2]
+    page = _kv4_page(cache.shape[2], dim, group)
+    table = _arg(table, "table", (None, None), (torch.int32,))
+    b, per = table.shape
+    lengths = _arg(lengths, "lengths", (b,), (torch.int32,))
+    if offsets is None:
+        if q.shape[0] != b:
+            raise SlimError(f"q: shape {tuple(q.shape)}, expected {b} sequences")
+        tq = b * q.shape[1]
+    else:
+        offsets = _arg(offsets, "offsets", (b + 1,), (torch.int32,))
+        tq = q.shape[0]
+    if heads < 1 or hq < 1 or hq % heads or hq > KV4_MAX_HEADS:
+        raise SlimError(f"q: {hq} heads, expected a multiple of the cache's {heads}, at most {KV4_MAX_HEADS}")
+    if b < 1 or b > KV4_MAX_SEQS or tq > KV4_MAX_T or per < 1 or per > KV4_MAX_SLOTS // page:
+        raise SlimError(f"table: shape {tuple(table.shape)} with {tq} query tokens is out of range")
+    out_dtype = q.dtype if out_dtype is None else out_dtype
+    ocode = _out_code(out_dtype)
+    if out is not None:
+        out = _arg(out, "out", tuple(q.shape), (out_dtype,))
+    dev = q.device
+    _ready(dev, q, cache, table, lengths, offsets, out)
+    if out is not None:
+        _outside(out, "out", q=q, cache=cache, table=table, lengths=lengths, offsets=offsets)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv4_attention(q, cache, table, lengths, group, offsets, scale, causal, out_dtype, out)
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+    qcode = _dtype_code(q)
+    need = _need("slim_kv4_attention_workspace", b, tq, 0 if offsets is None else 1, hq, heads, dim, per, page, qcode)
+    ws = _ws(need, dev) if need else None
+    st = lib.slim_kv4_attention(q.data_ptr(), qcode, tq, hq, cache.data_ptr(), pages, page, heads, dim, group,
+                                table.data_ptr(), b, per, lengths.data_ptr(),
+                                None if offsets is None else offsets.data_ptr(),
+                                dim ** -0.5 if scale is None else float(scale), 1 if causal else 0, out.data_ptr(),
+                                ocode, ws.data_ptr() if need else None, need, _raw_stream(dev.index))
+    if st:
+        check(st, "slim_kv4_attention")
+    return out
+
+
+def _draft_rows(t, name: str, rows: int):
+    """Strides of [b, rows, v] logits, strided but for a row's entries."""
+    b, _, v = t.shape
+    seq, row, step = t.stride()
+    if b == 0:
+        return 0, v
+    if b == 1:
+        seq = 0
+    if rows == 1:
+        row = v
+    if (v > 1 and step != 1) or row < v or seq < 0:
+        raise SlimError(f"{name}: a row's entries must be contiguous and rows must not overlap")
+    return seq, row
+
+
+def verify_draft(target, tokens, uniform, draft=None, temperature: float = 1.0):
+    """Drafted tokens against the target's probabilities, from given random numbers.  target [b, k + 1, v]
+    and draft [b, k, v] logits bf16/f32 (rows may be strided; draft None: tokens drafted without
+    probabilities), tokens int64 [b, k] (a negative one ends a sequence's draft), uniform float32
+    [b, k + 1] in [0, 1).  With p and q the softmax of target and draft over temperature, token j is
+    accepted while uniform[j] q_j(token) < p_j(token); then one is drawn with uniform[k], from
+    max(p_j - q_j, 0) or, after the last, from p -> dict(accepted int32 [b], ids int64 [b, k + 1]: the
+    accepted tokens, the drawn one, then -1).  In float64 throughout."""
+    torch = _torch()
+    lib = load_library()
+    target = _arg(target, "target", (None, None, None), _float_types())
+    b, k1, v = target.shape
+    k = k1 - 1
+    if not 1 <= k <= DRAFT_MAX_K:
+        raise SlimError(f"target: {k1} rows a sequence, expected 2 .. {DRAFT_MAX_K + 1}")
+    if v < 1:
+        raise SlimError("target: no entries")
+    tseq, trow = _draft_rows(target, "target", k1)
+    tokens = _arg(tokens, "tokens", (b, k), (torch.int64,))
+    uniform = _arg(uniform, "uniform", (b, k1), (torch.float32,))
+    dseq = drow = 0
+    if draft is not None:
+        draft = _arg(draft, "draft", (b, k, v), (target.dtype,))
+        dseq, drow = _draft_rows(draft, "draft", k)
+    temperature = float(temperature)
+    if not 0.0 < temperature < float("inf"):
+        raise SlimError(f"temperature {temperature} must be positive and finite")
+    dev = target.device
+    if dev.type != "cuda" or (draft is not None and not draft.is_cuda):
+        raise SlimError("tensors must live in GPU memory")
+    if draft is not None and draft.device != dev:
+        raise SlimError(f"tensors live on different devices: {dev}, {draft.device}")
+    _ready(dev, tokens, uniform)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return verify_draft(target, tokens, uniform, draft, temperature)
+    accepted = torch.empty((b,), dtype=torch.int32, device=dev)
+    ids = torch.empty((b, k1), dtype=torch.int64, device=dev)
+    need = _need("slim_verify_draft_workspace", b, k, v)
+    ws = _ws(need, dev) if need else None
+    st = lib.slim_verify_draft(target.data_ptr(), tseq, trow, None if draft is None else draft.data_ptr(), dseq, drow,
+                               _dtype_code(target), b, k, v, tokens.data_ptr(), uniform.data_ptr(), temperature,
+                               accepted.data_ptr(), ids.data_ptr(), ws.data_ptr() if need else None, need,
+                               _raw_stream(dev.index))
+    if st:
+        check(st, "slim_verify_draft")
+    return {"accepted": accepted, "ids": ids}
 
 
 def tau_table(lam: float = 0.1, n_tau: int = 50) -> np.ndarray:

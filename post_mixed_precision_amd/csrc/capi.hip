@@ -454,6 +454,136 @@ int slim_token_logprobs(const void *logits, int ldt, int64_t t, int64_t v, int64
   return err == hipSuccess ? SLIM_OK : hip_fail(err);
 }
 
+// ---------------------------------------------------------------- 4-bit key/value cache
+int64_t slim_kv4_words(int page, int dim, int group) {
+  return slim::kv4_shape(page, dim, group) ? slim::kv4_page_words(page, dim, group) : -1;
+}
+
+static bool kv4_cache_shape(int64_t pages, int page, int64_t heads, int dim, int group) {
+  return slim::kv4_shape(page, dim, group) && pages >= 1 && pages <= SLIM_KV4_MAX_SLOTS / page && heads >= 1 &&
+         heads <= SLIM_KV4_MAX_HEADS;
+}
+
+// Strides of [t, heads, dim] rows: no negative ones, and no product past 64 bits.
+static bool kv4_strides(int64_t row, int64_t head) {
+  return row >= 0 && head >= 0 && row <= ((int64_t)1 << 40) && head <= ((int64_t)1 << 40);
+}
+
+static slim::Kv4Rows kv4_rows(const void *p, int64_t heads, int64_t row, int64_t head, bool bf16) {
+  const int64_t unit = bf16 ? 8 : 4;
+  return {p, heads, row, head, aligned16(p) && row % unit == 0 && head % unit == 0};
+}
+
+int slim_kv4_append(const void *k, int64_t k_row, int64_t k_head, const void *v, int64_t v_row, int64_t v_head,
+                    int xdt, int64_t t, int64_t heads, int dim, int group, const int32_t *slots, uint32_t *cache,
+                    int64_t pages, int page, const float *rotary, int64_t npos, int rot, int interleaved,
+                    const int32_t *positions, const void *q, int64_t hq, int64_t q_row, int64_t q_head, void *q_out,
+                    void *stream) {
+  if (!valid_dtype(xdt)) return SLIM_E_DTYPE;
+  if (!kv4_cache_shape(pages, page, heads, dim, group) || t < 0 || t > SLIM_KV4_MAX_T || hq < 0 ||
+      hq > SLIM_KV4_MAX_HEADS)
+    return SLIM_E_SHAPE;
+  if (!kv4_strides(k_row, k_head) || !kv4_strides(v_row, v_head) || !kv4_strides(q_row, q_head)) return SLIM_E_SHAPE;
+  if (rotary && (rot < 2 || rot > dim || rot % 2 || npos < 1)) return SLIM_E_SHAPE;
+  if (t == 0) return SLIM_OK;
+  if (!k || !v || !slots || !cache || (rotary && !positions) || (hq > 0 && (!q || !q_out))) return SLIM_E_NULL;
+  const uintptr_t el = xdt == SLIM_BF16 ? 2 : 4;
+  if (!aligned16(cache) || (hq > 0 && !aligned16(q_out)) || (uintptr_t)k % el || (uintptr_t)v % el ||
+      (hq > 0 && (uintptr_t)q % el))
+    return SLIM_E_ALIGN;
+  const bool bf16 = xdt == SLIM_BF16;
+  slim::Kv4Append a = {};
+  a.q = kv4_rows(q, hq, q_row, q_head, bf16), a.k = kv4_rows(k, heads, k_row, k_head, bf16);
+  a.v = kv4_rows(v, heads, v_row, v_head, bf16);
+  a.q_out = q_out, a.slots = slots, a.positions = positions, a.rotary = rotary, a.cache = cache;
+  a.t = t, a.pages = pages, a.npos = npos, a.dim = dim, a.group = group, a.page = page, a.rot = rotary ? rot : 0;
+  a.bf16 = bf16, a.interleaved = interleaved != 0;
+  hipError_t err = slim::launch_kv4_append(a, (hipStream_t)stream);
+  return err == hipSuccess ? SLIM_OK : hip_fail(err);
+}
+
+int slim_kv4_read(const int32_t *slots, int64_t t, const uint32_t *cache, int64_t pages, int page, int64_t heads,
+                  int dim, int group, void *k_out, void *v_out, int odt, void *stream) {
+  if (!valid_dtype(odt)) return SLIM_E_DTYPE;
+  if (!kv4_cache_shape(pages, page, heads, dim, group) || t < 0 || t > SLIM_KV4_MAX_T) return SLIM_E_SHAPE;
+  if (t == 0) return SLIM_OK;
+  if (!slots || !cache || !k_out || !v_out) return SLIM_E_NULL;
+  if (!aligned16(cache) || !aligned16(k_out) || !aligned16(v_out)) return SLIM_E_ALIGN;
+  hipError_t err = slim::launch_kv4_read(slots, t, cache, pages, heads, dim, group, page, k_out, v_out,
+                                         odt == SLIM_BF16, (hipStream_t)stream);
+  return err == hipSuccess ? SLIM_OK : hip_fail(err);
+}
+
+static bool kv4_attention_shape(int64_t b, int64_t tq, bool uneven, int64_t hq, int64_t heads, int dim, int64_t per,
+                                int page) {
+  return slim::kv4_shape(page, dim, 32) && heads >= 1 && hq >= heads && hq <= SLIM_KV4_MAX_HEADS && hq % heads == 0 &&
+         b >= 1 && b <= SLIM_KV4_MAX_SEQS && tq >= 0 && tq <= SLIM_KV4_MAX_T && (uneven || tq % b == 0) && per >= 1 &&
+         per <= SLIM_KV4_MAX_SLOTS / page;
+}
+
+size_t slim_kv4_attention_workspace(int64_t b, int64_t tq, int uneven, int64_t hq, int64_t heads, int dim,
+                                    int64_t per, int page, int qdt) {
+  if (!valid_dtype(qdt) || !kv4_attention_shape(b, tq, uneven != 0, hq, heads, dim, per, page) || tq == 0) return 0;
+  return slim::kv4_plan(b, tq, !uneven, hq, heads, dim, per * page, qdt == SLIM_F32).ws_bytes;
+}
+
+int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uint32_t *cache, int64_t pages, int page,
+                       int64_t heads, int dim, int group, const int32_t *table, int64_t b, int64_t per,
+                       const int32_t *lengths, const int32_t *offsets, double scale, int causal, void *out, int odt,
+                       void *ws, size_t ws_bytes, void *stream) {
+  if (!valid_dtype(qdt) || !valid_dtype(odt)) return SLIM_E_DTYPE;
+  if (!kv4_cache_shape(pages, page, heads, dim, group)) return SLIM_E_SHAPE;
+  if (tq == 0 && b >= 0) return SLIM_OK;
+  if (!kv4_attention_shape(b, tq, offsets != nullptr, hq, heads, dim, per, page)) return SLIM_E_SHAPE;
+  if (!isfinite(scale) || !isfinite((float)scale)) return SLIM_E_PARAM;
+  if (!q || !cache || !table || !lengths || !out) return SLIM_E_NULL;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return SLIM_E_ALIGN;
+  const slim::Kv4Plan p = slim::kv4_plan(b, tq, !offsets, hq, heads, dim, per * page, qdt == SLIM_F32);
+  if (p.slots * heads > ((int64_t)1 << 31) / (16 * p.nq) / (p.nsplit > 1 ? p.nsplit : 1)) return SLIM_E_SHAPE;
+  if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes)) return SLIM_E_WORKSPACE;
+  if (p.ws_bytes > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
+  slim::Kv4Args a = {};
+  a.q = q, a.out = out, a.cache = cache, a.table = table, a.lengths = lengths, a.offsets = offsets;
+  a.b = b, a.tq = tq, a.hq = hq, a.hkv = heads, a.pages = pages, a.per = per, a.dim = dim, a.group = group;
+  a.page = page, a.scale = (float)scale, a.causal = causal != 0, a.qbf16 = qdt == SLIM_BF16, a.obf16 = odt == SLIM_BF16;
+  hipError_t err = slim::launch_kv4_attention(a, ws, p, (hipStream_t)stream);
+  return err == hipSuccess ? SLIM_OK : hip_fail(err);
+}
+
+// ---------------------------------------------------------------- verification of drafted tokens
+static bool draft_shape(int64_t b, int k, int64_t v) {
+  return b >= 0 && b <= SLIM_DRAFT_MAX_B && k >= 1 && k <= SLIM_DRAFT_MAX_K && v >= 1 && v <= SLIM_LOGPROB_MAX_V &&
+         b * (2 * k + 1) * v <= ((int64_t)1 << 40);
+}
+
+size_t slim_verify_draft_workspace(int64_t b, int k, int64_t v) {
+  return draft_shape(b, k, v) && b > 0 ? slim::draft_plan(b, k, v).ws_bytes : 0;
+}
+
+int slim_verify_draft(const void *target, int64_t t_seq, int64_t t_row, const void *draft, int64_t d_seq,
+                      int64_t d_row, int ldt, int64_t b, int k, int64_t v, const int64_t *tokens,
+                      const float *uniform, double temperature, int32_t *accepted, int64_t *ids, void *ws,
+                      size_t ws_bytes, void *stream) {
+  if (!valid_dtype(ldt)) return SLIM_E_DTYPE;
+  const int64_t most = (int64_t)1 << 40;
+  if (!draft_shape(b, k, v) || t_row < v || t_row > most || t_seq < 0 || t_seq > most) return SLIM_E_SHAPE;
+  if (draft && (d_row < v || d_row > most || d_seq < 0 || d_seq > most)) return SLIM_E_SHAPE;
+  if (!(temperature > 0.0) || !isfinite(temperature) || !isfinite(1.0 / temperature)) return SLIM_E_PARAM;
+  if (b == 0) return SLIM_OK;
+  if (!target || !tokens || !uniform || !accepted || !ids) return SLIM_E_NULL;
+  const uintptr_t el = ldt == SLIM_BF16 ? 2 : 4;
+  if ((uintptr_t)target % el || (uintptr_t)draft % el) return SLIM_E_ALIGN;
+  const slim::DraftPlan p = slim::draft_plan(b, k, v);
+  if (!ws || ws_bytes < p.ws_bytes) return SLIM_E_WORKSPACE;
+  if (!aligned16(ws)) return SLIM_E_ALIGN;
+  slim::DraftArgs a = {};
+  a.target = target, a.draft = draft, a.t_seq = t_seq, a.t_row = t_row, a.d_seq = d_seq, a.d_row = d_row;
+  a.tokens = tokens, a.uniform = uniform, a.accepted = accepted, a.ids = ids, a.b = b, a.v = v, a.k = k;
+  a.temperature = temperature, a.bf16 = ldt == SLIM_BF16;
+  hipError_t err = slim::launch_verify_draft(a, ws, p, (hipStream_t)stream);
+  return err == hipSuccess ? SLIM_OK : hip_fail(err);
+}
+
 // ---------------------------------------------------------------- timing
 int slim_timing_enable(int on) {
   std::lock_guard<std::mutex> lk(g_timer_mu);

@@ -1,0 +1,14 @@
+// Attention over the 4-bit cache, heads of 128 channels (a file of its own: the
+// kernels are compiled beside each other).
+#include "kv4_attn.hpp"
+
+namespace slim {
+namespace kv4 {
+
+hipError_t launch_dim128(const Kv4Args &a, float *ws, const Kv4Plan &p, hipStream_t st) {
+  if (a.group == 128) return launch_group<128, 128>(a, ws, p, st);
+  return a.group == 64 ? launch_group<128, 64>(a, ws, p, st) : launch_group<128, 32>(a, ws, p, st);
+}
+
+}  // namespace kv4
+}  // namespace slim

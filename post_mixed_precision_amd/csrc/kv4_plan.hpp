@@ -1,0 +1,56 @@
+// Layout of the 4-bit key/value cache and the host-side rules of its
+// attention (internal to libslim; plain C++, tested on the CPU).
+//
+// A page holds `page` tokens of one head as page / 16 records; a record holds
+// 16 tokens, dim channels, g channels to a group, k = dim / g:
+//   words [0, 2 dim)          key codes: word (16 lg + t) (dim / 32) + j has token t's channels
+//                             32 j + 8 lg .. +7, byte b: channel b low, channel b + 4 high nibble
+//   words [2 dim, 4 dim)      value codes: byte t % 4 of word (16 (t / 4) + r) (dim / 32) + a has
+//                             token t's channel 32 a + 2 r low, 32 a + 2 r + 1 high nibble
+//   words 4 dim + 16 q + t    the keys' pair of group q, token t: step (low half) and low end, bfloat16
+//   and 16 k words further    the values' pairs
+#pragma once
+#include <stdint.h>
+
+namespace slim {
+
+inline bool kv4_shape(int page, int dim, int group) {
+  return (page == 16 || page == 32 || page == 64 || page == 128 || page == 256) &&
+         (dim == 64 || dim == 128 || dim == 256) && (group == 32 || group == 64 || group == 128) && group <= dim;
+}
+inline int kv4_record_words(int dim, int group) { return 4 * dim + 32 * (dim / group); }
+inline int64_t kv4_page_words(int page, int dim, int group) {
+  return (int64_t)(page / 16) * kv4_record_words(dim, group);
+}
+
+// How an attention call is cut.  Rows (a sequence's query tokens times the
+// query heads of one key head) go in tiles of 16 nq; a tile's tokens over
+// `nsplit` workgroups, whose partial results are joined by a second kernel.
+struct Kv4Plan {
+  int nq;                    // tiles of 16 rows a wave holds
+  int64_t slots;             // row tiles, at most (uneven queries: some stay idle)
+  int nsplit;
+  size_t ws_bytes;
+};
+
+// b sequences, tq query tokens in all (uniform: tq / b each), max_len: the
+// tokens a row of the page table can name.
+inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t hkv, int dim, int64_t max_len,
+                        bool f32) {
+  Kv4Plan p;
+  const int64_t g = hq / hkv;
+  const int64_t per = (uniform ? tq / b : (tq + b - 1) / b) * g;   // rows of a sequence, on average
+  const int most = f32 ? (dim == 64 ? 2 : 1) : dim == 256 ? 2 : 4;
+  p.nq = per > 32 && most >= 4 ? 4 : per > 16 && most >= 2 ? 2 : 1;
+  const int64_t tm = 16 * p.nq;
+  p.slots = uniform ? b * ((per + tm - 1) / tm) : tq * g / tm + (b < tq ? b : tq);
+  const int64_t units = p.slots * hkv;
+  int64_t s = (512 + units - 1) / units;                   // two workgroups of 4 waves a CU
+  const int64_t useful = (max_len + 255) / 256;            // a wave takes two tiles of 32 tokens at least
+  s = s > useful ? useful : s;
+  p.nsplit = (int)(s < 1 ? 1 : s > 128 ? 128 : s);
+  p.ws_bytes = p.nsplit > 1 ? (size_t)units * p.nsplit * tm * (dim + 2) * 4 : 0;
+  return p;
+}
+
+}  // namespace slim

@@ -1,0 +1,50 @@
+// The 16 x 16 x 32 bfloat16 product and its operands from 4-bit codes and
+// float32, shared by the 4-bit products and the attention over the 4-bit cache.
+#pragma once
+#include "common.hpp"
+
+namespace slim {
+
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
+
+__device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- operands
+// The 8 codes of one word as bfloat16, in column order.  A byte below 16 read
+// as an e4m3 pattern is q 2^-9 exactly, so the scaled pair conversion gives
+// two bfloat16 codes at once.
+__device__ __forceinline__ uint4 q4_codes(uint32_t w) {
+  const uint32_t lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
+  uint4 r;
+  r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false));
+  r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true));
+  r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false));
+  r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true));
+  return r;
+}
+
+// 8 columns of a float32 row as three bfloat16 terms whose sum is exact
+// (truncation leaves 16, then 8 significant bits), but for what lies below
+// bfloat16's least value of 2^-133.
+__device__ __forceinline__ void split3(const uint4 &a, const uint4 &b, uint4 (&t)[3]) {
+  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t h[8], m[8], l[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    h[e] = u[e] & 0xffff0000u;
+    const float r1 = __uint_as_float(u[e]) - __uint_as_float(h[e]);
+    m[e] = __float_as_uint(r1) & 0xffff0000u;
+    l[e] = __float_as_uint(r1 - __uint_as_float(m[e]));
+  }
+  auto pk = [](uint32_t lo, uint32_t hi) __attribute__((always_inline)) {
+    return __builtin_amdgcn_perm(hi, lo, 0x07060302u);   // upper halves of two words
+  };
+  t[0] = make_uint4(pk(h[0], h[1]), pk(h[2], h[3]), pk(h[4], h[5]), pk(h[6], h[7]));
+  t[1] = make_uint4(pk(m[0], m[1]), pk(m[2], m[3]), pk(m[4], m[5]), pk(m[6], m[7]));
+  t[2] = make_uint4(pk(l[0], l[1]), pk(l[2], l[3]), pk(l[4], l[5]), pk(l[6], l[7]));
+}
+
+}  // namespace slim

@@ -1,10 +1,12 @@
 // Host-side launchers of the serving kernels: 4-bit products, the same grouped
-// by expert, and token log probabilities (internal to libslim).
+// by expert, token log probabilities, the 4-bit key/value cache with its
+// attention, and the verification of drafted tokens (internal to libslim).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
 
+#include "kv4_plan.hpp"
 #include "q4_plan.hpp"
 
 namespace slim {
@@ -39,5 +41,60 @@ LogprobPlan logprob_plan(int64_t t, int64_t v, int top, bool bf16);
 hipError_t launch_logprobs(const void *L, bool bf16, int64_t t, int64_t v, int64_t ld, const int64_t *ids, int top,
                            float *logprob, float *entropy, float *top_logprob, int32_t *top_id, void *ws,
                            const LogprobPlan &p, hipStream_t st);
+
+// ---- 4-bit key/value cache ----
+struct Kv4Rows {             // [t, heads, dim] of the call's type, strides in elements
+  const void *p;
+  int64_t heads, row, head;
+  bool vec;                  // rows and heads start at 16-byte boundaries
+};
+struct Kv4Append {
+  Kv4Rows q, k, v;           // q.p may be null (q.heads 0)
+  void *q_out;               // [t, q.heads, dim]
+  const int32_t *slots, *positions;
+  const float *rotary;       // [npos, rot] or null: cosines, then sines
+  uint32_t *cache;
+  int64_t t, pages, npos;
+  int dim, group, page, rot;
+  bool bf16, interleaved;
+};
+hipError_t launch_kv4_append(const Kv4Append &a, hipStream_t st);
+hipError_t launch_kv4_read(const int32_t *slots, int64_t t, const uint32_t *cache, int64_t pages, int64_t heads,
+                           int dim, int group, int page, void *k, void *v, bool bf16, hipStream_t st);
+
+struct Kv4Args {
+  const void *q;             // [tq, hq, dim]
+  void *out;                 // [tq, hq, dim]
+  const uint32_t *cache;
+  const int32_t *table;      // [b, per] pages of each sequence
+  const int32_t *lengths;    // [b]
+  const int32_t *offsets;    // b + 1 bounds of the sequences' query tokens, or null: tq / b each
+  int64_t b, tq, hq, hkv, pages, per;
+  int dim, group, page;
+  float scale;
+  bool causal, qbf16, obf16;
+};
+hipError_t launch_kv4_attention(const Kv4Args &a, void *ws, const Kv4Plan &p, hipStream_t st);
+
+// ---- Verification of drafted tokens ----
+struct DraftArgs {
+  const void *target, *draft;          // [b, k + 1, v] and [b, k, v] or null, strides in elements
+  int64_t t_seq, t_row, d_seq, d_row;
+  const int64_t *tokens;               // [b, k]
+  const float *uniform;                // [b, k + 1]
+  int32_t *accepted;                   // [b]
+  int64_t *ids;                        // [b, k + 1]
+  int64_t b, v;
+  int k;
+  double temperature;
+  bool bf16;
+};
+struct DraftPlan {
+  int nseg;                  // segments a row is cut into
+  int64_t seg;               // entries of a segment
+  size_t ws_bytes;
+};
+DraftPlan draft_plan(int64_t b, int k, int64_t v);
+hipError_t launch_verify_draft(const DraftArgs &a, void *ws, const DraftPlan &p, hipStream_t st);
 
 }  // namespace slim
