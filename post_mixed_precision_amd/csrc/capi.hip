@@ -539,7 +539,7 @@ int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uin
   if (!q || !cache || !table || !lengths || !out) return SLIM_E_NULL;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return SLIM_E_ALIGN;
   const slim::Kv4Plan p = slim::kv4_plan(b, tq, !offsets, hq, heads, dim, per * page, qdt == SLIM_F32);
-  if (p.slots * heads > ((int64_t)1 << 31) / (16 * p.nq) / (p.nsplit > 1 ? p.nsplit : 1)) return SLIM_E_SHAPE;
+  if (p.slots * heads > (((int64_t)1 << 31) - 1) / (p.tm > p.nsplit ? p.tm : p.nsplit)) return SLIM_E_SHAPE;
   if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes)) return SLIM_E_WORKSPACE;
   if (p.ws_bytes > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
   slim::Kv4Args a = {};

@@ -24,10 +24,12 @@ inline int64_t kv4_page_words(int page, int dim, int group) {
 }
 
 // How an attention call is cut.  Rows (a sequence's query tokens times the
-// query heads of one key head) go in tiles of 16 nq; a tile's tokens over
+// query heads of one key head) go in tiles of tm, a tile's tokens over
 // `nsplit` workgroups, whose partial results are joined by a second kernel.
 struct Kv4Plan {
+  bool tile;                 // many rows: four waves of 16 nq rows share the tokens; else each wave has its own
   int nq;                    // tiles of 16 rows a wave holds
+  int tm;
   int64_t slots;             // row tiles, at most (uneven queries: some stay idle)
   int nsplit;
   size_t ws_bytes;
@@ -40,16 +42,17 @@ inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t
   Kv4Plan p;
   const int64_t g = hq / hkv;
   const int64_t per = (uniform ? tq / b : (tq + b - 1) / b) * g;   // rows of a sequence, on average
-  const int most = f32 ? (dim == 64 ? 2 : 1) : dim == 256 ? 2 : 4;
-  p.nq = per > 32 && most >= 4 ? 4 : per > 16 && most >= 2 ? 2 : 1;
-  const int64_t tm = 16 * p.nq;
-  p.slots = uniform ? b * ((per + tm - 1) / tm) : tq * g / tm + (b < tq ? b : tq);
+  const bool wide = !f32 && dim < 256;                             // registers for two tiles of 16 rows
+  p.tile = per > (wide ? 32 : 16);
+  p.nq = wide && per > 16 ? 2 : 1;
+  p.tm = 16 * p.nq * (p.tile ? 4 : 1);
+  p.slots = uniform ? b * ((per + p.tm - 1) / p.tm) : tq * g / p.tm + (b < tq ? b : tq);
   const int64_t units = p.slots * hkv;
   int64_t s = (512 + units - 1) / units;                   // two workgroups of 4 waves a CU
-  const int64_t useful = (max_len + 255) / 256;            // a wave takes two tiles of 32 tokens at least
+  const int64_t useful = (max_len + 255) / 256;
   s = s > useful ? useful : s;
   p.nsplit = (int)(s < 1 ? 1 : s > 128 ? 128 : s);
-  p.ws_bytes = p.nsplit > 1 ? (size_t)units * p.nsplit * tm * (dim + 2) * 4 : 0;
+  p.ws_bytes = p.nsplit > 1 ? (size_t)units * p.nsplit * p.tm * (dim + 2) * 4 : 0;
   return p;
 }
 
