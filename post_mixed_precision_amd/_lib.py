@@ -80,7 +80,8 @@ _SIGS = {
                                  _c_i64, _c_i64, _c_vp, _c_vp]),
     "slim_kv4_read": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_int,
                                _c_vp]),
-    "slim_kv4_attention_workspace": (_c_sz, [_c_i64, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _c_i64, _c_int, _c_int]),
+    "slim_kv4_attention_workspace": (_c_sz, [_c_i64, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _c_int, _c_i64, _c_int,
+                                              _c_int]),
     "slim_kv4_attention": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_int, _c_int,
                                     _c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_dbl, _c_int, _c_vp, _c_int, _c_vp, _c_sz,
                                     _c_vp]),
@@ -898,7 +899,7 @@ def kv4_attention(q, cache, table, lengths, group: int, offsets=None, scale=None
     if out is None:
         out = torch.empty(q.shape, dtype=out_dtype, device=dev)
     qcode = _dtype_code(q)
-    need = _need("slim_kv4_attention_workspace", b, tq, 0 if offsets is None else 1, hq, heads, dim, per, page, qcode)
+    need = _need("slim_kv4_attention_workspace", b, tq, 0 if offsets is None else 1, hq, heads, dim, group, per, page, qcode)
     ws = _ws(need, dev) if need else None
     st = lib.slim_kv4_attention(q.data_ptr(), qcode, tq, hq, cache.data_ptr(), pages, page, heads, dim, group,
                                 table.data_ptr(), b, per, lengths.data_ptr(),

@@ -521,10 +521,10 @@ static bool kv4_attention_shape(int64_t b, int64_t tq, bool uneven, int64_t hq, 
          per <= SLIM_KV4_MAX_SLOTS / page;
 }
 
-size_t slim_kv4_attention_workspace(int64_t b, int64_t tq, int uneven, int64_t hq, int64_t heads, int dim,
+size_t slim_kv4_attention_workspace(int64_t b, int64_t tq, int uneven, int64_t hq, int64_t heads, int dim, int group,
                                     int64_t per, int page, int qdt) {
-  if (!valid_dtype(qdt) || !kv4_attention_shape(b, tq, uneven != 0, hq, heads, dim, per, page) || tq == 0) return 0;
-  return slim::kv4_plan(b, tq, !uneven, hq, heads, dim, per * page, qdt == SLIM_F32).ws_bytes;
+  if (!valid_dtype(qdt) || !valid_group(group) || group > dim || !kv4_attention_shape(b, tq, uneven != 0, hq, heads, dim, per, page) || tq == 0) return 0;
+  return slim::kv4_plan(b, tq, !uneven, hq, heads, dim, group, per * page, qdt == SLIM_F32).ws_bytes;
 }
 
 int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uint32_t *cache, int64_t pages, int page,
@@ -538,14 +538,15 @@ int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uin
   if (!isfinite(scale) || !isfinite((float)scale)) return SLIM_E_PARAM;
   if (!q || !cache || !table || !lengths || !out) return SLIM_E_NULL;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return SLIM_E_ALIGN;
-  const slim::Kv4Plan p = slim::kv4_plan(b, tq, !offsets, hq, heads, dim, per * page, qdt == SLIM_F32);
-  if (p.slots * heads > (((int64_t)1 << 31) - 1) / (p.tm > p.nsplit ? p.tm : p.nsplit)) return SLIM_E_SHAPE;
+  const slim::Kv4Plan p = slim::kv4_plan(b, tq, !offsets, hq, heads, dim, group, per * page, qdt == SLIM_F32);
+  if (((int64_t)p.slots + p.extra) * heads > INT32_MAX || (int64_t)p.slots * heads * p.tm > UINT32_MAX) return SLIM_E_SHAPE;
   if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes)) return SLIM_E_WORKSPACE;
   if (p.ws_bytes > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
   slim::Kv4Args a = {};
   a.q = q, a.out = out, a.cache = cache, a.table = table, a.lengths = lengths, a.offsets = offsets;
-  a.b = b, a.tq = tq, a.hq = hq, a.hkv = heads, a.pages = pages, a.per = per, a.dim = dim, a.group = group;
-  a.page = page, a.scale = (float)scale, a.causal = causal != 0, a.qbf16 = qdt == SLIM_BF16, a.obf16 = odt == SLIM_BF16;
+  a.b = (int)b, a.tq = (int)tq, a.ql = (int)(tq / b), a.hq = (int)hq, a.hkv = (int)heads, a.g = (int)(hq / heads);
+  a.pages = (int)pages, a.per = (int)per, a.cap = (int)(per * page), a.dim = dim, a.group = group, a.page = page;
+  a.scale = (float)scale, a.causal = causal != 0, a.qbf16 = qdt == SLIM_BF16, a.obf16 = odt == SLIM_BF16;
   hipError_t err = slim::launch_kv4_attention(a, ws, p, (hipStream_t)stream);
   return err == hipSuccess ? SLIM_OK : hip_fail(err);
 }

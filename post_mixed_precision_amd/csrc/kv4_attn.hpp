@@ -39,64 +39,162 @@ __device__ __forceinline__ uint32_t pk_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// The row tile of a slot: sequence, its first query token, its query tokens,
-// the tile's number inside it.
-struct RowTile {
-  int64_t q0;
-  int seq, ql, tile;
-  bool none, bad;            // no tile in this slot; bounds out of order
+// What a workgroup works on: a tile of a sequence's rows, for one key head,
+// over one of `nsplit` runs of the sequence's tokens.
+struct Work {
+  int64_t q0;                // the sequence's first query token
+  int seq, ql, len;          // its number, query tokens, tokens
+  int tile, split, nsplit;
+  int first;                 // number of the tile's first run, per head
+  int slot, slots;           // the tile's number over all sequences; how many there are
+  bool over;                 // its length is past its row of the page table
+  bool none, bad;            // nothing here; bounds out of order
 };
 
-// Uneven queries: every wave works the tiles out from the bounds (lane l
-// takes consecutive sequences), so no table or copy to the host is needed.
-__device__ __forceinline__ RowTile find_tile(const Kv4Args &a, int64_t slot, int tm) {
-  RowTile t = {};
-  const int64_t g = a.hq / a.hkv;
-  if (!a.offsets) {
-    const int64_t ql = a.tq / a.b;
-    const int tiles = (int)((ql * g + tm - 1) / tm);
-    t.seq = (int)(slot / tiles);
-    t.tile = tiles - 1 - (int)(slot - (int64_t)t.seq * tiles);   // the longest first
-    t.ql = (int)ql;
-    t.q0 = t.seq * ql;
-    return t;
+// Tokens of a sequence, 0 if there is nothing to attend to.
+__device__ __forceinline__ int length_of(const Kv4Args &a, int seq, bool &over) {
+  const int n = a.lengths[seq];
+  over = n > a.cap;
+  return over || n < 0 ? 0 : n;
+}
+
+// Running sums over the wave's lanes, by data-parallel moves (a shuffle
+// through LDS costs ten times as much, and every workgroup starts with these).
+template <class T>
+__device__ __forceinline__ T moved(T x, T none, int which) {
+  const int o = __builtin_bit_cast(int, none), v = __builtin_bit_cast(int, x);
+  int r;
+  switch (which) {
+    case 0: r = __builtin_amdgcn_update_dpp(o, v, 0x111, 0xf, 0xf, false); break;   // from 1, 2, 4, 8 lanes below
+    case 1: r = __builtin_amdgcn_update_dpp(o, v, 0x112, 0xf, 0xf, false); break;
+    case 2: r = __builtin_amdgcn_update_dpp(o, v, 0x114, 0xf, 0xf, false); break;
+    case 3: r = __builtin_amdgcn_update_dpp(o, v, 0x118, 0xf, 0xf, false); break;
+    case 4: r = __builtin_amdgcn_update_dpp(o, v, 0x142, 0xa, 0xf, false); break;   // the row's sum to the next row,
+    default: r = __builtin_amdgcn_update_dpp(o, v, 0x143, 0xc, 0xf, false); break;  // two rows' to the next two
   }
-  const int lane = threadIdx.x & 63, b = (int)a.b, per = (b + 63) >> 6;
-  int64_t mine = 0;
-  bool wrong = false;
-  for (int i = 0; i < per; ++i) {
-    const int s = lane * per + i;
-    if (s >= b) break;
-    const int64_t lo = a.offsets[s], hi = a.offsets[s + 1];
-    wrong |= lo < 0 || hi < lo || hi > a.tq;
-    mine += ((hi - lo) * g + tm - 1) / tm;
-  }
-  if (__any(wrong)) {
-    t.bad = true;
-    return t;
-  }
-  int64_t incl = mine;
+  return __builtin_bit_cast(T, r);
+}
+template <class T>
+__device__ __forceinline__ T running_sum(T x) {
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t up = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += up;
+  for (int i = 0; i < 6; ++i) x += moved<T>(x, (T)0, i);
+  return x;
+}
+template <class T>
+__device__ __forceinline__ T of_lane(T x, int lane) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+
+// ceil(x / y) for x < 2^26: the quotient by a reciprocal, put right.
+__device__ __forceinline__ int ceil_div(int x, int y) {
+  int r = (int)((float)x * __builtin_amdgcn_rcpf((float)y));
+  while ((int64_t)r * y < x) ++r;
+  while (r > 0 && (int64_t)(r - 1) * y >= x) --r;
+  return r;
+}
+
+// How the work is cut is worked out here, by every wave for itself, from the
+// lengths and bounds on the device (lane l takes consecutive sequences): a
+// tile's tokens go to one workgroup for every `chunk` of them, chunk being
+// the share of all tokens that spreads them over `extra` workgroups.  So
+// sequences of uneven lengths end together, no table or copy to the host is
+// needed, and at most slots + extra workgroups are used.  i: number of the run.
+__device__ __forceinline__ Work find_work(const Kv4Args &a, const Kv4Cut &cut, int i) {
+  Work w = {};
+  const int lane = threadIdx.x & 63, per = (a.b + 63) >> 6;
+  auto bounds = [&](int s, int &lo, int &hi) __attribute__((always_inline)) {
+    lo = a.offsets ? a.offsets[s] : s * a.ql;
+    hi = a.offsets ? a.offsets[s + 1] : lo + a.ql;
+  };
+  auto tiles_of = [&](int lo, int hi) __attribute__((always_inline)) {
+    return a.offsets ? (int)((unsigned)((hi - lo) * a.g + cut.tm - 1) >> cut.tm_log) : cut.tiles;
+  };
+  const bool cuts = cut.extra > 0;
+  float work = 0.0f;
+  bool wrong = false;
+  int t0 = 0;                       // records' tiles and row tiles of the lane's first sequence
+  int n0 = 0;
+  for (int x = 0; x < per; ++x) {
+    const int s = lane * per + x;
+    if (s >= a.b) break;
+    int lo, hi;
+    bounds(s, lo, hi);
+    wrong |= lo < 0 || hi < lo || hi > a.tq;
+    bool over;
+    const int n = hi < lo ? 0 : tiles_of(lo, hi), t = cuts ? (length_of(a, s, over) + 31) >> 5 : 0;
+    work += (float)n * (float)t;
+    if (x == 0) t0 = t, n0 = n;
   }
-  const uint64_t past = __ballot(incl > slot);
+  if (a.offsets && __any(wrong)) {
+    w.bad = true;
+    return w;
+  }
+  int chunk = 1 << 26;
+  if (cuts) {
+    // the sum's rounding is below (per + 6) 2^-24 of it, far inside the factor: the runs stay within `extra`
+    const float share = of_lane(running_sum(work), 63) * (1.01f / (float)cut.extra);
+    chunk = share < (float)cut.least ? cut.least : (int)share + 1;
+  }
+  auto runs_of = [&](int t) __attribute__((always_inline)) { return t <= chunk ? 1 : ceil_div(t, chunk); };
+  int tiles = n0, runs = n0 * runs_of(t0);
+  for (int x = 1; x < per; ++x) {
+    const int s = lane * per + x;
+    if (s >= a.b) break;
+    int lo, hi;
+    bounds(s, lo, hi);
+    bool over;
+    const int n = tiles_of(lo, hi);
+    tiles += n;
+    runs += n * runs_of(cuts ? (length_of(a, s, over) + 31) >> 5 : 0);
+  }
+  const int tsum = running_sum(tiles), rsum = running_sum(runs);
+  w.slots = of_lane(tsum, 63);
+  const uint64_t past = __ballot(rsum > i);
   if (!past) {
-    t.none = true;
-    return t;
+    w.none = true;
+    return w;
   }
   const int own = __ffsll((unsigned long long)past) - 1;
-  int64_t left = slot - __shfl(incl - mine, own, 64);
-  int s = own * per;
-  for (;; ++s) {             // ends: lane `own` has more than `left` tiles
-    const int64_t lo = a.offsets[s], hi = a.offsets[s + 1];
-    const int64_t n = ((hi - lo) * g + tm - 1) / tm;
-    if (left < n) {
-      t.seq = s, t.q0 = lo, t.ql = (int)(hi - lo), t.tile = (int)(n - 1 - left);
-      return t;
+  int first = of_lane(rsum - runs, own), slot = of_lane(tsum - tiles, own);
+  for (int s = own * per;; ++s) {   // ends: lane `own` has run i
+    int lo, hi;
+    bounds(s, lo, hi);
+    w.len = length_of(a, s, w.over);
+    const int n = tiles_of(lo, hi), r = cuts ? runs_of((w.len + 31) >> 5) : 1;
+    if (i >= first + n * r) {
+      first += n * r, slot += n;
+      continue;
     }
-    left -= n;
+    const int t = r == 1 ? i - first : (i - first) / r;
+    w.q0 = lo, w.seq = s, w.ql = hi - lo, w.nsplit = r;
+    w.first = first + t * r;
+    w.split = i - w.first;
+    w.slot = slot + t;
+    w.tile = n - 1 - t;             // the longest first
+    return w;
+  }
+}
+
+// What the join reads of a tile, in the workspace behind the partial results.
+struct __attribute__((aligned(16))) Joint {
+  int q0, ql, m0, first, runs;   // runs: 0 where there is no tile, -1 for bounds out of order
+  int pad[3];
+};
+__device__ __forceinline__ Joint *joints(const Kv4Args &a, const Kv4Cut &cut, int dim) {
+  return (Joint *)(cut.part + (int64_t)(cut.slots + cut.extra) * a.hkv * cut.tm * (dim + 2));
+}
+// Written by the first head's workgroups: a tile's first one, and for the numbers past the last tile any.
+__device__ __forceinline__ void note_joint(const Kv4Args &a, const Kv4Cut &cut, const Work &w, int run, int h, int dim) {
+  if (cut.extra == 0 || h != 0 || threadIdx.x != 0) return;
+  Joint j = {};
+  if (w.bad || run >= w.slots) {
+    j.runs = w.bad ? -1 : 0;
+    if (run < cut.slots) joints(a, cut, dim)[run] = j;
+    if (w.bad) return;
+  }
+  if (!w.none && w.split == 0) {
+    j.q0 = (int)w.q0, j.ql = w.ql, j.m0 = w.tile * cut.tm, j.first = w.first, j.runs = w.nsplit;
+    joints(a, cut, dim)[w.slot] = j;
   }
 }
 
@@ -111,14 +209,29 @@ __device__ __forceinline__ void store_out(const Kv4Args &a, int64_t at, float x)
   else ((float *)a.out)[at] = x;
 }
 
-// Bounds out of order: the slots share the rows out and make them NaN.
-__device__ __forceinline__ void nan_share(const Kv4Args &a, int64_t slot, int64_t slots, int h, int dim) {
-  const int64_t each = (a.tq + slots - 1) / slots, g = a.hq / a.hkv;
-  const int64_t lo = slot * each, hi = lo + each < a.tq ? lo + each : a.tq;
-  for (int64_t i = lo * g * dim + threadIdx.x; i < hi * g * dim; i += blockDim.x) {
-    const int64_t c = i % dim, r = i / dim;
-    store_out(a, (r / g * a.hq + h * g + r % g) * dim + c, kNaN);
+// Bounds out of order: the first `shares` workgroups of a head share the rows out and make them NaN.
+__device__ __forceinline__ void nan_share(const Kv4Args &a, int i, int shares, int h, int dim) {
+  const int each = (a.tq + shares - 1) / shares;
+  const int64_t lo = (int64_t)i * each, hi = lo + each < a.tq ? lo + each : a.tq;
+  for (int64_t x = lo * a.g * dim + threadIdx.x; x < hi * a.g * dim; x += blockDim.x) {
+    const int64_t c = x % dim, r = x / dim;
+    store_out(a, (r / a.g * a.hq + h * a.g + r % a.g) * dim + c, kNaN);
   }
+}
+
+// Partial results, by number of the run, head, row: sums, then (behind all sums) reference and sum of weights.
+__device__ __forceinline__ float *part_sum(const Kv4Args &a, const Kv4Cut &cut, int run, int h, int m, int dim) {
+  return cut.part + (((int64_t)run * a.hkv + h) * cut.tm + m) * dim;
+}
+__device__ __forceinline__ float2 *part_ml(const Kv4Args &a, const Kv4Cut &cut, int run, int h, int m, int dim) {
+  return (float2 *)(cut.part + (int64_t)(cut.slots + cut.extra) * a.hkv * cut.tm * dim) +
+         (((int64_t)run * a.hkv + h) * cut.tm + m);
+}
+
+// Row m of a sequence's for head h, query token i = m / g: its place among q's and out's heads.
+template <class K>
+__device__ __forceinline__ int64_t row_at(const Kv4Args &a, const K &k, int h, int m, int i) {
+  return (int64_t)(k.q0 + i) * a.hq + h * a.g + (m - i * a.g);
 }
 
 // What a wave keeps of its 16 NQ rows, and one step of the attention: 32
@@ -159,16 +272,15 @@ struct Rows {
   f32x4_t o[NQ][DIM / 16];   // sum P step code, rows (tokens' channels) by columns (rows)
 
   // Rows m0 + 16 n + lane % 16 of the sequence, those from `rows` on as zeros that attend to nothing.
-  __device__ __forceinline__ void start(const Kv4Args &a, const RowTile &rt, int h, int g, int len, int m0, int rows,
-                                        float c) {
+  __device__ __forceinline__ void start(const Kv4Args &a, const Work &k, int h, int m0, int rows, float c) {
     const int r16 = threadIdx.x & 15, lg = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       const int mm = m0 + 16 * n + r16;
       const bool real = mm < rows;
-      const int i = (real ? mm : 0) / g;
-      lim[n] = real ? limit_of(a, len, rt.ql, i) : 0;
-      const int64_t at = ((rt.q0 + i) * a.hq + (int64_t)h * g + ((real ? mm : 0) - i * g)) * DIM + 8 * lg;
+      const int i = (int)((unsigned)(real ? mm : 0) / (unsigned)a.g);
+      lim[n] = real ? limit_of(a, k.len, k.ql, i) : 0;
+      const int64_t at = row_at(a, k, h, real ? mm : 0, i) * DIM + 8 * lg;
 #pragma unroll
       for (int j = 0; j < NG; ++j) qs[n][j] = pl[n][j] = 0.0f;
 #pragma unroll
@@ -205,13 +317,14 @@ struct Rows {
   // 32 tokens from token `first` on.  Src: codes and pairs of the two records; a key's step is
   // given times scale log2 e.  EDGE: some row does not attend to all of them.
   template <bool EDGE, class Src>
-  __device__ __forceinline__ void attend(const Src &src, int first) {
+  __device__ __forceinline__ void attend(Src &src, int first) {
     const int tok = first + 4 * ((threadIdx.x & 63) >> 4);   // of entry 0; entry 4 b + v: + 16 b + v
     float x[NQ][8];
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[n][e] = -m[n];
+    src.keys();
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -253,6 +366,7 @@ struct Rows {
         ls[n] += x[n][e];
       }
     }
+    src.values();
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       float step[2][4], low[2][4];
@@ -293,6 +407,7 @@ struct Rows {
 
   // A new reference for the rows that need one: the maximum over the step's tokens.
   __device__ __forceinline__ void raise(int n, float top, float (&x)[8]) {
+    asm volatile("" : "+v"(top));   // nothing of this is done ahead of the branch
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const bool up = top > thr[n];
@@ -340,8 +455,9 @@ __device__ __forceinline__ float half_of(uint32_t w, bool high) {
 // The pages of a run of records: lane i holds that of record base + i (-1: outside the cache).
 struct Pages {
   const int32_t *table;
-  int64_t pages;
-  int last, shift, base, page;
+  const char *cache;         // the head's first record
+  unsigned bytes;            // of a page, all heads
+  int pages, last, shift, base, page;
   __device__ __forceinline__ void load(int from) {
     base = from;
     const int b = from + (int)(threadIdx.x & 63);
@@ -350,7 +466,16 @@ struct Pages {
   }
   // Of record b (past the last one: of the last); uniform over the wave.
   __device__ __forceinline__ int of(int b) const { return __builtin_amdgcn_readlane(page, b - base); }
+  // Where record b of a page (that of(b) gave; of a lost one: of page 0) lies.
+  template <int RECB>
+  __device__ __forceinline__ const char *at(int page_of, int b) const {
+    const unsigned in = (unsigned)(b < last ? b : last) & ((1u << shift) - 1);
+    return cache + (uint64_t)(unsigned)(page_of < 0 ? 0 : page_of) * bytes + in * RECB;
+  }
 };
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint32_t *p, uint32_t (&w)[N]) {
@@ -366,38 +491,124 @@ __device__ __forceinline__ void load_words(const uint32_t *p, uint32_t (&w)[N]) 
   }
 }
 
-// Two records in a wave's registers, codes expanded as they are used.
+typedef __attribute__((address_space(3))) void lds_void_t;
+typedef const __attribute__((address_space(1))) void global_void_t;
+
+// N 16-byte pieces of LDS at `at` + O..., read and waited for in one block: the
+// compiler would wait for every load in flight to LDS before a read of its own.
+template <int O0, int O1>
+__device__ __forceinline__ void lds_get(uint32_t at, uint4 &a, uint4 &b) {
+  u32x4_t x, y;
+  asm volatile("ds_read_b128 %0, %2 offset:%3\n\tds_read_b128 %1, %2 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(x), "=&v"(y)
+               : "v"(at), "n"(O0), "n"(O1)
+               : "memory");
+  a = __builtin_bit_cast(uint4, x), b = __builtin_bit_cast(uint4, y);
+}
+template <int O0, int O1>
+__device__ __forceinline__ void lds_get(uint32_t at, uint2 &a, uint2 &b) {
+  u32x2_t x, y;
+  asm volatile("ds_read_b64 %0, %2 offset:%3\n\tds_read_b64 %1, %2 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(x), "=&v"(y)
+               : "v"(at), "n"(O0), "n"(O1)
+               : "memory");
+  a = __builtin_bit_cast(uint2, x), b = __builtin_bit_cast(uint2, y);
+}
+// Two at `at` and two at `pair`.
+template <int O0, int O1, int P0, int P1>
+__device__ __forceinline__ void lds_get(uint32_t at, uint4 &a, uint4 &b, uint32_t pair, uint4 &c, uint4 &d) {
+  u32x4_t x, y, z, w;
+  asm volatile("ds_read_b128 %0, %4 offset:%6\n\tds_read_b128 %1, %4 offset:%7\n\t"
+               "ds_read_b128 %2, %5 offset:%8\n\tds_read_b128 %3, %5 offset:%9\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(x), "=&v"(y), "=&v"(z), "=&v"(w)
+               : "v"(at), "v"(pair), "n"(O0), "n"(O1), "n"(P0), "n"(P1)
+               : "memory");
+  a = __builtin_bit_cast(uint4, x), b = __builtin_bit_cast(uint4, y);
+  c = __builtin_bit_cast(uint4, z), d = __builtin_bit_cast(uint4, w);
+}
+
+// Waits until at most VM of this wave's loads are in flight (they complete in order).
+template <int VM>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | 7 << 4 | (VM >> 4) << 14);
+  asm volatile("" ::: "memory");
+}
+
+// Two records as they lie in the cache, in LDS; a wave's own.
 template <int DIM, int GROUP>
-struct RegTile {
-  static constexpr int NG = DIM / GROUP, W = DIM / 32, REC = 4 * DIM + 32 * NG;
+struct Ring {
+  static constexpr int NG = DIM / GROUP, W = DIM / 32, RECB = 16 * DIM + 128 * NG, TILEB = 2 * RECB;
+  static constexpr int LOADS = 2 * (DIM / 64 + 1);         // of a tile
+  static constexpr int STAGES = 2;
+  // The record at p to LDS at `to`, 16 bytes a lane.
+  static __device__ __forceinline__ void load(const char *p, char *to) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < DIM / 64; ++i)
+      __builtin_amdgcn_global_load_lds((global_void_t *)(p + 1024 * i + 16 * lane), (lds_void_t *)(to + 1024 * i), 16, 0,
+                                       0);
+    if (lane < 8 * NG)
+      __builtin_amdgcn_global_load_lds((global_void_t *)(p + 16 * DIM + 16 * lane), (lds_void_t *)(to + 16 * DIM), 16, 0,
+                                       0);
+  }
+};
+
+// The same as a source of operands: codes come from LDS when their turn comes and are expanded as they are used.
+template <int DIM, int GROUP>
+struct RingTile {
+  typedef Ring<DIM, GROUP> R;
+  static constexpr int NG = R::NG, W = R::W, RECB = R::RECB;
+  uint32_t codes, pairs;     // LDS addresses of this lane's codes and of its four tokens' pairs
+  int lost;                  // bit b: record b's page lies outside the cache
+  float c;
   uint32_t k[2][W], v[2][W];
   uint4 kp[2][NG], vp[2][NG];
-  bool lost[2];
-  float c;
-  __device__ __forceinline__ void load(const uint32_t *cache, int64_t heads, int h, int pb, const Pages &pg, int blk) {
-    const int lane = threadIdx.x & 63, lg = lane >> 4;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int page = pg.of(blk + b), at = blk + b < pg.last ? blk + b : pg.last;
-      lost[b] = page < 0;
-      const uint32_t *p = cache + (((int64_t)(page < 0 ? 0 : page) * heads + h) * pb + (at & (pb - 1))) * REC;
-      load_words(p + lane * W, k[b]);
-      load_words(p + 2 * DIM + lane * W, v[b]);
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        kp[b][j] = *(const uint4 *)(p + 4 * DIM + 16 * j + 4 * lg);
-        vp[b][j] = *(const uint4 *)(p + 4 * DIM + 16 * NG + 16 * j + 4 * lg);
-      }
+
+  template <int OFF>
+  __device__ __forceinline__ void words(uint32_t (&x)[2][W]) {
+    if constexpr (W == 2) {
+      uint2 a, b;
+      lds_get<OFF, OFF + RECB>(codes, a, b);
+      x[0][0] = a.x, x[0][1] = a.y, x[1][0] = b.x, x[1][1] = b.y;
+    } else if constexpr (W == 8) {
+      uint4 a, b, d, e;
+      lds_get<OFF, OFF + 16, OFF + RECB, OFF + RECB + 16>(codes, a, b, codes, d, e);
+      put(x[0], 0, a), put(x[0], 4, b), put(x[1], 0, d), put(x[1], 4, e);
     }
   }
-  __device__ __forceinline__ void spoil() {
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-      if (lost[b]) {
-#pragma unroll
-        for (int j = 0; j < NG; ++j) kp[b][j] = vp[b][j] = make_uint4(0x7fc0u, 0x7fc0u, 0x7fc0u, 0x7fc0u);
-      }
+  static __device__ __forceinline__ void put(uint32_t (&x)[W], int at, const uint4 &a) {
+    x[at] = a.x, x[at + 1] = a.y, x[at + 2] = a.z, x[at + 3] = a.w;
   }
+  template <int CODES, int PAIRS>
+  __device__ __forceinline__ void get(uint32_t (&x)[2][W], uint4 (&p)[2][NG]) {
+    if constexpr (W == 4) {
+      uint4 a, b;
+      lds_get<CODES, CODES + RECB, PAIRS, PAIRS + RECB>(codes, a, b, pairs, p[0][0], p[1][0]);
+      put(x[0], 0, a), put(x[1], 0, b);
+    } else {
+      words<CODES>(x);
+      lds_get<PAIRS, PAIRS + RECB>(pairs, p[0][0], p[1][0]);
+    }
+    more<PAIRS, 1>(p);
+    if (lost) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (lost >> b & 1) {
+#pragma unroll
+          for (int j = 0; j < NG; ++j) p[b][j] = make_uint4(0x7fc0u, 0x7fc0u, 0x7fc0u, 0x7fc0u);
+        }
+    }
+  }
+  template <int PAIRS, int J>
+  __device__ __forceinline__ void more(uint4 (&p)[2][NG]) {
+    if constexpr (J < NG) {
+      lds_get<PAIRS + 64 * J, PAIRS + 64 * J + RECB>(pairs, p[0][J], p[1][J]);
+      more<PAIRS, J + 1>(p);
+    }
+  }
+  __device__ __forceinline__ void keys() { get<0, 16 * DIM>(k, kp); }
+  __device__ __forceinline__ void values() { get<8 * DIM, 16 * DIM + 64 * NG>(v, vp); }
   __device__ __forceinline__ uint4 kcode(int b, int w) const { return q4_codes(k[b][w]); }
   __device__ __forceinline__ void vcode(int w, uint4 &even, uint4 &odd) const {
     const uint4 u = q4_codes(v[0][w]), y = q4_codes(v[1][w]);   // x, y: 4 tokens of the even channel; z, w: odd
@@ -406,44 +617,21 @@ struct RegTile {
   __device__ __forceinline__ void kpair(int b, int j, float (&step)[4], float (&low)[4]) const {
     const uint32_t w[4] = {kp[b][j].x, kp[b][j].y, kp[b][j].z, kp[b][j].w};
 #pragma unroll
-    for (int v2 = 0; v2 < 4; ++v2) step[v2] = half_of(w[v2], false) * c, low[v2] = half_of(w[v2], true);
+    for (int i = 0; i < 4; ++i) step[i] = half_of(w[i], false) * c, low[i] = half_of(w[i], true);
   }
   __device__ __forceinline__ void vpair(int b, int j, float (&step)[4], float (&low)[4]) const {
     const uint32_t w[4] = {vp[b][j].x, vp[b][j].y, vp[b][j].z, vp[b][j].w};
 #pragma unroll
-    for (int v2 = 0; v2 < 4; ++v2) step[v2] = half_of(w[v2], false), low[v2] = half_of(w[v2], true);
+    for (int i = 0; i < 4; ++i) step[i] = half_of(w[i], false), low[i] = half_of(w[i], true);
   }
 };
 
-// What a workgroup works on.
-struct Unit {
-  RowTile rt;
-  int64_t unit;
-  int split, h, g, rows, m0, len;
-  bool over, skip;
-};
-__device__ __forceinline__ Unit unit_of(const Kv4Args &a, int64_t slots, int nsplit, int tm, int dim) {
-  Unit u;
-  const int64_t units = slots * a.hkv;
-  u.split = (int)(blockIdx.x / units);
-  u.unit = blockIdx.x - u.split * units;
-  const int64_t slot = u.unit / a.hkv;
-  u.h = (int)(u.unit - slot * a.hkv);     // heads are neighbours: a head's rows meet in one XCD's L2
-  u.g = (int)(a.hq / a.hkv);
-  u.rt = find_tile(a, slot, tm);
-  u.skip = u.rt.none || u.rt.bad;
-  if (u.rt.bad && nsplit == 1) nan_share(a, slot, slots, u.h, dim);
-  if (u.skip) return u;
-  u.rows = u.rt.ql * u.g, u.m0 = u.rt.tile * tm;
-  const int given = a.lengths[u.rt.seq];
-  u.over = given > a.per * a.page;
-  u.len = u.over || given < 0 ? 0 : given;
-  return u;
-}
-
-__device__ __forceinline__ Pages pages_of(const Kv4Args &a, int seq, int kend) {
+template <int RECB>
+__device__ __forceinline__ Pages pages_of(const Kv4Args &a, int seq, int h, int kend) {
   Pages p;
-  p.table = a.table + seq * a.per;
+  p.bytes = (unsigned)(a.page >> 4) * RECB * a.hkv;      // below 2^31: 1024 heads of 16 records of 10 KB
+  p.cache = (const char *)a.cache + (unsigned)h * ((unsigned)(a.page >> 4) * RECB);
+  p.table = a.table + (int64_t)seq * a.per;
   p.pages = a.pages;
   p.last = (kend - 1) >> 4;
   p.shift = 31 - __builtin_clz((unsigned)a.page >> 4);
@@ -451,88 +639,140 @@ __device__ __forceinline__ Pages pages_of(const Kv4Args &a, int seq, int kend) {
   return p;
 }
 
+// Where share i of n equal shares of `all` (below 2^26) begins.
+__device__ __forceinline__ int share_of(int all, int i, int n) {
+  const unsigned each = (unsigned)all / (unsigned)n, rest = (unsigned)all - each * n;   // the first `rest` have one more
+  return (int)(each * i + (i < (int)rest ? i : rest));
+}
+
 // Few rows: every wave streams its own run of tokens for the same 16 NQ rows,
-// records ahead in registers; the waves' sums meet in LDS.
+// its records a tile ahead, straight to LDS (in registers they would leave
+// room for half the waves); the waves' sums meet in LDS.
+template <int DIM, int NQ, bool XF32>
+constexpr int stream_waves() {   // of a SIMD: what the registers allow
+  return XF32 ? (DIM == 64 ? 3 : DIM == 128 ? 2 : 1) : DIM == 64 ? (NQ == 1 ? 4 : 2) : DIM == 128 && NQ == 1 ? 3 : 2;
+}
 template <int DIM, int GROUP, int NQ, bool XF32>
-__global__ __launch_bounds__(256) void kv4_stream_kernel(const Kv4Args a, const int64_t slots, const int nsplit,
-                                                         float *__restrict__ part) {
-  constexpr int TM = 16 * NQ, W = DIM / 32, LDO = DIM + 4;
-  __shared__ __attribute__((aligned(16))) float s_o[4][16][LDO];
-  __shared__ float s_ml[4][16][2];
+__global__ __launch_bounds__(256, (stream_waves<DIM, NQ, XF32>())) void kv4_stream_kernel(const Kv4Args a, const Kv4Cut cut) {
+  typedef Ring<DIM, GROUP> R;
+  constexpr int TM = 16 * NQ, W = DIM / 32, LDO = DIM + 4, ST = R::STAGES;
+  union Lds {
+    char ring[4][ST][R::TILEB];
+    struct {
+      float o[4][16][LDO];
+      float ml[4][16][2];
+    } end;
+  };
+  __shared__ __attribute__((aligned(16))) Lds s;
 
-  const Unit u = unit_of(a, slots, nsplit, TM, DIM);
-  if (u.skip) return;
+  const unsigned run = blockIdx.x / (unsigned)a.hkv;
+  const int h = (int)(blockIdx.x - run * a.hkv);     // heads are neighbours: a head's rows meet in one XCD's L2
+  const Work k = find_work(a, cut, (int)run);
+  note_joint(a, cut, k, (int)run, h, DIM);
+  if (k.none) return;
+  if (k.bad) {
+    if ((int)run < cut.slots && cut.extra == 0) nan_share(a, (int)run, cut.slots, h, DIM);
+    return;
+  }
+  const int rows_all = k.ql * a.g, m0 = k.tile * TM;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r16 = lane & 15, lg = lane >> 4, g = u.g;
-  const int mrows = u.rows - u.m0 < TM ? u.rows - u.m0 : TM;
+  const int r16 = lane & 15, lg = lane >> 4;
+  const int mrows = rows_all - m0 < TM ? rows_all - m0 : TM;
   const float c = a.scale * 1.44269504088896340736f;
-  Rows<DIM, GROUP, NQ, XF32> rows;
-  rows.start(a, u.rt, u.h, g, u.len, u.m0, u.rows, c);
+  const int kend = limit_of(a, k.len, k.ql, (int)((unsigned)(m0 + mrows - 1) / (unsigned)a.g));   // the last row's
+  const int kall = limit_of(a, k.len, k.ql, (int)((unsigned)m0 / (unsigned)a.g));   // every row reaches these
+  const int tiles = (kend + 31) >> 5, parts = k.nsplit * 4, mine = k.split * 4 + wave;
+  const int t0 = share_of(tiles, mine, parts), t1 = share_of(tiles, mine + 1, parts);
 
-  const int kend = limit_of(a, u.len, u.rt.ql, (u.m0 + mrows - 1) / g);   // of the last row, the longest
-  const int kall = limit_of(a, u.len, u.rt.ql, u.m0 / g);                 // every row reaches these
-  const int tiles = (kend + 31) >> 5, parts = nsplit * 4, mine = u.split * 4 + wave;
-  const int t0 = (int)((int64_t)tiles * mine / parts), t1 = (int)((int64_t)tiles * (mine + 1) / parts);
-  if (t0 < t1) {
-    Pages pg = pages_of(a, u.rt.seq, kend);
-    const int pb = a.page >> 4;
-    typedef RegTile<DIM, GROUP> Tile;
-    Tile d0, d1;
-    d0.c = d1.c = c;
-    auto fetch = [&](int t, Tile &d) __attribute__((always_inline)) {
-      if (2 * t - pg.base >= 64) pg.load(2 * t);
-      d.load(a.cache, a.hkv, u.h, pb, pg, 2 * t);
-    };
-    auto step = [&](int t, Tile &d, Tile &next) __attribute__((always_inline)) {
-      if (t + 1 < t1) fetch(t + 1, next);
-      d.spoil();
-      if (32 * t + 32 <= kall) rows.template attend<false>(d, 32 * t);
-      else rows.template attend<true>(d, 32 * t);
-    };
-    pg.load(2 * t0);
-    fetch(t0, d0);
-    for (int t = t0; t < t1; t += 2) {
-      step(t, d0, d1);
-      if (t + 1 < t1) step(t + 1, d1, d0);
+  Pages pg = pages_of<R::RECB>(a, k.seq, h, kend);
+  int lost = 0;                                // two bits a tile, the newest lowest
+  // The last stages load the last tile again, so that every step has as many loads in flight.
+  auto fetch = [&](int t, int stage) __attribute__((always_inline)) {
+    if (t >= t1) t = t1 - 1;
+    if (2 * t - pg.base >= 64) pg.load(2 * t);
+    lost <<= 2;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int page = pg.of(2 * t + b);
+      if (page < 0) lost |= 1 << b;
+      R::load(pg.template at<R::RECB>(page, 2 * t + b), s.ring[wave][stage] + b * R::RECB);
     }
+  };
+  if (t0 < t1) {
+    pg.load(2 * t0);
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) fetch(t0 + i, i);
+  }
+  Rows<DIM, GROUP, NQ, XF32> rows;
+  rows.start(a, k, h, m0, rows_all, c);
+  if (t0 < t1) {
+    RingTile<DIM, GROUP> src;
+    src.c = c;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_void_t *)s.ring[wave][0];
+    int now = 0, next = ST - 1;
+    for (int t = t0; t < t1; ++t) {
+      fetch(t + ST - 1, next);                 // over the tile of the step before, whose reads have returned
+      wait_loads<(ST - 1) * R::LOADS>();
+      src.codes = base + now * R::TILEB + lane * (W * 4);
+      src.pairs = base + now * R::TILEB + lg * 16;
+      src.lost = lost >> (2 * (ST - 1)) & 3;
+      if (32 * t + 32 <= kall) rows.template attend<false>(src, 32 * t);
+      else rows.template attend<true>(src, 32 * t);
+      now = now + 1 == ST ? 0 : now + 1;
+      next = next + 1 == ST ? 0 : next + 1;
+    }
+    wait_loads<0>();
   }
 
-  rows.finish(u.over);
+  rows.finish(k.over);
+  __syncthreads();                             // the rings are read out and nothing is in flight to them
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     if (n > 0) __syncthreads();
-    if (lg == 0) s_ml[wave][r16][0] = rows.m[n], s_ml[wave][r16][1] = rows.ls[n];
+    if (lg == 0) s.end.ml[wave][r16][0] = rows.m[n], s.end.ml[wave][r16][1] = rows.ls[n];
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       float y[8];
       rows.channels(n, w, y);
-      float4 *p = (float4 *)&s_o[wave][r16][32 * w + 8 * lg];
+      float4 *p = (float4 *)&s.end.o[wave][r16][32 * w + 8 * lg];
       p[0] = make_float4(y[0], y[1], y[2], y[3]);
       p[1] = make_float4(y[4], y[5], y[6], y[7]);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * DIM; i += 256) {
-      const int r = i / DIM, ch = i % DIM, m = 16 * n + r;
-      if (m >= mrows) continue;
-      float top = s_ml[0][r][0];
+    // thread: one row, every 16th group of four channels
+    const int r = threadIdx.x >> 4, m = 16 * n + r;
+    if (m < mrows) {
+      float top = s.end.ml[0][r][0];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) top = fmaxf(top, s_ml[w][r][0]);
+      for (int w = 1; w < 4; ++w) top = fmaxf(top, s.end.ml[w][r][0]);
       const float ref = top == kNegInf ? 0.0f : top;
-      float sum = 0.0f, l2 = 0.0f;
+      float f[4], l2 = 0.0f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float f = exp2_any(s_ml[w][r][0] - ref);
-        l2 += f * s_ml[w][r][1];
-        sum += f * s_o[w][r][ch];
+        f[w] = exp2_any(s.end.ml[w][r][0] - ref);
+        l2 = __builtin_fmaf(f[w], s.end.ml[w][r][1], l2);
       }
-      if (nsplit == 1) {
-        const int mm = u.m0 + m, q = mm / g;
-        store_out(a, ((u.rt.q0 + q) * a.hq + (int64_t)u.h * g + (mm - q * g)) * DIM + ch, l2 == 0.0f ? 0.0f : sum / l2);
-      } else {
-        float *p = part + ((u.unit * nsplit + u.split) * TM + m) * (DIM + 2);
-        p[ch] = sum;
-        if (ch == 0) p[DIM] = top, p[DIM + 1] = l2;
+      const float inv = k.nsplit > 1 ? 1.0f : l2 == 0.0f ? 0.0f : 1.0f / l2;
+      const int mm = m0 + m;
+      const int64_t at = row_at(a, k, h, mm, (int)((unsigned)mm / (unsigned)a.g)) * DIM;
+      float *to = part_sum(a, cut, (int)run, h, m, DIM);
+#pragma unroll
+      for (int i = 0; i < DIM / 64; ++i) {
+        const int ch = 64 * i + 4 * (threadIdx.x & 15);
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float4 z = *(const float4 *)&s.end.o[w][r][ch];
+          y[0] = __builtin_fmaf(f[w], z.x, y[0]), y[1] = __builtin_fmaf(f[w], z.y, y[1]);
+          y[2] = __builtin_fmaf(f[w], z.z, y[2]), y[3] = __builtin_fmaf(f[w], z.w, y[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] *= inv;
+        if (k.nsplit > 1) *(float4 *)(to + ch) = make_float4(y[0], y[1], y[2], y[3]);
+        else if (a.obf16) *(uint2 *)((uint16_t *)a.out + at + ch) = make_uint2(pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3]));
+        else *(float4 *)((float *)a.out + at + ch) = make_float4(y[0], y[1], y[2], y[3]);
       }
+      if (k.nsplit > 1 && (threadIdx.x & 15) == 0) *part_ml(a, cut, (int)run, h, m, DIM) = make_float2(top, l2);
     }
   }
 }
@@ -550,6 +790,8 @@ template <int DIM, int GROUP>
 struct LdsPart {             // 32 tokens of it
   const LdsTile<DIM, GROUP> &t;
   int p;
+  __device__ __forceinline__ void keys() {}
+  __device__ __forceinline__ void values() {}
   __device__ __forceinline__ uint4 kcode(int b, int w) const {
     return t.k[(2 * p + b) * (DIM / 32) + w][threadIdx.x & 63];
   }
@@ -573,39 +815,47 @@ struct LdsPart {             // 32 tokens of it
 // come to registers while the tile before is worked on, and are expanded into
 // the other half of LDS behind it.
 template <int DIM, int GROUP, int NQ, bool XF32>
-__global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const int64_t slots, const int nsplit,
-                                                          float *__restrict__ part) {
+__global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const Kv4Cut cut) {
   typedef LdsTile<DIM, GROUP> Lds;
   constexpr int NG = Lds::NG, W = Lds::W, TB = Lds::TB, TOK = Lds::TOK, TM = 64 * NQ, REC = 4 * DIM + 32 * NG;
   constexpr int WPW = TB * W / 4;            // words of a record's lane that a wave expands
   constexpr int SW = TB == 4 ? 32 * NG : 16 * NG, NS = (SW + 63) / 64;   // pairs a wave brings
   __shared__ __attribute__((aligned(16))) Lds s[2];
 
-  const Unit u = unit_of(a, slots, nsplit, TM, DIM);
-  if (u.skip) return;
+  const unsigned run = blockIdx.x / (unsigned)a.hkv;
+  const int h = (int)(blockIdx.x - run * a.hkv);     // heads are neighbours: a head's rows meet in one XCD's L2
+  const Work k = find_work(a, cut, (int)run);
+  note_joint(a, cut, k, (int)run, h, DIM);
+  if (k.none) return;
+  if (k.bad) {
+    if ((int)run < cut.slots && cut.extra == 0) nan_share(a, (int)run, cut.slots, h, DIM);
+    return;
+  }
+  const int rows_all = k.ql * a.g, m0 = k.tile * TM;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r16 = lane & 15, lg = lane >> 4, g = u.g;
-  const int last = u.m0 + TM < u.rows ? u.m0 + TM : u.rows;              // past the workgroup's last row
-  const int w0 = u.m0 + 16 * NQ * wave, w1 = w0 + 16 * NQ < last ? w0 + 16 * NQ : last;
+  const int r16 = lane & 15, lg = lane >> 4;
+  const int last = m0 + TM < rows_all ? m0 + TM : rows_all;              // past the workgroup's last row
+  const int w0 = m0 + 16 * NQ * wave, w1 = w0 + 16 * NQ < last ? w0 + 16 * NQ : last;
   const float c = a.scale * 1.44269504088896340736f;
   Rows<DIM, GROUP, NQ, XF32> rows;
-  rows.start(a, u.rt, u.h, g, u.len, w0, u.rows, c);
+  rows.start(a, k, h, w0, rows_all, c);
 
-  const int kend = limit_of(a, u.len, u.rt.ql, (last - 1) / g);
-  const int wend = w1 > w0 ? limit_of(a, u.len, u.rt.ql, (w1 - 1) / g) : 0;   // this wave's rows reach this far,
-  const int wall = w1 > w0 ? limit_of(a, u.len, u.rt.ql, w0 / g) : 0;         // all of them this far
+  auto limit = [&](int m) __attribute__((always_inline)) {
+    return limit_of(a, k.len, k.ql, (int)((unsigned)m / (unsigned)a.g));
+  };
+  const int kend = limit(last - 1);
+  const int wend = w1 > w0 ? limit(w1 - 1) : 0, wall = w1 > w0 ? limit(w0) : 0;   // one, all of this wave's rows reach these
   const int tiles = (kend + TOK - 1) / TOK;
-  const int t0 = (int)((int64_t)tiles * u.split / nsplit), t1 = (int)((int64_t)tiles * (u.split + 1) / nsplit);
+  const int t0 = share_of(tiles, k.split, k.nsplit), t1 = share_of(tiles, k.split + 1, k.nsplit);
   if (t0 < t1) {
-    Pages pg = pages_of(a, u.rt.seq, kend);
-    const int pb = a.page >> 4;
+    Pages pg = pages_of<4 * REC>(a, k.seq, h, kend);
     const int blk = TB == 4 ? wave : wave >> 1, off = TB == 4 ? 0 : WPW * (wave & 1);
     const int soff = TB == 4 ? 0 : 16 * NG * (wave & 1);
     uint32_t kw[WPW], vw[WPW], sw[NS];
     auto fetch = [&](int t) __attribute__((always_inline)) {
       if (TB * t - pg.base >= 64) pg.load(TB * t);
-      const int b = TB * t + blk, page = pg.of(b), at = b < pg.last ? b : pg.last;
-      const uint32_t *p = a.cache + (((int64_t)(page < 0 ? 0 : page) * a.hkv + u.h) * pb + (at & (pb - 1))) * REC;
+      const int page = pg.of(TB * t + blk);
+      const uint32_t *p = (const uint32_t *)pg.template at<4 * REC>(page, TB * t + blk);
       load_words(p + lane * W + off, kw);
       load_words(p + 2 * DIM + lane * W + off, vw);
 #pragma unroll
@@ -646,7 +896,7 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
 #pragma unroll
       for (int p = 0; p < TB / 2; ++p) {
         const int first = t * TOK + 32 * p;
-        const LdsPart<DIM, GROUP> src = {d, p};
+        LdsPart<DIM, GROUP> src = {d, p};
         if (first + 32 <= wall) rows.template attend<false>(src, first);
         else if (first < wend) rows.template attend<true>(src, first);
       }
@@ -655,22 +905,22 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
     }
   }
 
-  rows.finish(u.over);
+  rows.finish(k.over);
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const int mm = w0 + 16 * n + r16;
     if (mm >= w1) continue;
-    const int q = mm / g;
-    const int64_t at = ((u.rt.q0 + q) * a.hq + (int64_t)u.h * g + (mm - q * g)) * DIM + 8 * lg;
-    float *p = part + ((u.unit * nsplit + u.split) * TM + (mm - u.m0)) * (DIM + 2);
+    const int64_t at = row_at(a, k, h, mm, (int)((unsigned)mm / (unsigned)a.g)) * DIM + 8 * lg;
+    float *p = part_sum(a, cut, (int)run, h, mm - m0, DIM);
     const float inv = rows.ls[n] == 0.0f ? 0.0f : 1.0f / rows.ls[n];
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       float y[8];
       rows.channels(n, w, y);
-      if (nsplit > 1) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) *(float2 *)(p + 32 * w + 8 * lg + e) = make_float2(y[e], y[e + 1]);
+      if (k.nsplit > 1) {
+        float4 *z = (float4 *)(p + 32 * w + 8 * lg);
+        z[0] = make_float4(y[0], y[1], y[2], y[3]);
+        z[1] = make_float4(y[4], y[5], y[6], y[7]);
       } else if (a.obf16) {
         uint32_t z[4];
 #pragma unroll
@@ -682,73 +932,82 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
         z[1] = make_float4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
       }
     }
-    if (nsplit > 1 && lg == 0) p[DIM] = rows.m[n], p[DIM + 1] = rows.ls[n];
+    if (k.nsplit > 1 && lg == 0) *part_ml(a, cut, (int)run, h, mm - m0, DIM) = make_float2(rows.m[n], rows.ls[n]);
   }
 }
 
-// Joins the splits of one row: thread (x, y) takes two channels of every
-// PARTS-th split, then the PARTS results meet in LDS.
-template <int DIM>
-__global__ __launch_bounds__(256) void kv4_join_kernel(const Kv4Args a, const int64_t slots, const int nsplit,
-                                                       const int tm, const float *__restrict__ part) {
-  constexpr int LANES = DIM / 2, PARTS = 256 / LANES;
-  __shared__ float s_m[PARTS], s_l[PARTS];
-  __shared__ float2 s_o[PARTS][LANES];
-  const int64_t unit = blockIdx.x / (unsigned)tm;
-  const int m = (int)(blockIdx.x % (unsigned)tm);
-  const int64_t slot = unit / a.hkv;
-  const int h = (int)(unit - slot * a.hkv);
-  const int g = (int)(a.hq / a.hkv);
-  const RowTile rt = find_tile(a, slot, tm);
-  if (rt.none) return;
-  if (rt.bad) {
-    if (m == 0) nan_share(a, slot, slots, h, DIM);
-    return;
-  }
-  const int mm = rt.tile * tm + m;
-  if (mm >= rt.ql * g) return;
-  const int x = threadIdx.x % LANES, y = threadIdx.x / LANES;
-  const float *p = part + (unit * nsplit * tm + m) * (DIM + 2);
-  const int64_t stride = (int64_t)tm * (DIM + 2);
-  float top = kNegInf, l = 0.0f;
-  float2 o = make_float2(0.0f, 0.0f);
-  for (int s = y; s < nsplit; s += PARTS) {
-    const float *q = p + s * stride;
-    const float ms = q[DIM], lq = q[DIM + 1];
-    const float2 u = *(const float2 *)(q + 2 * x);
-    const float m2 = fmaxf(top, ms), ref = m2 == kNegInf ? 0.0f : m2;
-    const float f0 = exp2_any(top - ref), f1 = exp2_any(ms - ref);
-    top = m2;
-    l = l * f0 + lq * f1;
-    o.x = o.x * f0 + u.x * f1;
-    o.y = o.y * f0 + u.y * f1;
-  }
-  if (x == 0) s_m[y] = top, s_l[y] = l;
-  s_o[y][x] = o;
-  __syncthreads();
-  if (y > 0) return;
-  float all = kNegInf;
+// Joins the runs of a row: PARTS waves share them (4 where there may be
+// many), lane l takes the DIM / 64 channels from DIM / 64 l on.  A wave has 64 runs' factors before
+// the first of their sums is read, so the reads do not wait for each other.
+template <int DIM, int PARTS>
+__global__ __launch_bounds__(256) void kv4_join_kernel(const Kv4Args a, const Kv4Cut cut) {
+  constexpr int CH = DIM / 64;
+  __shared__ float s_o[PARTS][DIM];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // tm is a multiple of 4: the rows of a workgroup are of one tile
+  const unsigned row = blockIdx.x * (4 / PARTS) + wave / PARTS, x = row >> cut.tm_log;   // uniform
+  const int m = (int)(row & (cut.tm - 1)), y = wave % PARTS;
+  const unsigned slot = x / (unsigned)a.hkv;
+  const int h = (int)(x - slot * a.hkv);
+  const Joint k = joints(a, cut, DIM)[slot];
+  const int mm = k.m0 + m, n = k.runs;
+  if (n < 0 && m < 4 / PARTS) nan_share(a, (int)slot, cut.slots, h, DIM);
+  if (n <= 1 || mm >= k.ql * a.g) return;         // uniform over what shares LDS
+  const int64_t next = (int64_t)a.hkv * cut.tm;   // rows from one run to the next
+  const float2 *ml = part_ml(a, cut, k.first, h, m, DIM);
+  const float2 u0 = lane < n ? ml[lane * next] : make_float2(kNegInf, 0.0f);
+  float top = u0.x;
+  for (int s = 64 + lane; s < n; s += 64) top = fmaxf(top, ml[s * next].x);
+  top = group_max<64>(top);
+  const float ref = top == kNegInf ? 0.0f : top;
+  float l = 0.0f, o[CH];
 #pragma unroll
-  for (int i = 0; i < PARTS; ++i) all = fmaxf(all, s_m[i]);
-  const float ref = all == kNegInf ? 0.0f : all;
-  float l2 = 0.0f, u = 0.0f, w = 0.0f;
+  for (int i = 0; i < CH; ++i) o[i] = 0.0f;
+  const float *p = part_sum(a, cut, k.first, h, m, DIM) + CH * lane;
+  for (int s0 = 0; s0 < n; s0 += 64) {
+    const float2 u = s0 == 0 ? u0 : s0 + lane < n ? ml[(s0 + lane) * next] : make_float2(kNegInf, 0.0f);
+    const float f = exp2_any(u.x - ref);
+    l += f * u.y;
+    const int s1 = n - s0 < 64 ? n - s0 : 64;
+#pragma unroll 8
+    for (int s = y; s < s1; s += PARTS) {
+      const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
+      const float *q = p + (s0 + s) * next * DIM;
+      float z[CH];
+      if constexpr (CH == 1) {
+        z[0] = q[0];
+      } else if constexpr (CH == 2) {
+        const float2 v = *(const float2 *)q;
+        z[0] = v.x, z[1] = v.y;
+      } else {
+        const float4 v = *(const float4 *)q;
+        z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
+      }
 #pragma unroll
-  for (int i = 0; i < PARTS; ++i) {
-    const float f = exp2_any(s_m[i] - ref);
-    l2 += f * s_l[i];
-    u += f * s_o[i][x].x;
-    w += f * s_o[i][x].y;
+      for (int i = 0; i < CH; ++i) o[i] = __builtin_fmaf(fs, z[i], o[i]);
+    }
   }
-  const int q = mm / g;
-  const int64_t at = ((rt.q0 + q) * a.hq + (int64_t)h * g + (mm - q * g)) * DIM + 2 * x;
-  store_out(a, at, l2 == 0.0f ? 0.0f : u / l2);
-  store_out(a, at + 1, l2 == 0.0f ? 0.0f : w / l2);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d, 64);
+  if constexpr (PARTS > 1) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) s_o[y][CH * lane + i] = o[i];
+    __syncthreads();
+    if (y > 0) return;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      for (int w = 1; w < PARTS; ++w) o[i] += s_o[w][CH * lane + i];
+  }
+  const int64_t at = row_at(a, k, h, mm, (int)((unsigned)mm / (unsigned)a.g)) * DIM + CH * lane;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) store_out(a, at + i, o[i] * inv);
 }
 
 template <int DIM, int GROUP>
-hipError_t launch_group(const Kv4Args &a, float *ws, const Kv4Plan &p, hipStream_t st) {
-  const unsigned grid = (unsigned)(p.slots * a.hkv * p.nsplit);
-#define RUN(KERNEL, NQ, X) KERNEL<DIM, GROUP, NQ, X><<<grid, 256, 0, st>>>(a, p.slots, p.nsplit, ws)
+hipError_t launch_group(const Kv4Args &a, const Kv4Cut &cut, const Kv4Plan &p, hipStream_t st) {
+  const unsigned grid = (unsigned)((int64_t)(p.slots + p.extra) * a.hkv);
+#define RUN(KERNEL, NQ, X) KERNEL<DIM, GROUP, NQ, X><<<grid, 256, 0, st>>>(a, cut)
   if (p.tile) {
     if (!a.qbf16) RUN(kv4_tile_kernel, 1, true);
     else if constexpr (DIM == 256) RUN(kv4_tile_kernel, 1, false);
@@ -761,14 +1020,16 @@ hipError_t launch_group(const Kv4Args &a, float *ws, const Kv4Plan &p, hipStream
   }
 #undef RUN
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.nsplit == 1) return e;
-  kv4_join_kernel<DIM><<<(unsigned)(p.slots * a.hkv * p.tm), 256, 0, st>>>(a, p.slots, p.nsplit, p.tm, ws);
+  if (e != hipSuccess || p.extra == 0) return e;
+  const int64_t rows = (int64_t)p.slots * a.hkv * p.tm;
+  if (p.most > 8) kv4_join_kernel<DIM, 4><<<(unsigned)rows, 256, 0, st>>>(a, cut);
+  else kv4_join_kernel<DIM, 1><<<(unsigned)(rows / 4), 256, 0, st>>>(a, cut);
   return hipGetLastError();
 }
 
-hipError_t launch_dim64(const Kv4Args &a, float *ws, const Kv4Plan &p, hipStream_t st);
-hipError_t launch_dim128(const Kv4Args &a, float *ws, const Kv4Plan &p, hipStream_t st);
-hipError_t launch_dim256(const Kv4Args &a, float *ws, const Kv4Plan &p, hipStream_t st);
+hipError_t launch_dim64(const Kv4Args &a, const Kv4Cut &cut, const Kv4Plan &p, hipStream_t st);
+hipError_t launch_dim128(const Kv4Args &a, const Kv4Cut &cut, const Kv4Plan &p, hipStream_t st);
+hipError_t launch_dim256(const Kv4Args &a, const Kv4Cut &cut, const Kv4Plan &p, hipStream_t st);
 
 }  // namespace kv4
 }  // namespace slim

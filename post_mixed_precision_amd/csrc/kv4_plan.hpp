@@ -24,21 +24,24 @@ inline int64_t kv4_page_words(int page, int dim, int group) {
 }
 
 // How an attention call is cut.  Rows (a sequence's query tokens times the
-// query heads of one key head) go in tiles of tm, a tile's tokens over
-// `nsplit` workgroups, whose partial results are joined by a second kernel.
+// query heads of one key head) go in tiles of tm.  Lengths are known on the
+// device only, so the tiles' tokens are cut there: into `extra` runs a head
+// beyond one for every tile, in proportion to their number.
 struct Kv4Plan {
   bool tile;                 // many rows: four waves of 16 nq rows share the tokens; else each wave has its own
   int nq;                    // tiles of 16 rows a wave holds
   int tm;
-  int64_t slots;             // row tiles, at most (uneven queries: some stay idle)
-  int nsplit;
+  int tiles;                 // row tiles of a sequence (uniform)
+  int slots;                 // row tiles, at most (uneven queries: some stay idle)
+  int extra;                 // runs beyond them, at most; 0: no joining
+  int least;                 // tiles of 32 tokens a run has at least (where a sequence has them)
+  int most;                  // runs a tile has on average, at most
   size_t ws_bytes;
 };
 
-// b sequences, tq query tokens in all (uniform: tq / b each), max_len: the
-// tokens a row of the page table can name.
-inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t hkv, int dim, int64_t max_len,
-                        bool f32) {
+// b sequences, tq query tokens in all (uniform: tq / b each), cap: the tokens
+// a row of the page table can name.
+inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t hkv, int dim, int group, int64_t cap, bool f32) {
   Kv4Plan p;
   const int64_t g = hq / hkv;
   const int64_t per = (uniform ? tq / b : (tq + b - 1) / b) * g;   // rows of a sequence, on average
@@ -46,13 +49,18 @@ inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t
   p.tile = per > (wide ? 32 : 16);
   p.nq = wide && per > 16 ? 2 : 1;
   p.tm = 16 * p.nq * (p.tile ? 4 : 1);
-  p.slots = uniform ? b * ((per + p.tm - 1) / p.tm) : tq * g / p.tm + (b < tq ? b : tq);
-  const int64_t units = p.slots * hkv;
-  int64_t s = (512 + units - 1) / units;                   // two workgroups of 4 waves a CU
-  const int64_t useful = (max_len + 255) / 256;
-  s = s > useful ? useful : s;
-  p.nsplit = (int)(s < 1 ? 1 : s > 128 ? 128 : s);
-  p.ws_bytes = p.nsplit > 1 ? (size_t)units * p.nsplit * p.tm * (dim + 2) * 4 : 0;
+  p.tiles = (int)((per + p.tm - 1) / p.tm);
+  p.slots = (int)(uniform ? b * p.tiles : tq * g / p.tm + (b < tq ? b : tq));
+  p.least = 8;
+  // as many workgroups as the card holds at once (by registers and LDS): one round, all runs alike
+  const int64_t want = 256 * (p.tile ? 3 : dim == 64 ? 4 : wide && p.nq == 1 ? 3 : 2);
+  const int64_t units = p.slots * hkv, tokens = (cap + 31) / 32;
+  int64_t extra = units >= want ? 0 : (want - units + hkv - 1) / hkv;
+  const int64_t useful = p.slots * ((tokens + p.least - 1) / p.least - 1);   // no run below `least`
+  p.extra = (int)(extra < useful ? extra : useful);
+  const int64_t most = (tokens + p.least - 1) / p.least;
+  p.most = (int)(most < p.extra / p.slots + 1 ? most : p.extra / p.slots + 1);
+  p.ws_bytes = p.extra > 0 ? (size_t)(p.slots + p.extra) * hkv * p.tm * (dim + 2) * 4 + (size_t)p.slots * 32 : 0;
   return p;
 }
 

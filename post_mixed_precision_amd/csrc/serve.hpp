@@ -68,11 +68,18 @@ struct Kv4Args {
   const uint32_t *cache;
   const int32_t *table;      // [b, per] pages of each sequence
   const int32_t *lengths;    // [b]
-  const int32_t *offsets;    // b + 1 bounds of the sequences' query tokens, or null: tq / b each
-  int64_t b, tq, hq, hkv, pages, per;
+  const int32_t *offsets;    // b + 1 bounds of the sequences' query tokens, or null: ql each
+  int b, tq, ql, hq, hkv, g, pages, per;   // g = hq / hkv
+  int cap;                   // tokens a row of the table can name
   int dim, group, page;
   float scale;
   bool causal, qbf16, obf16;
+};
+struct Kv4Cut {
+  float *part;               // partial results
+  int tm, tm_log;            // a power of two
+  int tiles;                 // row tiles a sequence, without offsets
+  int slots, extra, least;
 };
 hipError_t launch_kv4_attention(const Kv4Args &a, void *ws, const Kv4Plan &p, hipStream_t st);
 
