@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(HERE, "libslim.so")
 SLIM_F32, SLIM_BF16 = 0, 1
 LOGPROB_MAX_TOP = 64    # SLIM_LOGPROB_MAX_TOP
 KV4_MAX_SLOTS, KV4_MAX_HEADS, KV4_MAX_T, KV4_MAX_SEQS = 1 << 30, 1024, 1 << 20, 65536    # SLIM_KV4_MAX_*
-DRAFT_MAX_K = 32        # SLIM_DRAFT_MAX_K
+DRAFT_MAX_B, DRAFT_MAX_K = 65536, 32    # SLIM_DRAFT_MAX_*
+LOGPROB_MAX_V = 1 << 24    # SLIM_LOGPROB_MAX_V
 STATUS = {0: "SLIM_OK", -1: "SLIM_E_NULL", -2: "SLIM_E_SHAPE", -3: "SLIM_E_DTYPE",
           -4: "SLIM_E_PARAM", -5: "SLIM_E_WORKSPACE", -6: "SLIM_E_HIP", -7: "SLIM_E_ALIGN"}
 
@@ -742,36 +743,97 @@ def kv4_cache(pages: int, heads: int, dim: int, group: int, page: int = 64, devi
     return torch.zeros((pages, heads, words), dtype=torch.int32, device=device)
 
 
-def _kv4_heads(t, name: str, shape, dtype):
-    """[tokens, heads, dim] rows, strided but for the channels -> their strides."""
-    t = _arg(t, name, shape, (dtype,))
-    row, head, step = t.stride()
-    if t.numel() == 0:
+def _tensors(**ts):
+    """Every given argument that is not None is a tensor."""
+    tensor = _torch().Tensor
+    for name, t in ts.items():
+        if t is not None and not isinstance(t, tensor):
+            raise SlimError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+
+
+def _where(dev: int, strided, dense):
+    """Every tensor is in the memory of GPU `dev`; the dense ones are contiguous."""
+    for t in dense:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            if not t.is_contiguous():
+                raise SlimError("tensors must be contiguous")
+            break
+    else:
+        for t in strided:
+            if t is not None and t.get_device() != dev:
+                break
+        else:
+            if dev >= 0:
+                return
+    ts = [t for t in (*strided, *dense) if t is not None]
+    if not all(t.is_cuda for t in ts):
+        raise SlimError("tensors must live in GPU memory")
+    raise SlimError(f"tensors live on different devices: {sorted({str(t.device) for t in ts})}")
+
+
+def _span(shape, stride, size: int) -> int:
+    """Bytes from a tensor's first entry to past its last."""
+    n = 1
+    for count, step in zip(shape, stride):
+        if count == 0:
+            return 0
+        n += (count - 1) * step
+    return n * size
+
+
+def _want(name: str, shape, dtype, like, dtypes):
+    """Shape (None entries are free) and dtype of an argument, checked on what a plan is given."""
+    if dtype not in dtypes:
+        raise SlimError(f"{name}: dtype {dtype}, expected one of {list(dtypes)}")
+    if len(shape) != len(like) or any(b is not None and a != b for a, b in zip(shape, like)):
+        raise SlimError(f"{name}: shape {tuple(shape)}, expected {tuple('*' if s is None else s for s in like)}")
+
+
+def _kv4_heads(shape, stride, name: str):
+    """Strides of [tokens, heads, dim] rows, strided but for the channels."""
+    if 0 in shape:
         return 0, 0
+    row, head, step = stride
     if step != 1 or row < 0 or head < 0:
         raise SlimError(f"{name}: a head's channels must be contiguous")
-    return (0 if t.shape[0] == 1 else row), (0 if t.shape[1] == 1 else head)
+    return (0 if shape[0] == 1 else row), (0 if shape[1] == 1 else head)
 
 
-def _span(t):
-    """First and last byte of a tensor with nonnegative strides."""
-    a = t.data_ptr()
-    n = 1
-    for size, step in zip(t.shape, t.stride()):
-        if size == 0:
-            return a, a
-        n += (size - 1) * step
-    return a, a + n * t.element_size()
-
-
-def _outside(Y, yname: str, **ins):
-    """Y, which is written while other workgroups still read, shares no byte with an input."""
-    a, b = _span(Y)
-    for name, t in ins.items():
-        if t is not None:
-            lo, hi = _span(t)
-            if a < hi and lo < b:
-                raise SlimError(f"{yname}: overlaps {name}")
+@functools.lru_cache(maxsize=4096)
+def _append_plan(k, v, q, slots, cache, rotary, positions, group):
+    """Checks of kv4_append's shapes, strides and types (a tensor is (shape, dtype[, stride])), once for each
+    set of them -> the sizes the call passes."""
+    torch = _torch()
+    i32 = (torch.int32,)
+    _want("k", k[0], k[1], (None, None, None), _float_types())
+    t, heads, dim = k[0]
+    _want("cache", *cache, (None, heads, None), i32)
+    page = _kv4_page(cache[0][2], dim, group)
+    _want("v", v[0], v[1], k[0], (k[1],))
+    _want("slots", *slots, (t,), i32)
+    rot = npos = hq = 0
+    if (rotary is None) != (positions is None):
+        raise SlimError("rotary and positions are given together")
+    if rotary is not None:
+        _want("rotary", *rotary, (None, None), (torch.float32,))
+        npos, rot = rotary[0]
+        if npos < 1 or rot < 2 or rot > dim or rot % 2:
+            raise SlimError(f"rotary: shape {tuple(rotary[0])}, expected [positions, an even number up to {dim}]")
+        _want("positions", *positions, (t,), i32)
+    qs = (0, 0)
+    if q is not None:
+        _want("q", q[0], q[1], (t, None, dim), (k[1],))
+        hq = q[0][1]
+        if hq > KV4_MAX_HEADS:
+            raise SlimError(f"q: {hq} heads, at most {KV4_MAX_HEADS}")
+        qs = _kv4_heads(q[0], q[2], "q")
+    if t > KV4_MAX_T:
+        raise SlimError(f"k: {t} tokens, at most {KV4_MAX_T}")
+    size = 2 if k[1] == torch.bfloat16 else 4
+    reach = {"k": _span(k[0], k[2], size), "v": _span(v[0], v[2], size), "q": 0 if q is None else _span(q[0], q[2], size)}
+    code = SLIM_BF16 if k[1] == torch.bfloat16 else SLIM_F32
+    return (page, *_kv4_heads(k[0], k[2], "k"), *_kv4_heads(v[0], v[2], "v"), *qs, code, t, heads, dim, npos, rot, hq, reach,
+            cache[0][0] * cache[0][1] * cache[0][2] * 4)
 
 
 def kv4_append(k, v, slots, cache, group: int, rotary=None, positions=None, interleaved: bool = False, q=None):
@@ -782,76 +844,103 @@ def kv4_append(k, v, slots, cache, group: int, rotary=None, positions=None, inte
     of rot apart, or adjacent if interleaved, and so are q's [t, query heads, dim], which are returned
     (in q's dtype).  Writes the slots given and nothing else."""
     torch = _torch()
-    lib = load_library()
-    k = _arg(k, "k", (None, None, None), _float_types())
-    t, heads, dim = k.shape
-    cache = _arg(cache, "cache", (None, heads, None), (torch.int32,))
-    page = _kv4_page(cache.shape[2], dim, group)
-    krow, khead = _kv4_heads(k, "k", None, k.dtype)
-    vrow, vhead = _kv4_heads(v, "v", (t, heads, dim), k.dtype)
-    slots = _arg(slots, "slots", (t,), (torch.int32,))
-    rot = npos = qrow = qhead = hq = 0
-    if (rotary is None) != (positions is None):
-        raise SlimError("rotary and positions are given together")
-    if rotary is not None:
-        rotary = _arg(rotary, "rotary", (None, None), (torch.float32,))
-        npos, rot = rotary.shape
-        if npos < 1 or rot < 2 or rot > dim or rot % 2:
-            raise SlimError(f"rotary: shape {tuple(rotary.shape)}, expected [positions, an even number up to {dim}]")
-        positions = _arg(positions, "positions", (t,), (torch.int32,))
-    if q is not None:
-        qrow, qhead = _kv4_heads(q, "q", (t, None, dim), k.dtype)
-        hq = q.shape[1]
-        if hq > KV4_MAX_HEADS:
-            raise SlimError(f"q: {hq} heads, at most {KV4_MAX_HEADS}")
-    if t > KV4_MAX_T:
-        raise SlimError(f"k: {t} tokens, at most {KV4_MAX_T}")
-    dev = k.device
-    _ready(dev, slots, cache, rotary, positions)
-    for x in (k, v, q):
-        if x is not None and x.device != dev:
-            raise SlimError(f"tensors live on different devices: {dev}, {x.device}")
-    if dev.type != "cuda":
-        raise SlimError("tensors must live in GPU memory")
-    _outside(cache, "cache", k=k, v=v, q=q, slots=slots, rotary=rotary, positions=positions)
-    if dev.index != torch.cuda.current_device():
+    _tensors(k=k, v=v, slots=slots, cache=cache, rotary=rotary, positions=positions, q=q)
+    page, krow, khead, vrow, vhead, qrow, qhead, code, t, heads, dim, npos, rot, hq, reach, size = _append_plan(
+        (k.shape, k.dtype, k.stride()), (v.shape, v.dtype, v.stride()), None if q is None else (q.shape, q.dtype, q.stride()),
+        (slots.shape, slots.dtype), (cache.shape, cache.dtype), None if rotary is None else (rotary.shape, rotary.dtype),
+        None if positions is None else (positions.shape, positions.dtype), group)
+    dev = k.get_device()
+    _where(dev, (k, v, q), (slots, cache, rotary, positions))
+    kp, vp, sp, cp = k.data_ptr(), v.data_ptr(), slots.data_ptr(), cache.data_ptr()
+    rp = pp = qp = op = None
+    end = cp + size
+    if rot:
+        rp, pp = rotary.data_ptr(), positions.data_ptr()
+    if hq:
+        qp = q.data_ptr()
+    # the cache is written while other workgroups still read: it shares no byte with an input
+    if kp < end and cp < kp + reach["k"] or vp < end and cp < vp + reach["v"] or sp < end and cp < sp + 4 * t \
+            or rot and (rp < end and cp < rp + 4 * rot * npos or pp < end and cp < pp + 4 * t) \
+            or hq and qp < end and cp < qp + reach["q"]:
+        raise SlimError("cache: overlaps an input")
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return kv4_append(k, v, slots, cache, group, rotary, positions, interleaved, q)
-    out = None if q is None else torch.empty((t, hq, dim), dtype=k.dtype, device=dev)
-    st = lib.slim_kv4_append(k.data_ptr(), krow, khead, v.data_ptr(), vrow, vhead, _dtype_code(k), t, heads, dim, group,
-                             slots.data_ptr(), cache.data_ptr(), cache.shape[0], page,
-                             None if rotary is None else rotary.data_ptr(), npos, rot, 1 if interleaved else 0,
-                             None if rotary is None else positions.data_ptr(), q.data_ptr() if hq else None, hq, qrow,
-                             qhead, out.data_ptr() if hq else None, _raw_stream(dev.index))
+    out = None
+    if q is not None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        op = out.data_ptr() if hq else None
+    st = load_library().slim_kv4_append(kp, krow, khead, vp, vrow, vhead, code, t, heads, dim, group, sp, cp,
+                                        cache.shape[0], page, rp, npos, rot, 1 if interleaved else 0, pp, qp, hq, qrow,
+                                        qhead, op, _raw_stream(dev))
     if st:
         check(st, "slim_kv4_append")
     return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _read_plan(slots, cache, dim, group):
+    torch = _torch()
+    _want("slots", *slots, (None,), (torch.int32,))
+    _want("cache", *cache, (None, None, None), (torch.int32,))
+    page = _kv4_page(cache[0][2], dim, group)
+    if slots[0][0] > KV4_MAX_T:
+        raise SlimError(f"slots: {slots[0][0]} of them, at most {KV4_MAX_T}")
+    return page, slots[0][0], cache[0][0], cache[0][1]
 
 
 def kv4_read(slots, cache, dim: int, group: int, out_dtype=None):
     """What slots (int32 [t]) of a kv4_cache stand for -> (k, v) [t, heads, dim] in out_dtype (float32
     by default, exact; bfloat16 is rounded): 0 for a negative slot, NaN for one past the cache."""
     torch = _torch()
-    lib = load_library()
+    _tensors(slots=slots, cache=cache)
     out_dtype = torch.float32 if out_dtype is None else out_dtype
     code = _out_code(out_dtype)
-    slots = _arg(slots, "slots", (None,), (torch.int32,))
-    cache = _arg(cache, "cache", (None, None, None), (torch.int32,))
-    page = _kv4_page(cache.shape[2], dim, group)
-    t, heads = slots.shape[0], cache.shape[1]
-    if t > KV4_MAX_T:
-        raise SlimError(f"slots: {t} of them, at most {KV4_MAX_T}")
-    dev = cache.device
-    _ready(dev, slots, cache)
-    if dev.index != torch.cuda.current_device():
+    page, t, pages, heads = _read_plan((slots.shape, slots.dtype), (cache.shape, cache.dtype), dim, group)
+    dev = cache.get_device()
+    _where(dev, (), (slots, cache))
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return kv4_read(slots, cache, dim, group, out_dtype)
-    k, v = torch.empty((2, t, heads, dim), dtype=out_dtype, device=dev)
-    st = lib.slim_kv4_read(slots.data_ptr(), t, cache.data_ptr(), cache.shape[0], page, heads, dim, group, k.data_ptr(),
-                           v.data_ptr(), code, _raw_stream(dev.index))
+    k, v = torch.empty((2, t, heads, dim), dtype=out_dtype, device=cache.device).unbind(0)
+    st = load_library().slim_kv4_read(slots.data_ptr(), t, cache.data_ptr(), pages, page, heads, dim, group,
+                                      k.data_ptr(), v.data_ptr(), code, _raw_stream(dev))
     if st:
         check(st, "slim_kv4_read")
     return k, v
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_plan(q, cache, table, lengths, offsets, group, out_dtype, out):
+    """Checks of kv4_attention's shapes and types, once for each set -> the sizes the call passes."""
+    torch = _torch()
+    i32 = (torch.int32,)
+    _want("q", *q, (None, None, None, None) if offsets is None else (None, None, None), _float_types())
+    hq, dim = q[0][-2:]
+    _want("cache", *cache, (None, None, None), i32)
+    pages, heads = cache[0][:2]
+    page = _kv4_page(cache[0][2], dim, group)
+    _want("table", *table, (None, None), i32)
+    b, per = table[0]
+    _want("lengths", *lengths, (b,), i32)
+    if offsets is None:
+        if q[0][0] != b:
+            raise SlimError(f"q: shape {tuple(q[0])}, expected {b} sequences")
+        tq = b * q[0][1]
+    else:
+        _want("offsets", *offsets, (b + 1,), i32)
+        tq = q[0][0]
+    if heads < 1 or hq < 1 or hq % heads or hq > KV4_MAX_HEADS:
+        raise SlimError(f"q: {hq} heads, expected a multiple of the cache's {heads}, at most {KV4_MAX_HEADS}")
+    if b < 1 or b > KV4_MAX_SEQS or tq > KV4_MAX_T or per < 1 or per > KV4_MAX_SLOTS // page:
+        raise SlimError(f"table: shape {tuple(table[0])} with {tq} query tokens is out of range")
+    out_dtype = q[1] if out_dtype is None else out_dtype
+    if out is not None:
+        _want("out", *out, tuple(q[0]), (out_dtype,))
+    qcode, ocode = _out_code(q[1]), _out_code(out_dtype)
+    need = load_library().slim_kv4_attention_workspace(b, tq, 0 if offsets is None else 1, hq, heads, dim, group, per,
+                                                       page, qcode)
+    return qcode, tq, hq, pages, page, heads, dim, b, per, ocode, out_dtype, need
 
 
 def kv4_attention(q, cache, table, lengths, group: int, offsets=None, scale=None, causal: bool = True, out_dtype=None,
@@ -865,58 +954,41 @@ def kv4_attention(q, cache, table, lengths, group: int, offsets=None, scale=None
     out_dtype (q's by default).  Rows that attend to nothing are 0; rows outside the offsets are
     not written (a given out, apart from the inputs, keeps them)."""
     torch = _torch()
-    lib = load_library()
-    q = _arg(q, "q", (None, None, None, None) if offsets is None else (None, None, None), _float_types())
-    hq, dim = q.shape[-2:]
-    cache = _arg(cache, "cache", (None, None, None), (torch.int32,))
-    pages, heads = cache.shape[:2]
-    page = _kv4_page(cache.shape[2], dim, group)
-    table = _arg(table, "table", (None, None), (torch.int32,))
-    b, per = table.shape
-    lengths = _arg(lengths, "lengths", (b,), (torch.int32,))
-    if offsets is None:
-        if q.shape[0] != b:
-            raise SlimError(f"q: shape {tuple(q.shape)}, expected {b} sequences")
-        tq = b * q.shape[1]
-    else:
-        offsets = _arg(offsets, "offsets", (b + 1,), (torch.int32,))
-        tq = q.shape[0]
-    if heads < 1 or hq < 1 or hq % heads or hq > KV4_MAX_HEADS:
-        raise SlimError(f"q: {hq} heads, expected a multiple of the cache's {heads}, at most {KV4_MAX_HEADS}")
-    if b < 1 or b > KV4_MAX_SEQS or tq > KV4_MAX_T or per < 1 or per > KV4_MAX_SLOTS // page:
-        raise SlimError(f"table: shape {tuple(table.shape)} with {tq} query tokens is out of range")
-    out_dtype = q.dtype if out_dtype is None else out_dtype
-    ocode = _out_code(out_dtype)
+    _tensors(q=q, cache=cache, table=table, lengths=lengths, offsets=offsets, out=out)
+    qcode, tq, hq, pages, page, heads, dim, b, per, ocode, otype, need = _attention_plan(
+        (q.shape, q.dtype), (cache.shape, cache.dtype), (table.shape, table.dtype), (lengths.shape, lengths.dtype),
+        None if offsets is None else (offsets.shape, offsets.dtype), group, out_dtype,
+        None if out is None else (out.shape, out.dtype))
+    dev = q.get_device()
+    _where(dev, (), (q, cache, table, lengths, offsets, out))
     if out is not None:
-        out = _arg(out, "out", tuple(q.shape), (out_dtype,))
-    dev = q.device
-    _ready(dev, q, cache, table, lengths, offsets, out)
-    if out is not None:
-        _outside(out, "out", q=q, cache=cache, table=table, lengths=lengths, offsets=offsets)
-    if dev.index != torch.cuda.current_device():
+        a, e = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+        for name, t in (("q", q), ("cache", cache), ("table", table), ("lengths", lengths), ("offsets", offsets)):
+            if t is not None and t.data_ptr() < e and a < t.data_ptr() + t.numel() * t.element_size():
+                raise SlimError(f"out: overlaps {name}")
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return kv4_attention(q, cache, table, lengths, group, offsets, scale, causal, out_dtype, out)
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
-    qcode = _dtype_code(q)
-    need = _need("slim_kv4_attention_workspace", b, tq, 0 if offsets is None else 1, hq, heads, dim, group, per, page, qcode)
-    ws = _ws(need, dev) if need else None
-    st = lib.slim_kv4_attention(q.data_ptr(), qcode, tq, hq, cache.data_ptr(), pages, page, heads, dim, group,
-                                table.data_ptr(), b, per, lengths.data_ptr(),
-                                None if offsets is None else offsets.data_ptr(),
-                                dim ** -0.5 if scale is None else float(scale), 1 if causal else 0, out.data_ptr(),
-                                ocode, ws.data_ptr() if need else None, need, _raw_stream(dev.index))
+        out = torch.empty(q.shape, dtype=otype, device=q.device)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    st = load_library().slim_kv4_attention(q.data_ptr(), qcode, tq, hq, cache.data_ptr(), pages, page, heads, dim,
+                                           group, table.data_ptr(), b, per, lengths.data_ptr(),
+                                           None if offsets is None else offsets.data_ptr(),
+                                           dim ** -0.5 if scale is None else float(scale), 1 if causal else 0,
+                                           out.data_ptr(), ocode, ws.data_ptr() if need else None, need,
+                                           _raw_stream(dev))
     if st:
         check(st, "slim_kv4_attention")
     return out
 
 
-def _draft_rows(t, name: str, rows: int):
+def _draft_rows(shape, stride, name: str):
     """Strides of [b, rows, v] logits, strided but for a row's entries."""
-    b, _, v = t.shape
-    seq, row, step = t.stride()
+    b, rows, v = shape
     if b == 0:
         return 0, v
+    seq, row, step = stride
     if b == 1:
         seq = 0
     if rows == 1:
@@ -924,6 +996,26 @@ def _draft_rows(t, name: str, rows: int):
     if (v > 1 and step != 1) or row < v or seq < 0:
         raise SlimError(f"{name}: a row's entries must be contiguous and rows must not overlap")
     return seq, row
+
+
+@functools.lru_cache(maxsize=4096)
+def _verify_plan(target, tokens, uniform, draft):
+    torch = _torch()
+    _want("target", target[0], target[1], (None, None, None), _float_types())
+    b, k1, v = target[0]
+    k = k1 - 1
+    if not 1 <= k <= DRAFT_MAX_K:
+        raise SlimError(f"target: {k1} rows a sequence, expected 2 .. {DRAFT_MAX_K + 1}")
+    if not (1 <= v <= LOGPROB_MAX_V and b <= DRAFT_MAX_B):
+        raise SlimError(f"target: shape {tuple(target[0])} is out of range")
+    tseq, trow = _draft_rows(target[0], target[2], "target")
+    _want("tokens", *tokens, (b, k), (torch.int64,))
+    _want("uniform", *uniform, (b, k1), (torch.float32,))
+    dseq = drow = 0
+    if draft is not None:
+        _want("draft", draft[0], draft[1], (b, k, v), (target[1],))
+        dseq, drow = _draft_rows(draft[0], draft[2], "draft")
+    return tseq, trow, dseq, drow, _out_code(target[1]), b, k, v, load_library().slim_verify_draft_workspace(b, k, v)
 
 
 def verify_draft(target, tokens, uniform, draft=None, temperature: float = 1.0):
@@ -935,41 +1027,25 @@ def verify_draft(target, tokens, uniform, draft=None, temperature: float = 1.0):
     max(p_j - q_j, 0) or, after the last, from p -> dict(accepted int32 [b], ids int64 [b, k + 1]: the
     accepted tokens, the drawn one, then -1).  In float64 throughout."""
     torch = _torch()
-    lib = load_library()
-    target = _arg(target, "target", (None, None, None), _float_types())
-    b, k1, v = target.shape
-    k = k1 - 1
-    if not 1 <= k <= DRAFT_MAX_K:
-        raise SlimError(f"target: {k1} rows a sequence, expected 2 .. {DRAFT_MAX_K + 1}")
-    if v < 1:
-        raise SlimError("target: no entries")
-    tseq, trow = _draft_rows(target, "target", k1)
-    tokens = _arg(tokens, "tokens", (b, k), (torch.int64,))
-    uniform = _arg(uniform, "uniform", (b, k1), (torch.float32,))
-    dseq = drow = 0
-    if draft is not None:
-        draft = _arg(draft, "draft", (b, k, v), (target.dtype,))
-        dseq, drow = _draft_rows(draft, "draft", k)
+    _tensors(target=target, tokens=tokens, uniform=uniform, draft=draft)
+    tseq, trow, dseq, drow, code, b, k, v, need = _verify_plan(
+        (target.shape, target.dtype, target.stride()), (tokens.shape, tokens.dtype), (uniform.shape, uniform.dtype),
+        None if draft is None else (draft.shape, draft.dtype, draft.stride()))
     temperature = float(temperature)
     if not 0.0 < temperature < float("inf"):
         raise SlimError(f"temperature {temperature} must be positive and finite")
-    dev = target.device
-    if dev.type != "cuda" or (draft is not None and not draft.is_cuda):
-        raise SlimError("tensors must live in GPU memory")
-    if draft is not None and draft.device != dev:
-        raise SlimError(f"tensors live on different devices: {dev}, {draft.device}")
-    _ready(dev, tokens, uniform)
-    if dev.index != torch.cuda.current_device():
+    dev = target.get_device()
+    _where(dev, (target, draft), (tokens, uniform))
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return verify_draft(target, tokens, uniform, draft, temperature)
-    accepted = torch.empty((b,), dtype=torch.int32, device=dev)
-    ids = torch.empty((b, k1), dtype=torch.int64, device=dev)
-    need = _need("slim_verify_draft_workspace", b, k, v)
-    ws = _ws(need, dev) if need else None
-    st = lib.slim_verify_draft(target.data_ptr(), tseq, trow, None if draft is None else draft.data_ptr(), dseq, drow,
-                               _dtype_code(target), b, k, v, tokens.data_ptr(), uniform.data_ptr(), temperature,
-                               accepted.data_ptr(), ids.data_ptr(), ws.data_ptr() if need else None, need,
-                               _raw_stream(dev.index))
+    accepted = torch.empty(b, dtype=torch.int32, device=target.device)
+    ids = torch.empty((b, k + 1), dtype=torch.int64, device=target.device)
+    ws = torch.empty(need, dtype=torch.uint8, device=target.device) if need else None
+    st = load_library().slim_verify_draft(target.data_ptr(), tseq, trow, None if draft is None else draft.data_ptr(),
+                                          dseq, drow, code, b, k, v, tokens.data_ptr(), uniform.data_ptr(), temperature,
+                                          accepted.data_ptr(), ids.data_ptr(), ws.data_ptr() if need else None, need,
+                                          _raw_stream(dev))
     if st:
         check(st, "slim_verify_draft")
     return {"accepted": accepted, "ids": ids}
