@@ -10,9 +10,11 @@
 // throughout; the index is then a function of the inputs but for borders
 // nearer than 10^-15.
 //
-// Three launches: statistics of every row by segments (bound by reading the
-// logits and by the float64 powers), then the decision and the segment masses
-// of the row to draw from, then the segment and the entry.
+// Three launches: statistics of every row by segments, then the decision and
+// the segment masses of the row to draw from, then the segment and the entry.
+// The first one reads all logits once and forms a float64 power of each (15
+// float64 instructions, which run at the rate of float32's here): for bfloat16
+// logits the two take about as long.
 #include "common.hpp"
 #include "serve.hpp"
 #include "slim.h"
@@ -22,6 +24,42 @@ namespace slim {
 namespace {
 
 constexpr double kNegInf = -__builtin_inf();
+constexpr double kLog2e = 1.4426950408889634074;
+
+// 2^t for t up to 1023 (0 for -inf): t = n + f, |f| <= 1/2, and the polynomial
+// that meets 2^f at the 11 Chebyshev points of [-1/2, 1/2] (off by 3.2e-16 of the value at most).
+__device__ __forceinline__ double exp2_64(double t) {
+  t = fmax(t, -1100.0);
+  const double n = __builtin_rint(t), f = t - n;
+  double p = 0x1.e6063f7217bc6p-28;
+  p = __builtin_fma(p, f, 0x1.b675bca4eeebbp-24);
+  p = __builtin_fma(p, f, 0x1.62bfd47773353p-20);
+  p = __builtin_fma(p, f, 0x1.ffcb54062e698p-17);
+  p = __builtin_fma(p, f, 0x1.430913096fd9fp-13);
+  p = __builtin_fma(p, f, 0x1.5d87fe9d7a584p-10);
+  p = __builtin_fma(p, f, 0x1.3b2ab6fba1ddap-7);
+  p = __builtin_fma(p, f, 0x1.c6b08d703ce49p-5);
+  p = __builtin_fma(p, f, 0x1.ebfbdff82c598p-3);
+  p = __builtin_fma(p, f, 0x1.62e42fefa3a19p-1);
+  p = __builtin_fma(p, f, 1.0);
+  return __builtin_ldexp(p, (int)n);
+}
+
+// 2^(t / 64) with a table of 2^(i / 64): the rest |g| <= 1/2 of 1/64 needs the Taylor series to the fifth power
+// only (its rest is below 2^-54).  Half the work of exp2_64 where there is a logit after the other.
+__device__ __forceinline__ double exp2_64th(double t, const double (&table)[64]) {
+  constexpr double L = 0.69314718055994530942 / 64.0;
+  t = fmax(t, -70400.0);
+  const double n = __builtin_rint(t), g = t - n;
+  const int i = (int)n;
+  double p = L * L * L * L * L / 120.0;
+  p = __builtin_fma(p, g, L * L * L * L / 24.0);
+  p = __builtin_fma(p, g, L * L * L / 6.0);
+  p = __builtin_fma(p, g, L * L / 2.0);
+  p = __builtin_fma(p, g, L);
+  const double s = table[i & 63];
+  return __builtin_ldexp(__builtin_fma(p * g, s, s), i >> 6);
+}
 
 template <bool BF16>
 __device__ __forceinline__ float logit(const void *p, int64_t at) {
@@ -40,230 +78,296 @@ __device__ __forceinline__ RowOf row_of(const DraftArgs &a, int64_t seq, int j) 
   return {a.draft, seq * a.d_seq + (j - a.k - 1) * a.d_row};
 }
 
-// One segment's maximum and sum of powers, (max, sum); a NaN or +inf makes the sum NaN.
-template <bool BF16, int E>
+// One segment's maximum m and sum of 2^((x - m) log2 e / T), as (m, sum); a
+// NaN or +inf makes the sum NaN.  A thread takes 16-byte pieces (on the row's
+// own 16-byte grid: rows may start anywhere), the ragged ones at the row's
+// ends entry by entry.
+template <bool BF16, int PIECES>
 __global__ __launch_bounds__(256) void draft_stats_kernel(const DraftArgs a, const int nseg, double2 *__restrict__ st) {
+  constexpr int PER = BF16 ? 8 : 4, SIZE = BF16 ? 2 : 4;
   __shared__ float s_m[4];
-  __shared__ double s_z[4];
-  const int nr = a.draft ? 2 * a.k + 1 : a.k + 1;
-  const int64_t row = blockIdx.x / (unsigned)nseg;
-  const int s = (int)(blockIdx.x % (unsigned)nseg);
-  const int64_t seq = row / nr;
+  __shared__ double s_z[4], s_pow[64];
+  if (threadIdx.x < 64) s_pow[threadIdx.x] = exp2_64(threadIdx.x * (1.0 / 64.0));   // seen after the next barrier
+  const unsigned nr = a.draft ? 2 * a.k + 1 : a.k + 1;
+  const unsigned row = blockIdx.x / (unsigned)nseg, seq = row / nr;
+  const int s = (int)(blockIdx.x - row * nseg);
   const RowOf r = row_of(a, seq, (int)(row - seq * nr));
-  const int64_t v0 = (int64_t)s * (256 * E);
-  float x[E];
+  const char *first = (const char *)r.p + r.at * SIZE;
+  const int lead = (int)((uintptr_t)first & 15) / SIZE;    // entries of the grid before the row
+  float x[PIECES][PER];
+  const int64_t v0 = (int64_t)s * PIECES * 256 * PER - lead;
+  uint4 u[PIECES];
+  if (v0 >= 0 && v0 + PIECES * 256 * PER <= a.v) {         // all loads at once
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+      u[i] = *(const uint4 *)(first + (v0 + (i * 256 + (int)threadIdx.x) * PER) * SIZE);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const int64_t v = v0 + (i * 256 + (int)threadIdx.x) * PER;
+      if (v >= 0 && v + PER <= a.v) {
+        u[i] = *(const uint4 *)(first + v * SIZE);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          const uint32_t f = v + e >= 0 && v + e < a.v ? __float_as_uint(logit<BF16>(first, v + e)) : 0xff800000u;
+          if constexpr (!BF16) w[e] = f;
+          else if (e & 1) w[e >> 1] |= f;
+          else w[e >> 1] = f >> 16;
+        }
+        u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
   float m = -__builtin_inff();
   bool bad = false;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int64_t v = v0 + 256 * e + threadIdx.x;
-    x[e] = v < a.v ? logit<BF16>(r.p, r.at + v) : -__builtin_inff();
-    bad |= !(x[e] < __builtin_inff());
-    m = fmaxf(m, x[e]);
+  for (int i = 0; i < PIECES; ++i) {
+    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (BF16) {
+        x[i][2 * e] = __uint_as_float(w[e] << 16), x[i][2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      } else {
+        x[i][e] = __uint_as_float(w[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      bad |= !(x[i][e] < __builtin_inff());
+      m = fmaxf(m, x[i][e]);
+    }
   }
   m = group_max<64>(m);
   const int wave = threadIdx.x >> 6;
   if ((threadIdx.x & 63) == 0) s_m[wave] = m;
   __syncthreads();
   m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const double it = 1.0 / a.temperature, ref = m == -__builtin_inff() ? 0.0 : (double)m;
+  const double c = 64.0 * kLog2e / a.temperature, shift = m == -__builtin_inff() || bad ? 0.0 : -(double)m * c;
   double z = 0.0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) z += exp(((double)x[e] - ref) * it);
+  for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+    for (int e = 0; e < PER; ++e) z += exp2_64th(__builtin_fma((double)x[i][e], c, shift), s_pow);
   if (bad) z = __builtin_nan("");
   z = wave_sum(z);
   if ((threadIdx.x & 63) == 0) s_z[wave] = z;
   __syncthreads();
-  if (threadIdx.x == 0) st[(int64_t)blockIdx.x] = make_double2((double)m, (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]));
-}
-
-// A row's maximum and sum from its segments'; every lane of the wave has them.
-__device__ __forceinline__ double2 row_stat(const double2 *st, int nseg, double it) {
-  const int lane = threadIdx.x & 63;
-  double m = kNegInf;
-  for (int s = lane; s < nseg; s += 64) m = fmax(m, st[s].x);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = fmax(m, __shfl_xor(m, d, 64));
-  const double ref = m == kNegInf ? 0.0 : m;
-  double z = 0.0;
-  for (int s = lane; s < nseg; s += 64) z += st[s].y * exp((st[s].x - ref) * it);
-  return make_double2(ref, wave_sum(z));
+  if (threadIdx.x == 0) st[blockIdx.x] = make_double2((double)m, (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]));
 }
 
 // What is drawn from: p, or max(p - q, 0) with q of the draft's row or 1 at `token`.
 struct Mass {
-  RowOf t, d;
-  double tm, tz, dm, dz, it;
   int64_t token;             // of a draft without probabilities, else -1
-  bool minus;
-  template <bool BF16>
-  __device__ __forceinline__ double at(int64_t v) const {
-    const double p = exp(((double)logit<BF16>(t.p, t.at + v) - tm) * it) / tz;
-    if (!minus) return p;
-    if (v == token) return 0.0;
-    if (token >= 0) return p;
-    return fmax(p - exp(((double)logit<BF16>(d.p, d.at + v) - dm) * it) / dz, 0.0);
+  double c, tm, tz, dm, dz;  // log2 e / T; the rows' shifts and reciprocal sums
+  int taken, minus;
+  int64_t pad;
+};
+// Of entry v with logits x (target) and y (draft; any number if there is none).
+__device__ __forceinline__ double mass_of(const Mass &m, float x, float y, int64_t v) {
+  const double p = exp2_64(__builtin_fma((double)x, m.c, m.tm)) * m.tz;
+  if (!m.minus) return p;
+  if (m.token >= 0) return v == m.token ? 0.0 : p;
+  return fmax(p - exp2_64(__builtin_fma((double)y, m.c, m.dm)) * m.dz, 0.0);
+}
+// The masses of 8 entries first, first + STEP, ...; 0 from `end` on.  All loads before the first power.
+template <bool BF16, int STEP>
+__device__ __forceinline__ void masses(const DraftArgs &a, int64_t seq, const Mass &m, int64_t first, int64_t end,
+                                       double (&z)[8]) {
+  const RowOf t = row_of(a, seq, m.taken), d = m.minus && a.draft ? row_of(a, seq, a.k + 1 + m.taken) : t;
+  float x[8], y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int64_t v = first + STEP * e, in = v < end ? v : end - 1;
+    x[e] = logit<BF16>(t.p, t.at + in);
+    y[e] = logit<BF16>(d.p, d.at + in);
   }
-};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int64_t v = first + STEP * e;
+    z[e] = v < end ? mass_of(m, x[e], y[e], v) : 0.0;
+  }
+}
 
-// Decided by every workgroup of a sequence for itself (its rows' statistics are a few KB).
-struct Decision {
-  Mass mass;
-  int taken;
-};
+// Every workgroup of a sequence decides for itself: 16 lanes join the segments
+// of a row, then lane j of each wave judges token j.
 template <bool BF16>
-__device__ __forceinline__ Decision decide(const DraftArgs &a, int64_t seq, const double2 *st, int nseg,
-                                           double2 (&s_row)[2 * SLIM_DRAFT_MAX_K + 1]) {
-  const int nr = a.draft ? 2 * a.k + 1 : a.k + 1, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const double it = 1.0 / a.temperature;
-  for (int j = wave; j < nr; j += 4) {
-    const double2 r = row_stat(st + (seq * nr + j) * nseg, nseg, it);
-    if (lane == 0) s_row[j] = r;
+__device__ __forceinline__ Mass decide(const DraftArgs &a, int64_t seq, const double2 *st, int nseg,
+                                       double2 (&s_row)[2 * SLIM_DRAFT_MAX_K + 1]) {
+  const int nr = a.draft ? 2 * a.k + 1 : a.k + 1, lane = threadIdx.x & 63;
+  const double c = kLog2e / a.temperature;
+  const int64_t x = lane < a.k ? a.tokens[seq * a.k + lane] : -1;
+  const float u = lane < a.k ? a.uniform[seq * (a.k + 1) + lane] : 0.0f;
+  float tx = 0.0f, dx = 0.0f;                    // asked for here, needed after the rows
+  if (x >= 0 && x < a.v) {
+    const RowOf t = row_of(a, seq, lane);
+    tx = logit<BF16>(t.p, t.at + x);
+    if (a.draft) {
+      const RowOf d = row_of(a, seq, a.k + 1 + lane);
+      dx = logit<BF16>(d.p, d.at + x);
+    }
+  }
+  for (int j0 = 0; j0 < nr; j0 += 16) {
+    const int j = j0 + (threadIdx.x >> 4), l = threadIdx.x & 15;
+    if (j < nr) {
+      const double2 *p = st + (seq * nr + j) * nseg;
+      const double2 f = l < nseg ? p[l] : make_double2(kNegInf, 0.0);
+      double m = f.x;
+      for (int s = 16 + l; s < nseg; s += 16) m = fmax(m, p[s].x);
+#pragma unroll
+      for (int x = 1; x < 16; x <<= 1) m = fmax(m, __shfl_xor(m, x, 64));
+      const double shift = m == kNegInf ? 0.0 : -m * c;
+      double z = f.y * exp2_64(__builtin_fma(f.x, c, shift));
+      for (int s = 16 + l; s < nseg; s += 16) z += p[s].y * exp2_64(__builtin_fma(p[s].x, c, shift));
+      z = group_sum<16>(z);
+      if (l == 0) s_row[j] = make_double2(shift, 1.0 / z);   // nothing but -inf: 1 / 0, and 0 * inf is a NaN below
+    }
   }
   __syncthreads();
   bool good = false;
-  if (lane < a.k) {
-    const int64_t x = a.tokens[seq * a.k + lane];
-    if (x >= 0 && x < a.v) {
-      const RowOf t = row_of(a, seq, lane);
-      const double2 ts = s_row[lane];
-      const double p = exp(((double)logit<BF16>(t.p, t.at + x) - ts.x) * it) / ts.y;
-      double q = 1.0;
-      if (a.draft) {
-        const RowOf d = row_of(a, seq, a.k + 1 + lane);
-        const double2 ds = s_row[a.k + 1 + lane];
-        q = exp(((double)logit<BF16>(d.p, d.at + x) - ds.x) * it) / ds.y;
-      }
-      good = (double)a.uniform[seq * (a.k + 1) + lane] * q < p;
-    }
+  if (x >= 0 && x < a.v) {                       // lanes below k
+    const double p = exp2_64(__builtin_fma((double)tx, c, s_row[lane].x)) * s_row[lane].y;
+    double q = 1.0;
+    if (a.draft) q = exp2_64(__builtin_fma((double)dx, c, s_row[a.k + 1 + lane].x)) * s_row[a.k + 1 + lane].y;
+    good = (double)u * q < p;
   }
-  const uint64_t no = ~__ballot(good);
-  Decision c;
-  c.taken = no ? __ffsll((unsigned long long)no) - 1 : 64;
-  if (c.taken > a.k) c.taken = a.k;
-  const int j = c.taken;
-  const int64_t x = j < a.k ? a.tokens[seq * a.k + j] : -1;
-  Mass &m = c.mass;
-  m.minus = x >= 0;
-  m.token = m.minus && !a.draft ? x : -1;
-  m.t = row_of(a, seq, j);
-  m.tm = s_row[j].x, m.tz = s_row[j].y, m.it = it;
-  m.d = m.t, m.dm = m.dz = 0.0;
-  if (m.minus && a.draft) {
-    m.d = row_of(a, seq, a.k + 1 + j);
-    m.dm = s_row[a.k + 1 + j].x, m.dz = s_row[a.k + 1 + j].y;
+  const uint64_t no = ~__ballot(good);           // lanes from k on are in it
+  Mass m = {};
+  m.taken = __ffsll((unsigned long long)no) - 1;
+  const int j = m.taken;
+  const int64_t refused = __shfl(x, j, 64);      // lane k: -1
+  m.minus = refused >= 0;
+  m.token = m.minus && !a.draft ? refused : -1;
+  m.c = c, m.tm = s_row[j].x, m.tz = s_row[j].y;
+  if (m.minus && a.draft) m.dm = s_row[a.k + 1 + j].x, m.dz = s_row[a.k + 1 + j].y;
+  return m;
+}
+
+// The masses of runs of kRun entries, `each` of them a workgroup (several
+// where there are many: every workgroup decides first).
+constexpr int kRun = 2048;
+template <bool BF16>
+__global__ __launch_bounds__(256) void draft_mass_kernel(const DraftArgs a, const int nseg, const int runs,
+                                                         const int each, const double2 *__restrict__ st,
+                                                         double *__restrict__ mass, Mass *__restrict__ drawn) {
+  __shared__ double2 s_row[2 * SLIM_DRAFT_MAX_K + 1];
+  __shared__ double s_z[2][4];
+  const unsigned per = (unsigned)(runs + each - 1) / (unsigned)each, seq = blockIdx.x / per;
+  const int s0 = (int)(blockIdx.x - seq * per) * each, s1 = s0 + each < runs ? s0 + each : runs;
+  const Mass m = decide<BF16>(a, seq, st, nseg, s_row);
+  if (s0 == 0 && threadIdx.x == 0) drawn[seq] = m;
+  for (int s = s0; s < s1; ++s) {
+    double x[8];
+    masses<BF16, 256>(a, seq, m, (int64_t)s * kRun + threadIdx.x, a.v, x);
+    const double z = wave_sum(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
+    if ((threadIdx.x & 63) == 0) s_z[s & 1][threadIdx.x >> 6] = z;
+    __syncthreads();                             // one a run: the next run's sums go to the other half
+    if (threadIdx.x == 0)
+      mass[(int64_t)seq * runs + s] = (s_z[s & 1][0] + s_z[s & 1][1]) + (s_z[s & 1][2] + s_z[s & 1][3]);
   }
-  return c;
+}
+
+__device__ __forceinline__ double wave_running_sum(double x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double up = __shfl_up(x, d, 64);
+    if (lane >= d) x += up;
+  }
+  return x;
 }
 
 template <bool BF16>
-__global__ __launch_bounds__(256) void draft_mass_kernel(const DraftArgs a, const int nseg, const int64_t seg,
-                                                         const double2 *__restrict__ st, double *__restrict__ mass) {
-  __shared__ double2 s_row[2 * SLIM_DRAFT_MAX_K + 1];
+__global__ __launch_bounds__(256) void draft_pick_kernel(const DraftArgs a, const int runs,
+                                                         const double *__restrict__ mass,
+                                                         const Mass *__restrict__ drawn) {
   __shared__ double s_z[4];
-  const int64_t seq = blockIdx.x / (unsigned)nseg;
-  const int s = (int)(blockIdx.x % (unsigned)nseg);
-  const Decision c = decide<BF16>(a, seq, st, nseg, s_row);
-  const int64_t v0 = s * seg, v1 = v0 + seg < a.v ? v0 + seg : a.v;
-  double z = 0.0;
-  for (int64_t v = v0 + threadIdx.x; v < v1; v += 256) z += c.mass.template at<BF16>(v);
-  z = wave_sum(z);
-  if ((threadIdx.x & 63) == 0) s_z[threadIdx.x >> 6] = z;
-  __syncthreads();
-  if (threadIdx.x == 0) mass[blockIdx.x] = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
-}
-
-template <bool BF16>
-__global__ __launch_bounds__(256) void draft_pick_kernel(const DraftArgs a, const int nseg, const int64_t seg,
-                                                         const double2 *__restrict__ st,
-                                                         const double *__restrict__ mass) {
-  __shared__ double2 s_row[2 * SLIM_DRAFT_MAX_K + 1];
-  __shared__ double s_z[4];
-  __shared__ double s_left;
-  __shared__ int s_seg;
-  __shared__ unsigned long long s_hit, s_last;
+  __shared__ int s_hit[4], s_last[4];
   const int64_t seq = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  Decision c = decide<BF16>(a, seq, st, nseg, s_row);
-  const double *ms = mass + seq * nseg;
-  if (tid == 0) {
-    double all = 0.0;
-    for (int s = 0; s < nseg; ++s) all += ms[s];
-    const double want = (double)a.uniform[seq * (a.k + 1) + a.k] * all;
-    double run = 0.0;
-    int hit = -1, last = -1;
-    double at = 0.0, lastat = 0.0;
-    for (int s = 0; s < nseg; ++s) {
-      if (ms[s] > 0.0) last = s, lastat = run;
-      if (hit < 0 && run + ms[s] > want) hit = s, at = run;
-      run += ms[s];
+  const Mass m = drawn[seq];
+  const double *ms = mass + seq * runs;
+  // every wave finds the run: the first whose running mass exceeds what is wanted (with a uniform of 1 or
+  // more: the last that has any)
+  const double first = lane < runs ? ms[lane] : 0.0;
+  double all = first;
+  for (int s = 64 + lane; s < runs; s += 64) all += ms[s];
+  all = wave_sum(all);
+  const double want = (double)a.uniform[seq * (a.k + 1) + a.k] * all;
+  int hs = -1, last = -1;
+  double left = 0.0, run = 0.0, lastleft = 0.0;
+  if (all > 0.0) {                               // a NaN: a row without a distribution
+    for (int s0 = 0; s0 < runs && hs < 0; s0 += 64) {
+      const double x = s0 == 0 ? first : s0 + lane < runs ? ms[s0 + lane] : 0.0, incl = wave_running_sum(x);
+      const uint64_t over = __ballot(x > 0.0 && run + incl > want), some = __ballot(x > 0.0);
+      const int at = over ? __ffsll((unsigned long long)over) - 1 : some ? 63 - __clzll((long long)some) : -1;
+      if (at >= 0) {
+        const double before = want - (run + __shfl(incl - x, at, 64));
+        if (over) hs = s0 + at, left = before;
+        else last = s0 + at, lastleft = before;
+      }
+      run += __shfl(incl, 63, 64);
     }
-    if (hit < 0) hit = last, at = lastat;
-    s_seg = all > 0.0 ? hit : -1;       // NaN: a row without a distribution
-    s_left = want - at;
-    s_hit = s_last = ~0ull;
+    if (hs < 0) hs = last, left = lastleft;
   }
-  __syncthreads();
   int64_t pick = -1;
-  const int hs = s_seg;
-  if (hs >= 0) {
-    const int64_t v0 = hs * seg, v1 = v0 + seg < a.v ? v0 + seg : a.v;
-    const double left = s_left;
-    double before = 0.0;
-    for (int64_t b = v0; b < v1; b += 2048) {
-      double x[8], sum = 0.0;
-      int lastpos = -1;
+  if (hs >= 0) {                                 // the same in every wave
+    double x[8], sum = 0.0;
+    masses<BF16, 1>(a, seq, m, (int64_t)hs * kRun + 8 * tid, a.v, x);
+    int lastpos = -1;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t v = b + 8 * tid + e;
-        x[e] = v < v1 ? c.mass.template at<BF16>(v) : 0.0;
-        if (x[e] > 0.0) lastpos = e;
-        sum += x[e];
-      }
-      double incl = sum;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const double up = __shfl_up(incl, d, 64);
-        if (lane >= d) incl += up;
-      }
-      if (lane == 63) s_z[wave] = incl;
-      __syncthreads();
-      double run = before + (incl - sum);
-      for (int w = 0; w < wave; ++w) run += s_z[w];
-      int hit = -1;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        run += x[e];
-        if (hit < 0 && x[e] > 0.0 && run > left) hit = e;
-      }
-      if (hit >= 0) atomicMin(&s_hit, (unsigned long long)(b + 8 * tid + hit));
-      if (lastpos >= 0) atomicMin(&s_last, ~0ull - 1 - (unsigned long long)(b + 8 * tid + lastpos));
-      before += (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
-      __syncthreads();
-      if (s_hit != ~0ull) break;
+    for (int e = 0; e < 8; ++e) {
+      if (x[e] > 0.0) lastpos = 8 * tid + e;
+      sum += x[e];
     }
-    // rounding can leave the segment's running sum just short of its mass: its last entry then
-    pick = s_hit != ~0ull ? (int64_t)s_hit : s_last != ~0ull ? (int64_t)(~0ull - 1 - s_last) : -1;
+    const double incl = wave_running_sum(sum);
+    if (lane == 63) s_z[wave] = incl;
+    __syncthreads();
+    double at = incl - sum;
+    for (int w = 0; w < wave; ++w) at += s_z[w];
+    int hit = kRun;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      at += x[e];
+      if (hit == kRun && x[e] > 0.0 && at > left) hit = 8 * tid + e;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      hit = min(hit, __shfl_xor(hit, d, 64));
+      lastpos = max(lastpos, __shfl_xor(lastpos, d, 64));
+    }
+    if (lane == 0) s_hit[wave] = hit, s_last[wave] = lastpos;
+    __syncthreads();
+    hit = min(min(s_hit[0], s_hit[1]), min(s_hit[2], s_hit[3]));
+    lastpos = max(max(s_last[0], s_last[1]), max(s_last[2], s_last[3]));
+    // rounding can leave the run's running sum just short of its mass: its last entry then
+    const int in = hit < kRun ? hit : lastpos;
+    if (in >= 0) pick = (int64_t)hs * kRun + in;
   }
   if (tid <= a.k)
-    a.ids[seq * (a.k + 1) + tid] = tid < c.taken ? a.tokens[seq * a.k + tid] : tid == c.taken ? pick : -1;
-  if (tid == 0) a.accepted[seq] = c.taken;
+    a.ids[seq * (a.k + 1) + tid] = tid < m.taken ? a.tokens[seq * a.k + tid] : tid == m.taken ? pick : -1;
+  if (tid == 0) a.accepted[seq] = m.taken;
 }
 
+// Logits a thread of the first kernel holds: 8 (few rows: more workgroups) or 32.
 template <bool BF16>
 hipError_t launch(const DraftArgs &a, void *ws, const DraftPlan &p, hipStream_t st) {
   const int nr = a.draft ? 2 * a.k + 1 : a.k + 1;
-  double2 *stat = (double2 *)ws;
+  Mass *drawn = (Mass *)ws;
+  double2 *stat = (double2 *)(drawn + a.b);
   double *mass = (double *)(stat + a.b * nr * p.nseg);
   const unsigned rows = (unsigned)(a.b * nr * p.nseg);
-  if (p.seg == 2048) draft_stats_kernel<BF16, 8><<<rows, 256, 0, st>>>(a, p.nseg, stat);
-  else draft_stats_kernel<BF16, 32><<<rows, 256, 0, st>>>(a, p.nseg, stat);
+  constexpr int PIECE = BF16 ? 8 : 4;
+  if (p.few) draft_stats_kernel<BF16, 8 / PIECE><<<rows, 256, 0, st>>>(a, p.nseg, stat);
+  else draft_stats_kernel<BF16, 32 / PIECE><<<rows, 256, 0, st>>>(a, p.nseg, stat);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  draft_mass_kernel<BF16><<<(unsigned)(a.b * p.nseg), 256, 0, st>>>(a, p.nseg, p.seg, stat, mass);
+  const unsigned groups = (unsigned)(a.b * ((p.runs + p.each - 1) / p.each));
+  draft_mass_kernel<BF16><<<groups, 256, 0, st>>>(a, p.nseg, p.runs, p.each, stat, mass, drawn);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  draft_pick_kernel<BF16><<<(unsigned)a.b, 256, 0, st>>>(a, p.nseg, p.seg, stat, mass);
+  draft_pick_kernel<BF16><<<(unsigned)a.b, 256, 0, st>>>(a, p.runs, mass, drawn);
   return hipGetLastError();
 }
 
@@ -271,10 +375,14 @@ hipError_t launch(const DraftArgs &a, void *ws, const DraftPlan &p, hipStream_t 
 
 DraftPlan draft_plan(int64_t b, int k, int64_t v) {
   DraftPlan p;
-  const int64_t rows = b * (2 * k + 1);
-  p.seg = rows * ((v + 2047) / 2048) <= 1024 ? 2048 : 8192;   // few rows: more workgroups
-  p.nseg = (int)((v + p.seg - 1) / p.seg);
-  p.ws_bytes = (size_t)rows * p.nseg * 16 + (size_t)b * p.nseg * 8;
+  const int64_t rows = b * (2 * k + 1), wide = v + 7;         // a row's 16-byte grid may start 7 entries before it
+  p.few = rows * ((wide + 2047) / 2048) <= 1024;
+  const int64_t seg = p.few ? 2048 : 8192;
+  p.nseg = (int)((wide + seg - 1) / seg);
+  p.runs = (int)((v + kRun - 1) / kRun);
+  const int64_t each = b * p.runs / 768;                       // three workgroups a CU
+  p.each = (int)(each < 1 ? 1 : each > 8 ? 8 : each);
+  p.ws_bytes = (size_t)b * sizeof(Mass) + (size_t)rows * p.nseg * 16 + (size_t)b * p.runs * 8;
   return p;
 }
 

@@ -97,8 +97,9 @@ struct DraftArgs {
   bool bf16;
 };
 struct DraftPlan {
+  bool few;                  // segments of 2048 entries, not 8192
   int nseg;                  // segments a row is cut into
-  int64_t seg;               // entries of a segment
+  int runs, each;            // runs its masses are summed over; of those, a workgroup's
   size_t ws_bytes;
 };
 DraftPlan draft_plan(int64_t b, int k, int64_t v);
