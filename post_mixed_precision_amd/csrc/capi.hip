@@ -497,7 +497,8 @@ int slim_kv4_append(const void *k, int64_t k_row, int64_t k_head, const void *v,
   a.v = kv4_rows(v, heads, v_row, v_head, bf16);
   a.q_out = q_out, a.slots = slots, a.positions = positions, a.rotary = rotary, a.cache = cache;
   a.t = t, a.pages = pages, a.npos = npos, a.dim = dim, a.group = group, a.page = page, a.rot = rotary ? rot : 0;
-  a.bf16 = bf16, a.interleaved = interleaved != 0;
+  a.bf16 = bf16, a.interleaved = interleaved != 0, a.page_log = __builtin_ctz(page);
+  a.rvec = aligned16(rotary) && rot % 4 == 0;
   hipError_t err = slim::launch_kv4_append(a, (hipStream_t)stream);
   return err == hipSuccess ? SLIM_OK : hip_fail(err);
 }

@@ -19,6 +19,8 @@
 // float32 numbers are exact there, so a pair costs one rounding) and rounded
 // to float32 once: every code is a function of the inputs alone, whatever
 // kernel or order computed it.
+#include <type_traits>
+
 #include "common.hpp"
 #include "serve.hpp"
 
@@ -68,27 +70,38 @@ __device__ __forceinline__ void rotate8(const Kv4Append &a, const Kv4Rows &s, in
                                         float (&x)[8]) {
   const int half = a.rot >> 1;
   if (c0 >= a.rot) return;
+  // products of float32 numbers are exact in float64, so a fused sum rounds as a separate one would
   if (a.interleaved) {
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
       const int i = (c0 + e) >> 1;
       if (c0 + e < a.rot) {
         const double c = row[i], n = row[half + i], u = x[e], w = x[e + 1];
-        x[e] = (float)(u * c - w * n);
-        x[e + 1] = (float)(w * c + u * n);
+        x[e] = (float)__builtin_fma(u, c, -(w * n));
+        x[e + 1] = (float)__builtin_fma(w, c, u * n);
       }
     }
     return;
   }
   float y[8];
-  if ((half & 7) == 0) {                    // the partners are 8 consecutive channels too
-    load8<BF16>(s.p, at + (c0 < half ? c0 + half : c0 - half), s.vec, y);
-  } else {
+  if ((half & 7) == 0) {                    // the partners, and the angles, are 8 consecutive ones too
+    const bool low = c0 < half;
+    const int i = low ? c0 : c0 - half;
+    float co[8], si[8];
+    load8<BF16>(s.p, at + (low ? c0 + half : c0 - half), s.vec, y);
+    load8<false>(row, i, a.rvec, co);
+    load8<false>(row, half + i, a.rvec, si);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = c0 + e;
-      y[e] = c < a.rot ? load1<BF16>(s.p, at + (c < half ? c + half : c - half)) : 0.0f;
+      const double w = low ? -y[e] : y[e];
+      x[e] = (float)__builtin_fma((double)x[e], (double)co[e], w * (double)si[e]);
     }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = c0 + e;
+    y[e] = c < a.rot ? load1<BF16>(s.p, at + (c < half ? c + half : c - half)) : 0.0f;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -96,9 +109,29 @@ __device__ __forceinline__ void rotate8(const Kv4Append &a, const Kv4Rows &s, in
     if (c < a.rot) {
       const int i = c < half ? c : c - half;
       const double co = row[i], si = row[half + i], u = x[e], w = y[e];
-      x[e] = c < half ? (float)(u * co - w * si) : (float)(u * co + w * si);
+      x[e] = (float)__builtin_fma(u, co, c < half ? -(w * si) : w * si);
     }
   }
+}
+
+// Least and greatest over aligned groups of W = 4, 8 or 16 lanes by data-parallel moves.
+template <int W, class Op>
+__device__ __forceinline__ float over_lanes(float x, Op op) {
+  auto from = [&](auto ctrl) __attribute__((always_inline)) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  x = op(x, from(std::integral_constant<int, 0xb1>()));                 // lane ^ 1
+  x = op(x, from(std::integral_constant<int, 0x4e>()));                 // lane ^ 2
+  if (W >= 8) x = op(x, from(std::integral_constant<int, 0x141>()));    // lane ^ 7 of 8
+  if (W >= 16) x = op(x, from(std::integral_constant<int, 0x140>()));   // lane ^ 15 of 16
+  return x;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef __attribute__((__vector_size__(2 * sizeof(float)))) float f32x2;
+  typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
 struct Pair {
@@ -118,8 +151,8 @@ __device__ __forceinline__ Pair group_pair(const float (&x)[8]) {
     fin &= fabsf(x[e]) < __uint_as_float(0x7f800000u);
   }
   if (!fin) hi = __uint_as_float(0x7f800000u);             // carries through the maximum
-  lo = group_min<W>(lo);
-  hi = group_max<W>(hi);
+  lo = over_lanes<W>(lo, [](float a, float b) { return fminf(a, b); });
+  hi = over_lanes<W>(hi, [](float a, float b) { return fmaxf(a, b); });
   uint32_t u = __float_as_uint(lo);
   u = (u >> 31 ? u + 0xffffu : u) & 0xffff0000u;
   Pair p;
@@ -145,14 +178,14 @@ __device__ __forceinline__ Pair group_pair(const float (&x)[8]) {
 template <bool BF16, int DIM, int GROUP>
 __global__ __launch_bounds__(256) void kv4_append_kernel(const Kv4Append a) {
   constexpr int L = DIM / 8, W = GROUP / 8, NG = DIM / GROUP, REC = 4 * DIM + 32 * NG;
-  const int64_t item = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const unsigned item = blockIdx.x * (256 / L) + threadIdx.x / L;      // below 2^20 tokens of 3 x 1024 heads, and a block
   const int l = threadIdx.x % L;
-  const int64_t per = a.q.heads + 2 * a.k.heads;
-  const int64_t tok = item / per;
+  const unsigned per = (unsigned)(a.q.heads + 2 * a.k.heads);
+  const unsigned tok = item / per;
   if (tok >= a.t) return;
-  int64_t h = item - tok * per;
+  int h = (int)(item - tok * per);
   const int kind = h < a.q.heads ? 0 : h < a.q.heads + a.k.heads ? 1 : 2;
-  h -= kind == 0 ? 0 : kind == 1 ? a.q.heads : a.q.heads + a.k.heads;
+  h -= (int)(kind == 0 ? 0 : kind == 1 ? a.q.heads : a.q.heads + a.k.heads);
   const Kv4Rows &s = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
   int64_t slot = 0;
   if (kind > 0) {
@@ -177,7 +210,7 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(const Kv4Append a) {
     if (BF16) {
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16_bits(x[2 * i]) | f32_to_bf16_bits(x[2 * i + 1]) << 16;
+      for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
       *(uint4 *)((uint16_t *)a.q_out + o) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       ((float4 *)((float *)a.q_out + o))[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -191,10 +224,8 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(const Kv4Append a) {
 #pragma unroll
   for (int e = 0; e < 8; ++e)   // a NaN step gives NaN here, which the clamp makes 0
     code[e] = (uint32_t)fminf(fmaxf(rintf((x[e] - p.low) * inv), 0.0f), 15.0f);
-  const int pg = a.page >> 4;
-  const int64_t page = slot / a.page;
-  const int in = (int)(slot - page * a.page), t16 = in & 15;
-  uint32_t *rec = a.cache + ((page * a.k.heads + h) * pg + (in >> 4)) * REC;
+  const int log = a.page_log, in = (int)slot & (a.page - 1), t16 = in & 15;
+  uint32_t *rec = a.cache + ((((slot >> log) * a.k.heads + h) << (log - 4)) + (in >> 4)) * REC;
   if (kind == 1) {
     uint32_t w = 0;
 #pragma unroll
@@ -213,25 +244,24 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(const Kv4Append a) {
 template <int DIM, int GROUP>
 __global__ __launch_bounds__(256) void kv4_read_kernel(const int32_t *__restrict__ slots, int64_t t,
                                                        const uint32_t *__restrict__ cache, int64_t pages,
-                                                       int64_t heads, int page, void *__restrict__ k,
+                                                       int heads, int page_log, void *__restrict__ k,
                                                        void *__restrict__ v, bool bf16) {
   constexpr int L = DIM / 8, W = GROUP / 8, NG = DIM / GROUP, REC = 4 * DIM + 32 * NG;
-  const int64_t item = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const unsigned item = blockIdx.x * (256 / L) + threadIdx.x / L;
   const int l = threadIdx.x % L;
-  const int64_t tok = item / (2 * heads);
+  const unsigned tok = item / (unsigned)(2 * heads);
   if (tok >= t) return;
-  const int64_t hh = item - tok * 2 * heads;
+  const int hh = (int)(item - tok * 2 * heads);
   const bool val = hh >= heads;
-  const int64_t h = val ? hh - heads : hh;
+  const int h = val ? hh - heads : hh;
   const int64_t slot = slots[tok];
   float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (slot >= pages * page) {
+  if (slot >= pages << page_log) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(0x7fc00000u);
   } else if (slot >= 0) {
-    const int64_t pg = slot / page;
-    const int in = (int)(slot - pg * page), t16 = in & 15;
-    const uint32_t *rec = cache + ((pg * heads + h) * (page >> 4) + (in >> 4)) * REC;
+    const int in = (int)slot & ((1 << page_log) - 1), t16 = in & 15;
+    const uint32_t *rec = cache + ((((slot >> page_log) * heads + h) << (page_log - 4)) + (in >> 4)) * REC;
     const uint32_t pair = rec[4 * DIM + (val ? 16 * NG : 0) + 16 * (l / W) + t16];
     const float step = __uint_as_float(pair << 16), low = __uint_as_float(pair & 0xffff0000u);
     uint32_t code[8];
@@ -250,12 +280,12 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(const int32_t *__restrict
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = (float)code[e] * step + low;
   }
-  const int64_t o = (tok * heads + h) * DIM + 8 * l;
+  const int64_t o = ((int64_t)tok * heads + h) * DIM + 8 * l;
   void *out = val ? v : k;
   if (bf16) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16_bits(x[2 * i]) | f32_to_bf16_bits(x[2 * i + 1]) << 16;
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
     *(uint4 *)((uint16_t *)out + o) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
     ((float4 *)((float *)out + o))[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -299,7 +329,7 @@ hipError_t launch_kv4_read(const int32_t *slots, int64_t t, const uint32_t *cach
                            int dim, int group, int page, void *k, void *v, bool bf16, hipStream_t st) {
   const int64_t items = t * 2 * heads, per = 256 / (dim / 8);
   const unsigned grid = (unsigned)((items + per - 1) / per);
-#define F(D, G) kv4_read_kernel<D, G><<<grid, 256, 0, st>>>(slots, t, cache, pages, heads, page, k, v, bf16)
+#define F(D, G) kv4_read_kernel<D, G><<<grid, 256, 0, st>>>(slots, t, cache, pages, (int)heads, __builtin_ctz(page), k, v, bf16)
   KV4_BY_SHAPE(dim, group, F);
 #undef F
   return hipGetLastError();

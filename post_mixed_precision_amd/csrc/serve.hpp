@@ -55,8 +55,9 @@ struct Kv4Append {
   const float *rotary;       // [npos, rot] or null: cosines, then sines
   uint32_t *cache;
   int64_t t, pages, npos;
-  int dim, group, page, rot;
+  int dim, group, page, page_log, rot;
   bool bf16, interleaved;
+  bool rvec;                 // the table's rows start at 16-byte boundaries
 };
 hipError_t launch_kv4_append(const Kv4Append &a, hipStream_t st);
 hipError_t launch_kv4_read(const int32_t *slots, int64_t t, const uint32_t *cache, int64_t pages, int64_t heads,
