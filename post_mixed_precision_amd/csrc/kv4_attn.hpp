@@ -788,16 +788,15 @@ struct LdsTile {
 };
 template <int DIM, int GROUP>
 struct LdsPart {             // 32 tokens of it
+  static constexpr int W = DIM / 32;
   const LdsTile<DIM, GROUP> &t;
   int p;
   __device__ __forceinline__ void keys() {}
   __device__ __forceinline__ void values() {}
-  __device__ __forceinline__ uint4 kcode(int b, int w) const {
-    return t.k[(2 * p + b) * (DIM / 32) + w][threadIdx.x & 63];
-  }
+  __device__ __forceinline__ uint4 kcode(int b, int w) const { return t.k[(2 * p + b) * W + w][threadIdx.x & 63]; }
   __device__ __forceinline__ void vcode(int w, uint4 &even, uint4 &odd) const {
-    even = t.v[p * (DIM / 16) + 2 * w][threadIdx.x & 63];
-    odd = t.v[p * (DIM / 16) + 2 * w + 1][threadIdx.x & 63];
+    even = t.v[p * 2 * W + 2 * w][threadIdx.x & 63];
+    odd = t.v[p * 2 * W + 2 * w + 1][threadIdx.x & 63];
   }
   __device__ __forceinline__ void take(const float (&from)[LdsTile<DIM, GROUP>::TOK], int b, float (&x)[4]) const {
     const float4 u = *(const float4 *)&from[32 * p + 16 * b + 4 * ((threadIdx.x & 63) >> 4)];

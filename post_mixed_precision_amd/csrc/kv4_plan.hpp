@@ -51,12 +51,16 @@ inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t
   p.tm = 16 * p.nq * (p.tile ? 4 : 1);
   p.tiles = (int)((per + p.tm - 1) / p.tm);
   p.slots = (int)(uniform ? b * p.tiles : tq * g / p.tm + (b < tq ? b : tq));
-  p.least = 8;
-  // as many workgroups as the card holds at once (by registers and LDS): one round, all runs alike
-  const int64_t want = 256 * (p.tile ? 3 : dim == 64 ? 4 : wide && p.nq == 1 ? 3 : 2);
-  const int64_t units = p.slots * hkv, tokens = (cap + 31) / 32;
-  int64_t extra = units >= want ? 0 : (want - units + hkv - 1) / hkv;
-  const int64_t useful = p.slots * ((tokens + p.least - 1) / p.least - 1);   // no run below `least`
+  // Runs enough to fill the card once, by what registers and LDS let a CU hold (16 sequences of up to 8192, g =
+  // 128: 768 runs 35 us, 512 38, 1024 38; 131072 tokens, g = 64: 512 47, 768 50).  Many rows: 512 (2048 tokens of 32
+  // heads: 95 us, 768 102), but where queries are uneven the longest tiles decide (1024 and 657 queries over 4096 and
+  // 657 tokens: 768 147 us, 512 177).  However many tiles there are, one sequence may be far longer than the
+  // others: 256 runs more, unless the table says that none can be.
+  p.least = p.tile ? 32 : 8;
+  const int64_t want = p.tile ? (uniform ? 512 : 768) : wide && p.nq == 1 && (dim == 64 || group == 128) ? 768 : 512;
+  const int64_t units = p.slots * hkv, tokens = (cap + 31) / 32, spare = cap > 2048 ? 256 : 0;
+  const int64_t extra = ((want - units > spare ? want - units : spare) + hkv - 1) / hkv;
+  const int64_t useful = p.slots * ((tokens + p.least - 1) / p.least - 1);   // runs are no shorter than `least`
   p.extra = (int)(extra < useful ? extra : useful);
   const int64_t most = (tokens + p.least - 1) / p.least;
   p.most = (int)(most < p.extra / p.slots + 1 ? most : p.extra / p.slots + 1);
