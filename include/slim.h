@@ -581,10 +581,11 @@ int slim_kv4_read(const int32_t *slots, int64_t t, const uint32_t *cache, int64_
  * weights enter as three bfloat16 terms otherwise (what lies below 2^-133 is
  * dropped).  The result is rounded once.  For given sizes the order of the
  * sums is fixed.  out must not overlap an input.  1 <= b <= tq unless tq = 0
- * (a no-op), tq <= SLIM_KV4_MAX_T, hq <= SLIM_KV4_MAX_HEADS, scale finite.
+ * (a no-op), b <= SLIM_KV4_MAX_SEQS, tq <= SLIM_KV4_MAX_T, hq <=
+ * SLIM_KV4_MAX_HEADS, tq hq below 2^27, scale finite.
  * Workspace: slim_kv4_attention_workspace(...) bytes, which may be 0.
  * ---------------------------------------------------------------------- */
-#define SLIM_KV4_MAX_SEQS 65536
+#define SLIM_KV4_MAX_SEQS 4096
 size_t slim_kv4_attention_workspace(int64_t b, int64_t tq, int uneven, int64_t hq, int64_t heads, int dim, int group,
                                     int64_t per, int page, int qdt);
 int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uint32_t *cache, int64_t pages, int page,
@@ -611,7 +612,7 @@ int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uin
  * -inf) accepts nothing; if there is nothing to draw from (such a row, or p_j
  * nowhere above q_j) the drawn id is -1.
  * 0 <= b <= SLIM_DRAFT_MAX_B (0 is a no-op), 1 <= k <= SLIM_DRAFT_MAX_K,
- * 1 <= v <= SLIM_LOGPROB_MAX_V, b (2 k + 1) v <= 2^40, temperature > 0.  Workspace:
+ * 1 <= v <= SLIM_LOGPROB_MAX_V, b (2 k + 1) v <= 2^36, temperature > 0.  Workspace:
  * slim_verify_draft_workspace(b, k, v) bytes.
  * ---------------------------------------------------------------------- */
 #define SLIM_DRAFT_MAX_B 65536

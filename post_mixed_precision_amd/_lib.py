@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(HERE, "libslim.so")
 
 SLIM_F32, SLIM_BF16 = 0, 1
 LOGPROB_MAX_TOP = 64    # SLIM_LOGPROB_MAX_TOP
-KV4_MAX_SLOTS, KV4_MAX_HEADS, KV4_MAX_T, KV4_MAX_SEQS = 1 << 30, 1024, 1 << 20, 65536    # SLIM_KV4_MAX_*
+KV4_MAX_SLOTS, KV4_MAX_HEADS, KV4_MAX_T, KV4_MAX_SEQS = 1 << 30, 1024, 1 << 20, 4096    # SLIM_KV4_MAX_*
 DRAFT_MAX_B, DRAFT_MAX_K = 65536, 32    # SLIM_DRAFT_MAX_*
 LOGPROB_MAX_V = 1 << 24    # SLIM_LOGPROB_MAX_V
 STATUS = {0: "SLIM_OK", -1: "SLIM_E_NULL", -2: "SLIM_E_SHAPE", -3: "SLIM_E_DTYPE",
@@ -743,10 +743,13 @@ def kv4_cache(pages: int, heads: int, dim: int, group: int, page: int = 64, devi
     return torch.zeros((pages, heads, words), dtype=torch.int32, device=device)
 
 
-def _tensors(**ts):
-    """Every given argument that is not None is a tensor."""
+def _tensors(optional=None, **ts):
+    """Every given argument is a tensor; those of `optional` may be None."""
     tensor = _torch().Tensor
     for name, t in ts.items():
+        if not isinstance(t, tensor):
+            raise SlimError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    for name, t in (optional or {}).items():
         if t is not None and not isinstance(t, tensor):
             raise SlimError(f"{name}: expected a torch tensor, got {type(t).__name__}")
 
@@ -844,7 +847,7 @@ def kv4_append(k, v, slots, cache, group: int, rotary=None, positions=None, inte
     of rot apart, or adjacent if interleaved, and so are q's [t, query heads, dim], which are returned
     (in q's dtype).  Writes the slots given and nothing else."""
     torch = _torch()
-    _tensors(k=k, v=v, slots=slots, cache=cache, rotary=rotary, positions=positions, q=q)
+    _tensors({"rotary": rotary, "positions": positions, "q": q}, k=k, v=v, slots=slots, cache=cache)
     page, krow, khead, vrow, vhead, qrow, qhead, code, t, heads, dim, npos, rot, hq, reach, size = _append_plan(
         (k.shape, k.dtype, k.stride()), (v.shape, v.dtype, v.stride()), None if q is None else (q.shape, q.dtype, q.stride()),
         (slots.shape, slots.dtype), (cache.shape, cache.dtype), None if rotary is None else (rotary.shape, rotary.dtype),
@@ -932,7 +935,7 @@ def _attention_plan(q, cache, table, lengths, offsets, group, out_dtype, out):
         tq = q[0][0]
     if heads < 1 or hq < 1 or hq % heads or hq > KV4_MAX_HEADS:
         raise SlimError(f"q: {hq} heads, expected a multiple of the cache's {heads}, at most {KV4_MAX_HEADS}")
-    if b < 1 or b > KV4_MAX_SEQS or tq > KV4_MAX_T or per < 1 or per > KV4_MAX_SLOTS // page:
+    if b < 1 or b > KV4_MAX_SEQS or tq > KV4_MAX_T or tq * hq >= 1 << 27 or per < 1 or per > KV4_MAX_SLOTS // page:
         raise SlimError(f"table: shape {tuple(table[0])} with {tq} query tokens is out of range")
     out_dtype = q[1] if out_dtype is None else out_dtype
     if out is not None:
@@ -954,7 +957,7 @@ def kv4_attention(q, cache, table, lengths, group: int, offsets=None, scale=None
     out_dtype (q's by default).  Rows that attend to nothing are 0; rows outside the offsets are
     not written (a given out, apart from the inputs, keeps them)."""
     torch = _torch()
-    _tensors(q=q, cache=cache, table=table, lengths=lengths, offsets=offsets, out=out)
+    _tensors({"offsets": offsets, "out": out}, q=q, cache=cache, table=table, lengths=lengths)
     qcode, tq, hq, pages, page, heads, dim, b, per, ocode, otype, need = _attention_plan(
         (q.shape, q.dtype), (cache.shape, cache.dtype), (table.shape, table.dtype), (lengths.shape, lengths.dtype),
         None if offsets is None else (offsets.shape, offsets.dtype), group, out_dtype,
@@ -1006,7 +1009,7 @@ def _verify_plan(target, tokens, uniform, draft):
     k = k1 - 1
     if not 1 <= k <= DRAFT_MAX_K:
         raise SlimError(f"target: {k1} rows a sequence, expected 2 .. {DRAFT_MAX_K + 1}")
-    if not (1 <= v <= LOGPROB_MAX_V and b <= DRAFT_MAX_B):
+    if not (1 <= v <= LOGPROB_MAX_V and b <= DRAFT_MAX_B and b * (2 * k + 1) * v <= 1 << 36):
         raise SlimError(f"target: shape {tuple(target[0])} is out of range")
     tseq, trow = _draft_rows(target[0], target[2], "target")
     _want("tokens", *tokens, (b, k), (torch.int64,))
@@ -1027,7 +1030,7 @@ def verify_draft(target, tokens, uniform, draft=None, temperature: float = 1.0):
     max(p_j - q_j, 0) or, after the last, from p -> dict(accepted int32 [b], ids int64 [b, k + 1]: the
     accepted tokens, the drawn one, then -1).  In float64 throughout."""
     torch = _torch()
-    _tensors(target=target, tokens=tokens, uniform=uniform, draft=draft)
+    _tensors({"draft": draft}, target=target, tokens=tokens, uniform=uniform)
     tseq, trow, dseq, drow, code, b, k, v, need = _verify_plan(
         (target.shape, target.dtype, target.stride()), (tokens.shape, tokens.dtype), (uniform.shape, uniform.dtype),
         None if draft is None else (draft.shape, draft.dtype, draft.stride()))

@@ -518,8 +518,9 @@ int slim_kv4_read(const int32_t *slots, int64_t t, const uint32_t *cache, int64_
 static bool kv4_attention_shape(int64_t b, int64_t tq, bool uneven, int64_t hq, int64_t heads, int dim, int64_t per,
                                 int page) {
   return slim::kv4_shape(page, dim, 32) && heads >= 1 && hq >= heads && hq <= SLIM_KV4_MAX_HEADS && hq % heads == 0 &&
-         b >= 1 && b <= SLIM_KV4_MAX_SEQS && tq >= 0 && tq <= SLIM_KV4_MAX_T && (uneven || tq % b == 0) && per >= 1 &&
-         per <= SLIM_KV4_MAX_SLOTS / page;
+         b >= 1 && b <= SLIM_KV4_MAX_SEQS && tq >= 0 && tq <= SLIM_KV4_MAX_T &&
+         tq * hq < (1 << 27) &&   // fewer than 2^24 workgroups: a launch has less than 2^32 threads
+         (uneven || tq % b == 0) && per >= 1 && per <= SLIM_KV4_MAX_SLOTS / page;
 }
 
 size_t slim_kv4_attention_workspace(int64_t b, int64_t tq, int uneven, int64_t hq, int64_t heads, int dim, int group,
@@ -540,7 +541,6 @@ int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uin
   if (!q || !cache || !table || !lengths || !out) return SLIM_E_NULL;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return SLIM_E_ALIGN;
   const slim::Kv4Plan p = slim::kv4_plan(b, tq, !offsets, hq, heads, dim, group, per * page, qdt == SLIM_F32);
-  if (((int64_t)p.slots + p.extra) * heads > INT32_MAX || (int64_t)p.slots * heads * p.tm > UINT32_MAX) return SLIM_E_SHAPE;
   if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes)) return SLIM_E_WORKSPACE;
   if (p.ws_bytes > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
   slim::Kv4Args a = {};
@@ -555,7 +555,7 @@ int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uin
 // ---------------------------------------------------------------- verification of drafted tokens
 static bool draft_shape(int64_t b, int k, int64_t v) {
   return b >= 0 && b <= SLIM_DRAFT_MAX_B && k >= 1 && k <= SLIM_DRAFT_MAX_K && v >= 1 && v <= SLIM_LOGPROB_MAX_V &&
-         b * (2 * k + 1) * v <= ((int64_t)1 << 40);
+         b * (2 * k + 1) * v <= ((int64_t)1 << 36);
 }
 
 size_t slim_verify_draft_workspace(int64_t b, int k, int64_t v) {

@@ -178,7 +178,7 @@ __device__ __forceinline__ Pair group_pair(const float (&x)[8]) {
 template <bool BF16, int DIM, int GROUP>
 __global__ __launch_bounds__(256) void kv4_append_kernel(const Kv4Append a) {
   constexpr int L = DIM / 8, W = GROUP / 8, NG = DIM / GROUP, REC = 4 * DIM + 32 * NG;
-  const unsigned item = blockIdx.x * (256 / L) + threadIdx.x / L;      // below 2^20 tokens of 3 x 1024 heads, and a block
+  const unsigned item = blockIdx.x * (256 / L) + threadIdx.x / L;
   const int l = threadIdx.x % L;
   const unsigned per = (unsigned)(a.q.heads + 2 * a.k.heads);
   const unsigned tok = item / per;
@@ -312,27 +312,52 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(const int32_t *__restrict
 
 }  // namespace
 
-hipError_t launch_kv4_append(const Kv4Append &a, hipStream_t st) {
-  const int64_t items = a.t * (a.q.heads + 2 * a.k.heads), per = 256 / (a.dim / 8);
-  const unsigned grid = (unsigned)((items + per - 1) / per);
+// Tokens a launch takes: it has less than 2^32 threads, and items are counted in 32 bits.
+static int64_t tokens_a_launch(int64_t heads, int dim) { return ((int64_t)1 << 31) / (heads * (dim / 8)); }
+
+hipError_t launch_kv4_append(const Kv4Append &all, hipStream_t st) {
+  const int64_t heads = all.q.heads + 2 * all.k.heads, per = 256 / (all.dim / 8), most = tokens_a_launch(heads, all.dim);
+  const int64_t size = all.bf16 ? 2 : 4;
+  for (int64_t t0 = 0; t0 < all.t; t0 += most) {
+    Kv4Append a = all;
+    a.t = all.t - t0 < most ? all.t - t0 : most;
+    a.k.p = (const char *)all.k.p + t0 * all.k.row * size;
+    a.v.p = (const char *)all.v.p + t0 * all.v.row * size;
+    if (all.q.p) {
+      a.q.p = (const char *)all.q.p + t0 * all.q.row * size;
+      a.q_out = (char *)all.q_out + t0 * all.q.heads * all.dim * size;
+    }
+    a.slots = all.slots + t0;
+    if (all.positions) a.positions = all.positions + t0;
+    const unsigned grid = (unsigned)((a.t * heads + per - 1) / per);
 #define F(D, G)                                                                \
   do {                                                                         \
     if (a.bf16) kv4_append_kernel<true, D, G><<<grid, 256, 0, st>>>(a);        \
     else kv4_append_kernel<false, D, G><<<grid, 256, 0, st>>>(a);              \
   } while (0)
-  KV4_BY_SHAPE(a.dim, a.group, F);
+    KV4_BY_SHAPE(a.dim, a.group, F);
 #undef F
-  return hipGetLastError();
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_kv4_read(const int32_t *slots, int64_t t, const uint32_t *cache, int64_t pages, int64_t heads,
                            int dim, int group, int page, void *k, void *v, bool bf16, hipStream_t st) {
-  const int64_t items = t * 2 * heads, per = 256 / (dim / 8);
-  const unsigned grid = (unsigned)((items + per - 1) / per);
-#define F(D, G) kv4_read_kernel<D, G><<<grid, 256, 0, st>>>(slots, t, cache, pages, (int)heads, __builtin_ctz(page), k, v, bf16)
-  KV4_BY_SHAPE(dim, group, F);
+  const int64_t per = 256 / (dim / 8), most = tokens_a_launch(2 * heads, dim), row = heads * dim * (bf16 ? 2 : 4);
+  for (int64_t t0 = 0; t0 < t; t0 += most) {
+    const int64_t n = t - t0 < most ? t - t0 : most;
+    const unsigned grid = (unsigned)((n * 2 * heads + per - 1) / per);
+#define F(D, G)                                                                                              \
+  kv4_read_kernel<D, G><<<grid, 256, 0, st>>>(slots + t0, n, cache, pages, (int)heads, __builtin_ctz(page), \
+                                              (char *)k + t0 * row, (char *)v + t0 * row, bf16)
+    KV4_BY_SHAPE(dim, group, F);
 #undef F
-  return hipGetLastError();
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace slim

@@ -110,6 +110,13 @@ __device__ __forceinline__ Work find_work(const Kv4Args &a, const Kv4Cut &cut, i
     return a.offsets ? (int)((unsigned)((hi - lo) * a.g + cut.tm - 1) >> cut.tm_log) : cut.tiles;
   };
   const bool cuts = cut.extra > 0;
+  if (!cuts && !a.offsets) {                   // a run a tile, as many for each sequence
+    w.seq = (int)((unsigned)i / (unsigned)cut.tiles);
+    w.q0 = (int64_t)w.seq * a.ql, w.ql = a.ql, w.nsplit = 1, w.first = i;
+    w.tile = cut.tiles - 1 - (i - w.seq * cut.tiles);
+    w.len = length_of(a, w.seq, w.over);
+    return w;
+  }
   float work = 0.0f;
   bool wrong = false;
   int t0 = 0;                       // records' tiles and row tiles of the lane's first sequence
@@ -133,7 +140,7 @@ __device__ __forceinline__ Work find_work(const Kv4Args &a, const Kv4Cut &cut, i
   if (cuts) {
     // the sum's rounding is below (per + 6) 2^-24 of it, far inside the factor: the runs stay within `extra`
     const float share = of_lane(running_sum(work), 63) * (1.01f / (float)cut.extra);
-    chunk = share < (float)cut.least ? cut.least : (int)share + 1;
+    chunk = share < (float)cut.least ? cut.least : (int)fminf(share, (float)(1 << 26)) + 1;
   }
   auto runs_of = [&](int t) __attribute__((always_inline)) { return t <= chunk ? 1 : ceil_div(t, chunk); };
   int tiles = n0, runs = n0 * runs_of(t0);
@@ -1005,16 +1012,17 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(const Kv4Args a, const Kv
 
 template <int DIM, int GROUP>
 hipError_t launch_group(const Kv4Args &a, const Kv4Cut &cut, const Kv4Plan &p, hipStream_t st) {
+  constexpr bool WIDE = DIM < 256;      // as kv4_plan has it
   const unsigned grid = (unsigned)((int64_t)(p.slots + p.extra) * a.hkv);
 #define RUN(KERNEL, NQ, X) KERNEL<DIM, GROUP, NQ, X><<<grid, 256, 0, st>>>(a, cut)
   if (p.tile) {
     if (!a.qbf16) RUN(kv4_tile_kernel, 1, true);
-    else if constexpr (DIM == 256) RUN(kv4_tile_kernel, 1, false);
-    else RUN(kv4_tile_kernel, 2, false);
+    else if constexpr (WIDE && DIM / GROUP < 4) RUN(kv4_tile_kernel, 2, false);
+    else RUN(kv4_tile_kernel, 1, false);
   } else {
     if (!a.qbf16) RUN(kv4_stream_kernel, 1, true);
     else if (p.nq == 1) RUN(kv4_stream_kernel, 1, false);
-    else if constexpr (DIM < 256) RUN(kv4_stream_kernel, 2, false);
+    else if constexpr (WIDE) RUN(kv4_stream_kernel, 2, false);
     else return hipErrorInvalidValue;
   }
 #undef RUN

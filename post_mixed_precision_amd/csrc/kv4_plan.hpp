@@ -10,6 +10,7 @@
 //   words 4 dim + 16 q + t    the keys' pair of group q, token t: step (low half) and low end, bfloat16
 //   and 16 k words further    the values' pairs
 #pragma once
+#include <stddef.h>
 #include <stdint.h>
 
 namespace slim {
@@ -41,13 +42,17 @@ struct Kv4Plan {
 
 // b sequences, tq query tokens in all (uniform: tq / b each), cap: the tokens
 // a row of the page table can name.
-inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t hkv, int dim, int group, int64_t cap, bool f32) {
+inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t hkv, int dim, int group, int64_t cap,
+                        bool f32) {
   Kv4Plan p;
   const int64_t g = hq / hkv;
   const int64_t per = (uniform ? tq / b : (tq + b - 1) / b) * g;   // rows of a sequence, on average
   const bool wide = !f32 && dim < 256;                             // registers for two tiles of 16 rows
-  p.tile = per > (wide ? 32 : 16);
-  p.nq = wide && per > 16 ? 2 : 1;
+  // Up to 64 rows the stream reads the cache again for every 32 (or 16) of them, from L2, and is still ahead of tiles
+  // that most of a workgroup's waves idle in (40 rows of 16 sequences of up to 8192: 95 us, tiles 108; 64 rows: 81 and
+  // 109; 96 rows: 113 and 107; float32, 40 rows: 24 and 27).
+  p.tile = per > 64;
+  p.nq = wide && per > 16 && !(p.tile && dim / group >= 4) ? 2 : 1;   // (many rows, small groups: 237 TFLOP/s, one 263)
   p.tm = 16 * p.nq * (p.tile ? 4 : 1);
   p.tiles = (int)((per + p.tm - 1) / p.tm);
   p.slots = (int)(uniform ? b * p.tiles : tq * g / p.tm + (b < tq ? b : tq));
@@ -56,12 +61,13 @@ inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t
   // heads: 95 us, 768 102), but where queries are uneven the longest tiles decide (1024 and 657 queries over 4096 and
   // 657 tokens: 768 147 us, 512 177).  However many tiles there are, one sequence may be far longer than the
   // others: 256 runs more, unless the table says that none can be.
-  p.least = p.tile ? 32 : 8;
-  const int64_t want = p.tile ? (uniform ? 512 : 768) : wide && p.nq == 1 && (dim == 64 || group == 128) ? 768 : 512;
+  const int64_t want = p.tile ? (uniform ? 512 : 768) : !f32 && p.nq == 1 && (dim == 64 || group == dim) ? 768 : 512;
+  p.least = p.tile && p.slots * hkv >= 256 ? 32 : 8;
   const int64_t units = p.slots * hkv, tokens = (cap + 31) / 32, spare = cap > 2048 ? 256 : 0;
   const int64_t extra = ((want - units > spare ? want - units : spare) + hkv - 1) / hkv;
   const int64_t useful = p.slots * ((tokens + p.least - 1) / p.least - 1);   // runs are no shorter than `least`
-  p.extra = (int)(extra < useful ? extra : useful);
+  // every wave goes through all lengths to cut: not for thousands of sequences, which fill the card by themselves
+  p.extra = b > 1024 || units * p.tm >= (1 << 23) ? 0 : (int)(extra < useful ? extra : useful);
   const int64_t most = (tokens + p.least - 1) / p.least;
   p.most = (int)(most < p.extra / p.slots + 1 ? most : p.extra / p.slots + 1);
   p.ws_bytes = p.extra > 0 ? (size_t)(p.slots + p.extra) * hkv * p.tm * (dim + 2) * 4 + (size_t)p.slots * 32 : 0;

@@ -286,6 +286,20 @@ def test_attention(slim, lengths, n, hq, heads, dim, group, page, qdt, odt, caus
     assert torch.equal(out, again)
 
 
+# every head size and group on every kernel: few rows, some, many
+EVERY = [([97, 40 + n], n, 3, 1, dim, group, 32, qdt, qdt, True)
+         for dim in (64, 128, 256) for group in (32, 64, 128) if group <= dim for qdt in ("bf16", "f32")
+         for n in (2, 9, 25)]
+# and enough runs for the join by four waves
+JOINED = [([3000 + n, 1700], n, 3, 1, 128, 64, 64, "bf16", "bf16", True) for n in (1, 9, 25)] + \
+         [([2500 + n], n, 3, 1, dim, 64, 64, "f32", "f32", True) for dim in (64, 256) for n in (1, 25)]
+
+
+@pytest.mark.parametrize("lengths,n,hq,heads,dim,group,page,qdt,odt,causal", EVERY + JOINED)
+def test_attention_every_kernel(slim, lengths, n, hq, heads, dim, group, page, qdt, odt, causal):
+    test_attention(slim, lengths, n, hq, heads, dim, group, page, qdt, odt, causal)
+
+
 @pytest.mark.parametrize("qdt", ["bf16", "f32"])
 @pytest.mark.parametrize("counts,lengths,heads,hq,dim,group,page", [
     ([3, 0, 1, 20], [40, 9, 1, 300], 2, 6, 64, 32, 16),
@@ -518,3 +532,252 @@ def test_verify_draft_shared_rows(slim):
     assert torch.equal(a["ids"], b["ids"])
     out = slim.verify_draft(target[:0].cuda(), _gpu(tokens[:0]), _gpu(uniform[:0]))
     assert out["accepted"].shape == (0,) and out["ids"].shape == (0, 3)
+
+
+# ---------------------------------------------------------------- as they are used
+def _step(slim, st):
+    """A decode step with drafted tokens: cache, attention, an output layer in 4 bits, the drafts judged."""
+    q = slim.kv4_append(st["k"], st["v"], st["slots"], st["cache"], st["group"], rotary=st["rotary"],
+                        positions=st["positions"], q=st["q"])
+    b, n = st["tokens"].shape[0], st["tokens"].shape[1] + 1
+    o = slim.kv4_attention(q.view(b, n, *q.shape[1:]), st["cache"], st["table"], st["lengths"], st["group"])
+    h = o.reshape(b * n, -1)
+    logits = slim.q4_linear(h, st["head"], st["vocabulary"], 128)
+    out = slim.verify_draft(logits.view(b, n, -1), st["tokens"], st["uniform"], draft=st["draft"], temperature=0.9)
+    return {"q": q, "o": o, "logits": logits, **out}
+
+
+def _step_state(slim, seed, dt="bf16"):
+    rng = np.random.default_rng(seed)
+    b, n, hq, heads, dim, group, page, vocabulary = 3, 4, 4, 2, 64, 32, 16, 517
+    lengths = [70, 33, 4]
+    st = {"group": group, "vocabulary": vocabulary, "cache": slim.kv4_cache(20, heads, dim, group, page)}
+    table = rng.permutation(20)[:15].reshape(3, 5).astype(np.int32)
+    st["table"], st["lengths"] = _gpu(table), _i32(lengths)
+    past_k, past_v = [], []
+    rot = _table(rng, 100, dim)
+    st["rotary"] = _gpu(rot)
+    slot = lambda i, p: int(table[i, p // page]) * page + p % page  # noqa: E731
+    for i, length in enumerate(lengths):
+        m = length - n
+        k, v = _rows(rng, m, heads, dim, dt), _rows(rng, m, heads, dim, dt, False)
+        past_k.append(k), past_v.append(v)
+        if m:
+            slim.kv4_append(k.cuda(), v.cuda(), _i32([slot(i, p) for p in range(m)]), st["cache"], group,
+                            rotary=st["rotary"], positions=_i32(range(m)))
+    k, v, q = (_rows(rng, b * n, h, dim, dt, c) for h, c in ((heads, True), (heads, False), (hq, False)))
+    pos = [length - n + j for length in lengths for j in range(n)]
+    st["k"], st["v"], st["q"], st["positions"] = k.cuda(), v.cuda(), q.cuda(), _i32(pos)
+    st["slots"] = _i32([slot(i // n, p) for i, p in enumerate(pos)])
+    codes = rng.integers(0, 16, size=(vocabulary, hq * dim), dtype=np.uint8)
+    scale = rng.uniform(0.02, 0.05, (vocabulary, hq * dim // 128)).astype(np.float32)
+    zero = rng.uniform(6, 9, (vocabulary, hq * dim // 128)).astype(np.float32)
+    st["head"] = slim.pack4(_gpu(codes), _gpu(scale), _gpu(zero), 128)
+    st["draft"] = _gpu(rng.standard_normal((b, n - 1, vocabulary)).astype(np.float32) * 2)
+    st["tokens"] = _gpu(rng.integers(0, vocabulary, (b, n - 1)))
+    st["uniform"] = _gpu(rng.random((b, n)).astype(np.float32))
+    host = dict(lengths=lengths, n=n, rot=rot, k=k, v=v, q=q, pos=pos, past_k=past_k, past_v=past_v, codes=codes,
+                scale=scale, zero=zero, group=group, dim=dim)
+    return st, host
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_decode_step(slim, dt):
+    """The operators one after another, each against its definition on what the one before it gave."""
+    st, h = _step_state(slim, 1, dt)
+    out = _step(slim, st)
+    qr = oracle.rotate(_host(h["q"]), h["rot"], h["pos"], False)
+    np.testing.assert_array_equal(out["q"].float().cpu().numpy(), oracle.bf16_round(qr) if dt == "bf16" else qr)
+    n = h["n"]
+    ctx = Context.__new__(Context)
+    ctx.group, ctx.k, ctx.v = h["group"], [], []
+    for i, length in enumerate(h["lengths"]):
+        new = slice(i * n, (i + 1) * n)
+        k = np.concatenate([oracle.rotate(_host(h["past_k"][i]), h["rot"], range(length - n), False),
+                            oracle.rotate(_host(h["k"][new]), h["rot"], h["pos"][new], False)])
+        v = np.concatenate([oracle.as_f32(_host(x)) for x in (h["past_v"][i], h["v"][new])])
+        for x, to in ((k, ctx.k), (v, ctx.v)):
+            z = oracle.kv4_quantize(x, h["group"])
+            to.append((z, oracle.kv4_values(*z, h["group"])))
+        _check(ctx, i, out["o"][i], out["q"][new], h["dim"] ** -0.5, True, dt, dt)
+    want = oracle.q4_linear(_host(out["o"].reshape(len(h["lengths"]) * n, -1)), h["codes"], h["scale"], h["zero"], 128)
+    assert np.abs(out["logits"].cpu().numpy() - want).max() < 1e-4 * np.abs(want).max()
+    acc, ids, margin = oracle.verify_draft(out["logits"].view(-1, n, st["vocabulary"]).cpu().numpy(), st["tokens"].cpu().numpy(),
+                                           st["uniform"].cpu().numpy(), st["draft"].cpu().numpy(), 0.9)
+    assert (margin > 1e-11).all()
+    np.testing.assert_array_equal(out["accepted"].cpu().numpy(), acc)
+    np.testing.assert_array_equal(out["ids"].cpu().numpy(), ids)
+
+
+def _equal(a, b):
+    return all(torch.equal(a[k], b[k]) for k in a)
+
+
+def test_a_step_on_a_side_stream_and_from_graphs(slim):
+    """On another stream than the inputs' own, and from two captured graphs replayed in turns with other inputs and
+    eager work between."""
+    st, _ = _step_state(slim, 2)
+    eager = _step(slim, st)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = _step(slim, st)
+    side.synchronize()
+    assert _equal(eager, again)
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = _step(slim, st)
+        graphs.append((gr, out))
+    for turn in range(5):
+        fresh, _ = _step_state(slim, 10 + turn)
+        for name in ("k", "v", "q", "tokens", "uniform", "draft", "table", "lengths", "slots", "positions", "rotary", "head"):
+            st[name].copy_(fresh[name])
+        st["cache"].copy_(fresh["cache"])
+        kept = st["cache"].clone()
+        eager = _step(slim, st)
+        after = st["cache"].clone()
+        st["cache"].copy_(kept)
+        gr, out = graphs[turn % 2]
+        gr.replay()
+        torch.cuda.synchronize()
+        assert _equal(eager, out) and torch.equal(st["cache"], after)
+
+
+def test_steps_from_two_threads(slim):
+    """Steps from two host threads, each on a stream of its own, against what each gives alone."""
+    import threading
+    states = [_step_state(slim, 20 + i)[0] for i in range(2)]
+    alone = [_step(slim, st) for st in states]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(30):
+                out = _step(slim, states[i])
+                stream.synchronize()
+                if not _equal(out, alone[i]):
+                    wrong.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong
+
+
+def test_long_rows_in_graphs(slim):
+    """Calls with a workspace (runs that are joined; many rows), captured twice, replayed in turns."""
+    ctx = Context(slim, 6, [3000, 900], 2, 128, 128, 64)
+    rng = np.random.default_rng(7)
+    q = _rows(rng, 2 * 40, 4, 128, "bf16", False).view(2, 40, 4, 128).cuda()
+    one = _rows(rng, 2, 4, 128, "bf16", False).view(2, 1, 4, 128).cuda()
+    table, lengths = _gpu(ctx.table), _i32([3000, 900])
+
+    def run():
+        return [slim.kv4_attention(x, ctx.cache, table, lengths, 128) for x in (q, one)]
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = run()
+        graphs.append((gr, out))
+    for turn in range(6):
+        q.copy_(_rows(rng, 2 * 40, 4, 128, "bf16", False).view(2, 40, 4, 128))
+        lengths.copy_(_i32([3000 - 100 * turn, 900 - turn]))
+        eager = run()
+        graphs[turn % 2][0].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(eager, graphs[turn % 2][1]))
+
+
+def test_many_sequences_of_uneven_lengths(slim):
+    """More sequences than a wave has lanes with a long one among them: its runs, the others whole."""
+    rng = np.random.default_rng(8)
+    lengths = [int(x) for x in rng.integers(0, 50, 130)]
+    lengths[77] = 5000
+    ctx = Context(slim, 11, lengths, 1, 64, 64, 32)
+    q = _rows(rng, 130, 2, 64, "bf16", False).view(130, 1, 2, 64)
+    out = slim.kv4_attention(q.cuda(), ctx.cache, _gpu(ctx.table), _i32(lengths), 64)
+    for i in range(130):
+        if lengths[i]:
+            _check(ctx, i, out[i], q[i], 64 ** -0.5, True, "bf16", "bf16")
+        else:
+            assert not out[i].any()
+
+
+def test_the_most_sequences(slim):
+    """4096 of them, uniform and by offsets."""
+    rng = np.random.default_rng(9)
+    lengths = [int(x) for x in rng.integers(0, 5, 4096)]
+    ctx = Context(slim, 12, lengths, 1, 64, 32, 16)
+    q = _rows(rng, 4096, 1, 64, "bf16", False)
+    out = slim.kv4_attention(q.view(4096, 1, 1, 64).cuda(), ctx.cache, _gpu(ctx.table), _i32(lengths), 32)
+    off = slim.kv4_attention(q.cuda(), ctx.cache, _gpu(ctx.table), _i32(lengths), 32, offsets=_i32(range(4097)))
+    assert torch.equal(out.view(4096, 1, 64), off)
+    for i in list(range(0, 4096, 97)) + [4095]:
+        if lengths[i]:
+            _check(ctx, i, out[i], q[i:i + 1], 64 ** -0.5, True, "bf16", "bf16")
+        else:
+            assert not out[i].any()
+
+
+def test_append_in_several_launches(slim):
+    """More items than a launch takes: tokens of 1024 heads (values checked at both ends and around the seam)."""
+    heads, dim, page = 1024, 64, 16
+    per = (1 << 31) // (2 * heads * (dim // 8))          # tokens a launch takes without queries
+    t = per + 5
+    one = torch.randn((1, heads, dim), device="cuda:0").to(torch.bfloat16)
+    rows = one.expand(t, heads, dim)
+    slots = torch.full((t,), -1, dtype=torch.int32, device="cuda:0")
+    put = [0, 1, per - 1, per, per + 4]
+    for i, x in enumerate(put):
+        slots[x] = i
+    cache = slim.kv4_cache(1, heads, dim, 32, page)
+    slim.kv4_append(rows, rows, slots, cache, 32)
+    want = slim.kv4_cache(1, heads, dim, 32, page)
+    slim.kv4_append(one.expand(5, heads, dim).contiguous(), one.expand(5, heads, dim).contiguous(), _i32(range(5)), want, 32)
+    assert torch.equal(cache, want)
+
+
+def test_verify_draft_extremes(slim):
+    """The most drafted tokens; rows of 2^24 logits; thousands of sequences of a small vocabulary."""
+    target, dr, tokens, uniform = _drafts(40, 1, 32, 50, "f32")
+    dr = target[:, :32].clone()                          # all accepted
+    acc, _ = _verify(slim, target, tokens, uniform, dr)
+    assert acc[0] == 32
+    v = 1 << 24
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(3)
+    target = torch.randn((1, 2, v), generator=gen, device="cuda:0").to(torch.bfloat16)
+    u = torch.tensor([[0.5, 0.73]], device="cuda:0")
+    out = slim.verify_draft(target, torch.tensor([[5]], device="cuda:0"), u)
+    p = torch.softmax(target[0, 0].double(), 0)
+    assert float(p[5]) < 0.4 and int(out["accepted"][0]) == 0
+    p[5] = 0
+    run = p.cumsum(0)
+    assert int(out["ids"][0, 0]) == int((run <= u[0, 1].double() * run[-1]).sum())
+    b = 5000
+    target, dr, tokens, uniform = _drafts(41, b, 1, 7, "f32")
+    acc, _ = _verify(slim, target, tokens, uniform, dr)
+    assert 0 < acc.mean() < 1
+
+
+def test_outputs_over_inputs_are_refused(slim):
+    cache = slim.kv4_cache(3, 2, 64, 32, 16)
+    q = torch.zeros((4, 1, 4, 64), device="cuda:0")
+    with pytest.raises(slim.SlimError, match="out: overlaps q"):
+        slim.kv4_attention(q, cache, _i32([[0, 1]] * 4), _i32([1] * 4), 32, out=q)
+    words = cache.view(-1)
+    with pytest.raises(slim.SlimError, match="overlaps"):
+        slim.kv4_append(torch.zeros((5, 2, 64), device="cuda:0"), torch.zeros((5, 2, 64), device="cuda:0"), words[:5],
+                        cache, 32)
+    k = words[:640].view(torch.float32).view(5, 2, 64)
+    with pytest.raises(slim.SlimError, match="overlaps"):
+        slim.kv4_append(k, k, _i32(range(5)), cache, 32)
+    host = torch.zeros((5, 2, 64))
+    with pytest.raises(slim.SlimError, match="GPU"):
+        slim.kv4_append(host, host, _i32(range(5)), cache, 32)
