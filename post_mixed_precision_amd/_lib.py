@@ -871,7 +871,7 @@ def kv4_append(k, v, slots, cache, group: int, rotary=None, positions=None, inte
             return kv4_append(k, v, slots, cache, group, rotary, positions, interleaved, q)
     out = None
     if q is not None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         op = out.data_ptr() if hq else None
     st = load_library().slim_kv4_append(kp, krow, khead, vp, vrow, vhead, code, t, heads, dim, group, sp, cp,
                                         cache.shape[0], page, rp, npos, rot, 1 if interleaved else 0, pp, qp, hq, qrow,
@@ -973,7 +973,7 @@ def kv4_attention(q, cache, table, lengths, group: int, offsets=None, scale=None
         with torch.cuda.device(dev):
             return kv4_attention(q, cache, table, lengths, group, offsets, scale, causal, out_dtype, out)
     if out is None:
-        out = torch.empty(q.shape, dtype=otype, device=q.device)
+        out = torch.empty_like(q) if otype == q.dtype else torch.empty(q.shape, dtype=otype, device=q.device)
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     st = load_library().slim_kv4_attention(q.data_ptr(), qcode, tq, hq, cache.data_ptr(), pages, page, heads, dim,
                                            group, table.data_ptr(), b, per, lengths.data_ptr(),

@@ -942,22 +942,22 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
   }
 }
 
-// Joins the runs of a row: PARTS waves share them (4 where there may be
+// Joins the runs of a row: PARTS waves share them (1, or 4 or 16 where there may be
 // many), lane l takes the DIM / 64 channels from DIM / 64 l on.  A wave has 64 runs' factors before
 // the first of their sums is read, so the reads do not wait for each other.
 template <int DIM, int PARTS>
-__global__ __launch_bounds__(256) void kv4_join_kernel(const Kv4Args a, const Kv4Cut cut) {
-  constexpr int CH = DIM / 64;
+__global__ __launch_bounds__(PARTS == 16 ? 1024 : 256) void kv4_join_kernel(const Kv4Args a, const Kv4Cut cut) {
+  constexpr int CH = DIM / 64, ROWS = PARTS == 1 ? 4 : 1;     // rows a workgroup
   __shared__ float s_o[PARTS][DIM];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // tm is a multiple of 4: the rows of a workgroup are of one tile
-  const unsigned row = blockIdx.x * (4 / PARTS) + wave / PARTS, x = row >> cut.tm_log;   // uniform
+  const unsigned row = blockIdx.x * ROWS + wave / PARTS, x = row >> cut.tm_log;   // uniform
   const int m = (int)(row & (cut.tm - 1)), y = wave % PARTS;
   const unsigned slot = x / (unsigned)a.hkv;
   const int h = (int)(x - slot * a.hkv);
   const Joint k = joints(a, cut, DIM)[slot];
   const int mm = k.m0 + m, n = k.runs;
-  if (n < 0 && m < 4 / PARTS) nan_share(a, (int)slot, cut.slots, h, DIM);
+  if (n < 0 && m < ROWS) nan_share(a, (int)slot, cut.slots, h, DIM);
   if (n <= 1 || mm >= k.ql * a.g) return;         // uniform over what shares LDS
   const int64_t next = (int64_t)a.hkv * cut.tm;   // rows from one run to the next
   const float2 *ml = part_ml(a, cut, k.first, h, m, DIM);
@@ -1029,7 +1029,8 @@ hipError_t launch_group(const Kv4Args &a, const Kv4Cut &cut, const Kv4Plan &p, h
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.extra == 0) return e;
   const int64_t rows = (int64_t)p.slots * a.hkv * p.tm;
-  if (p.most > 8) kv4_join_kernel<DIM, 4><<<(unsigned)rows, 256, 0, st>>>(a, cut);
+  if (p.most > 16) kv4_join_kernel<DIM, 16><<<(unsigned)rows, 1024, 0, st>>>(a, cut);
+  else if (p.most > 8) kv4_join_kernel<DIM, 4><<<(unsigned)rows, 256, 0, st>>>(a, cut);
   else kv4_join_kernel<DIM, 1><<<(unsigned)(rows / 4), 256, 0, st>>>(a, cut);
   return hipGetLastError();
 }

@@ -61,7 +61,7 @@ inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t
   // heads: 95 us, 768 102), but where queries are uneven the longest tiles decide (1024 and 657 queries over 4096 and
   // 657 tokens: 768 147 us, 512 177).  However many tiles there are, one sequence may be far longer than the
   // others: 256 runs more, unless the table says that none can be.
-  const int64_t want = p.tile ? (uniform ? 512 : 768) : !f32 && p.nq == 1 && (dim == 64 || group == dim) ? 768 : 512;
+  const int64_t want = p.tile ? (uniform ? 512 : 768) : b > 1 && !f32 && p.nq == 1 && group == 128 && dim == 128 ? 768 : 512;
   p.least = p.tile && p.slots * hkv >= 256 ? 32 : 8;
   const int64_t units = p.slots * hkv, tokens = (cap + 31) / 32, spare = cap > 2048 ? 256 : 0;
   const int64_t extra = ((want - units > spare ? want - units : spare) + hkv - 1) / hkv;
