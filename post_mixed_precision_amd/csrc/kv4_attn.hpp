@@ -20,6 +20,8 @@
 // as one word.  A row's statistics are per lane as well; only the maximum
 // crosses lanes.
 #pragma once
+#include <type_traits>
+
 #include "mma16.hpp"
 #include "serve.hpp"
 
@@ -245,15 +247,20 @@ __device__ __forceinline__ int64_t row_at(const Kv4Args &a, const K &k, int h, i
 // tokens (two records) for all of them.
 //
 // Weights are 2^(S - m) with S in powers of two and m the row's reference: the
-// maximum of the row's first tokens, moved up only once a score exceeds it by
-// `kSlack` (weights then reach 2^kSlack at most, far inside float32 and
-// bfloat16).  So a step needs no maximum across lanes and no rescaling, but
-// for the first ones: each lane compares its own scores.
+// maximum of the row's first tokens less kLift, moved up only once a weight
+// would exceed 2^kMost.  So a step needs no maximum across lanes and no
+// rescaling, but for the first ones: each lane compares its own scores.
 //
-// Weights times steps are rounded to the sum of two bfloat16 terms (2^-16):
-// with one term (2^-9) the outputs' error was twice that of their own
+// Few rows: weights times steps are rounded to the sum of two bfloat16 terms
+// (2^-16): with one term (2^-9) the outputs' error was twice that of their own
 // rounding to bfloat16.  Float32 queries and weights enter as three terms.
-constexpr float kSlack = 10.0f;
+//
+// Many rows of bfloat16: values are dequantized after all, once for the
+// workgroup, to float16 (2^-12 of the value), and weights are float16 too (2^-12;
+// with the lift, weights down to 2^-33 of a row's largest count).  The products
+// of codes with weights in two terms cost twice the matrix instructions and, per weight, six
+// vector instructions more.
+constexpr float kLift = 8.0f, kMost = 15.0f;
 
 // 8 numbers as two bfloat16 terms, the first truncated, the second rounded.
 __device__ __forceinline__ void split2(const float (&x)[8], uint4 (&t)[2]) {
@@ -268,6 +275,12 @@ __device__ __forceinline__ void split2(const float (&x)[8], uint4 (&t)[2]) {
   t[1] = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+__device__ __forceinline__ uint32_t pk_half(float lo, float hi) {
+  typedef __attribute__((__vector_size__(2 * sizeof(float)))) float f32x2;
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_t));
+}
+
 template <int DIM, int GROUP, int NQ, bool XF32>
 struct Rows {
   static constexpr int NG = DIM / GROUP, W = DIM / 32, GS = GROUP / 32, NTQ = XF32 ? 3 : 1, NTP = XF32 ? 3 : 2;
@@ -276,7 +289,8 @@ struct Rows {
   int lim[NQ];               // tokens a row attends to
   float m[NQ], thr[NQ];      // reference; what a score may exceed it by (-inf: no reference yet)
   float ls[NQ], pl[NQ][NG];  // this lane's share of sum P and of sum P low
-  f32x4_t o[NQ][DIM / 16];   // sum P step code, rows (tokens' channels) by columns (rows)
+  f32x4_t o[NQ][DIM / 16];   // sum P step code (or P value), channels by rows
+  f32x4_t lh[NQ];            // sum P of the steps by float16, in every entry
 
   // Rows m0 + 16 n + lane % 16 of the sequence, those from `rows` on as zeros that attend to nothing.
   __device__ __forceinline__ void start(const Kv4Args &a, const Work &k, int h, int m0, int rows, float c) {
@@ -316,17 +330,17 @@ struct Rows {
         qs[n][j] *= c;
       }
       m[n] = 0.0f, thr[n] = kNegInf, ls[n] = 0.0f;
+      lh[n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i2 = 0; i2 < DIM / 16; ++i2) o[n][i2] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
   }
 
-  // 32 tokens from token `first` on.  Src: codes and pairs of the two records; a key's step is
-  // given times scale log2 e.  EDGE: some row does not attend to all of them.
+  // Weights of 32 tokens, tok the lane's first one (entry 4 b + v: token tok + 16 b + v).  Src: codes
+  // and pairs of the two records; a key's step is given times scale log2 e.  EDGE: some row does
+  // not attend to all of them.
   template <bool EDGE, class Src>
-  __device__ __forceinline__ void attend(Src &src, int first) {
-    const int tok = first + 4 * ((threadIdx.x & 63) >> 4);   // of entry 0; entry 4 b + v: + 16 b + v
-    float x[NQ][8];
+  __device__ __forceinline__ void weigh(Src &src, int tok, float (&x)[NQ][8]) {
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -357,6 +371,8 @@ struct Rows {
             x[n][4 * b + v] = __builtin_fmaf(step[v], acc[n][v], x[n][4 * b + v]);
           }
       }
+    float top[NQ];
+    bool up = false;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       if (EDGE) {
@@ -364,16 +380,31 @@ struct Rows {
         for (int e = 0; e < 8; ++e)
           if (tok + 16 * (e >> 2) + (e & 3) >= lim[n]) x[n][e] = kNegInf;
       }
-      float top = fmaxf(fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])),
-                        fmaxf(fmaxf(x[n][4], x[n][5]), fmaxf(x[n][6], x[n][7])));
-      if (__any(top > thr[n])) raise(n, top, x[n]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[n][e] = exp2_any(x[n][e]);
-        ls[n] += x[n][e];
-      }
+      top[n] = fmaxf(fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])),
+                     fmaxf(fmaxf(x[n][4], x[n][5]), fmaxf(x[n][6], x[n][7])));
+      up |= top[n] > thr[n];
     }
+    if (__any(up)) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) raise(n, top[n], x[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[n][e] = exp2_any(x[n][e]);
+  }
+
+  // 32 tokens from token `first` on, values by their codes.
+  template <bool EDGE, class Src>
+  __device__ __forceinline__ void attend(Src &src, int first) {
+    const int tok = first + 4 * ((threadIdx.x & 63) >> 4);
+    float x[NQ][8];
+    weigh<EDGE>(src, tok, x);
     src.values();
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ls[n] += x[n][e];
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       float step[2][4], low[2][4];
@@ -412,17 +443,54 @@ struct Rows {
     }
   }
 
+  // The same with the values themselves, finite, as float16.
+  template <bool EDGE, class Src>
+  __device__ __forceinline__ void attend_half(Src &src, int first) {
+    float x[NQ][8];
+    weigh<EDGE>(src, first + 4 * ((threadIdx.x & 63) >> 4), x);
+    const uint4 ones = make_uint4(0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u);
+    uint4 pf[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      pf[n] = make_uint4(pk_half(x[n][0], x[n][1]), pk_half(x[n][2], x[n][3]), pk_half(x[n][4], x[n][5]),
+                         pk_half(x[n][6], x[n][7]));
+      lh[n] = mfma16_half(ones, pf[n], lh[n]);   // the sum of the weights as they are multiplied
+    }
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      uint4 even, odd;
+      src.vcode(w, even, odd);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        o[n][2 * w] = mfma16_half(even, pf[n], o[n][2 * w]);
+        o[n][2 * w + 1] = mfma16_half(odd, pf[n], o[n][2 * w + 1]);
+      }
+    }
+  }
+  // From sums of values times `unit` by float16 to sums of values.
+  __device__ __forceinline__ void leave_half(float unit) {
+    const bool first = (threadIdx.x & 63) < 16;   // the other lanes of a row have the same sum of weights
+    const float f = 1.0f / unit;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      ls[n] = first ? lh[n][0] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < DIM / 16; ++i) o[n][i] *= f;
+    }
+  }
+
   // A new reference for the rows that need one: the maximum over the step's tokens.
   __device__ __forceinline__ void raise(int n, float top, float (&x)[8]) {
     asm volatile("" : "+v"(top));   // nothing of this is done ahead of the branch
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const bool up = top > thr[n];
-    const float f = !up ? 1.0f : thr[n] == kNegInf ? 0.0f : exp2_any(-top);   // sums of no token are 0
-    const float by = up ? top : 0.0f;
+    const float by = up ? top - kLift : 0.0f;
+    const float f = !up ? 1.0f : thr[n] == kNegInf ? 0.0f : exp2_any(-by);   // sums of no token are 0
     m[n] += by;
-    if (up) thr[n] = kSlack;
+    if (up) thr[n] = kMost;
     ls[n] *= f;
+    lh[n] *= f;
 #pragma unroll
     for (int j = 0; j < NG; ++j) pl[n][j] *= f;
 #pragma unroll
@@ -480,6 +548,23 @@ struct Pages {
     return cache + (uint64_t)(unsigned)(page_of < 0 ? 0 : page_of) * bytes + in * RECB;
   }
 };
+
+// Greatest over aligned groups of 16 lanes.
+__device__ __forceinline__ uint32_t over_row(uint32_t x) {
+  auto with = [&](uint32_t y) __attribute__((always_inline)) { x = x > y ? x : y; };
+  with((uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xb1, 0xf, 0xf, true));    // lane ^ 1
+  with((uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4e, 0xf, 0xf, true));    // lane ^ 2
+  with((uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x141, 0xf, 0xf, true));   // lane ^ 7 of 8
+  with((uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x140, 0xf, 0xf, true));   // lane ^ 15 of 16
+  return x;
+}
+
+// Two float16 numbers x y + z, each rounded once.
+__device__ __forceinline__ uint32_t fma_half(uint32_t x, uint32_t y, uint32_t z) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, x),
+                                                               __builtin_bit_cast(f16x2_t, y),
+                                                               __builtin_bit_cast(f16x2_t, z)));
+}
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
@@ -790,8 +875,9 @@ template <int DIM, int GROUP>
 struct LdsTile {
   static constexpr int NG = DIM / GROUP, W = DIM / 32, TB = DIM == 256 ? 2 : 4, TOK = 16 * TB;
   uint4 k[TB * W][64];
-  uint4 v[TB / 2 * (DIM / 16)][64];
+  uint4 v[TB / 2 * (DIM / 16)][64];          // or values, float16
   float pair[4][NG][TOK];    // keys' steps (times scale log2 e) and low ends, values' steps and low ends
+  uint32_t size[TB][NG];     // greatest magnitude of a record's values, as bits (none finite: above infinity's)
 };
 template <int DIM, int GROUP>
 struct LdsPart {             // 32 tokens of it
@@ -819,7 +905,11 @@ struct LdsPart {             // 32 tokens of it
 
 // Many rows: four waves of 16 NQ rows each share the tokens.  A tile's codes
 // come to registers while the tile before is worked on, and are expanded into
-// the other half of LDS behind it.
+// the other half of LDS behind it: keys to bfloat16 codes; values, for bfloat16
+// queries, to float16 numbers in a unit that makes the first tile's greatest
+// one 8 to 16.  Should a tile not fit that (an entry past 2^14 units; a record's whole group
+// below 2^-11 units, where float16 runs out of bits; a NaN, which must not meet a
+// weight of 0), the rest is done by the values' codes, as for float32 queries.
 template <int DIM, int GROUP, int NQ, bool XF32>
 __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const Kv4Cut cut) {
   typedef LdsTile<DIM, GROUP> Lds;
@@ -857,7 +947,10 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
     Pages pg = pages_of<4 * REC>(a, k.seq, h, kend);
     const int blk = TB == 4 ? wave : wave >> 1, off = TB == 4 ? 0 : WPW * (wave & 1);
     const int soff = TB == 4 ? 0 : 16 * NG * (wave & 1);
+    constexpr int GS = GROUP / 32, NV = WPW > GS ? WPW / GS : 1;   // groups of the words that a wave expands
     uint32_t kw[WPW], vw[WPW], sw[NS];
+    uint4 vp[XF32 ? 1 : NV];                 // their pairs of this lane's four tokens
+    float unit = 1.0f;
     auto fetch = [&](int t) __attribute__((always_inline)) {
       if (TB * t - pg.base >= 64) pg.load(TB * t);
       const int page = pg.of(TB * t + blk);
@@ -870,13 +963,59 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
         sw[i] = x < SW ? p[4 * DIM + soff + x] : 0u;
         if (page < 0) sw[i] = 0x7fc0u;
       }
+      if constexpr (!XF32) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          vp[i] = *(const uint4 *)(p + 4 * DIM + 16 * NG + 16 * (off / GS + i) + 4 * lg);
+          if (page < 0) vp[i] = make_uint4(0x7fc0u, 0x7fc0u, 0x7fc0u, 0x7fc0u);
+        }
+      }
     };
-    auto expand = [&](Lds &d) __attribute__((always_inline)) {
+    // The greatest magnitude that each group of the wave's record holds, for all to see.
+    auto measure = [&](Lds &d, int t) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int x = soff + lane + 64 * i;
+        const float step = half_of(sw[i], false), low = half_of(sw[i], true);
+        const float far = __builtin_fmaf(15.0f, step, low);        // a NaN step makes it one
+        uint32_t u = __float_as_uint(far) & 0x7fffffffu;
+        u = u > (__float_as_uint(low) & 0x7fffffffu) ? u : __float_as_uint(low) & 0x7fffffffu;
+        if (TOK * t + 16 * blk + (x & 15) >= kend) u = 0u;         // nobody attends to it
+        u = over_row(u);
+        if (lane + 64 * i < SW && x >= 16 * NG && (x & 15) == 0) d.size[blk][x / 16 % NG] = u;
+      }
+    };
+    // CODES: values as bfloat16 codes, else as float16 numbers.
+    auto expand = [&](Lds &d, int t, auto codes) __attribute__((always_inline)) {
+      constexpr bool CODES = decltype(codes)::value;
+      uint32_t st[NV][2], lo[NV][2];
+      if constexpr (!CODES) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          uint32_t w[4] = {vp[i].x, vp[i].y, vp[i].z, vp[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (TOK * t + 16 * blk + 4 * lg + e >= kend) w[e] = 0u;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            st[i][e] = pk_half(half_of(w[2 * e], false) * unit, half_of(w[2 * e + 1], false) * unit);
+            lo[i][e] = pk_half(half_of(w[2 * e], true) * unit, half_of(w[2 * e + 1], true) * unit);
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < WPW; ++i) {
         const int w = off + i;
         d.k[blk * W + w][lane] = q4_codes(kw[i]);
-        const uint4 y = q4_codes(vw[i]);
+        uint4 y;
+        if constexpr (CODES) {
+          y = q4_codes(vw[i]);
+        } else {
+          y = q4_codes_half(vw[i]);
+          const int j = WPW > GS ? i / GS : 0;
+          y.x = fma_half(y.x, st[j][0], lo[j][0]), y.y = fma_half(y.y, st[j][1], lo[j][1]);
+          y.z = fma_half(y.z, st[j][0], lo[j][0]), y.w = fma_half(y.w, st[j][1], lo[j][1]);
+        }
         uint2 *e = (uint2 *)&d.v[(blk >> 1) * (DIM / 16) + 2 * w][lane];
         uint2 *o = (uint2 *)&d.v[(blk >> 1) * (DIM / 16) + 2 * w + 1][lane];
         e[blk & 1] = make_uint2(y.x, y.y);
@@ -885,28 +1024,74 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int x = soff + lane + 64 * i;
-        if (lane + 64 * i < SW) {
-          const int kv = x / (16 * NG), j = x / 16 % NG;
+        const int kv = x / (16 * NG), j = x / 16 % NG;
+        if (lane + 64 * i < SW && (CODES || kv == 0)) {
           d.pair[2 * kv][j][16 * blk + (x & 15)] = half_of(sw[i], false) * (kv ? 1.0f : c);
           d.pair[2 * kv + 1][j][16 * blk + (x & 15)] = half_of(sw[i], true);
         }
       }
+      if constexpr (!CODES) measure(d, t);
     };
+    constexpr std::integral_constant<bool, true> kCodes{};
+    constexpr std::integral_constant<bool, false> kNumbers{};
+
     pg.load(TB * t0);
     fetch(t0);
-    expand(s[0]);
-    __syncthreads();
-    for (int t = t0; t < t1; ++t) {
+    int t = t0;
+    if constexpr (!XF32) {
+      measure(s[0], t0);
+      __syncthreads();
+      uint32_t most = 0u;
+#pragma unroll
+      for (int i = 0; i < TB * NG; ++i) {
+        const uint32_t u = s[0].size[i / NG][i % NG];
+        most = most > u ? most : u;
+      }
+      // 2^(130 - e) for the biased exponent e of the greatest, within 2^+-100 (nothing finite, nothing but 0: 1)
+      const int e = (int)(most >> 23);
+      const int up = e == 0 || e == 255 ? 0 : 130 - e < -100 ? -100 : 130 - e > 100 ? 100 : 130 - e;
+      unit = __uint_as_float((uint32_t)(up + 127) << 23);
+      expand(s[0], t0, kNumbers);
+      __syncthreads();
+      for (; t < t1; ++t) {
+        const Lds &d = s[(t - t0) & 1];
+        bool fits = true;                    // the same in every wave
+#pragma unroll
+        for (int i = 0; i < TB * NG; ++i) {
+          const uint32_t u = __builtin_amdgcn_readfirstlane(d.size[i / NG][i % NG]);
+          const float x = __uint_as_float(u) * unit;
+          fits &= u == 0u || (x < 0x1p14f && x >= 0x1p-11f);
+        }
+        if (!fits) break;
+        if (t + 1 < t1) fetch(t + 1);
+#pragma unroll
+        for (int p = 0; p < TB / 2; ++p) {
+          const int first = t * TOK + 32 * p;
+          LdsPart<DIM, GROUP> src = {d, p};
+          if (first + 32 <= wall) rows.template attend_half<false>(src, first);
+          else if (first < wend) rows.template attend_half<true>(src, first);
+        }
+        if (t + 1 < t1) expand(s[(t + 1 - t0) & 1], t + 1, kNumbers);   // read last before the barrier of the step before
+        __syncthreads();
+      }
+      rows.leave_half(unit);
+    }
+    if (t < t1) {                            // the registers still hold tile t; of what it is in LDS only `size` is read
+      expand(s[(t - t0) & 1], t, kCodes);
+      __syncthreads();
+    }
+    for (; t < t1; ++t) {
       const Lds &d = s[(t - t0) & 1];
       if (t + 1 < t1) fetch(t + 1);
-#pragma unroll
+      constexpr int U = XF32 ? TB / 2 : 1;
+#pragma unroll U
       for (int p = 0; p < TB / 2; ++p) {
         const int first = t * TOK + 32 * p;
         LdsPart<DIM, GROUP> src = {d, p};
-        if (first + 32 <= wall) rows.template attend<false>(src, first);
+        if (XF32 && first + 32 <= wall) rows.template attend<false>(src, first);
         else if (first < wend) rows.template attend<true>(src, first);
       }
-      if (t + 1 < t1) expand(s[(t + 1 - t0) & 1]);   // read last before the barrier of the step before
+      if (t + 1 < t1) expand(s[(t + 1 - t0) & 1], t + 1, kCodes);
       __syncthreads();
     }
   }
