@@ -3,13 +3,14 @@
 //   S[r, t] = scale sum_c q[r, c] k[t, c],  o[r] = sum_t softmax_t(S[r, t]) v[t]   over t < limit(r),
 //   k[t, c] = code[t, c] step[t, j] + low[t, j]   (j the group of c; v alike)
 //
-// Nothing is dequantized.  Codes are exact in bfloat16, so with Q_j the sum
-// of q over group j
+// Codes are exact in bfloat16, so with Q_j the sum of q over group j
 //   S[r, t] = scale sum_j (step[t, j] (sum_{c in j} q[r, c] code[t, c]) + low[t, j] Q_j[r]),
 //   o[r, c] = sum_t (P[r, t] step[t, j]) code[t, c] + sum_t P[r, t] low[t, j],
-// where the products with codes go to the matrix cores and the rest is float32.
-// P step is the one thing that is rounded: to bfloat16 where q is bfloat16
-// (as the outputs are), to three bfloat16 terms where q is float32.
+// where the products with codes go to the matrix cores and the rest is float32:
+// nothing is dequantized.  P step is the one thing that is rounded: to two
+// bfloat16 terms where q is bfloat16, to three where q and P step are float32.
+// For many rows of bfloat16 the second product is one of float16 weights with
+// float16 values instead, wherever the values' range allows that.
 //
 // Rows are the query tokens of a sequence times the query heads of one key
 // head, 16 a tile.  S is formed transposed (tokens by rows): its accumulator
@@ -256,10 +257,11 @@ __device__ __forceinline__ int64_t row_at(const Kv4Args &a, const K &k, int h, i
 // rounding to bfloat16.  Float32 queries and weights enter as three terms.
 //
 // Many rows of bfloat16: values are dequantized after all, once for the
-// workgroup, to float16 (2^-12 of the value), and weights are float16 too (2^-12;
-// with the lift, weights down to 2^-33 of a row's largest count).  The products
-// of codes with weights in two terms cost twice the matrix instructions and, per weight, six
-// vector instructions more.
+// workgroup, to float16 (step, low end and value each within 2^-11 of themselves), and
+// weights are float16 too (2^-11, or 2^-33 of the row's largest weight, by the
+// lift).  The products of codes with weights in two terms cost twice the
+// matrix instructions and six vector instructions more a weight: 8 sequences
+// of 4096, causal, 32 + 8 heads of 128, took 1702 us by them, 1548 us so.
 constexpr float kLift = 8.0f, kMost = 15.0f;
 
 // 8 numbers as two bfloat16 terms, the first truncated, the second rounded.
@@ -877,7 +879,7 @@ struct LdsTile {
   uint4 k[TB * W][64];
   uint4 v[TB / 2 * (DIM / 16)][64];          // or values, float16
   float pair[4][NG][TOK];    // keys' steps (times scale log2 e) and low ends, values' steps and low ends
-  uint32_t size[TB][NG];     // greatest magnitude of a record's values, as bits (none finite: above infinity's)
+  __attribute__((aligned(16))) uint32_t note[4];          // of each wave, on its records' values: greatest magnitude as bits, then whether float16 fits
 };
 template <int DIM, int GROUP>
 struct LdsPart {             // 32 tokens of it
@@ -907,9 +909,11 @@ struct LdsPart {             // 32 tokens of it
 // come to registers while the tile before is worked on, and are expanded into
 // the other half of LDS behind it: keys to bfloat16 codes; values, for bfloat16
 // queries, to float16 numbers in a unit that makes the first tile's greatest
-// one 8 to 16.  Should a tile not fit that (an entry past 2^14 units; a record's whole group
-// below 2^-11 units, where float16 runs out of bits; a NaN, which must not meet a
-// weight of 0), the rest is done by the values' codes, as for float32 queries.
+// one 8 to 16.  Should a tile not fit that (a value past 2^14 units; a token's whole group
+// below 2^-9 units though not 0, where its step would run out of float16's bits; a
+// NaN, which must not meet a weight of 0), the rest is done by the values' codes,
+// as for float32 queries.
+constexpr float kHalfMost = 0x1p14f, kHalfLeast = 0x1p-9f;
 template <int DIM, int GROUP, int NQ, bool XF32>
 __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const Kv4Cut cut) {
   typedef LdsTile<DIM, GROUP> Lds;
@@ -971,19 +975,15 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
         }
       }
     };
-    // The greatest magnitude that each group of the wave's record holds, for all to see.
-    auto measure = [&](Lds &d, int t) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const int x = soff + lane + 64 * i;
-        const float step = half_of(sw[i], false), low = half_of(sw[i], true);
-        const float far = __builtin_fmaf(15.0f, step, low);        // a NaN step makes it one
-        uint32_t u = __float_as_uint(far) & 0x7fffffffu;
-        u = u > (__float_as_uint(low) & 0x7fffffffu) ? u : __float_as_uint(low) & 0x7fffffffu;
-        if (TOK * t + 16 * blk + (x & 15) >= kend) u = 0u;         // nobody attends to it
-        u = over_row(u);
-        if (lane + 64 * i < SW && x >= 16 * NG && (x & 15) == 0) d.size[blk][x / 16 % NG] = u;
-      }
+    // Magnitude, as bits, of the greatest value of a group of one token (NaN: above infinity's; of keys
+    // and of tokens that nobody attends to: 0), by the lane that holds its pair.
+    auto size_of = [&](int t, int i) __attribute__((always_inline)) {
+      const int x = soff + lane + 64 * i;
+      const float step = half_of(sw[i], false), low = half_of(sw[i], true);
+      const float far = __builtin_fmaf(15.0f, step, low);          // a NaN step makes it one
+      const uint32_t u = __float_as_uint(far) & 0x7fffffffu, l = __float_as_uint(low) & 0x7fffffffu;
+      const bool counts = lane + 64 * i < SW && x >= 16 * NG && TOK * t + 16 * blk + (x & 15) < kend;
+      return !counts ? 0u : u > l ? u : l;
     };
     // CODES: values as bfloat16 codes, else as float16 numbers.
     auto expand = [&](Lds &d, int t, auto codes) __attribute__((always_inline)) {
@@ -1030,7 +1030,17 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
           d.pair[2 * kv + 1][j][16 * blk + (x & 15)] = half_of(sw[i], true);
         }
       }
-      if constexpr (!CODES) measure(d, t);
+      if constexpr (!CODES) {
+        bool fits = true;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const uint32_t u = size_of(t, i);
+          const float x = __uint_as_float(u) * unit;
+          fits &= u == 0u || (x < kHalfMost && x >= kHalfLeast);
+        }
+        const bool all = __all(fits);
+        if (lane == 0) d.note[wave] = all;
+      }
     };
     constexpr std::integral_constant<bool, true> kCodes{};
     constexpr std::integral_constant<bool, false> kNumbers{};
@@ -1039,12 +1049,23 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
     fetch(t0);
     int t = t0;
     if constexpr (!XF32) {
-      measure(s[0], t0);
-      __syncthreads();
       uint32_t most = 0u;
 #pragma unroll
-      for (int i = 0; i < TB * NG; ++i) {
-        const uint32_t u = s[0].size[i / NG][i % NG];
+      for (int i = 0; i < NS; ++i) {
+        const uint32_t u = size_of(t0, i);
+        most = most > u ? most : u;
+      }
+      most = over_row(most);
+#pragma unroll
+      for (int i = 0; i < 64; i += 16) {
+        const uint32_t u = of_lane(most, i);
+        most = most > u ? most : u;
+      }
+      if (lane == 0) s[1].note[wave] = most;   // that of s[0] is written next
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t u = s[1].note[i];
         most = most > u ? most : u;
       }
       // 2^(130 - e) for the biased exponent e of the greatest, within 2^+-100 (nothing finite, nothing but 0: 1)
@@ -1055,14 +1076,8 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
       __syncthreads();
       for (; t < t1; ++t) {
         const Lds &d = s[(t - t0) & 1];
-        bool fits = true;                    // the same in every wave
-#pragma unroll
-        for (int i = 0; i < TB * NG; ++i) {
-          const uint32_t u = __builtin_amdgcn_readfirstlane(d.size[i / NG][i % NG]);
-          const float x = __uint_as_float(u) * unit;
-          fits &= u == 0u || (x < 0x1p14f && x >= 0x1p-11f);
-        }
-        if (!fits) break;
+        const uint4 fits = *(const uint4 *)d.note;
+        if (!__builtin_amdgcn_readfirstlane(fits.x & fits.y & fits.z & fits.w)) break;   // all waves
         if (t + 1 < t1) fetch(t + 1);
 #pragma unroll
         for (int p = 0; p < TB / 2; ++p) {
@@ -1076,7 +1091,7 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
       }
       rows.leave_half(unit);
     }
-    if (t < t1) {                            // the registers still hold tile t; of what it is in LDS only `size` is read
+    if (t < t1) {                            // the registers still hold tile t; of what it is in LDS only `note` is read
       expand(s[(t - t0) & 1], t, kCodes);
       __syncthreads();
     }

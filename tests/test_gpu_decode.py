@@ -3,9 +3,14 @@ drafted tokens - against the oracle, through the binding.
 
 The cache is compared word for word.  Attention's tolerance, from the arithmetic (see _attention): a
 score's error is at most 2^-23 (dim + 16) of scale sum |q| (|code step| + |low|), plus what rounding
-its power's argument adds, and it enters the weights as a factor; weights of the second product round
-by 2^-8 (bfloat16 q) or not (three terms); sums over the tokens add 2^-23 a term of a lane's chain; a
-bfloat16 output adds 2^-8 of the value.
+its power's argument adds, and it enters the weights as a factor; sums over the tokens add 2^-23 a term of
+a lane's chain; a bfloat16 output adds 2^-8 of the value.  Weights times steps are rounded to three
+bfloat16 terms (float32 q, nothing is lost) or two (bfloat16 q, few rows: 2^-8 of what the first
+leaves, below 2^-15 as it is truncated).  Many rows of bfloat16 have both factors in float16, whose
+rounding is at most 2^-11: a value is code step + low, each of step, low and value rounded once, and a
+group is no smaller than 2^-9 of a unit in which float16's least halves are 2^-25, so 15 codes and two
+roundings more of those are below 2^-12 of the group; a weight moves by 2^-11 of itself or by 2^-25
+beside a greatest one of at least 2^8, and the sum it is divided by moves with it.
 """
 import numpy as np
 import pytest
@@ -180,7 +185,7 @@ def test_nothing_to_append_or_read(slim):
 class Context:
     """A cache with sequences of given lengths on shuffled pages, and their values."""
 
-    def __init__(self, slim, seed, lengths, heads, dim, group, page, dt="bf16", spare=2):
+    def __init__(self, slim, seed, lengths, heads, dim, group, page, dt="bf16", spare=2, values=None):
         rng = np.random.default_rng(seed)
         need = [max(0, -(-n // page)) for n in lengths]
         per = max(1, max(need))
@@ -194,6 +199,8 @@ class Context:
             self.table[i, :need[i]] = order[used:used + need[i]]
             used += need[i]
             k, v = _rows(rng, max(n, 0), heads, dim, dt), _rows(rng, max(n, 0), heads, dim, dt, False)
+            if values is not None:
+                v = torch.from_numpy(values(rng, v.float().numpy())).to(DT[dt])
             at = np.arange(max(n, 0))
             slots = (self.table[i, at // page] * page + at % page).astype(np.int32)
             slim.kv4_append(k.cuda(), v.cuda(), _gpu(slots), self.cache, group)
@@ -203,8 +210,8 @@ class Context:
         self.lengths, self.group, self.page, self.pages = list(lengths), group, page, pages
 
 
-def _attention(ctx, i, q, scale, causal, odt, qdt):
-    """float64 result of sequence i and its tolerance."""
+def _attention(ctx, i, q, scale, causal, odt, qdt, many=True):
+    """float64 result of sequence i and its tolerance; many: rows may be taken by float16."""
     q = oracle.as_f64(_host(q)) if isinstance(q, torch.Tensor) else q
     k, v = ctx.k[i][1].astype(np.float64), ctx.v[i][1].astype(np.float64)
     want = oracle.attention(q, k, v, scale, causal)
@@ -230,12 +237,17 @@ def _attention(ctx, i, q, scale, causal, odt, qdt):
             ds = 2.0 ** -23 * ((dim + 16) * abs(scale) * ((kc + kl)[:reach, hh] @ np.abs(q[a, h])) + 4 * np.abs(s).max() + 8)
             part, whole = p @ vc[:reach, hh], p @ (vc + vl)[:reach, hh]
             chain = 2.0 ** -23 * (reach / 16 + 64)
-            tol[a, h] = (2.0 ** -8 if qdt == "bf16" else 0) * part + (2 * ds.max() + chain) * whole
-    return want, tol + (2.0 ** -8 * np.abs(want) if odt == "bf16" else 0) + 1e-30
+            tol[a, h] = (2.0 ** -15 if qdt == "bf16" else 0) * part + (2 * ds.max() + chain) * whole
+            if qdt == "bf16" and many:
+                x = np.abs(v[:reach, hh])
+                top = np.repeat(x.reshape(reach, -1, g).max(-1), g, -1)
+                lost = 2.0 ** -11 * (vc + vl)[:reach, hh] + 2.0 ** -11 * x + 2.0 ** -12 * top
+                tol[a, h] += p @ lost + (2.0 ** -11 * p + 2.0 ** -33) @ (x + np.abs(want[a, h]))
+    return want, tol + (2.0 ** -8 * np.abs(want) if odt == "bf16" else 0) + 2.0 ** -120
 
 
-def _check(ctx, i, got, q, scale, causal, odt, qdt, what=""):
-    want, tol = _attention(ctx, i, q, scale, causal, odt, qdt)
+def _check(ctx, i, got, q, scale, causal, odt, qdt, what="", many=True):
+    want, tol = _attention(ctx, i, q, scale, causal, odt, qdt, many)
     got = got.double().cpu().numpy()
     worst = np.max(np.abs(got - want) / tol) if got.size else 0.0
     assert worst <= 1, f"{what} sequence {i}: {worst} of the tolerance"
@@ -280,7 +292,7 @@ def test_attention(slim, lengths, n, hq, heads, dim, group, page, qdt, odt, caus
         if length == 0:
             assert not out[i].any()
         else:
-            _check(ctx, i, out[i], q[i], dim ** -0.5, causal, odt, qdt)
+            _check(ctx, i, out[i], q[i], dim ** -0.5, causal, odt, qdt, many=n * hq // heads > 64)
     again = slim.kv4_attention(q.cuda(), ctx.cache, _gpu(ctx.table), _i32(lengths), group, causal=causal,
                                out_dtype=DT[odt])
     assert torch.equal(out, again)
@@ -418,6 +430,76 @@ def test_attention_peaks(slim):
     np.testing.assert_allclose(out[0, 0, 0].cpu().numpy(), ctx.v[0][1].mean(0)[0], atol=1e-4)
     out = slim.kv4_attention(q.cuda(), ctx.cache, _gpu(ctx.table), _i32([600]), 128, scale=-0.3)
     _check(ctx, 0, out[0], q[0], -0.3, True, "f32", "f32")
+
+
+def _scaled(f):
+    """Values whose size goes by the token, as f(rng, n) has it."""
+    return lambda rng, v: (v.astype(np.float64) * f(rng, len(v))[:, None, None]).astype(np.float32)
+
+
+RANGES = {
+    "grow": _scaled(lambda rng, n: 2.0 ** np.linspace(0, 40, n)),         # past the range many times
+    "shrink": _scaled(lambda rng, n: 2.0 ** np.linspace(0, -40, n)),
+    "first": _scaled(lambda rng, n: np.where(np.arange(n) < 3, 2.0 ** 20, 1.0)),
+    "last": _scaled(lambda rng, n: np.where(np.arange(n) > n - 4, 2.0 ** 20, 1.0)),
+    "mixed": _scaled(lambda rng, n: rng.choice([0.0, 1.0, 2.0 ** -6, 2.0 ** -14, 2.0 ** -30], n)),
+    "near": _scaled(lambda rng, n: 2.0 ** rng.uniform(-8, 0, n)),          # small ones, but inside it
+    "tiny": _scaled(lambda rng, n: np.full(n, 2.0 ** -95)),
+    "tinier": _scaled(lambda rng, n: np.full(n, 2.0 ** -110)),             # past what the unit goes to
+    "huge": _scaled(lambda rng, n: np.full(n, 2.0 ** 95)),
+    "constant": lambda rng, v: np.broadcast_to(rng.standard_normal((len(v), 1, 1)), v.shape).astype(np.float32),
+    "offset": lambda rng, v: (100 + 0.5 * v).astype(np.float32),
+    "one group": lambda rng, v: v * np.where(np.arange(v.shape[2]) < 32, np.float32(2.0 ** 18), np.float32(1)),
+}
+
+
+@pytest.mark.parametrize("lengths,n,hq,heads,dim,group", [
+    ([400, 90], 70, 2, 2, 128, 128),
+    ([2500], 90, 2, 1, 64, 32),             # runs joined
+    ([333, 150], 40, 2, 1, 256, 64),
+])
+@pytest.mark.parametrize("what", RANGES)
+def test_attention_many_rows_ranges(slim, what, lengths, n, hq, heads, dim, group):
+    """Values inside and past what float16 holds beside the first ones, for many rows."""
+    ctx = Context(slim, 11, lengths, heads, dim, group, 32, values=RANGES[what])
+    q = 3 * _rows(np.random.default_rng(1), len(lengths) * n, hq, dim, "bf16", False).view(len(lengths), n, hq, dim)
+    for causal in (True, False):
+        out = slim.kv4_attention(q.cuda(), ctx.cache, _gpu(ctx.table), _i32(lengths), group, causal=causal,
+                                 out_dtype=torch.float32)
+        for i in range(len(lengths)):
+            _check(ctx, i, out[i], q[i], dim ** -0.5, causal, "f32", "bf16", f"{what} {causal}")
+
+
+def test_attention_many_rows_of_nothing(slim):
+    """Values of 0 are 0, and so are rows before the first token."""
+    ctx = Context(slim, 12, [100, 20], 2, 64, 64, 16, values=lambda rng, v: 0 * v)
+    q = _rows(np.random.default_rng(1), 180, 4, 64, "bf16", False).view(2, 90, 4, 64).cuda()
+    out = slim.kv4_attention(q, ctx.cache, _gpu(ctx.table), _i32([100, 20]), 64)
+    assert not out.any()
+    ctx = Context(slim, 12, [100, 20], 2, 64, 64, 16)
+    out = slim.kv4_attention(q, ctx.cache, _gpu(ctx.table), _i32([100, 20]), 64)
+    assert not out[1, :70].any()
+    _check(ctx, 1, out[1], q[1].cpu(), 64 ** -0.5, True, "bf16", "bf16")
+
+
+@pytest.mark.parametrize("length,n", [(150, 100), (2000, 70), (70, 70)])
+@pytest.mark.parametrize("where", ["key", "value", "infinite value"])
+def test_attention_many_rows_nan_behind_a_row(slim, length, n, where):
+    ctx = Context(slim, 13, [length], 2, 128, 64, 16)
+    bad = length - n // 2
+    k = torch.from_numpy(ctx.k[0][1][bad:bad + 1]).to(torch.bfloat16).cuda()
+    v = torch.from_numpy(ctx.v[0][1][bad:bad + 1]).to(torch.bfloat16).cuda()
+    (k if where == "key" else v)[0, 1, 70] = float("inf" if where[0] == "i" else "nan")
+    slot = int(ctx.table[0, bad // 16]) * 16 + bad % 16
+    slim.kv4_append(k, v, _i32([slot]), ctx.cache, 64)
+    q = _rows(np.random.default_rng(0), n, 4, 128, "bf16", False).view(1, n, 4, 128)
+    out = slim.kv4_attention(q.cuda(), ctx.cache, _gpu(ctx.table), _i32([length]), 64)[0]
+    first = bad - (length - n)                       # the row whose own token is the bad one
+    spoilt = out[first:, 2:] if where == "key" else out[first:, 2:, 64:]
+    assert torch.isnan(spoilt).all()
+    want, tol = _attention(ctx, 0, q[0], 128 ** -0.5, True, "bf16", "bf16")
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert np.all(err[:first] <= tol[:first])        # no NaN either
 
 
 def test_attention_pages_past_32_bits(slim):
