@@ -99,7 +99,7 @@ __device__ __forceinline__ int ceil_div(int x, int y) {
 // How the work is cut is worked out here, by every wave for itself, from the
 // lengths and bounds on the device (lane l takes consecutive sequences): a
 // tile's tokens go to one workgroup for every `chunk` of them, chunk being
-// the share of all tokens that spreads them over `extra` workgroups.  So
+// a share of all tokens that spreads them over `slots` + `extra` workgroups.  So
 // sequences of uneven lengths end together, no table or copy to the host is
 // needed, and at most slots + extra workgroups are used.  i: number of the run.
 __device__ __forceinline__ Work find_work(const Kv4Args &a, const Kv4Cut &cut, int i) {
@@ -140,25 +140,46 @@ __device__ __forceinline__ Work find_work(const Kv4Args &a, const Kv4Cut &cut, i
     return w;
   }
   int chunk = 1 << 26;
-  if (cuts) {
-    // the sum's rounding is below (per + 6) 2^-24 of it, far inside the factor: the runs stay within `extra`
-    const float share = of_lane(running_sum(work), 63) * (1.01f / (float)cut.extra);
-    chunk = share < (float)cut.least ? cut.least : (int)fminf(share, (float)(1 << 26)) + 1;
-  }
   auto runs_of = [&](int t) __attribute__((always_inline)) { return t <= chunk ? 1 : ceil_div(t, chunk); };
-  int tiles = n0, runs = n0 * runs_of(t0);
+  int tiles = n0;
   for (int x = 1; x < per; ++x) {
     const int s = lane * per + x;
     if (s >= a.b) break;
     int lo, hi;
     bounds(s, lo, hi);
-    bool over;
-    const int n = tiles_of(lo, hi);
-    tiles += n;
-    runs += n * runs_of(cuts ? (length_of(a, s, over) + 31) >> 5 : 0);
+    tiles += tiles_of(lo, hi);
   }
-  const int tsum = running_sum(tiles), rsum = running_sum(runs);
+  const int tsum = running_sum(tiles);
   w.slots = of_lane(tsum, 63);
+  int runs = 0, rsum = 0;
+  auto count = [&]() __attribute__((always_inline)) {
+    runs = n0 * runs_of(t0);
+    for (int x = 1; x < per; ++x) {
+      const int s = lane * per + x;
+      if (s >= a.b) break;
+      int lo, hi;
+      bounds(s, lo, hi);
+      bool over;
+      runs += tiles_of(lo, hi) * runs_of(cuts ? (length_of(a, s, over) + 31) >> 5 : 0);
+    }
+    rsum = running_sum(runs);
+  };
+  if (!cuts) {
+    count();
+  } else {
+    // Every tile's number of runs is rounded up, so spread over `extra` the runs are never too many,
+    // and spread over all of them just enough where the tiles divide evenly: the smallest size of three
+    // that fits (4000 tokens, 512 float32 queries: 309 TFLOP/s, the last alone 239; 3 sequences of up to
+    // 3000: 414 and 362), or the last where a lane has several sequences.  The sum's rounding is
+    // below (per + 6) 2^-24 of it, far inside the factor.
+    const float all = of_lane(running_sum(work), 63) * 1.01f;
+    for (int i = per == 1 ? 2 : 0;; --i) {
+      const float share = all / (float)(cut.extra + (w.slots * i >> 1));
+      chunk = share < (float)cut.least ? cut.least : (int)fminf(share, (float)(1 << 26)) + 1;
+      count();
+      if (i <= 0 || of_lane(rsum, 63) <= cut.slots + cut.extra) break;
+    }
+  }
   const uint64_t past = __ballot(rsum > i);
   if (!past) {
     w.none = true;

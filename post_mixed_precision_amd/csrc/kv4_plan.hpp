@@ -57,11 +57,12 @@ inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t
   p.tiles = (int)((per + p.tm - 1) / p.tm);
   p.slots = (int)(uniform ? b * p.tiles : tq * g / p.tm + (b < tq ? b : tq));
   // Runs enough to fill the card once, by what registers and LDS let a CU hold (16 sequences of up to 8192, g =
-  // 128: 768 runs 35 us, 512 38, 1024 38; 131072 tokens, g = 64: 512 47, 768 50).  Many rows: 512 (2048 tokens of 32
-  // heads: 95 us, 768 102), but where queries are uneven the longest tiles decide (1024 and 657 queries over 4096 and
-  // 657 tokens: 768 147 us, 512 177).  However many tiles there are, one sequence may be far longer than the
+  // 128: 768 runs 35 us, 512 38, 1024 38; 131072 tokens, g = 64: 512 47, 768 50).  Many rows: 512 (one
+  // sequence of 65536 tokens: 438 TFLOP/s, 768 384; 2 of 8192, 256 queries: 568 and 497), but some tiles of `slots`
+  // are idle where queries are uneven (560, 512 and 768 runs, TFLOP/s: 3 sequences of up to 3000 and 500 queries 419,
+  // 362, 402; 8 of up to 2048 and 300 394, 387, 318; 2 of up to 1500 and 900 337, 271, 333).  However many tiles there are, one sequence may be far longer than the
   // others: 256 runs more, unless the table says that none can be.
-  const int64_t want = p.tile ? (uniform ? 512 : 768) : b > 1 && !f32 && p.nq == 1 && group == 128 && dim == 128 ? 768 : 512;
+  const int64_t want = p.tile ? (uniform ? 512 : 560) : b > 1 && !f32 && p.nq == 1 && group == 128 && dim == 128 ? 768 : 512;
   p.least = p.tile && p.slots * hkv >= 256 ? 32 : 8;
   const int64_t units = p.slots * hkv, tokens = (cap + 31) / 32, spare = cap > 2048 ? 256 : 0;
   const int64_t extra = ((want - units > spare ? want - units : spare) + hkv - 1) / hkv;
