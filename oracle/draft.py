@@ -41,13 +41,13 @@ def verify_draft(target, tokens, uniform, draft=None, temperature: float = 1.0):
                 break
             px, qx = (p[x], q[x]) if x < v else (0.0, 0.0)
             bar = float(uniform[i, j]) * qx
-            if x < v:
+            if x < v and (px or bar):            # two powers of 0 are that exactly, on either side
                 margin[i] = min(margin[i], abs(bar - px) / max(px, bar, 1e-300))
             if bar < px:
                 ids[i, j] = x
                 j += 1
                 continue
-            mass = np.maximum(p - q, 0.0)
+            mass = np.where(p - q > 2.0 ** -44 * p, p - q, 0.0)
             break
         accepted[i] = j
         if mass is None or not mass.sum() > 0:

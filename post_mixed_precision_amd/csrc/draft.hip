@@ -2,19 +2,21 @@
 //
 //   p_j = softmax(target[j] / T), q_j = softmax(draft[j] / T)   (no draft: q_j is 1 at the drafted token)
 //   token x_j is taken while u_j q_j(x_j) < p_j(x_j);  at the first that is not, the next token is drawn from
-//   max(p_j - q_j, 0), after the last from p:  the first entry whose running sum exceeds u_k times the whole.
+//   max(p_j - q_j, 0) (0 up to 2^-44 p_j), after the last from p:  the first entry whose running sum exceeds u_k times the whole.
 //
 // The drawn token is an index: with 10^5 entries a running sum moves by 10^-5
 // an entry and less, so float32 sums (off by 10^-7 and more) would draw a
 // neighbour once in a hundred.  Powers, sums and comparisons are float64
 // throughout; the index is then a function of the inputs but for borders
-// nearer than 10^-15.
+// nearer than 10^-13.
 //
 // Three launches: statistics of every row by segments, then the decision and
 // the segment masses of the row to draw from, then the segment and the entry.
-// The first one reads all logits once and forms a float64 power of each (15
-// float64 instructions, which run at the rate of float32's here): for bfloat16
-// logits the two take about as long.
+// The first one reads all logits once and forms a float64 power of each (17
+// vector instructions, 9 of them float64, which run at the rate of float32's
+// here): 352 rows of 131072 bfloat16 logits take 37 us, their loads alone 23.  Segments twice as long
+// took as long, half as long 41 us, and so did workgroups that go on to the next
+// segment with its loads in flight (46); all but the powers' work: 41 with six instructions more a power.
 #include "common.hpp"
 #include "serve.hpp"
 #include "slim.h"
@@ -45,26 +47,46 @@ __device__ __forceinline__ double exp2_64(double t) {
   return __builtin_ldexp(p, (int)n);
 }
 
-// 2^(t / 64) with a table of 2^(i / 64): the rest |g| <= 1/2 of 1/64 needs the Taylor series to the fifth power
-// only (its rest is below 2^-54).  Half the work of exp2_64 where there is a logit after the other.
-__device__ __forceinline__ double exp2_64th(double t, const double (&table)[64]) {
-  constexpr double L = 0.69314718055994530942 / 64.0;
-  t = fmax(t, -70400.0);
-  const double n = __builtin_rint(t), g = t - n;
-  const int i = (int)n;
-  double p = L * L * L * L * L / 120.0;
-  p = __builtin_fma(p, g, L * L * L * L / 24.0);
-  p = __builtin_fma(p, g, L * L * L / 6.0);
-  p = __builtin_fma(p, g, L * L / 2.0);
-  p = __builtin_fma(p, g, L);
-  const double s = table[i & 63];
-  return __builtin_ldexp(__builtin_fma(p * g, s, s), i >> 6);
+// 2^(t / 256) for t = n + g, n whole, |g| <= 1/2, from a table of 2^(i / 256): the polynomial that meets
+// (2^(g / 256) - 1) / g at the 3 Chebyshev points of [-1/2, 1/2] is off by 3.5e-14 at most.  n is the low
+// word of kMagic + t; added to an entry's high word 12 bits up it sets the
+// exponent (n >= -1022 * 256), its own low 8 bits being taken off in the table.
+constexpr double kMagic = 0x1.8p52, kLowest = -1020.0 * 256.0;
+typedef double PowTable[256];
+__device__ __forceinline__ void make_table(PowTable &table) {   // by 256 threads, seen after the next barrier
+  uint2 w = __builtin_bit_cast(uint2, exp2_64(threadIdx.x * (1.0 / 256.0)));
+  w.y -= threadIdx.x << 12;
+  table[threadIdx.x] = __builtin_bit_cast(double, w);
+}
+__device__ __forceinline__ double exp2_256th(double magic_t, double g, const PowTable &table) {
+  const uint32_t i = (uint32_t)__double2loint(magic_t);
+  double p = 0x1.c6b08f7c960adp-29;
+  p = __builtin_fma(p, g, 0x1.ebfbe3a9ac80bp-19);
+  p = __builtin_fma(p, g, 0x1.62e42fefa39efp-9);
+  uint2 w = __builtin_bit_cast(uint2, table[i & 255]);
+  asm("v_lshl_add_u32 %0, %1, 12, %2" : "=v"(w.y) : "v"(i), "v"(w.y));   // else three instructions of 64 bits
+  const double s = __builtin_bit_cast(double, w);
+  return __builtin_fma(p * g, s, s);
+}
+// 2^(t / 256), 0 below 2^-1020 and for NaN.
+__device__ __forceinline__ double exp2_256th(double t, const PowTable &table) {
+  const double u = fmax(t, kLowest), y = u + kMagic, z = exp2_256th(y, u - (y - kMagic), table);
+  return t > kLowest ? z : 0.0;
+}
+// max(x, y) for a y that is a number; fmaxf also makes a signalling x quiet, by an instruction of its own.
+__device__ __forceinline__ float at_least(float x, float y) {
+  float z;
+  asm("v_max_f32 %0, %1, %2" : "=v"(z) : "v"(x), "v"(y));
+  return z;
 }
 
 template <bool BF16>
 __device__ __forceinline__ float logit(const void *p, int64_t at) {
   return BF16 ? bf16_bits_to_f32(((const uint16_t *)p)[at]) : ((const float *)p)[at];
 }
+
+// What a logit's difference to its row's maximum is multiplied by (finite: 0 stays 0).
+__device__ __forceinline__ double power_of(const DraftArgs &a) { return fmin(kLog2e / a.temperature, 1e300); }
 
 __device__ __forceinline__ double wave_sum(double v) { return group_sum<64>(v); }
 
@@ -86,8 +108,9 @@ template <bool BF16, int PIECES>
 __global__ __launch_bounds__(256) void draft_stats_kernel(const DraftArgs a, const int nseg, double2 *__restrict__ st) {
   constexpr int PER = BF16 ? 8 : 4, SIZE = BF16 ? 2 : 4;
   __shared__ float s_m[4];
-  __shared__ double s_z[4], s_pow[64];
-  if (threadIdx.x < 64) s_pow[threadIdx.x] = exp2_64(threadIdx.x * (1.0 / 64.0));   // seen after the next barrier
+  __shared__ double s_z[4];
+  __shared__ PowTable s_pow;
+  make_table(s_pow);
   const unsigned nr = a.draft ? 2 * a.k + 1 : a.k + 1;
   const unsigned row = blockIdx.x / (unsigned)nseg, seq = row / nr;
   const int s = (int)(blockIdx.x - row * nseg);
@@ -144,12 +167,28 @@ __global__ __launch_bounds__(256) void draft_stats_kernel(const DraftArgs a, con
   if ((threadIdx.x & 63) == 0) s_m[wave] = m;
   __syncthreads();
   m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const double c = 64.0 * kLog2e / a.temperature, shift = m == -__builtin_inff() || bad ? 0.0 : -(double)m * c;
+  const double c = 256.0 * power_of(a), md = m == -__builtin_inff() || bad ? 0.0 : (double)m;
   double z = 0.0;
+  const double whole = __builtin_rint(-md * c), low = md + kLowest / c;
+  if (fabs(whole) < 0x1p45 && low > -0x1p127) {
+    // about a whole number `whole` near -m c: fma(x, c, kMagic + whole) is then n in the low word, and g takes
+    // one more; entries below `low`, -inf too, become 2^-1020, beside a sum of 1 and more
+    const float least = (float)low;
+    const double base = kMagic + whole;
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i)
+    for (int i = 0; i < PIECES; ++i)
 #pragma unroll
-    for (int e = 0; e < PER; ++e) z += exp2_64th(__builtin_fma((double)x[i][e], c, shift), s_pow);
+      for (int e = 0; e < PER; ++e) {
+        const double xd = (double)at_least(x[i][e], least), y = __builtin_fma(xd, c, base);
+        z += exp2_256th(y, __builtin_fma(xd, c, base - y), s_pow);
+      }
+    z *= exp2_64(__builtin_fma(md, -c, -whole) * (1.0 / 256.0));
+  } else {                                                 // logits of 10^11 (of the type's lowest, say): x - m first
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int e = 0; e < PER; ++e) z += exp2_256th(((double)x[i][e] - md) * c, s_pow);
+  }
   if (bad) z = __builtin_nan("");
   z = wave_sum(z);
   if ((threadIdx.x & 63) == 0) s_z[wave] = z;
@@ -160,21 +199,23 @@ __global__ __launch_bounds__(256) void draft_stats_kernel(const DraftArgs a, con
 // What is drawn from: p, or max(p - q, 0) with q of the draft's row or 1 at `token`.
 struct Mass {
   int64_t token;             // of a draft without probabilities, else -1
-  double c, tm, tz, dm, dz;  // log2 e / T; the rows' shifts and reciprocal sums
+  double c, tm, tz, dm, dz;  // 256 log2 e / T; the rows' maxima and reciprocal sums
   int taken, minus;
   int64_t pad;
 };
 // Of entry v with logits x (target) and y (draft; any number if there is none).
-__device__ __forceinline__ double mass_of(const Mass &m, float x, float y, int64_t v) {
-  const double p = exp2_64(__builtin_fma((double)x, m.c, m.tm)) * m.tz;
+__device__ __forceinline__ double mass_of(const Mass &m, float x, float y, int64_t v, const PowTable &table) {
+  const double p = exp2_256th(((double)x - m.tm) * m.c, table) * m.tz;
   if (!m.minus) return p;
   if (m.token >= 0) return v == m.token ? 0.0 : p;
-  return fmax(p - exp2_64(__builtin_fma((double)y, m.c, m.dm)) * m.dz, 0.0);
+  // the rows' sums differ in their last bits even for equal rows (their grids differ), and of those nothing is drawn
+  const double d = p - exp2_256th(((double)y - m.dm) * m.c, table) * m.dz;
+  return d > 0x1p-44 * p ? d : 0.0;
 }
 // The masses of 8 entries first, first + STEP, ...; 0 from `end` on.  All loads before the first power.
 template <bool BF16, int STEP>
 __device__ __forceinline__ void masses(const DraftArgs &a, int64_t seq, const Mass &m, int64_t first, int64_t end,
-                                       double (&z)[8]) {
+                                       const PowTable &table, double (&z)[8]) {
   const RowOf t = row_of(a, seq, m.taken), d = m.minus && a.draft ? row_of(a, seq, a.k + 1 + m.taken) : t;
   float x[8], y[8];
 #pragma unroll
@@ -186,7 +227,7 @@ __device__ __forceinline__ void masses(const DraftArgs &a, int64_t seq, const Ma
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int64_t v = first + STEP * e;
-    z[e] = v < end ? mass_of(m, x[e], y[e], v) : 0.0;
+    z[e] = v < end ? mass_of(m, x[e], y[e], v, table) : 0.0;
   }
 }
 
@@ -196,7 +237,7 @@ template <bool BF16>
 __device__ __forceinline__ Mass decide(const DraftArgs &a, int64_t seq, const double2 *st, int nseg,
                                        double2 (&s_row)[2 * SLIM_DRAFT_MAX_K + 1]) {
   const int nr = a.draft ? 2 * a.k + 1 : a.k + 1, lane = threadIdx.x & 63;
-  const double c = kLog2e / a.temperature;
+  const double c = power_of(a);        // a power's argument is (x - m) c: exact where x is m, however large
   const int64_t x = lane < a.k ? a.tokens[seq * a.k + lane] : -1;
   const float u = lane < a.k ? a.uniform[seq * (a.k + 1) + lane] : 0.0f;
   float tx = 0.0f, dx = 0.0f;                    // asked for here, needed after the rows
@@ -217,19 +258,19 @@ __device__ __forceinline__ Mass decide(const DraftArgs &a, int64_t seq, const do
       for (int s = 16 + l; s < nseg; s += 16) m = fmax(m, p[s].x);
 #pragma unroll
       for (int x = 1; x < 16; x <<= 1) m = fmax(m, __shfl_xor(m, x, 64));
-      const double shift = m == kNegInf ? 0.0 : -m * c;
-      double z = f.y * exp2_64(__builtin_fma(f.x, c, shift));
-      for (int s = 16 + l; s < nseg; s += 16) z += p[s].y * exp2_64(__builtin_fma(p[s].x, c, shift));
+      if (m == kNegInf) m = 0.0;
+      double z = f.y * exp2_64((f.x - m) * c);
+      for (int s = 16 + l; s < nseg; s += 16) z += p[s].y * exp2_64((p[s].x - m) * c);
       z = group_sum<16>(z);
-      if (l == 0) s_row[j] = make_double2(shift, 1.0 / z);   // nothing but -inf: 1 / 0, and 0 * inf is a NaN below
+      if (l == 0) s_row[j] = make_double2(m, 1.0 / z);   // nothing but -inf: 1 / 0, and 0 * inf is a NaN below
     }
   }
   __syncthreads();
   bool good = false;
   if (x >= 0 && x < a.v) {                       // lanes below k
-    const double p = exp2_64(__builtin_fma((double)tx, c, s_row[lane].x)) * s_row[lane].y;
+    const double p = exp2_64(((double)tx - s_row[lane].x) * c) * s_row[lane].y;
     double q = 1.0;
-    if (a.draft) q = exp2_64(__builtin_fma((double)dx, c, s_row[a.k + 1 + lane].x)) * s_row[a.k + 1 + lane].y;
+    if (a.draft) q = exp2_64(((double)dx - s_row[a.k + 1 + lane].x) * c) * s_row[a.k + 1 + lane].y;
     good = (double)u * q < p;
   }
   const uint64_t no = ~__ballot(good);           // lanes from k on are in it
@@ -239,7 +280,7 @@ __device__ __forceinline__ Mass decide(const DraftArgs &a, int64_t seq, const do
   const int64_t refused = __shfl(x, j, 64);      // lane k: -1
   m.minus = refused >= 0;
   m.token = m.minus && !a.draft ? refused : -1;
-  m.c = c, m.tm = s_row[j].x, m.tz = s_row[j].y;
+  m.c = 256.0 * c, m.tm = s_row[j].x, m.tz = s_row[j].y;
   if (m.minus && a.draft) m.dm = s_row[a.k + 1 + j].x, m.dz = s_row[a.k + 1 + j].y;
   return m;
 }
@@ -253,13 +294,15 @@ __global__ __launch_bounds__(256) void draft_mass_kernel(const DraftArgs a, cons
                                                          double *__restrict__ mass, Mass *__restrict__ drawn) {
   __shared__ double2 s_row[2 * SLIM_DRAFT_MAX_K + 1];
   __shared__ double s_z[2][4];
+  __shared__ PowTable s_pow;
+  make_table(s_pow);
   const unsigned per = (unsigned)(runs + each - 1) / (unsigned)each, seq = blockIdx.x / per;
   const int s0 = (int)(blockIdx.x - seq * per) * each, s1 = s0 + each < runs ? s0 + each : runs;
   const Mass m = decide<BF16>(a, seq, st, nseg, s_row);
   if (s0 == 0 && threadIdx.x == 0) drawn[seq] = m;
   for (int s = s0; s < s1; ++s) {
     double x[8];
-    masses<BF16, 256>(a, seq, m, (int64_t)s * kRun + threadIdx.x, a.v, x);
+    masses<BF16, 256>(a, seq, m, (int64_t)s * kRun + threadIdx.x, a.v, s_pow, x);
     const double z = wave_sum(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
     if ((threadIdx.x & 63) == 0) s_z[s & 1][threadIdx.x >> 6] = z;
     __syncthreads();                             // one a run: the next run's sums go to the other half
@@ -283,9 +326,12 @@ __global__ __launch_bounds__(256) void draft_pick_kernel(const DraftArgs a, cons
                                                          const double *__restrict__ mass,
                                                          const Mass *__restrict__ drawn) {
   __shared__ double s_z[4];
+  __shared__ PowTable s_pow;
   __shared__ int s_hit[4], s_last[4];
   const int64_t seq = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  make_table(s_pow);
+  __syncthreads();
   const Mass m = drawn[seq];
   const double *ms = mass + seq * runs;
   // every wave finds the run: the first whose running mass exceeds what is wanted (with a uniform of 1 or
@@ -314,7 +360,7 @@ __global__ __launch_bounds__(256) void draft_pick_kernel(const DraftArgs a, cons
   int64_t pick = -1;
   if (hs >= 0) {                                 // the same in every wave
     double x[8], sum = 0.0;
-    masses<BF16, 1>(a, seq, m, (int64_t)hs * kRun + 8 * tid, a.v, x);
+    masses<BF16, 1>(a, seq, m, (int64_t)hs * kRun + 8 * tid, a.v, s_pow, x);
     int lastpos = -1;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {

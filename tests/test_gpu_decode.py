@@ -549,6 +549,32 @@ def _verify(slim, target, tokens, uniform, draft, temperature=1.0):
     return acc, ids
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("temperature", [1.0, 1e-300, 1e300, 1e36])
+@pytest.mark.parametrize("v", [700, 9001])
+def test_draft_extreme_logits(slim, dt, draft, temperature, v):
+    """Masks of the type's lowest value, whole rows of it, logits of 10^30, temperatures near 0 and infinity."""
+    rng = np.random.default_rng(v)
+    low = float(torch.finfo(DT[dt]).min)
+    b, k = 7, 2
+    t = 3 * rng.standard_normal((b, k + 1, v))
+    t[0] = low
+    t[1][:, ::2] = low
+    t[2] *= 1e30
+    t[3][:, 7:] = -np.inf
+    t[4] = np.where(rng.random(t[4].shape) < 0.5, 1e20, 0.99e20)
+    t[5][:, :v // 2] = -np.inf
+    t[5][:, v // 2:] = low
+    t[6][:, v - 3:] = 50.0
+    d = t[[6, 1, 2, 3, 0, 4, 5], :k] + 0.0
+    target, dr = torch.from_numpy(t).to(DT[dt]), torch.from_numpy(d).to(DT[dt])
+    tokens = rng.integers(0, v, (b, k))
+    tokens[3], tokens[6, 0] = 3, v - 1
+    u = rng.random((b, k + 1)).astype(np.float32)
+    _verify(slim, target, tokens, u, dr if draft else None, temperature)
+
+
 DRAFTS = [
     (1, 1, 1, "f32", True, 0, 1.0),
     (1, 4, 1000, "f32", True, 0, 1.0),
