@@ -593,7 +593,7 @@ int slim_kv4_read(const int32_t *slots, int64_t t, const uint32_t *cache, int64_
  * ---------------------------------------------------------------------- */
 #define SLIM_KV4_MAX_SEQS 4096
 size_t slim_kv4_attention_workspace(int64_t b, int64_t tq, int uneven, int64_t hq, int64_t heads, int dim, int group,
-                                    int64_t per, int page, int qdt);
+                                    int64_t per, int page, int qdt, int odt);
 int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uint32_t *cache, int64_t pages, int page,
                        int64_t heads, int dim, int group, const int32_t *table, int64_t b, int64_t per,
                        const int32_t *lengths, const int32_t *offsets, double scale, int causal, void *out, int odt,

@@ -82,7 +82,7 @@ _SIGS = {
     "slim_kv4_read": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_int,
                                _c_vp]),
     "slim_kv4_attention_workspace": (_c_sz, [_c_i64, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _c_int, _c_i64, _c_int,
-                                              _c_int]),
+                                              _c_int, _c_int]),
     "slim_kv4_attention": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_int, _c_int,
                                     _c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_dbl, _c_int, _c_vp, _c_int, _c_vp, _c_sz,
                                     _c_vp]),
@@ -942,7 +942,7 @@ def _attention_plan(q, cache, table, lengths, offsets, group, out_dtype, out):
         _want("out", *out, tuple(q[0]), (out_dtype,))
     qcode, ocode = _out_code(q[1]), _out_code(out_dtype)
     need = load_library().slim_kv4_attention_workspace(b, tq, 0 if offsets is None else 1, hq, heads, dim, group, per,
-                                                       page, qcode)
+                                                       page, qcode, ocode)
     return qcode, tq, hq, pages, page, heads, dim, b, per, ocode, out_dtype, need
 
 

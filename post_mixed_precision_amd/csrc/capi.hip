@@ -524,9 +524,11 @@ static bool kv4_attention_shape(int64_t b, int64_t tq, bool uneven, int64_t hq, 
 }
 
 size_t slim_kv4_attention_workspace(int64_t b, int64_t tq, int uneven, int64_t hq, int64_t heads, int dim, int group,
-                                    int64_t per, int page, int qdt) {
-  if (!valid_dtype(qdt) || !valid_group(group) || group > dim || !kv4_attention_shape(b, tq, uneven != 0, hq, heads, dim, per, page) || tq == 0) return 0;
-  return slim::kv4_plan(b, tq, !uneven, hq, heads, dim, group, per * page, qdt == SLIM_F32).ws_bytes;
+                                    int64_t per, int page, int qdt, int odt) {
+  if (!valid_dtype(qdt) || !valid_dtype(odt) || !valid_group(group) || group > dim ||
+      !kv4_attention_shape(b, tq, uneven != 0, hq, heads, dim, per, page) || tq == 0)
+    return 0;
+  return slim::kv4_plan(b, tq, !uneven, hq, heads, dim, group, per * page, qdt == SLIM_F32 || odt == SLIM_F32).ws_bytes;
 }
 
 int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uint32_t *cache, int64_t pages, int page,
@@ -540,7 +542,8 @@ int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uin
   if (!isfinite(scale) || !isfinite((float)scale)) return SLIM_E_PARAM;
   if (!q || !cache || !table || !lengths || !out) return SLIM_E_NULL;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return SLIM_E_ALIGN;
-  const slim::Kv4Plan p = slim::kv4_plan(b, tq, !offsets, hq, heads, dim, group, per * page, qdt == SLIM_F32);
+  const slim::Kv4Plan p = slim::kv4_plan(b, tq, !offsets, hq, heads, dim, group, per * page,
+                                          qdt == SLIM_F32 || odt == SLIM_F32);
   if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes)) return SLIM_E_WORKSPACE;
   if (p.ws_bytes > 0 && !aligned16(ws)) return SLIM_E_ALIGN;
   slim::Kv4Args a = {};

@@ -8,7 +8,7 @@
 //   o[r, c] = sum_t (P[r, t] step[t, j]) code[t, c] + sum_t P[r, t] low[t, j],
 // where the products with codes go to the matrix cores and the rest is float32:
 // nothing is dequantized.  P step is the one thing that is rounded: to two
-// bfloat16 terms where q is bfloat16, to three where q and P step are float32.
+// bfloat16 terms where q and the output are bfloat16, to three elsewhere.
 // For many rows of bfloat16 the second product is one of float16 weights with
 // float16 values instead, wherever the values' range allows that.
 //
@@ -275,7 +275,8 @@ __device__ __forceinline__ int64_t row_at(const Kv4Args &a, const K &k, int h, i
 //
 // Few rows: weights times steps are rounded to the sum of two bfloat16 terms
 // (2^-16): with one term (2^-9) the outputs' error was twice that of their own
-// rounding to bfloat16.  Float32 queries and weights enter as three terms.
+// rounding to bfloat16.  Weights of float32
+// outputs, and float32 queries and their weights, enter as three terms.
 //
 // Many rows of bfloat16: values are dequantized after all, once for the
 // workgroup, to float16 (step, low end and value each within 2^-11 of themselves), and
@@ -284,6 +285,8 @@ __device__ __forceinline__ int64_t row_at(const Kv4Args &a, const K &k, int h, i
 // matrix instructions and six vector instructions more a weight: 8 sequences
 // of 4096, causal, 32 + 8 heads of 128, took 1702 us by them, 1548 us so.
 constexpr float kLift = 8.0f, kMost = 15.0f;
+// What rows are held by: bfloat16 queries and outputs, bfloat16 queries with float32 outputs, float32 queries.
+constexpr int kBf16 = 0, kMixed = 1, kF32 = 2;
 
 // 8 numbers as two bfloat16 terms, the first truncated, the second rounded.
 __device__ __forceinline__ void split2(const float (&x)[8], uint4 (&t)[2]) {
@@ -304,9 +307,9 @@ __device__ __forceinline__ uint32_t pk_half(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_t));
 }
 
-template <int DIM, int GROUP, int NQ, bool XF32>
+template <int DIM, int GROUP, int NQ, int X>
 struct Rows {
-  static constexpr int NG = DIM / GROUP, W = DIM / 32, GS = GROUP / 32, NTQ = XF32 ? 3 : 1, NTP = XF32 ? 3 : 2;
+  static constexpr int NG = DIM / GROUP, W = DIM / 32, GS = GROUP / 32, NTQ = X == kF32 ? 3 : 1, NTP = X == kBf16 ? 2 : 3;
   uint4 qf[NQ][W][NTQ];      // the rows' queries as operands
   float qs[NQ][NG];          // their sums over each group, times scale log2 e
   int lim[NQ];               // tokens a row attends to
@@ -329,7 +332,7 @@ struct Rows {
       for (int j = 0; j < NG; ++j) qs[n][j] = pl[n][j] = 0.0f;
 #pragma unroll
       for (int j = 0; j < W; ++j) {
-        if constexpr (XF32) {
+        if constexpr (X == kF32) {
           const float4 *p = (const float4 *)((const float *)a.q + at + 32 * j);
           float4 u = p[0], w = p[1];
           if (!real) u = w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -444,7 +447,7 @@ struct Rows {
           if (EDGE && tok + 16 * (e >> 2) + (e & 3) >= lim[n]) y[e] = z = 0.0f;   // NaN pairs of masked tokens
           pl[n][j] = __builtin_fmaf(x[n][e], z, pl[n][j]);
         }
-        if constexpr (XF32)
+        if constexpr (X != kBf16)
           split3(make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])),
                  make_uint4(__float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]), __float_as_uint(y[7])),
                  pf[n]);
@@ -763,12 +766,12 @@ __device__ __forceinline__ int share_of(int all, int i, int n) {
 // Few rows: every wave streams its own run of tokens for the same 16 NQ rows,
 // its records a tile ahead, straight to LDS (in registers they would leave
 // room for half the waves); the waves' sums meet in LDS.
-template <int DIM, int NQ, bool XF32>
+template <int DIM, int NQ, int X>
 constexpr int stream_waves() {   // of a SIMD: what the registers allow
-  return XF32 ? (DIM == 64 ? 3 : DIM == 128 ? 2 : 1) : DIM == 64 ? (NQ == 1 ? 4 : 2) : DIM == 128 && NQ == 1 ? 3 : 2;
+  return X == kF32 ? (DIM == 64 ? 3 : DIM == 128 ? 2 : 1) : DIM == 64 ? (NQ == 1 ? 4 : 2) : DIM == 128 && NQ == 1 ? 3 : 2;
 }
-template <int DIM, int GROUP, int NQ, bool XF32>
-__global__ __launch_bounds__(256, (stream_waves<DIM, NQ, XF32>())) void kv4_stream_kernel(const Kv4Args a, const Kv4Cut cut) {
+template <int DIM, int GROUP, int NQ, int X>
+__global__ __launch_bounds__(256, (stream_waves<DIM, NQ, X>())) void kv4_stream_kernel(const Kv4Args a, const Kv4Cut cut) {
   typedef Ring<DIM, GROUP> R;
   constexpr int TM = 16 * NQ, W = DIM / 32, LDO = DIM + 4, ST = R::STAGES;
   union Lds {
@@ -818,7 +821,7 @@ __global__ __launch_bounds__(256, (stream_waves<DIM, NQ, XF32>())) void kv4_stre
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) fetch(t0 + i, i);
   }
-  Rows<DIM, GROUP, NQ, XF32> rows;
+  Rows<DIM, GROUP, NQ, X> rows;
   rows.start(a, k, h, m0, rows_all, c);
   if (t0 < t1) {
     RingTile<DIM, GROUP> src;
@@ -929,13 +932,13 @@ struct LdsPart {             // 32 tokens of it
 // Many rows: four waves of 16 NQ rows each share the tokens.  A tile's codes
 // come to registers while the tile before is worked on, and are expanded into
 // the other half of LDS behind it: keys to bfloat16 codes; values, for bfloat16
-// queries, to float16 numbers in a unit that makes the first tile's greatest
+// queries and outputs, to float16 numbers in a unit that makes the first tile's greatest
 // one 8 to 16.  Should a tile not fit that (a value past 2^14 units; a token's whole group
 // below 2^-9 units though not 0, where its step would run out of float16's bits; a
 // NaN, which must not meet a weight of 0), the rest is done by the values' codes,
 // as for float32 queries.
 constexpr float kHalfMost = 0x1p14f, kHalfLeast = 0x1p-9f;
-template <int DIM, int GROUP, int NQ, bool XF32>
+template <int DIM, int GROUP, int NQ, int X>
 __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const Kv4Cut cut) {
   typedef LdsTile<DIM, GROUP> Lds;
   constexpr int NG = Lds::NG, W = Lds::W, TB = Lds::TB, TOK = Lds::TOK, TM = 64 * NQ, REC = 4 * DIM + 32 * NG;
@@ -958,7 +961,7 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
   const int last = m0 + TM < rows_all ? m0 + TM : rows_all;              // past the workgroup's last row
   const int w0 = m0 + 16 * NQ * wave, w1 = w0 + 16 * NQ < last ? w0 + 16 * NQ : last;
   const float c = a.scale * 1.44269504088896340736f;
-  Rows<DIM, GROUP, NQ, XF32> rows;
+  Rows<DIM, GROUP, NQ, X> rows;
   rows.start(a, k, h, w0, rows_all, c);
 
   auto limit = [&](int m) __attribute__((always_inline)) {
@@ -974,7 +977,7 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
     const int soff = TB == 4 ? 0 : 16 * NG * (wave & 1);
     constexpr int GS = GROUP / 32, NV = WPW > GS ? WPW / GS : 1;   // groups of the words that a wave expands
     uint32_t kw[WPW], vw[WPW], sw[NS];
-    uint4 vp[XF32 ? 1 : NV];                 // their pairs of this lane's four tokens
+    uint4 vp[X == kBf16 ? NV : 1];                 // their pairs of this lane's four tokens
     float unit = 1.0f;
     auto fetch = [&](int t) __attribute__((always_inline)) {
       if (TB * t - pg.base >= 64) pg.load(TB * t);
@@ -988,7 +991,7 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
         sw[i] = x < SW ? p[4 * DIM + soff + x] : 0u;
         if (page < 0) sw[i] = 0x7fc0u;
       }
-      if constexpr (!XF32) {
+      if constexpr (X == kBf16) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           vp[i] = *(const uint4 *)(p + 4 * DIM + 16 * NG + 16 * (off / GS + i) + 4 * lg);
@@ -1069,7 +1072,7 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
     pg.load(TB * t0);
     fetch(t0);
     int t = t0;
-    if constexpr (!XF32) {
+    if constexpr (X == kBf16) {
       uint32_t most = 0u;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
@@ -1119,12 +1122,12 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
     for (; t < t1; ++t) {
       const Lds &d = s[(t - t0) & 1];
       if (t + 1 < t1) fetch(t + 1);
-      constexpr int U = XF32 ? TB / 2 : 1;
+      constexpr int U = X == kBf16 ? 1 : TB / 2;
 #pragma unroll U
       for (int p = 0; p < TB / 2; ++p) {
         const int first = t * TOK + 32 * p;
         LdsPart<DIM, GROUP> src = {d, p};
-        if (XF32 && first + 32 <= wall) rows.template attend<false>(src, first);
+        if (X != kBf16 && first + 32 <= wall) rows.template attend<false>(src, first);
         else if (first < wend) rows.template attend<true>(src, first);
       }
       if (t + 1 < t1) expand(s[(t + 1 - t0) & 1], t + 1, kCodes);
@@ -1290,14 +1293,17 @@ hipError_t launch_group(const Kv4Args &a, const Kv4Cut &cut, const Kv4Plan &p, h
   constexpr bool WIDE = DIM < 256;      // as kv4_plan has it
   const unsigned grid = (unsigned)((int64_t)(p.slots + p.extra) * a.hkv);
 #define RUN(KERNEL, NQ, X) KERNEL<DIM, GROUP, NQ, X><<<grid, 256, 0, st>>>(a, cut)
+  const bool mixed = a.qbf16 && !a.obf16;
   if (p.tile) {
-    if (!a.qbf16) RUN(kv4_tile_kernel, 1, true);
-    else if constexpr (WIDE && DIM / GROUP < 4) RUN(kv4_tile_kernel, 2, false);
-    else RUN(kv4_tile_kernel, 1, false);
+    if (!a.qbf16) RUN(kv4_tile_kernel, 1, kF32);
+    else if (mixed) RUN(kv4_tile_kernel, 1, kMixed);
+    else if constexpr (WIDE && DIM / GROUP < 4) RUN(kv4_tile_kernel, 2, kBf16);
+    else RUN(kv4_tile_kernel, 1, kBf16);
   } else {
-    if (!a.qbf16) RUN(kv4_stream_kernel, 1, true);
-    else if (p.nq == 1) RUN(kv4_stream_kernel, 1, false);
-    else if constexpr (WIDE) RUN(kv4_stream_kernel, 2, false);
+    if (!a.qbf16) RUN(kv4_stream_kernel, 1, kF32);
+    else if (mixed) RUN(kv4_stream_kernel, 1, kMixed);
+    else if (p.nq == 1) RUN(kv4_stream_kernel, 1, kBf16);
+    else if constexpr (WIDE) RUN(kv4_stream_kernel, 2, kBf16);
     else return hipErrorInvalidValue;
   }
 #undef RUN

@@ -41,7 +41,7 @@ struct Kv4Plan {
 };
 
 // b sequences, tq query tokens in all (uniform: tq / b each), cap: the tokens
-// a row of the page table can name.
+// a row of the page table can name; f32: queries or outputs are float32.
 inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t hkv, int dim, int group, int64_t cap,
                         bool f32) {
   Kv4Plan p;

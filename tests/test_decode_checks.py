@@ -93,19 +93,19 @@ def test_attention_abi(lib):
     assert call(scale=float("nan")) == -4 and call(scale=float("inf")) == -4 and call(scale=1e300) == -4
     assert call(q=ODD) == -7 and call(cache=ODD) == -7 and call(out=ODD) == -7
     assert call(tq=0, q=None, out=None) == 0
-    need = lib.slim_kv4_attention_workspace(4, 4, 0, 8, 4, 64, 32, 1000, 16, 1)
+    need = lib.slim_kv4_attention_workspace(4, 4, 0, 8, 4, 64, 32, 1000, 16, 1, 1)
     assert need > 0
     assert call(wsb=need - 1) == -5 and call(ws=None) == -5 and call(ws=ODD) == -7
-    assert lib.slim_kv4_attention_workspace(4, 5, 0, 8, 4, 64, 32, 1000, 16, 1) == 0
-    assert lib.slim_kv4_attention_workspace(4, 4, 0, 8, 4, 64, 128, 1000, 16, 1) == 0
-    assert lib.slim_kv4_attention_workspace(4, 4, 0, 8, 4, 64, 32, 1, 16, 1) == 0      # 16 tokens: nothing to join
+    assert lib.slim_kv4_attention_workspace(4, 5, 0, 8, 4, 64, 32, 1000, 16, 1, 1) == 0
+    assert lib.slim_kv4_attention_workspace(4, 4, 0, 8, 4, 64, 128, 1000, 16, 1, 1) == 0
+    assert lib.slim_kv4_attention_workspace(4, 4, 0, 8, 4, 64, 32, 1, 16, 1, 1) == 0      # 16 tokens: nothing to join
 
 
 def test_attention_workspace_of_extreme_shapes(lib):
     for qdt in (0, 1):
         for b, tq in ((1, 1), (4096, 4096), (1, 1 << 20), (1024, 1 << 20)):
             for hq, heads in ((1, 1), (1024, 1), (1024, 1024)):
-                need = lib.slim_kv4_attention_workspace(b, tq, 1, hq, heads, 256, 32, 1 << 22, 256, qdt)
+                need = lib.slim_kv4_attention_workspace(b, tq, 1, hq, heads, 256, 32, 1 << 22, 256, qdt, qdt)
                 assert need < 1 << 38
 
 

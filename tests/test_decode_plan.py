@@ -65,8 +65,11 @@ def runs(p, rows, lengths):
         work = f(0)
         for n, t in zip(tiles, t32):
             work += f(n) * f(t)
-        share = work * (f(1.01) / f(p["extra"]))
-        chunk = p["least"] if share < p["least"] else int(min(share, f(1 << 26))) + 1
+        for more in (sum(tiles), sum(tiles) // 2, 0) if len(rows) <= 64 else (0,):
+            share = work * f(1.01) / f(p["extra"] + more)
+            chunk = p["least"] if share < p["least"] else int(min(share, f(1 << 26))) + 1
+            if sum(n * max(1, -(-t // chunk)) for n, t in zip(tiles, t32)) <= p["slots"] + p["extra"]:
+                break
     out, first = [], 0
     for n, t in zip(tiles, t32):
         r = 1 if t <= chunk else -(-t // chunk)
@@ -85,17 +88,17 @@ def test_words(lib):
 
 def test_every_kernel_has_a_gpu_case(lib):
     seen = set()
-    for lengths, n, hq, heads, dim, group, page, qdt, _, _ in gpu.ATTENTION + gpu.EVERY + gpu.JOINED:
+    for lengths, n, hq, heads, dim, group, page, qdt, odt, _ in gpu.ATTENTION + gpu.EVERY + gpu.JOINED:
         cap = max(1, max(-(-x // page) for x in lengths)) * page
-        p = plan(lib, len(lengths), len(lengths) * n, 1, hq, heads, dim, group, cap, qdt == "f32")
-        seen.add((dim, group, qdt, p["tile"], p["nq"]))
+        p = plan(lib, len(lengths), len(lengths) * n, 1, hq, heads, dim, group, cap, "f32" in (qdt, odt))
+        seen.add((dim, group, "mixed" if (qdt, odt) == ("bf16", "f32") else qdt, p["tile"], p["nq"]))
         seen.add(("joined", p["extra"] > 0, p["most"] > 8))
     assert ("joined", True, True) in seen and ("joined", True, False) in seen and ("joined", False, False) in seen
     for dim in (64, 128, 256):
         for group in (32, 64, 128):
             if group > dim:
                 continue
-            for qdt in ("bf16", "f32"):
+            for qdt in ("bf16", "f32", "mixed"):
                 kinds = {s[3:] for s in seen if s[:3] == (dim, group, qdt)}
                 wide = qdt == "bf16" and dim < 256
                 want = {(0, 1), (1, 2 if wide and dim // group < 4 else 1)} | ({(0, 2)} if wide else set())

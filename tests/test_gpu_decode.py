@@ -5,8 +5,8 @@ The cache is compared word for word.  Attention's tolerance, from the arithmetic
 score's error is at most 2^-23 (dim + 16) of scale sum |q| (|code step| + |low|), plus what rounding
 its power's argument adds, and it enters the weights as a factor; sums over the tokens add 2^-23 a term of
 a lane's chain; a bfloat16 output adds 2^-8 of the value.  Weights times steps are rounded to three
-bfloat16 terms (float32 q, nothing is lost) or two (bfloat16 q, few rows: 2^-8 of what the first
-leaves, below 2^-15 as it is truncated).  Many rows of bfloat16 have both factors in float16, whose
+bfloat16 terms (float32 q or output, nothing is lost) or two (bfloat16, few rows: 2^-8 of what the first
+leaves, below 2^-15 as it is truncated).  Many rows of bfloat16 (outputs too) have both factors in float16, whose
 rounding is at most 2^-11: a value is code step + low, each of step, low and value rounded once, and a
 group is no smaller than 2^-9 of a unit in which float16's least halves are 2^-25, so 15 codes and two
 roundings more of those are below 2^-12 of the group; a weight moves by 2^-11 of itself or by 2^-25
@@ -211,7 +211,8 @@ class Context:
 
 
 def _attention(ctx, i, q, scale, causal, odt, qdt, many=True):
-    """float64 result of sequence i and its tolerance; many: rows may be taken by float16."""
+    """float64 result of sequence i and its tolerance; many: bfloat16 rows may be taken by float16."""
+    short = qdt == "bf16" and odt == "bf16"
     q = oracle.as_f64(_host(q)) if isinstance(q, torch.Tensor) else q
     k, v = ctx.k[i][1].astype(np.float64), ctx.v[i][1].astype(np.float64)
     want = oracle.attention(q, k, v, scale, causal)
@@ -237,8 +238,8 @@ def _attention(ctx, i, q, scale, causal, odt, qdt, many=True):
             ds = 2.0 ** -23 * ((dim + 16) * abs(scale) * ((kc + kl)[:reach, hh] @ np.abs(q[a, h])) + 4 * np.abs(s).max() + 8)
             part, whole = p @ vc[:reach, hh], p @ (vc + vl)[:reach, hh]
             chain = 2.0 ** -23 * (reach / 16 + 64)
-            tol[a, h] = (2.0 ** -15 if qdt == "bf16" else 0) * part + (2 * ds.max() + chain) * whole
-            if qdt == "bf16" and many:
+            tol[a, h] = (2.0 ** -15 if short else 0) * part + (2 * ds.max() + chain) * whole
+            if short and many:
                 x = np.abs(v[:reach, hh])
                 top = np.repeat(x.reshape(reach, -1, g).max(-1), g, -1)
                 lost = 2.0 ** -11 * (vc + vl)[:reach, hh] + 2.0 ** -11 * x + 2.0 ** -12 * top
@@ -299,9 +300,9 @@ def test_attention(slim, lengths, n, hq, heads, dim, group, page, qdt, odt, caus
 
 
 # every head size and group on every kernel: few rows, some, many
-EVERY = [([97, 40 + n], n, 3, 1, dim, group, 32, qdt, qdt, True)
-         for dim in (64, 128, 256) for group in (32, 64, 128) if group <= dim for qdt in ("bf16", "f32")
-         for n in (2, 9, 25)]
+EVERY = [([97, 40 + n], n, 3, 1, dim, group, 32, qdt, odt, True)
+         for dim in (64, 128, 256) for group in (32, 64, 128) if group <= dim
+         for qdt, odt in (("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")) for n in (2, 9, 25)]
 # and enough runs for the join by four waves
 JOINED = [([3000 + n, 1700], n, 3, 1, 128, 64, 64, "bf16", "bf16", True) for n in (1, 9, 25)] + \
          [([2500 + n], n, 3, 1, dim, 64, 64, "f32", "f32", True) for dim in (64, 256) for n in (1, 25)]
@@ -459,15 +460,16 @@ RANGES = {
     ([333, 150], 40, 2, 1, 256, 64),
 ])
 @pytest.mark.parametrize("what", RANGES)
-def test_attention_many_rows_ranges(slim, what, lengths, n, hq, heads, dim, group):
+@pytest.mark.parametrize("odt", ["bf16", "f32"])
+def test_attention_many_rows_ranges(slim, odt, what, lengths, n, hq, heads, dim, group):
     """Values inside and past what float16 holds beside the first ones, for many rows."""
     ctx = Context(slim, 11, lengths, heads, dim, group, 32, values=RANGES[what])
     q = 3 * _rows(np.random.default_rng(1), len(lengths) * n, hq, dim, "bf16", False).view(len(lengths), n, hq, dim)
     for causal in (True, False):
         out = slim.kv4_attention(q.cuda(), ctx.cache, _gpu(ctx.table), _i32(lengths), group, causal=causal,
-                                 out_dtype=torch.float32)
+                                 out_dtype=DT[odt])
         for i in range(len(lengths)):
-            _check(ctx, i, out[i], q[i], dim ** -0.5, causal, "f32", "bf16", f"{what} {causal}")
+            _check(ctx, i, out[i], q[i], dim ** -0.5, causal, odt, "bf16", f"{what} {causal}")
 
 
 def test_attention_many_rows_of_nothing(slim):
