@@ -364,8 +364,8 @@ struct Rows {
 
   // Weights of 32 tokens, tok the lane's first one (entry 4 b + v: token tok + 16 b + v).  Src: codes
   // and pairs of the two records; a key's step is given times scale log2 e.  EDGE: some row does
-  // not attend to all of them.
-  template <bool EDGE, class Src>
+  // not attend to all of them.  HALF: the sums are those by float16, the others are not yet there.
+  template <bool EDGE, bool HALF, class Src>
   __device__ __forceinline__ void weigh(Src &src, int tok, float (&x)[NQ][8]) {
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -412,7 +412,7 @@ struct Rows {
     }
     if (__any(up)) {
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) raise(n, top[n], x[n]);
+      for (int n = 0; n < NQ; ++n) raise<HALF>(n, top[n], x[n]);
     }
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -425,7 +425,7 @@ struct Rows {
   __device__ __forceinline__ void attend(Src &src, int first) {
     const int tok = first + 4 * ((threadIdx.x & 63) >> 4);
     float x[NQ][8];
-    weigh<EDGE>(src, tok, x);
+    weigh<EDGE, false>(src, tok, x);
     src.values();
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -473,7 +473,7 @@ struct Rows {
   template <bool EDGE, class Src>
   __device__ __forceinline__ void attend_half(Src &src, int first) {
     float x[NQ][8];
-    weigh<EDGE>(src, first + 4 * ((threadIdx.x & 63) >> 4), x);
+    weigh<EDGE, true>(src, first + 4 * ((threadIdx.x & 63) >> 4), x);
     const uint4 ones = make_uint4(0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u);
     uint4 pf[NQ];
 #pragma unroll
@@ -501,11 +501,14 @@ struct Rows {
     for (int n = 0; n < NQ; ++n) {
       ls[n] = first ? lh[n][0] : 0.0f;
 #pragma unroll
+      for (int j = 0; j < NG; ++j) pl[n][j] = 0.0f;
+#pragma unroll
       for (int i = 0; i < DIM / 16; ++i) o[n][i] *= f;
     }
   }
 
   // A new reference for the rows that need one: the maximum over the step's tokens.
+  template <bool HALF>
   __device__ __forceinline__ void raise(int n, float top, float (&x)[8]) {
     asm volatile("" : "+v"(top));   // nothing of this is done ahead of the branch
     top = fmaxf(top, __shfl_xor(top, 16, 64));
@@ -515,10 +518,13 @@ struct Rows {
     const float f = !up ? 1.0f : thr[n] == kNegInf ? 0.0f : exp2_any(-by);   // sums of no token are 0
     m[n] += by;
     if (up) thr[n] = kMost;
-    ls[n] *= f;
-    lh[n] *= f;
+    if (HALF) {
+      lh[n] *= f;
+    } else {
+      ls[n] *= f;
 #pragma unroll
-    for (int j = 0; j < NG; ++j) pl[n][j] *= f;
+      for (int j = 0; j < NG; ++j) pl[n][j] *= f;
+    }
 #pragma unroll
     for (int i = 0; i < DIM / 16; ++i) o[n][i] *= f;
 #pragma unroll
@@ -535,10 +541,13 @@ struct Rows {
       if (thr[n] == kNegInf) m[n] = kNegInf;
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
-        pl[n][j] += __shfl_xor(pl[n][j], 16, 64);
-        pl[n][j] += __shfl_xor(pl[n][j], 32, 64);
+        float x = pl[n][j];
+        x += __shfl_xor(x, 16, 64);
+        x += __shfl_xor(x, 32, 64);
 #pragma unroll
-        for (int w = GS * j; w < GS * (j + 1); ++w) o[n][2 * w] += pl[n][j], o[n][2 * w + 1] += pl[n][j];
+        for (int i = 2 * GS * j; i < 2 * GS * (j + 1); ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) o[n][i][v] += x;
       }
     }
   }
