@@ -174,7 +174,9 @@ __device__ __forceinline__ Pair group_pair(const float (&x)[8]) {
 // wave 4 heads of 128.  Items run over the heads of q, k and v of a token.
 // Nothing is shared between lanes but the groups' extremes, and every word or
 // byte of the cache is written by one lane, so no write reads what another
-// token wrote.
+// token wrote.  Bound by memory for many tokens (2048 of 64 + 8 heads of 128, g = 64:
+// 98 MB in 25 us; the copy's rate would be 21) and by one chain of reads for
+// few (3.8 us).
 template <bool BF16, int DIM, int GROUP>
 __global__ __launch_bounds__(256) void kv4_append_kernel(const Kv4Append a) {
   constexpr int L = DIM / 8, W = GROUP / 8, NG = DIM / GROUP, REC = 4 * DIM + 32 * NG;
@@ -240,7 +242,8 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(const Kv4Append a) {
   if (l % W == 0) rec[4 * DIM + (kind == 2 ? 16 * NG : 0) + 16 * (l / W) + t16] = p.word;
 }
 
-// The values of given slots.  A lane reads 8 channels, as above.
+// The values of given slots.  A lane reads 8 channels, as above (512 slots of 8
+// heads of 128 as float32: 7.4 us).
 template <int DIM, int GROUP>
 __global__ __launch_bounds__(256) void kv4_read_kernel(const int32_t *__restrict__ slots, int64_t t,
                                                        const uint32_t *__restrict__ cache, int64_t pages,
