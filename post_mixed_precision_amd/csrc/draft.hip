@@ -170,10 +170,10 @@ __global__ __launch_bounds__(256) void draft_stats_kernel(const DraftArgs a, con
   const double c = 256.0 * power_of(a), md = m == -__builtin_inff() || bad ? 0.0 : (double)m;
   double z = 0.0;
   const double whole = __builtin_rint(-md * c), low = md + kLowest / c;
-  if (fabs(whole) < 0x1p45 && low > -0x1p127) {
+  const float least = (float)low;
+  if (fabs(whole) < 0x1p45 && low > -0x1p127 && fabs((double)least - low) * c < 256.0) {
     // about a whole number `whole` near -m c: fma(x, c, kMagic + whole) is then n in the low word, and g takes
-    // one more; entries below `low`, -inf too, become 2^-1020, beside a sum of 1 and more
-    const float least = (float)low;
+    // one more; entries below `least`, -inf too, become 2^-1020, or that and its rounding, beside a sum of 1 and more
     const double base = kMagic + whole;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(256) void draft_stats_kernel(const DraftArgs a, con
         z += exp2_256th(y, __builtin_fma(xd, c, base - y), s_pow);
       }
     z *= exp2_64(__builtin_fma(md, -c, -whole) * (1.0 / 256.0));
-  } else {                                                 // logits of 10^11 (of the type's lowest, say): x - m first
+  } else {   // logits of 10^11 (of the type's lowest, say), or no float between m and `low`: x - m first
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
 #pragma unroll

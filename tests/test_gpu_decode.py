@@ -577,6 +577,26 @@ def test_draft_extreme_logits(slim, dt, draft, temperature, v):
     _verify(slim, target, tokens, u, dr if draft else None, temperature)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("temperature", [1e-5, 1e-8, 1e-9, 1e-10, 1e-12, 1e-40, 1e-305])
+def test_draft_small_temperatures(slim, dt, temperature):
+    """As far as the greatest logit alone has weight, whether it is 0, near 0 or large; the next float below it has
+    none, and equal ones share."""
+    rng = np.random.default_rng(4)
+    b, k, v = 5, 2, 5000
+    t = -np.abs(rng.standard_normal((b, k + 1, v))) - 0.01
+    t[0][:, 17] = 0.0
+    t[1] += 20
+    t[2][:, 40:44] = 0.0
+    t[3] *= 1e-30
+    t[4] = 3e4 - np.abs(t[4])
+    target = torch.from_numpy(t).to(DT[dt])
+    tokens = target.float().argmax(-1)[:, :k].numpy().copy()
+    tokens[1, 1] = (tokens[1, 1] + 1) % v
+    u = (0.1 + 0.8 * rng.random((b, k + 1))).astype(np.float32)
+    _verify(slim, target, tokens, u, None, temperature)
+
+
 DRAFTS = [
     (1, 1, 1, "f32", True, 0, 1.0),
     (1, 4, 1000, "f32", True, 0, 1.0),
