@@ -185,7 +185,7 @@ def test_nothing_to_append_or_read(slim):
 class Context:
     """A cache with sequences of given lengths on shuffled pages, and their values."""
 
-    def __init__(self, slim, seed, lengths, heads, dim, group, page, dt="bf16", spare=2, values=None):
+    def __init__(self, slim, seed, lengths, heads, dim, group, page, dt="bf16", spare=2, values=None, keys=None):
         rng = np.random.default_rng(seed)
         need = [max(0, -(-n // page)) for n in lengths]
         per = max(1, max(need))
@@ -199,6 +199,8 @@ class Context:
             self.table[i, :need[i]] = order[used:used + need[i]]
             used += need[i]
             k, v = _rows(rng, max(n, 0), heads, dim, dt), _rows(rng, max(n, 0), heads, dim, dt, False)
+            if keys is not None:
+                k = torch.from_numpy(keys(rng, k.float().numpy())).to(DT[dt])
             if values is not None:
                 v = torch.from_numpy(values(rng, v.float().numpy())).to(DT[dt])
             at = np.arange(max(n, 0))
@@ -470,6 +472,24 @@ def test_attention_many_rows_ranges(slim, odt, what, lengths, n, hq, heads, dim,
                                  out_dtype=DT[odt])
         for i in range(len(lengths)):
             _check(ctx, i, out[i], q[i], dim ** -0.5, causal, odt, "bf16", f"{what} {causal}")
+
+
+@pytest.mark.parametrize("n", [1, 100])
+@pytest.mark.parametrize("far", [18, 24, 30])
+def test_attention_small_weights_count(slim, n, far):
+    """One token has nearly all the weight and a value of 0: what is left are the others, 2^-far each."""
+    def keys(rng, k):
+        return np.where(np.arange(len(k)) == 5, 1.0, 0.5)[:, None, None] * np.ones(k.shape, np.float32)
+
+    def values(rng, v):
+        v = 1 + 0.2 * v
+        v[5] = 0
+        return v
+    ctx = Context(slim, 14, [900], 1, 128, 64, 16, values=values, keys=lambda rng, k: keys(rng, k).astype(np.float32))
+    q = torch.full((1, n, 2, 128), far * np.log(2) / 64, dtype=torch.bfloat16)
+    out = slim.kv4_attention(q.cuda(), ctx.cache, _gpu(ctx.table), _i32([900]), 64, causal=False, scale=1.0)
+    _check(ctx, 0, out[0], q[0], 1.0, False, "bf16", "bf16", many=n > 32)
+    assert (out > 0).all()
 
 
 def test_attention_many_rows_of_nothing(slim):
