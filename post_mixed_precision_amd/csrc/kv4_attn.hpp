@@ -187,7 +187,7 @@ __device__ __forceinline__ Work find_work(const Kv4Args &a, const Kv4Cut &cut, i
   }
   const int own = __ffsll((unsigned long long)past) - 1;
   int first = of_lane(rsum - runs, own), slot = of_lane(tsum - tiles, own);
-  for (int s = own * per;; ++s) {   // ends: lane `own` has run i
+  for (int s = own * per; s < a.b; ++s) {   // lane `own` has run i
     int lo, hi;
     bounds(s, lo, hi);
     w.len = length_of(a, s, w.over);
@@ -204,6 +204,8 @@ __device__ __forceinline__ Work find_work(const Kv4Args &a, const Kv4Cut &cut, i
     w.tile = n - 1 - t;             // the longest first
     return w;
   }
+  w.none = true;                    // lengths written to meanwhile: still an end
+  return w;
 }
 
 // What the join reads of a tile, in the workspace behind the partial results.
