@@ -579,13 +579,15 @@ int slim_kv4_read(const int32_t *slots, int64_t t, const uint32_t *cache, int64_
  * the softmax are float32.  The weights of the second product (probability
  * times step) enter as two bfloat16 terms if q and out are bfloat16 (2^-16 of
  * themselves is lost).  Above 64 rows (query tokens times hq / heads) a
- * sequence on average these have weights and dequantized values in float16
- * instead (2^-11 of either; weights 2^-33 below a row's greatest are lost),
- * but for values that are 2^11 times the first tokens' or 2^-12 of them, and
- * all behind such a one, which are taken as before.  Otherwise weights, and
- * float32 q, enter as three bfloat16 terms (what lies below 2^-133 is dropped).  Weights are
- * scaled to as much as 2^15 in the sums: values past 2^112 over the number of tokens may
- * overflow.  The result is rounded once.  The same call gives the same bits.
+ * sequence on average, or 32 where dim is four groups or more and per * page
+ * above 512, these have weights and dequantized values in float16 instead
+ * (2^-11 of either; weights 2^-33 below a row's greatest are lost), but for
+ * values that are 2^11 times the first tokens' or 2^-12 of them, and all behind
+ * such a one, which are taken as before.  Otherwise weights, and float32 q,
+ * enter as three bfloat16 terms (what lies below 2^-133 is dropped).  Weights
+ * are scaled to as much as 2^15 in the sums: values past 2^112 over the number
+ * of tokens may overflow.  The result is rounded once.  The same call gives the
+ * same bits.
  * out must not overlap an input.  1 <= b <= tq unless tq = 0
  * (a no-op), b <= SLIM_KV4_MAX_SEQS, tq <= SLIM_KV4_MAX_T, hq <=
  * SLIM_KV4_MAX_HEADS, tq hq below 2^27, scale finite.

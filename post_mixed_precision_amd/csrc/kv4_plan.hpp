@@ -49,9 +49,11 @@ inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t
   const int64_t per = (uniform ? tq / b : (tq + b - 1) / b) * g;   // rows of a sequence, on average
   const bool wide = !f32 && dim < 256;                             // registers for two tiles of 16 rows
   // Up to 64 rows the stream reads the cache again for every 32 (or 16) of them, from L2, and is still ahead of tiles
-  // that most of a workgroup's waves idle in (40 rows of 16 sequences of up to 8192: 95 us, tiles 108; 64 rows: 81 and
-  // 109; 96 rows: 113 and 107; float32, 40 rows: 24 and 27).
-  p.tile = per > 64;
+  // that most of a workgroup's waves idle in (40 rows of 16 sequences of up to 8192: 72 us, tiles 81; 64 rows: 70 and
+  // 78; 96 rows: 108 and 81; float32, 40 rows of 8: 44 and 45).  With four groups a head or more it has too few
+  // registers left (40 rows, g = 32: 127 and 81; 32 rows: 81 and 78; heads of 256, g = 64, 48 rows of 8 sequences: 83
+  // and 68), unless the context is so short that the first tile's start counts (300 tokens: 14 and 22; 1000: 25 and 21).
+  p.tile = per > (dim / group >= 4 && cap > 512 ? 32 : 64);
   p.nq = wide && per > 16 && !(p.tile && dim / group >= 4) ? 2 : 1;   // (many rows, small groups: 237 TFLOP/s, one 263)
   p.tm = 16 * p.nq * (p.tile ? 4 : 1);
   p.tiles = (int)((per + p.tm - 1) / p.tm);
@@ -60,8 +62,8 @@ inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t
   // 128: 768 runs 35 us, 512 38, 1024 38; 131072 tokens, g = 64: 512 47, 768 50).  Many rows: 512 (one
   // sequence of 65536 tokens: 438 TFLOP/s, 768 384; 2 of 8192, 256 queries: 568 and 497), but some tiles of `slots`
   // are idle where queries are uneven (560, 512 and 768 runs, TFLOP/s: 3 sequences of up to 3000 and 500 queries 419,
-  // 362, 402; 8 of up to 2048 and 300 394, 387, 318; 2 of up to 1500 and 900 337, 271, 333).  However many tiles there are, one sequence may be far longer than the
-  // others: 256 runs more, unless the table says that none can be.
+  // 362, 402; 8 of up to 2048 and 300 394, 387, 318; 2 of up to 1500 and 900 337, 271, 333).  However many tiles there
+  // are, one sequence may be far longer than the others: 256 runs more, unless the table says that none can be.
   const int64_t want = p.tile ? (uniform ? 512 : 560) : b > 1 && !f32 && p.nq == 1 && group == 128 && dim == 128 ? 768 : 512;
   p.least = p.tile && p.slots * hkv >= 256 ? 32 : 8;
   const int64_t units = p.slots * hkv, tokens = (cap + 31) / 32, spare = cap > 2048 ? 256 : 0;

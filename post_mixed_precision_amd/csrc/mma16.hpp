@@ -1,4 +1,4 @@
-// The 16 x 16 x 32 bfloat16 product and its operands from 4-bit codes and
+// The 16 x 16 x 32 bfloat16 (and float16) product and its operands from 4-bit codes and
 // float32, shared by the 4-bit products and the attention over the 4-bit cache.
 #pragma once
 #include "common.hpp"

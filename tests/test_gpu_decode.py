@@ -295,7 +295,7 @@ def test_attention(slim, lengths, n, hq, heads, dim, group, page, qdt, odt, caus
         if length == 0:
             assert not out[i].any()
         else:
-            _check(ctx, i, out[i], q[i], dim ** -0.5, causal, odt, qdt, many=n * hq // heads > 64)
+            _check(ctx, i, out[i], q[i], dim ** -0.5, causal, odt, qdt, many=n * hq // heads > 32)
     again = slim.kv4_attention(q.cuda(), ctx.cache, _gpu(ctx.table), _i32(lengths), group, causal=causal,
                                out_dtype=DT[odt])
     assert torch.equal(out, again)
@@ -305,6 +305,9 @@ def test_attention(slim, lengths, n, hq, heads, dim, group, page, qdt, odt, caus
 EVERY = [([97, 40 + n], n, 3, 1, dim, group, 32, qdt, odt, True)
          for dim in (64, 128, 256) for group in (32, 64, 128) if group <= dim
          for qdt, odt in (("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")) for n in (2, 9, 25)]
+# tiles for fewer rows where a head has four groups or more
+EVERY += [([700, 90 + n], n, 3, 1, dim, dim // 4, 32, qdt, odt, True) for dim in (128, 256)
+          for qdt, odt in (("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")) for n in (11, 21)]
 # and enough runs for the join by four waves
 JOINED = [([3000 + n, 1700], n, 3, 1, 128, 64, 64, "bf16", "bf16", True) for n in (1, 9, 25)] + \
          [([2500 + n], n, 3, 1, dim, 64, 64, "f32", "f32", True) for dim in (64, 256) for n in (1, 25)]
