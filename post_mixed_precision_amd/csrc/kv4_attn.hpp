@@ -288,7 +288,7 @@ __device__ __forceinline__ int64_t row_at(const Kv4Args &a, const K &k, int h, i
 // Many rows of bfloat16: values are dequantized after all, once for the
 // workgroup, to float16 (step, low end and value each within 2^-11 of themselves), and
 // weights are float16 too (2^-11, or 2^-33 of the row's largest weight, by the
-// lift).  The products of codes with weights in two terms cost twice the
+// lift; a lift of 11 took 3%, of 14 10% longer, as references then move more often).  The products of codes with weights in two terms cost twice the
 // matrix instructions and six vector instructions more a weight: 8 sequences
 // of 4096, causal, 32 + 8 heads of 128, took 1702 us by them, 1548 us so (and
 // 1412 with what came after).
@@ -965,7 +965,8 @@ struct LdsPart {             // 32 tokens of it
 // the other half of LDS behind it: keys to bfloat16 codes; values, for bfloat16
 // queries and outputs, to float16 numbers in a unit that makes the first tile's greatest
 // one 8 to 16.  Should a tile not fit that (a value past 2^14 units; a token's whole group
-// below 2^-9 units though not 0, where its step would run out of float16's bits; a
+// below 2^-9 units, where its step would run out of float16's bits, or 0: if that token has
+// a row's whole weight, what is left are weights that float16 rounds to 2^-33 of it; a
 // NaN, which must not meet a weight of 0), the rest is done by the values' codes,
 // as for float32 queries.  Two loops, not a branch in one: that spilled registers.
 // 8 sequences of 4096, causal, 32 + 8 heads of 128: 1412 us, 779 TFLOP/s; the
@@ -1032,15 +1033,16 @@ __global__ __launch_bounds__(256, 2) void kv4_tile_kernel(const Kv4Args a, const
         }
       }
     };
-    // Magnitude, as bits, of the greatest value of a group of one token (NaN: above infinity's; of keys
-    // and of tokens that nobody attends to: 0), by the lane that holds its pair.
+    // Magnitude, as bits, of the greatest value of a group of one token (NaN: above infinity's; 0: float32's
+    // least number, which float16 does not fit; of keys and of tokens that nobody attends to: 0), by the lane that
+    // holds its pair.
     auto size_of = [&](int t, int i) __attribute__((always_inline)) {
       const int x = soff + lane + 64 * i;
       const float step = half_of(sw[i], false), low = half_of(sw[i], true);
       const float far = __builtin_fmaf(15.0f, step, low);          // a NaN step makes it one
       const uint32_t u = __float_as_uint(far) & 0x7fffffffu, l = __float_as_uint(low) & 0x7fffffffu;
       const bool counts = lane + 64 * i < SW && x >= 16 * NG && TOK * t + 16 * blk + (x & 15) < kend;
-      return !counts ? 0u : u > l ? u : l;
+      return !counts ? 0u : (u > l ? u : l) | 1u;
     };
     // CODES: values as bfloat16 codes, else as float16 numbers.
     auto expand = [&](Lds &d, int t, auto codes) __attribute__((always_inline)) {

@@ -495,6 +495,31 @@ def test_attention_small_weights_count(slim, n, far):
     assert (out > 0).all()
 
 
+@pytest.mark.parametrize("zero", ["all channels", "one group"])
+@pytest.mark.parametrize("length", [900, 2500])
+@pytest.mark.parametrize("far", [22, 26, 30, 36])
+def test_attention_many_rows_beside_a_value_of_zero(slim, far, length, zero):
+    """Nearly all the weight on a token whose value is 0, in one group or in all: what is left are weights 2^-far below
+    it, and those count as exactly as in a call of few rows (no float16 allowance)."""
+    at = 41 if length == 900 else length - 3         # of the first tile, of the last one
+
+    def keys(rng, k):
+        return np.where(np.arange(len(k)) == at, 1.0, 0.5)[:, None, None].astype(np.float32) * np.ones_like(k)
+
+    def values(rng, v):
+        v = 1 + 0.2 * v
+        v[at, :, 64 if zero[0] == "o" else 0:] = 0
+        return v
+    ctx = Context(slim, 15, [length], 1, 128, 64, 16, values=values, keys=keys)
+    q = torch.full((1, 100, 2, 128), far * np.log(2) / 64, dtype=torch.bfloat16)
+    out = slim.kv4_attention(q.cuda(), ctx.cache, _gpu(ctx.table), _i32([length]), 64, causal=False, scale=1.0)
+    want, tol = _attention(ctx, 0, q[0], 1.0, False, "bf16", "bf16", many=False)
+    err = np.abs(out[0].double().cpu().numpy() - want)
+    assert np.all((err <= tol)[..., 64:])            # the other group's are one weight's, and within it as well
+    if zero[0] == "a":
+        assert np.all(err <= tol)
+
+
 def test_attention_many_rows_of_nothing(slim):
     """Values of 0 are 0, and so are rows before the first token."""
     ctx = Context(slim, 12, [100, 20], 2, 64, 64, 16, values=lambda rng, v: 0 * v)
