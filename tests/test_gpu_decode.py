@@ -361,6 +361,72 @@ def test_attention_many_sequences(slim):
             _check(ctx, i, out[off[i]:off[i + 1]], q[off[i]:off[i + 1]], 64 ** -0.5, True, "bf16", "bf16")
 
 
+def _by_tiles(ctx, tq, grp, dim):
+    """Whether a call's rows are taken as many rows are: by the average of all sequences, as the header states it."""
+    cap = ctx.table.shape[1] * ctx.page
+    return -(-tq // len(ctx.lengths)) * grp > (32 if dim // ctx.group >= 4 and cap > 512 else 64)
+
+
+def _batch(slim, ctx, counts, hq, dim, qdt, seed):
+    """A batch by offsets, every sequence judged by the rounding of its call and no more."""
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    tq, heads = int(off[-1]), ctx.cache.shape[1]
+    many = _by_tiles(ctx, tq, hq // heads, dim)
+    q = _rows(np.random.default_rng(seed), tq, hq, dim, qdt, False)
+    out = slim.kv4_attention(q.cuda(), ctx.cache, _gpu(ctx.table), _i32(ctx.lengths), ctx.group, offsets=_gpu(off))
+    for i, length in enumerate(ctx.lengths):
+        a, b = int(off[i]), int(off[i + 1])
+        if length == 0:
+            assert not out[a:b].any()
+        elif b > a:
+            _check(ctx, i, out[a:b], q[a:b], dim ** -0.5, True, qdt, qdt, f"many rows {many}", many=many)
+    return many
+
+
+@pytest.mark.parametrize("qdt", ["bf16", "f32"])
+@pytest.mark.parametrize("b,grp,prompt,group,many", [
+    (64, 1, 300, 64, False),                 # the prompt's rows in the kernel of few rows
+    (64, 1, 300, 32, False),
+    (32, 4, 600, 64, True),                  # single tokens in the kernel of many rows
+    (16, 8, 200, 128, True),
+    (40, 8, 100, 32, False),
+])
+def test_attention_a_prompt_among_single_tokens(slim, qdt, b, grp, prompt, group, many):
+    """One call for a prompt and many sequences of a token each, of all lengths: whichever kernel the average chooses."""
+    rng = np.random.default_rng(b + grp)
+    at = b // 3
+    lengths = [int(x) for x in rng.integers(1, 900, b)]
+    lengths[at], lengths[5] = prompt + 150, 1
+    counts = [1] * b
+    counts[at] = prompt
+    ctx = Context(slim, 16, lengths, 1, 128, group, 32, qdt)
+    assert _batch(slim, ctx, counts, grp, 128, qdt, 1) == many
+
+
+@pytest.mark.parametrize("b,most,long", [(150, 3, 60), (1100, 2, 3000), (1100, 1, 5000), (4096, 1, 4)])
+def test_attention_few_rows_of_many_sequences(slim, b, most, long):
+    """Few rows a sequence in batches of fewer and more than 1024 sequences (those are not cut), one of them far longer
+    than the others."""
+    rng = np.random.default_rng(b + most)
+    counts = [int(x) for x in rng.integers(0, most + 1, b)]
+    lengths = [c + int(x) if c else 0 for c, x in zip(counts, rng.integers(0, 4, b))]
+    counts[b // 2], lengths[b // 2] = most, long
+    ctx = Context(slim, 17, lengths, 1, 64, 32, 16)
+    assert not _batch(slim, ctx, counts, 2, 64, "bf16", 2)
+
+
+@pytest.mark.parametrize("qdt", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,lengths,heads,hq,dim,group,page", [
+    ([3, 0, 1, 20], [40, 9, 1, 300], 2, 6, 64, 32, 16),
+    ([1, 1, 1, 1, 1], [5, 700, 0, 33, 64], 1, 8, 128, 128, 64),
+    ([0, 0, 7], [0, 50, 7], 3, 3, 256, 128, 16),
+])
+def test_attention_uneven_few_rows(slim, qdt, counts, lengths, heads, hq, dim, group, page):
+    """Uneven batches of few rows, without the allowance that many rows have."""
+    ctx = Context(slim, 7, lengths, heads, dim, group, page, qdt)
+    assert not _batch(slim, ctx, counts, hq, dim, qdt, 8)
+
+
 @pytest.mark.parametrize("offsets", [[0, 5, 3, 12], [0, -1, 4, 12], [0, 4, 8, 13]])
 @pytest.mark.parametrize("lengths", [[30, 30, 30], [3000, 30, 30]])
 def test_attention_bad_offsets(slim, offsets, lengths):
