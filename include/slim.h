@@ -576,21 +576,33 @@ int slim_kv4_read(const int32_t *slots, int64_t t, const uint32_t *cache, int64_
  * What lies past a length, or after a row's last token, does not matter, NaN included.
  *
  * Codes enter exactly, steps and low ends are applied in float32, sums and
- * the softmax are float32.  The weights of the second product (probability
- * times step) enter as two bfloat16 terms if q and out are bfloat16 (2^-16 of
- * themselves is lost).  Above 64 rows (query tokens times hq / heads) a
- * sequence on average, or 32 where dim is four groups or more and per * page
- * above 512, these have weights and dequantized values in float16 instead
- * (2^-11 of either; weights 2^-33 below a row's greatest are lost), but for
- * values that are 2^11 times the first tokens' or 2^-12 of them, and all behind
- * such a one, which are taken as before.  Otherwise weights, and float32 q,
- * enter as three bfloat16 terms (what lies below 2^-133 is dropped).  Weights
- * are scaled to as much as 2^15 in the sums: values past 2^112 over the number
- * of tokens may overflow.  The result is rounded once.  The same call gives the
- * same bits.
- * out must not overlap an input.  1 <= b <= tq unless tq = 0
- * (a no-op), b <= SLIM_KV4_MAX_SEQS, tq <= SLIM_KV4_MAX_T, hq <=
- * SLIM_KV4_MAX_HEADS, tq hq below 2^27, scale finite.
+ * the softmax are float32.  A score is the sum of q with a group's codes, times
+ * the step, and of q times the low end; each can be several times the score, so
+ * that float32 outputs are further off than those of elementary float32
+ * operations where contexts are short: over 11 tokens 5e-7 of their norm (1e-7),
+ * over 300 8e-7 (4e-7); over 20000 1.6e-6 (1.8e-6).
+ * The weights of the second product (probability times step) enter as two
+ * bfloat16 terms if q and out are bfloat16 (2^-16 of themselves is lost).
+ * Otherwise weights, and float32 q, enter as three.  What of a term lies below
+ * 2^-133 is dropped.
+ * Many rows: above 64 rows (query tokens times hq / heads) a sequence, or 32
+ * where dim is four groups or more and per * page above 512, bfloat16 q and out
+ * have weights and dequantized values in float16.  The average over all sequences
+ * decides for every one.  Step, low end and value are then rounded by 2^-11
+ * each, a weight by 2^-11 of itself or 2^-33 of its row's greatest, whichever is
+ * more.  That is so in each run of tokens that a workgroup takes, until 64 of
+ * them (32 where dim is 256) come with a value whose greatest entry in some group
+ * is 0, NaN or outside 2^-12 to 2^10 times (give or take a factor of 2) the
+ * greatest of the run's first 64 (32): they and the rest of the run enter as with few rows.
+ * Weights are scaled to as much as 2^15 in the sums: values past 2^112 over the
+ * number of tokens may overflow.  The result is rounded once.  The same call
+ * gives the same bits.
+ * A sequence's tokens are spread over the card, but not past 1024 sequences or
+ * 2^23 rows: then one workgroup a head and 16 to 128 rows reads all of a sequence
+ * (one of 131072 tokens among 1023 of 100: 155 us, among 1024 995).
+ * out must not overlap an input.  1 <= b <= SLIM_KV4_MAX_SEQS, tq <=
+ * SLIM_KV4_MAX_T (0 is a no-op), without offsets a multiple of b; hq <=
+ * SLIM_KV4_MAX_HEADS, tq hq below 2^27, scale finite in float32.
  * Workspace: slim_kv4_attention_workspace(...) bytes, which may be 0.
  * ---------------------------------------------------------------------- */
 #define SLIM_KV4_MAX_SEQS 4096
@@ -621,7 +633,8 @@ int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uin
  * nowhere above q_j) the drawn id is -1.  Differences p_j - q_j up to 2^-44 p_j
  * count as 0.
  * 0 <= b <= SLIM_DRAFT_MAX_B (0 is a no-op), 1 <= k <= SLIM_DRAFT_MAX_K,
- * 1 <= v <= SLIM_LOGPROB_MAX_V, b (2 k + 1) v <= 2^36, temperature > 0.  Workspace:
+ * 1 <= v <= SLIM_LOGPROB_MAX_V, b (2 k + 1) v <= 2^36, temperature positive, it
+ * and 1 / temperature finite.  Workspace:
  * slim_verify_draft_workspace(b, k, v) bytes.
  * ---------------------------------------------------------------------- */
 #define SLIM_DRAFT_MAX_B 65536
