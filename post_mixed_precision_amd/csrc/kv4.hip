@@ -174,9 +174,11 @@ __device__ __forceinline__ Pair group_pair(const float (&x)[8]) {
 // wave 4 heads of 128.  Items run over the heads of q, k and v of a token.
 // Nothing is shared between lanes but the groups' extremes, and every word or
 // byte of the cache is written by one lane, so no write reads what another
-// token wrote.  Bound by memory for many tokens (2048 of 64 + 8 heads of 128, g = 64:
-// 98 MB in 25 us; the copy's rate would be 21) and by one chain of reads for
-// few (3.8 us).
+// token wrote.  2048 tokens of 64 + 8 heads of 128, g = 64: 79 MB in 25 us, 3.2
+// TB/s (a copy of 4 GiB has 4.7, that would be 17 us).  The vector unit is 47%
+// busy, and a lane waits for its one load of 16 bytes, its partner's, which is
+// loaded twice, and the table's, loaded again for every head.  Few tokens:
+// one chain of reads (3.8 us).
 template <bool BF16, int DIM, int GROUP>
 __global__ __launch_bounds__(256) void kv4_append_kernel(const Kv4Append a) {
   constexpr int L = DIM / 8, W = GROUP / 8, NG = DIM / GROUP, REC = 4 * DIM + 32 * NG;
@@ -242,8 +244,10 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(const Kv4Append a) {
   if (l % W == 0) rec[4 * DIM + (kind == 2 ? 16 * NG : 0) + 16 * (l / W) + t16] = p.word;
 }
 
-// The values of given slots.  A lane reads 8 channels, as above (512 slots of 8
-// heads of 128 as float32: 7.4 us).
+// The values of given slots.  A lane reads 8 channels, as above.  2048 slots of 8
+// heads of 128 as float32: 19 MB in 7.4 to 8.0 us (4 at the copy's rate).  The
+// value codes are read byte by byte, and neighbouring tokens, whose bytes share a
+// word, go to workgroups of other XCDs: 14 MB are fetched for 2.4.
 template <int DIM, int GROUP>
 __global__ __launch_bounds__(256) void kv4_read_kernel(const int32_t *__restrict__ slots, int64_t t,
                                                        const uint32_t *__restrict__ cache, int64_t pages,

@@ -291,7 +291,7 @@ __device__ __forceinline__ int64_t row_at(const Kv4Args &a, const K &k, int h, i
 // lift; a lift of 11 took 3%, of 14 10% longer, as references then move more often).  The products of codes with weights in two terms cost twice the
 // matrix instructions and six vector instructions more a weight: 8 sequences
 // of 4096, causal, 32 + 8 heads of 128, took 1702 us by them, 1548 us so (and
-// 1412 with what came after).
+// 1408 with what came after).
 constexpr float kLift = 8.0f, kMost = 15.0f;
 // What rows are held by: bfloat16 queries and outputs, bfloat16 queries with float32 outputs, float32 queries.
 constexpr int kBf16 = 0, kMixed = 1, kF32 = 2;
@@ -776,7 +776,7 @@ struct RingTile {
 template <int RECB>
 __device__ __forceinline__ Pages pages_of(const Kv4Args &a, int seq, int h, int kend) {
   Pages p;
-  p.bytes = (unsigned)(a.page >> 4) * RECB * a.hkv;      // below 2^31: 1024 heads of 16 records of 10 KB
+  p.bytes = (unsigned)(a.page >> 4) * RECB * a.hkv;      // below 2^27: 1024 heads of 16 records of 5 KB
   p.cache = (const char *)a.cache + (unsigned)h * ((unsigned)(a.page >> 4) * RECB);
   p.table = a.table + (int64_t)seq * a.per;
   p.pages = a.pages;
@@ -969,7 +969,7 @@ struct LdsPart {             // 32 tokens of it
 // a row's whole weight, what is left are weights that float16 rounds to 2^-33 of it; a
 // NaN, which must not meet a weight of 0), the rest is done by the values' codes,
 // as for float32 queries.  Two loops, not a branch in one: that spilled registers.
-// 8 sequences of 4096, causal, 32 + 8 heads of 128: 1412 us, 779 TFLOP/s; the
+// 8 sequences of 4096, causal, 32 + 8 heads of 128: 1408 us, 781 TFLOP/s; the
 // matrix unit is 26% and the vector unit 45% busy (two prompts of 1024 and 657).
 constexpr float kHalfMost = 0x1p14f, kHalfLeast = 0x1p-9f;
 template <int DIM, int GROUP, int NQ, int X>

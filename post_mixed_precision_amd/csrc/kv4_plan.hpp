@@ -53,13 +53,20 @@ inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t
   // 78; 96 rows: 108 and 81; float32, 40 rows of 8: 44 and 45).  With four groups a head or more it has too few
   // registers left (40 rows, g = 32: 127 and 81; 32 rows: 81 and 78; heads of 256, g = 64, 48 rows of 8 sequences: 83
   // and 68), unless the context is so short that the first tile's start counts (300 tokens: 14 and 22; 1000: 25 and 21).
+  // The average decides for all of a batch, also for one prompt among single tokens.  Such a call takes longer than one
+  // for the single tokens and one for the prompt would (us: one call, the two; single tokens over up to 4096): 31 and a
+  // prompt of 1024, 32 + 8 heads 83, 29 + 37; 63 and one of 512, 32 + 32 heads 151, 145 + 25; 64 and one of 2048, 64 + 8
+  // heads 198, 48 + 105, 32 + 32 heads 277, 147 + 75.
   p.tile = per > (dim / group >= 4 && cap > 512 ? 32 : 64);
   p.nq = wide && per > 16 && !(p.tile && dim / group >= 4) ? 2 : 1;   // (many rows, small groups: 237 TFLOP/s, one 263)
   p.tm = 16 * p.nq * (p.tile ? 4 : 1);
   p.tiles = (int)((per + p.tm - 1) / p.tm);
   p.slots = (int)(uniform ? b * p.tiles : tq * g / p.tm + (b < tq ? b : tq));
-  // Runs enough to fill the card once, by what registers and LDS let a CU hold (16 sequences of up to 8192, g =
-  // 128: 768 runs 35 us, 512 38, 1024 38; 131072 tokens, g = 64: 512 47, 768 50).  Many rows: 512 (one
+  // Few rows: 512 runs, or 768, as many as a CU holds three of, for batches of 16 rows of heads of 128 and g = 128 (us by
+  // 512, 768 and 1024 runs: 16 sequences of up to 8192 34.7, 34.8, 37.9; 8 of 32768 46.8, 43.3, 46.9; 5 drafts of 8 over
+  // 3001, 40 heads 29.6, 25.5, 29.5).  Elsewhere more gain less or nothing (16 of up to 8192: heads of 64 27.7, 26.3, 27.2;
+  // g = 64 39.6, 38.9, 41.4; g = 32 51.5, 48.0, 51.5; heads of 256 54.4, 57.1, 60.8; float32 39.5, 42.7, 44.1; one of 131072
+  // tokens, g = 64 41.4, 42.5, 45.2).  Many rows: 512 (one
   // sequence of 65536 tokens: 438 TFLOP/s, 768 384; 2 of 8192, 256 queries: 568 and 497), but some tiles of `slots`
   // are idle where queries are uneven (560, 512 and 768 runs, TFLOP/s: 3 sequences of up to 3000 and 500 queries 419,
   // 362, 402; 8 of up to 2048 and 300 394, 387, 318; 2 of up to 1500 and 900 337, 271, 333).  However many tiles there
@@ -69,7 +76,8 @@ inline Kv4Plan kv4_plan(int64_t b, int64_t tq, bool uniform, int64_t hq, int64_t
   const int64_t units = p.slots * hkv, tokens = (cap + 31) / 32, spare = cap > 2048 ? 256 : 0;
   const int64_t extra = ((want - units > spare ? want - units : spare) + hkv - 1) / hkv;
   const int64_t useful = p.slots * ((tokens + p.least - 1) / p.least - 1);   // runs are no shorter than `least`
-  // every wave goes through all lengths to cut: not for thousands of sequences, which fill the card by themselves
+  // every wave goes through all lengths to cut: not for thousands of sequences, which fill the card by themselves but
+  // for a long one among them (131072 tokens among 1023 of 100, 8 + 1 heads: 155 us, among 1024: 995)
   p.extra = b > 1024 || units * p.tm >= (1 << 23) ? 0 : (int)(extra < useful ? extra : useful);
   const int64_t most = (tokens + p.least - 1) / p.least;
   p.most = (int)(most < p.extra / p.slots + 1 ? most : p.extra / p.slots + 1);
