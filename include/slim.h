@@ -630,8 +630,9 @@ int slim_kv4_attention(const void *q, int qdt, int64_t tq, int64_t hq, const uin
  * one, then -1.  Everything is computed in float64.  A token >= v is refused.
  * A row without a distribution (a NaN or +inf among its logits, or nothing but
  * -inf) accepts nothing; if there is nothing to draw from (such a row, or p_j
- * nowhere above q_j) the drawn id is -1.  Differences p_j - q_j up to 2^-44 p_j
- * count as 0.
+ * nowhere above q_j) the drawn id is -1.  Differences p_j - q_j up to 2^-44 p_j,
+ * and where one is drawn powers e^((x - the row's greatest) / temperature) below
+ * 2^-1020, count as 0.
  * 0 <= b <= SLIM_DRAFT_MAX_B (0 is a no-op), 1 <= k <= SLIM_DRAFT_MAX_K,
  * 1 <= v <= SLIM_LOGPROB_MAX_V, b (2 k + 1) v <= 2^36, temperature positive, it
  * and 1 / temperature finite.  Workspace:

@@ -767,6 +767,17 @@ def test_verify_draft_ends(slim):
     assert acc[2] == 2 and ids[4, 0] == -1 and ids[6, 0] == -1 and ids[7, 0] == 5 and acc[9] == 2 and ids[9, 2] == -1
 
 
+@pytest.mark.parametrize("far,drawn", [(-30.0, 9), (-706.0, 9), (-708.0, -1), (-800.0, -1)])
+def test_verify_draft_least_powers(slim, far, drawn):
+    """What is left to draw from is one entry e^far of the greatest: 2^-1018.5 counts, 2^-1021.4 is 0, as the header has it."""
+    target = torch.full((1, 2, 300), -float("inf"))
+    target[0, :, 3] = 0.0
+    dr = target[:, :1].clone()
+    target[0, :, 9] = far
+    out = slim.verify_draft(target.cuda(), _gpu(np.array([[5]])), _gpu(np.array([[0.5, 0.5]], np.float32)), draft=dr.cuda())
+    assert int(out["accepted"][0]) == 0 and out["ids"][0].tolist() == [drawn, -1]
+
+
 def test_verify_draft_shared_rows(slim):
     """One target row for every sequence (stride 0), and no sequences at all."""
     target, dr, tokens, uniform = _drafts(2, 6, 2, 500, "bf16")
